@@ -343,6 +343,134 @@ int kv_retrieve_chunks_cachegen(const kv_paged* paged, const kv_seq* seqs, const
                                 int64_t* out_tokens, void* workspace, size_t workspace_bytes,
                                 hipStream_t stream);
 
+/* ---- A model step on the paged pool: append, attend, weights, evict.
+ *
+ * A step gives every sequence some new tokens (one when decoding, a prompt or
+ * a part of one before).  Their q, k and v are rows of one array; sequence s
+ * has rows [q_start[s], q_start[s+1]).  lens[s] counts the tokens in the
+ * sequence's own pages AFTER the step: the new tokens are the last
+ * q_start[s+1] - q_start[s] of them.  Sequences that share a prefix form a
+ * group: its pages are in their own table, held once, ahead of every own
+ * token.  Tables, lengths, rows and groups are read on the device when the
+ * kernels run, so a captured graph follows their changes; the host gives
+ * bounds, which size the launches, and what exceeds a bound is cut to it.
+ * A page id outside the pool leaves its tokens out (not written, not seen)
+ * and sets fault bit 1.  Limits: num_pages * page_size < 2^31; attention and
+ * weights need head_dim % 8 == 0 and head_dim <= 256.  Every call works on
+ * the current device; workspaces are DEVICE memory, 256-byte aligned, whose
+ * contents on entry do not matter, and calls that share one must be ordered. */
+typedef struct {
+    int32_t n;            /* sequences (rows of the table), at most 2^24 */
+    int32_t max_len;      /* bound of lens; <= stride * page_size */
+    const int32_t* table; /* DEVICE int32[n][stride]: page id of tokens [P*i, P*(i+1)); only the entries of the
+                             first lens tokens are read */
+    int64_t stride;       /* entries of a row */
+    const int32_t* lens;  /* DEVICE int32[n]: tokens cached */
+} kv_tables;
+
+typedef struct {
+    kv_tables own;              /* the sequences and their own pages */
+    kv_tables prefix;           /* the groups' shared prefixes; n = 0: none */
+    const int32_t* q_start;     /* DEVICE int32[own.n + 1], ascending */
+    const int32_t* group_start; /* DEVICE int32[prefix.n + 1], ascending: group g holds sequences
+                                   [group_start[g], group_start[g+1]); a sequence of no group has no prefix */
+    int32_t n_rows;             /* rows of q, k and v */
+    int32_t max_new;            /* bound of one sequence's rows */
+    int32_t max_group_rows;     /* bound of one group's rows */
+} kv_step;
+
+typedef enum { KV_TYPE_BF16 = 0, KV_TYPE_FP16 = 1, KV_TYPE_FP32 = 2 } kv_type;
+
+/* [n_rows][heads][head_dim] on the DEVICE, the last dimension contiguous,
+ * strides in elements (so q, k and v can be parts of one projection's rows). */
+typedef struct {
+    void* data;
+    int64_t row_stride, head_stride;
+} kv_rows;
+
+/* Rotary positions: pair j of a head's first `rot` elements -- (j, j + rot/2),
+ * or (2j, 2j + 1) when interleaved -- turns by position * freqs[j], times
+ * gain; the other elements pass. */
+typedef struct {
+    const double* freqs; /* DEVICE float64[rot / 2]: radians per position (any scaling for long contexts is in here) */
+    int32_t rot;         /* even, <= head_dim and <= 512; 0: nothing is rotated */
+    int32_t interleaved;
+    float gain;
+} kv_rope;
+
+/* What eviction knows of the cached tokens, per slot (token in the own pages
+ * in table order), contiguous [layers of the call][n][heads][cap]. */
+typedef struct {
+    float* weights;     /* DEVICE: accumulated attention weight */
+    int32_t* positions; /* DEVICE: position of the token in the slot */
+    int32_t heads;      /* num_kv_heads (each head evicts on its own) or 1 (a token stays or goes with all heads) */
+    int64_t cap;        /* slots of a row, >= max_len */
+} kv_slots;
+
+typedef struct {
+    const float* in; /* DEVICE float32 [n][num_kv_heads][cap]; NULL: zeros; may be out */
+    float* out;      /* DEVICE, same shape */
+    int64_t cap;
+} kv_sums;
+
+/* Rotate the new tokens' q into q_out and write their rotated k and their v
+ * into layer `layer`'s pages, in one launch.  q, k and v have one type; q_out
+ * has it too, or is bf16; q and q_out may both be NULL (then q_heads and
+ * q_out_type are not looked at), and q_out may be q itself.  The arithmetic
+ * is float32 with angles formed in 64 bits, each result rounded once.
+ * positions: DEVICE int32[n_rows], any value.  A row of no sequence gets its
+ * q_out and is not cached; tokens that a too small lens[s] leaves no slot for
+ * are not cached either.  slots (NULL: none): one layer's weights of the new
+ * slots are set to 0 and their positions to the tokens'.  The slots written
+ * by one call must be distinct. */
+int kv_append(const kv_paged* paged, const kv_step* step, int32_t layer, const kv_rows* q, const kv_rows* k,
+              const kv_rows* v, const kv_rows* q_out, int32_t q_heads, kv_type type, kv_type q_out_type,
+              const int32_t* positions, const kv_rope* rope, const kv_slots* slots, hipStream_t stream);
+
+/* Attention of the new tokens (bf16 q, [n_rows][q_heads][head_dim]; q_heads a
+ * multiple of num_kv_heads, consecutive query heads share a KV head): each row
+ * sees the whole prefix of its sequence's group and the own tokens up to
+ * itself.  out (bf16) = softmax(scale * q.k) v; lse (DEVICE float32
+ * [n_rows][q_heads]) = log sum exp(scale * q.k).  A row that sees nothing gets
+ * out 0 and lse -infinity; rows of no sequence are left as they were.  What a
+ * row does not see never reaches it, NaN and infinities included.  A group's
+ * prefix is read once for all its sequences.  scale > 0; q needs 16-byte
+ * aligned address and strides, out 8-byte aligned ones.
+ * kv_attend_workspace_bytes depends on the bounds only; 0 on a malformed
+ * argument. */
+size_t kv_attend_workspace_bytes(const kv_paged* paged, const kv_step* step, int32_t q_heads);
+int kv_attend(const kv_paged* paged, const kv_step* step, int32_t layer, const kv_rows* q, int32_t q_heads,
+              float scale, const kv_rows* out, float* lse, void* workspace, size_t workspace_bytes,
+              hipStream_t stream);
+
+/* Add to every cached token's sum the attention weight that the new tokens
+ * give it: sums->out[s][h][t] = in[s][h][t] + sum over the rows that see token
+ * t and the query heads of KV head h of exp(scale * q.k_t - lse[row]), with
+ * the lse of kv_attend (a row whose lse is -infinity adds nothing).  prefix:
+ * the same per group over all its sequences' rows.  Either may be NULL: then
+ * those sums are not computed.  Entries at and past lens are left as they
+ * were.  No atomics: the same call gives the same bits. */
+int kv_add_weights(const kv_paged* paged, const kv_step* step, int32_t layer, const kv_rows* q, const float* lse,
+                   int32_t q_heads, float scale, const kv_sums* own, const kv_sums* prefix, hipStream_t stream);
+
+/* Evict down to `keep` tokens, for layers [layer_begin, layer_end) at once: of
+ * a row (layer, sequence, head of slots) with n = lens[s] > keep tokens, the
+ * `recent` newest (positions above the largest one minus recent) and, of the
+ * others, those with the largest weights stay, ties to the lowest slot, a NaN
+ * below every number; keep in all.  Kept tokens in slots >= keep move -- K, V,
+ * weight and position -- into the free slots below, the k-th to the k-th, both
+ * ascending; the others do not move.  Rows with n <= keep stay as they are.
+ * out_lens[s] (DEVICE, not `lens` itself) = min(lens[s], keep): the lengths
+ * for the next step; pages past them are the caller's to reuse.  out's first
+ * min(n, keep) slots of each row are written; out may be in (both of its
+ * arrays), then only moved slots are.  The pages of one call must be
+ * distinct.  Shared prefixes are evicted by passing their table. */
+size_t kv_evict_workspace_bytes(const kv_paged* paged, const kv_tables* tables, int32_t n_layers, int32_t heads,
+                                int32_t keep);
+int kv_evict(const kv_paged* paged, const kv_tables* tables, int32_t layer_begin, int32_t layer_end,
+             const kv_slots* in, const kv_slots* out, int32_t keep, int32_t recent, int32_t* out_lens,
+             void* workspace, size_t workspace_bytes, hipStream_t stream);
+
 /* Message for the last non-OK return on this thread ("" if none). */
 const char* kv_last_error(void);
 

@@ -27,6 +27,7 @@ __all__ = ["FMT_BF16", "FMT_FP8", "FMT_FP8_E5M2", "FMT_K16_V8", "FMT_CACHEGEN", 
            "store", "store_layer", "store_layers", "store_cachegen", "retrieve_cachegen",
            "retrieve", "retrieve_noalloc", "retrieve_layer", "retrieve_layer_ex", "retrieve_layers", "take_faults",
            "copy_bytes",
+           "Tables", "Step", "Rope", "append", "attend", "add_weights", "evict",
            "library_path", "load"]
 
 FMT_BF16 = 0          # K and V bf16, copied bit for bit
@@ -73,6 +74,46 @@ class _KvSeq(ctypes.Structure):
     ]
 
 
+class _KvTables(ctypes.Structure):
+    _fields_ = [
+        ("n", ctypes.c_int32),
+        ("max_len", ctypes.c_int32),
+        ("table", ctypes.c_void_p),
+        ("stride", ctypes.c_int64),
+        ("lens", ctypes.c_void_p),
+    ]
+
+
+class _KvStep(ctypes.Structure):
+    _fields_ = [
+        ("own", _KvTables),
+        ("prefix", _KvTables),
+        ("q_start", ctypes.c_void_p),
+        ("group_start", ctypes.c_void_p),
+        ("n_rows", ctypes.c_int32),
+        ("max_new", ctypes.c_int32),
+        ("max_group_rows", ctypes.c_int32),
+    ]
+
+
+class _KvRows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class _KvRope(ctypes.Structure):
+    _fields_ = [("freqs", ctypes.c_void_p), ("rot", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("gain", ctypes.c_float)]
+
+
+class _KvSlots(ctypes.Structure):
+    _fields_ = [("weights", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("heads", ctypes.c_int32),
+                ("cap", ctypes.c_int64)]
+
+
+class _KvSums(ctypes.Structure):
+    _fields_ = [("inp", ctypes.c_void_p), ("out", ctypes.c_void_p), ("cap", ctypes.c_int64)]
+
+
 def library_path() -> str:
     return _LIB_PATH
 
@@ -87,6 +128,7 @@ def load():
                                "`python -m paged_kv_movement_amd.build` (there is no fallback)")
     L = ctypes.CDLL(_LIB_PATH)
     P, S = ctypes.POINTER(_KvPaged), ctypes.POINTER(_KvSeq)
+    T, B, R, O, W, M = (ctypes.POINTER(c) for c in (_KvStep, _KvTables, _KvRows, _KvRope, _KvSlots, _KvSums))
     i32, i64, vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p
     sig = {
         "kv_chunk_bytes": (ctypes.c_size_t, [P, i64, ctypes.c_int]),
@@ -107,6 +149,12 @@ def load():
         "kv_retrieve_chunks_ws": (ctypes.c_int, [P, S, vp, ctypes.c_int, ctypes.c_int, vp, vp, ctypes.c_size_t, vp]),
         "kv_retrieve_chunks_noalloc": (ctypes.c_int, [P, S, vp, ctypes.c_int, ctypes.c_int, vp, vp]),
         "kv_retrieve_chunks_cachegen": (ctypes.c_int, [P, S, vp, ctypes.c_int, vp, vp, vp, vp, ctypes.c_size_t, vp]),
+        "kv_append": (ctypes.c_int, [P, T, i32, R, R, R, R, i32, ctypes.c_int, ctypes.c_int, vp, O, W, vp]),
+        "kv_attend_workspace_bytes": (ctypes.c_size_t, [P, T, i32]),
+        "kv_attend": (ctypes.c_int, [P, T, i32, R, i32, ctypes.c_float, R, vp, vp, ctypes.c_size_t, vp]),
+        "kv_add_weights": (ctypes.c_int, [P, T, i32, R, vp, i32, ctypes.c_float, M, M, vp]),
+        "kv_evict_workspace_bytes": (ctypes.c_size_t, [P, B, i32, i32, i32]),
+        "kv_evict": (ctypes.c_int, [P, B, i32, i32, W, W, i32, i32, vp, vp, ctypes.c_size_t, vp]),
         "kv_last_error": (ctypes.c_char_p, []),
         "kv_take_faults": (ctypes.c_int, []),
         "kv_copy_bytes": (ctypes.c_int, [vp, vp, ctypes.c_size_t, vp]),
@@ -578,3 +626,344 @@ def copy_blocks(dst, src, nbytes: int, block_bytes: int, permute: int, stream=No
     kv_copy_blocks): permute = COPY_SCATTERED_READS or COPY_SCATTERED_WRITES."""
     _check(load().kv_copy_blocks(dst.data_ptr(), src.data_ptr(), nbytes, block_bytes, permute,
                                  _stream_handle(stream)))
+
+
+# ---- a model step on the paged pool: append, attend, add_weights, evict
+
+def _here(*tensors) -> None:
+    """Every tensor on the current device (the calls launch there)."""
+    import torch
+    cur = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and not (t.is_cuda and t.device.index == cur):
+            raise KvError(KV_EINVAL, f"every tensor must be on the current device (cuda:{cur}), got {t.device}")
+
+
+def _ref(struct):
+    return None if struct is None else ctypes.byref(struct)
+
+
+class Tables:
+    """Block tables and lengths of a batch, both on the device.
+
+    ``table``: int32 [n, entries], page ids of each sequence in token order (the
+    last dimension contiguous); ``lens``: int32 [n], tokens cached, read when
+    a call's kernels run; ``max_len``: the host's bound of them, which sizes
+    the launches (a longer length is cut to it)."""
+
+    def __init__(self, table, lens, max_len: int):
+        import torch
+        _need(table.dtype == torch.int32 and table.dim() == 2 and table.is_cuda
+              and (table.stride(1) == 1 or table.size(1) <= 1),
+              "table must be an int32 device tensor [sequences, entries], entries contiguous")
+        _need(lens.dtype == torch.int32 and lens.is_contiguous() and lens.is_cuda
+              and tuple(lens.shape) == (table.size(0),), "lens must be a contiguous int32 device tensor [sequences]")
+        _need(0 <= max_len < 1 << 31, "max_len must be in [0, 2^31)")
+        self.table, self.lens, self.max_len, self.n = table, lens, int(max_len), table.size(0)
+        # rows further apart than their entries (a view) are reached through the stride
+        _need(table.size(0) <= 1 or table.stride(0) >= table.size(1), "table's rows must not overlap")
+        self._entries = table.size(1)
+        self.c = _KvTables(self.n, self.max_len, table.data_ptr(), table.stride(0) if self.n > 1 else table.size(1),
+                           lens.data_ptr())
+
+    def _check(self, paged: Paged) -> None:
+        if self.max_len > self._entries * paged.page_size:
+            raise KvError(KV_ERANGE, f"max_len {self.max_len} beyond the block table "
+                                     f"({self._entries} pages of {paged.page_size})")
+
+    def evict_workspace_bytes(self, paged: Paged, n_layers: int, heads: int, keep: int) -> int:
+        """Device bytes evict needs (kv_evict_workspace_bytes)."""
+        n = load().kv_evict_workspace_bytes(ctypes.byref(paged.c), ctypes.byref(self.c), n_layers, heads, keep)
+        if n == 0:
+            _check(KV_EINVAL)
+        return int(n)
+
+    def new_evict_workspace(self, paged: Paged, n_layers: int, heads: int, keep: int):
+        """A device tensor of evict_workspace_bytes (torch aligns it to 256)."""
+        import torch
+        return torch.empty(self.evict_workspace_bytes(paged, n_layers, heads, keep), dtype=torch.uint8,
+                           device=self.table.device)
+
+
+class Step:
+    """One step of a batch: which rows of q, k and v are whose new tokens, and
+    which sequences share a prefix.
+
+    ``own``: Tables of the sequences' own pages, lengths with the new tokens
+    counted; ``new_tokens``: the new tokens of each sequence; ``prefix``:
+    Tables of the shared prefixes, one row per group; ``group_sizes``: the
+    sequences of each group, in order (sequences left over share nothing).
+    The tables' contents and lengths may change between calls; a Step keeps
+    no result."""
+
+    def __init__(self, paged: Paged, own: Tables, new_tokens, prefix: Tables | None = None, group_sizes=None):
+        import torch
+        new = [int(x) for x in new_tokens]
+        sizes = [int(x) for x in (group_sizes or [])]
+        _need(len(new) == own.n and all(x >= 0 for x in new), f"need {own.n} counts of new tokens, none negative")
+        _need(len(sizes) == (0 if prefix is None else prefix.n) and all(x >= 0 for x in sizes),
+              "need one group size per row of prefix, none negative")
+        _need(sum(sizes) <= own.n, "the groups hold more sequences than there are")
+        own._check(paged)
+        if prefix is not None:
+            prefix._check(paged)
+        starts, groups = [0], [0]
+        for x in new:
+            starts.append(starts[-1] + x)
+        for x in sizes:
+            groups.append(groups[-1] + x)
+        _need(starts[-1] < 1 << 31, "too many rows")
+        dev = own.table.device
+        self.own, self.prefix, self.n_rows = own, prefix, starts[-1]
+        self.q_start = torch.tensor(starts, dtype=torch.int32).to(dev)
+        self.group_start = torch.tensor(groups, dtype=torch.int32).to(dev)
+        self.paged = paged
+        self.c = _KvStep(own.c, prefix.c if prefix is not None else _KvTables(), self.q_start.data_ptr(),
+                         self.group_start.data_ptr(), self.n_rows, max(new, default=0),
+                         max((starts[groups[i + 1]] - starts[groups[i]] for i in range(len(sizes))), default=0))
+        self._tensors = [paged.k_addrs, paged.v_addrs, own.table, own.lens, self.q_start, self.group_start]
+        if prefix is not None:
+            self._tensors += [prefix.table, prefix.lens]
+        self._on_streams = set()
+        _here(*self._tensors)
+
+    def attend_workspace_bytes(self, q_heads: int) -> int:
+        """Device bytes attend needs (kv_attend_workspace_bytes)."""
+        n = load().kv_attend_workspace_bytes(ctypes.byref(self.paged.c), ctypes.byref(self.c), q_heads)
+        if n == 0:
+            _check(KV_EINVAL)
+        return int(n)
+
+    def new_attend_workspace(self, q_heads: int):
+        """A device tensor of attend_workspace_bytes (torch aligns it to 256)."""
+        import torch
+        return torch.empty(self.attend_workspace_bytes(q_heads), dtype=torch.uint8, device=self.own.table.device)
+
+    def _rows(self, t, heads, what, types):
+        """(kv_rows of a tensor [n_rows, heads, head_dim], its type)."""
+        _need(t.dtype in types, f"{what} has type {t.dtype}")
+        _need(tuple(t.shape) == (self.n_rows, heads, self.paged.head_dim),
+              f"{what} must be [{self.n_rows}, {heads}, {self.paged.head_dim}], got {list(t.shape)}")
+        row, head, last = t.stride()
+        _need(last == 1 or self.paged.head_dim == 1, f"{what}: the last dimension must be contiguous")
+        return _KvRows(t.data_ptr(), row, head)
+
+    def _call(self, paged, stream, *tensors) -> int | None:
+        _need(paged is self.paged or paged.c.page_size == self.paged.c.page_size
+              and paged.head_dim == self.paged.head_dim and paged.num_kv_heads == self.paged.num_kv_heads,
+              "the step was made for a pool of another shape")
+        _here(*self._tensors, *tensors)
+        if stream is not None:
+            _used_on(stream, self._tensors, self._on_streams)
+            _used_on(stream, tensors)
+        return _stream_handle(stream)
+
+
+class Rope:
+    """Rotary positions: ``rot`` elements of each head turn in pairs, (j, j +
+    rot/2) or, ``interleaved``, (2j, 2j + 1); pair j by position * base^(-2j/rot).
+
+    ``scaling`` for contexts longer than ``original_length``, by ``factor``:
+    "linear" (all positions divided), "ntk" (base * factor^(rot/(rot-2))),
+    "yarn" (pairs of more than ``fast`` turns in the original length stay,
+    those of fewer than ``slow`` are divided, a ramp between; rotated values
+    times 0.1 ln(factor) + 1 unless ``gain`` is given) or "wavelength" (the
+    same by wavelength, with the ramp between ``low`` and ``high`` turns)."""
+
+    def __init__(self, rot: int, base: float = 10000.0, interleaved: bool = False, scaling: str = "none",
+                 factor: float = 1.0, original_length: int = 8192, fast: float = 32.0, slow: float = 1.0,
+                 low: float = 1.0, high: float = 4.0, gain: float | None = None, device="cuda"):
+        import torch
+        f, g = self.frequencies(rot, base, scaling, factor, original_length, fast, slow, low, high)
+        self.rot, self.interleaved = int(rot), bool(interleaved)
+        self.gain = float(g if gain is None else gain)
+        self.freqs = torch.tensor(f, dtype=torch.float64).to(device)
+        self.c = _KvRope(self.freqs.data_ptr(), self.rot, int(self.interleaved), self.gain)
+
+    @staticmethod
+    def frequencies(rot, base=10000.0, scaling="none", factor=1.0, original_length=8192, fast=32.0, slow=1.0,
+                    low=1.0, high=4.0):
+        """(radians per position of each pair, gain), in Python's 64-bit floats."""
+        import math
+        _need(rot >= 0 and rot % 2 == 0, "rot must be even")
+        _need(base > 1.0 and factor > 0.0 and original_length > 0, "need base > 1, factor > 0, original_length > 0")
+        _need(scaling in ("none", "linear", "ntk", "yarn", "wavelength"), f"unknown scaling {scaling!r}")
+        gain = 1.0
+        if scaling == "ntk":
+            _need(rot >= 4, "ntk needs rot >= 4")
+            base = base * factor ** (rot / (rot - 2))
+        f = [base ** (-2.0 * j / rot) for j in range(rot // 2)]
+        if scaling == "linear":
+            f = [x / factor for x in f]
+        elif scaling == "yarn":
+            _need(fast > slow > 0.0, "need fast > slow > 0")
+
+            def pair_of(turns):
+                return rot * math.log(original_length / (turns * 2 * math.pi)) / (2 * math.log(base))
+            lo, hi = max(math.floor(pair_of(fast)), 0), min(math.ceil(pair_of(slow)), rot - 1)
+            keep = [1.0 - min(max((j - lo) / max(hi - lo, 0.001), 0.0), 1.0) for j in range(rot // 2)]
+            f = [x / factor * (1.0 - k) + x * k for x, k in zip(f, keep)]
+            gain = 0.1 * math.log(factor) + 1.0 if factor > 1.0 else 1.0
+        elif scaling == "wavelength":
+            _need(high > low, "need high > low")
+            turns = [original_length * x / (2 * math.pi) for x in f]
+            keep = [min(max((t - low) / (high - low), 0.0), 1.0) for t in turns]
+            f = [(1.0 - k) * x / factor + k * x for x, k in zip(f, keep)]
+        return f, gain
+
+
+def _types():
+    import torch
+    return {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def _slots(weights, positions, shape, what):
+    """kv_slots of contiguous [*shape, heads, cap] tensors."""
+    import torch
+    for t, dt, name in ((weights, torch.float32, "weights"), (positions, torch.int32, "positions")):
+        _need(t is not None and t.dtype == dt and t.is_contiguous() and t.dim() == len(shape) + 2
+              and tuple(t.shape[:len(shape)]) == tuple(shape),
+              f"{what} {name} must be a contiguous {dt} device tensor {list(shape)} + [heads, slots]")
+    _need(weights.shape == positions.shape, f"{what} weights and positions must have one shape")
+    return _KvSlots(weights.data_ptr(), positions.data_ptr(), weights.shape[-2], weights.shape[-1])
+
+
+def append(paged: Paged, step: Step, layer: int, q, k, v, positions, rope: Rope, q_out=None, weights=None,
+           slot_positions=None, stream=None):
+    """Rotate the new tokens' q and k and write k and v into layer ``layer``'s
+    pages (kv_append).  q [rows, q_heads, D] (None: only k and v), k and v
+    [rows, H, D]: bf16, fp16 or float32, any row and head strides;
+    ``positions``: int32 [rows].  ``q_out``: where the rotated q goes (q
+    itself, or a tensor of q's type or bf16; None: a new tensor of q's type).
+    ``weights`` / ``slot_positions`` [sequences, H or 1, slots]: this layer's
+    eviction state; the new slots' weights become 0 and their positions the
+    tokens'.  Returns the rotated q."""
+    import torch
+    types = _types()
+    st = step
+    H = paged.num_kv_heads
+    ck, cv = st._rows(k, H, "k", types), st._rows(v, H, "v", types)
+    _need(k.dtype == v.dtype and (q is None or q.dtype == k.dtype), "q, k and v must have one type")
+    _need(positions.dtype == torch.int32 and positions.is_contiguous() and tuple(positions.shape) == (st.n_rows,),
+          f"positions must be a contiguous int32 device tensor [{st.n_rows}]")
+    cq = co = None
+    q_heads, out_type = 0, types[k.dtype]
+    if q is not None:
+        _need(q.dim() == 3, "q must be [rows, q_heads, head_dim]")
+        q_heads = q.shape[1]
+        cq = st._rows(q, q_heads, "q", types)
+        if q_out is None:
+            q_out = torch.empty((st.n_rows, q_heads, paged.head_dim), dtype=q.dtype, device=q.device)
+        co = st._rows(q_out, q_heads, "q_out", (q.dtype, torch.bfloat16))
+        out_type = types[q_out.dtype]
+    else:
+        _need(q_out is None, "q_out without q")
+    cs = None
+    if weights is not None or slot_positions is not None:
+        cs = _slots(weights, slot_positions, (st.own.n,), "append:")
+    h = st._call(paged, stream, q, k, v, positions, rope.freqs, q_out, weights, slot_positions)
+    _check(load().kv_append(ctypes.byref(paged.c), ctypes.byref(st.c), layer, _ref(cq), ctypes.byref(ck),
+                            ctypes.byref(cv), _ref(co), q_heads, types[k.dtype], out_type, positions.data_ptr(),
+                            ctypes.byref(rope.c), _ref(cs), h))
+    return q_out
+
+
+def _q(paged, step, q):
+    import torch
+    _need(q.dim() == 3, "q must be [rows, q_heads, head_dim]")
+    return step._rows(q, q.shape[1], "q", (torch.bfloat16,)), q.shape[1]
+
+
+def _scale(paged, scale) -> float:
+    return paged.head_dim ** -0.5 if scale is None else float(scale)
+
+
+def attend(paged: Paged, step: Step, layer: int, q, scale=None, out=None, lse=None, workspace=None, stream=None):
+    """Attention of the new tokens' bf16 q [rows, q_heads, D] over their
+    group's shared prefix and their own pages up to themselves (kv_attend).
+    ``scale``: 1/sqrt(D) unless given.  ``workspace``: a device uint8 tensor of
+    step.attend_workspace_bytes(q_heads) (None: one is allocated for the call).
+    Returns (out bf16 like q, lse float32 [rows, q_heads])."""
+    import torch
+    cq, heads = _q(paged, step, q)
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if lse is None:
+        lse = torch.empty((step.n_rows, heads), dtype=torch.float32, device=q.device)
+    co = step._rows(out, heads, "out", (torch.bfloat16,))
+    _need(lse.dtype == torch.float32 and lse.is_contiguous() and tuple(lse.shape) == (step.n_rows, heads),
+          f"lse must be a contiguous float32 device tensor [{step.n_rows}, {heads}]")
+    if workspace is None:
+        workspace = step.new_attend_workspace(heads)
+    ws, n_ws = _workspace(workspace)
+    h = step._call(paged, stream, q, out, lse, workspace)
+    _check(load().kv_attend(ctypes.byref(paged.c), ctypes.byref(step.c), layer, ctypes.byref(cq), heads,
+                            _scale(paged, scale), ctypes.byref(co), lse.data_ptr(), ws, n_ws, h))
+    return out, lse
+
+
+def _sums(inp, out, n, heads, what):
+    import torch
+    if out is None:
+        out = inp
+    if out is None:
+        return None, None
+    for t in (inp, out):
+        _need(t is None or (t.dtype == torch.float32 and t.is_contiguous() and t.dim() == 3
+                            and tuple(t.shape[:2]) == (n, heads) and t.shape == out.shape),
+              f"{what} must be contiguous float32 device tensors [{n}, {heads}, slots] of one shape")
+    return _KvSums(inp.data_ptr() if inp is not None else None, out.data_ptr(), out.shape[2]), out
+
+
+def add_weights(paged: Paged, step: Step, layer: int, q, lse, weights=None, prefix_weights=None, scale=None,
+                out=None, prefix_out=None, stream=None):
+    """Add the attention weights of the new tokens' q to every cached token's
+    running sum (kv_add_weights): ``weights`` [sequences, H, slots] for the
+    own pages, ``prefix_weights`` [groups, H, slots] for the shared prefixes
+    (either may be None: not computed), in place, or into ``out`` /
+    ``prefix_out`` (with weights None: from zero).  ``lse``: what attend
+    returned.  Returns (own sums, prefix sums)."""
+    import torch
+    cq, heads = _q(paged, step, q)
+    _need(lse.dtype == torch.float32 and lse.is_contiguous() and tuple(lse.shape) == (step.n_rows, heads),
+          f"lse must be a contiguous float32 device tensor [{step.n_rows}, {heads}]")
+    co, out = _sums(weights, out, step.own.n, paged.num_kv_heads, "weights")
+    cp, prefix_out = _sums(prefix_weights, prefix_out, step.prefix.n if step.prefix is not None else 0,
+                           paged.num_kv_heads, "prefix weights")
+    h = step._call(paged, stream, q, lse, weights, prefix_weights, out, prefix_out)
+    _check(load().kv_add_weights(ctypes.byref(paged.c), ctypes.byref(step.c), layer, ctypes.byref(cq),
+                                 lse.data_ptr(), heads, _scale(paged, scale), _ref(co), _ref(cp), h))
+    return out, prefix_out
+
+
+def evict(paged: Paged, tables: Tables, layer_begin: int, layer_end: int, weights, positions, keep: int,
+          recent: int = 0, out_weights=None, out_positions=None, out_lens=None, workspace=None, stream=None):
+    """Evict each (layer, sequence, head) down to ``keep`` tokens by weight,
+    the ``recent`` newest protected, and move what stays into the first slots
+    (kv_evict).  ``weights`` float32 and ``positions`` int32 [layers, sequences,
+    H or 1, slots], updated in place unless out_weights / out_positions
+    [layers, sequences, H or 1, >= keep] are given.  ``workspace``: a device
+    uint8 tensor of tables.evict_workspace_bytes(...) (None: allocated for the
+    call).  Returns the new lengths, an int32 tensor [sequences]."""
+    import torch
+    shape = (layer_end - layer_begin, tables.n)
+    ci = _slots(weights, positions, shape, "evict:")
+    if out_weights is None and out_positions is None:
+        out_weights, out_positions, co = weights, positions, ci
+    else:
+        co = _slots(out_weights, out_positions, shape, "evict: out")
+    tables._check(paged)
+    if out_lens is None:
+        out_lens = torch.empty((tables.n,), dtype=torch.int32, device=tables.table.device)
+    _need(out_lens.dtype == torch.int32 and out_lens.is_contiguous() and tuple(out_lens.shape) == (tables.n,),
+          f"out_lens must be a contiguous int32 device tensor [{tables.n}]")
+    if workspace is None:
+        workspace = tables.new_evict_workspace(paged, shape[0], ci.heads, keep)
+    ws, n_ws = _workspace(workspace)
+    used = (paged.k_addrs, paged.v_addrs, tables.table, tables.lens, weights, positions, out_weights, out_positions,
+            out_lens, workspace)
+    _here(*used)
+    _used_on(stream, used)
+    _check(load().kv_evict(ctypes.byref(paged.c), ctypes.byref(tables.c), layer_begin, layer_end, ctypes.byref(ci),
+                           ctypes.byref(co), keep, recent, out_lens.data_ptr(), ws, n_ws, _stream_handle(stream)))
+    return out_lens

@@ -1,0 +1,102 @@
+// kv_step.hpp -- what the kernels of a model step share (append, attend,
+// weights, evict): the layer's pool, block tables with their lengths on the
+// device, and the new tokens' rows.
+//
+// Lengths, row ranges and groups are read from device memory, so a captured
+// graph follows them; every value read is cut to the bound that the host
+// gave, which sizes the grids and the workspaces, and no access depends on
+// the device values alone.  A page id outside the pool makes its tokens
+// invisible (or unwritten) and sets a fault bit.
+#pragma once
+
+#include "kv_common.hpp"
+
+namespace kvmove {
+
+using f32x4 = __attribute__((ext_vector_type(4))) float;
+using bf16x8 = __attribute__((ext_vector_type(8))) __bf16;
+using gf32x4 = __attribute__((address_space(1))) f32x4;
+
+struct PoolArg {
+    uint64_t k_pages;        // uint64[L]: layer K pool addresses
+    uint64_t v_pages;
+    uint32_t num_pages;
+    uint32_t page_size;
+    uint32_t page_magic;     // t / page_size = (t * page_magic) >> page_shift for t < 2^31
+    uint32_t page_shift;
+    uint32_t heads;          // KV heads
+    uint32_t dim;            // elements of a head
+    int32_t layer;
+};
+
+struct TablesArg {
+    uint64_t table;          // int32[n][stride]: page ids
+    uint64_t lens;           // int32[n]: tokens cached
+    int64_t stride;
+    int32_t n;
+    int32_t max_len;         // lens beyond it are cut to it
+};
+
+struct StepArg {
+    TablesArg own;
+    TablesArg prefix;
+    uint64_t q_start;        // int32[own.n + 1]: first new-token row of each sequence
+    uint64_t group_start;    // int32[prefix.n + 1]: first sequence of each group
+    int32_t n_rows;
+    int32_t max_new;         // rows of one sequence beyond it are not taken
+    int32_t max_group_rows;  // rows of one group beyond it are not taken
+};
+
+struct Rows {
+    int32_t first, count;
+};
+
+__device__ __forceinline__ int32_t clamp_i32(int32_t x, int32_t lo, int32_t hi)
+{
+    return x < lo ? lo : x > hi ? hi : x;
+}
+
+__device__ __forceinline__ int32_t table_len(const TablesArg& t, int32_t i)
+{
+    return clamp_i32(gptr<const gi32>(t.lens)[i], 0, t.max_len);
+}
+
+__device__ __forceinline__ Rows seq_rows(const StepArg& a, int32_t s)
+{
+    const int32_t b = clamp_i32(gptr<const gi32>(a.q_start)[s], 0, a.n_rows);
+    const int32_t e = clamp_i32(gptr<const gi32>(a.q_start)[s + 1], b, a.n_rows);
+    return {b, e - b < a.max_new ? e - b : a.max_new};
+}
+
+__device__ __forceinline__ Rows group_rows(const StepArg& a, int32_t g)
+{
+    const int32_t s0 = clamp_i32(gptr<const gi32>(a.group_start)[g], 0, a.own.n);
+    const int32_t s1 = clamp_i32(gptr<const gi32>(a.group_start)[g + 1], s0, a.own.n);
+    const int32_t b = clamp_i32(gptr<const gi32>(a.q_start)[s0], 0, a.n_rows);
+    const int32_t e = clamp_i32(gptr<const gi32>(a.q_start)[s1], b, a.n_rows);
+    return {b, e - b < a.max_group_rows ? e - b : a.max_group_rows};
+}
+
+__device__ __forceinline__ uint32_t page_of(const PoolArg& p, uint32_t t)
+{
+    return uint32_t((uint64_t(t) * p.page_magic) >> p.page_shift);
+}
+
+// Index of the interval [start[i], start[i + 1]) that holds x, or -1; every
+// lane of the wave gets it.  One load per 64 intervals and no dependent chain.
+__device__ __forceinline__ int32_t wave_find(uint64_t start, int32_t n, int32_t x)
+{
+    const int32_t lane = threadIdx.x & 63;
+    for (int32_t i0 = 0; i0 < n; i0 += 64) {
+        const int32_t i = i0 + lane;
+        bool here = false;
+        if (i < n) here = gptr<const gi32>(start)[i] <= x && x < gptr<const gi32>(start)[i + 1];
+        const uint64_t m = __ballot(here);
+        if (m != 0) return i0 + __builtin_ctzll(m);
+    }
+    return -1;
+}
+
+__device__ __forceinline__ void raise_fault_lane(unsigned bit) { atomicOr(&g_kv_faults, bit); }
+
+}  // namespace kvmove

@@ -1,0 +1,507 @@
+// kv_step_entry.hpp -- host side of the model-step entry points (append,
+// attend, weights, evict): argument checks, launch shapes, workspaces.
+// Included by kvmove.hip, whose helpers (fail, ok, check_paged, ceil_div,
+// max_blocks) it uses.
+#pragma once
+
+namespace {
+
+int check_tables(const kv_paged* p, const kv_tables* t, const char* what)
+{
+    if (t->n < 0 || t->n > (1 << 24)) return fail(KV_EINVAL, "%s: %d sequences outside [0, 2^24]", what, t->n);
+    if (t->max_len < 0) return fail(KV_EINVAL, "%s: max_len < 0", what);
+    if (t->n == 0) return KV_OK;
+    if (t->lens == nullptr) return fail(KV_EINVAL, "%s: lens is NULL", what);
+    if (t->max_len > 0 && t->table == nullptr) return fail(KV_EINVAL, "%s: table is NULL", what);
+    if (t->stride < 0 || t->stride > INT32_MAX)
+        return fail(KV_EINVAL, "%s: stride %lld outside [0, 2^31)", what, (long long)t->stride);
+    if (t->max_len > t->stride * p->page_size)
+        return fail(KV_ERANGE, "%s: max_len %d beyond the block table (%lld pages of %d)", what, t->max_len,
+                    (long long)t->stride, p->page_size);
+    return KV_OK;
+}
+
+// The pool as the step kernels take it: rows of a layer are numbered in 31 bits.
+int check_step_pool(const kv_paged* p, int32_t layer_begin, int32_t layer_end)
+{
+    int rc = check_paged(p);
+    if (rc != KV_OK) return rc;
+    if (layer_begin < 0 || layer_end <= layer_begin || layer_end > p->num_layers)
+        return fail(KV_EINVAL, "layers [%d, %d) are not a non-empty range inside [0, %d)", layer_begin, layer_end,
+                    p->num_layers);
+    if (p->num_pages > INT32_MAX / p->page_size)
+        return fail(KV_EINVAL, "num_pages * page_size = %lld * %d rows: must stay below 2^31",
+                    (long long)p->num_pages, p->page_size);
+    return KV_OK;
+}
+
+int check_step(const kv_paged* p, const kv_step* s)
+{
+    if (s == nullptr) return fail(KV_EINVAL, "step is NULL");
+    int rc = check_tables(p, &s->own, "own");
+    if (rc == KV_OK) rc = check_tables(p, &s->prefix, "prefix");
+    if (rc != KV_OK) return rc;
+    if (s->n_rows < 0 || s->max_new < 0 || s->max_group_rows < 0)
+        return fail(KV_EINVAL, "n_rows, max_new and max_group_rows must be >= 0");
+    if (s->own.n > 0 && s->q_start == nullptr) return fail(KV_EINVAL, "q_start is NULL");
+    if (s->prefix.n > 0 && s->group_start == nullptr) return fail(KV_EINVAL, "group_start is NULL");
+    return KV_OK;
+}
+
+bool misaligned(const void* p, uintptr_t to) { return reinterpret_cast<uintptr_t>(p) % to != 0; }
+
+// [n_rows][heads][dim] with strides in elements of `size` bytes: vectors of
+// 16 bytes can be used.
+bool rows_vectors(const kv_rows& x, int64_t size)
+{
+    return !misaligned(x.data, 16) && x.row_stride * size % 16 == 0 && x.head_stride * size % 16 == 0;
+}
+
+PoolArg pool_arg(const kv_paged* p, int32_t layer)
+{
+    PoolArg a{};
+    a.k_pages = reinterpret_cast<uint64_t>(p->k_pages);
+    a.v_pages = reinterpret_cast<uint64_t>(p->v_pages);
+    a.num_pages = uint32_t(p->num_pages);
+    a.page_size = uint32_t(p->page_size);
+    // t / P for t < 2^31: with 2^s >= P, magic = floor(2^(31 + s) / P) + 1 is off by at most 2^s / 2^(31 + s)
+    uint32_t s = 0;
+    while ((int64_t(1) << s) < p->page_size) ++s;
+    a.page_magic = uint32_t((uint64_t(1) << (31 + s)) / uint64_t(p->page_size) + 1);
+    a.page_shift = 31 + s;
+    a.heads = uint32_t(p->num_kv_heads);
+    a.dim = uint32_t(p->head_dim);
+    a.layer = layer;
+    return a;
+}
+
+TablesArg tables_arg(const kv_tables* t)
+{
+    return {reinterpret_cast<uint64_t>(t->table), reinterpret_cast<uint64_t>(t->lens), t->stride, t->n, t->max_len};
+}
+
+StepArg step_arg(const kv_step* s)
+{
+    StepArg a{};
+    a.own = tables_arg(&s->own);
+    a.prefix = tables_arg(&s->prefix);
+    a.q_start = reinterpret_cast<uint64_t>(s->q_start);
+    a.group_start = reinterpret_cast<uint64_t>(s->group_start);
+    a.n_rows = s->n_rows;
+    a.max_new = s->max_new;
+    a.max_group_rows = s->max_group_rows;
+    return a;
+}
+
+int launch(KernelFn k, int64_t grid, int block, void* arg, hipStream_t stream, unsigned grid_y = 1)
+{
+    if (grid <= 0) return KV_OK;
+    if (grid > max_blocks(block)) return fail(KV_EINVAL, "%lld workgroups exceed one launch", (long long)grid);
+    void* args[] = {arg};
+    const hipError_t e = hipLaunchKernel(k, dim3(unsigned(grid), grid_y), dim3(block), args, 0, stream);
+    if (e != hipSuccess) return fail(KV_EHIP, "kernel launch failed: %s", hipGetErrorString(e));
+    return KV_OK;
+}
+
+template <class TI, class TO>
+KernelFn append_kernel(bool vectors)
+{
+    return vectors ? reinterpret_cast<KernelFn>(&append_rows<TI, TO, 8>)
+                   : reinterpret_cast<KernelFn>(&append_rows<TI, TO, 1>);
+}
+
+int append(const kv_paged* paged, const kv_step* step, int32_t layer, const kv_rows* q, const kv_rows* k,
+           const kv_rows* v, const kv_rows* q_out, int32_t q_heads, kv_type type, kv_type q_out_type,
+           const int32_t* positions, const kv_rope* rope, const kv_slots* slots, hipStream_t stream)
+{
+    int rc = check_step_pool(paged, layer, layer + 1);
+    if (rc == KV_OK) rc = check_step(paged, step);
+    if (rc != KV_OK) return rc;
+    if (rope == nullptr || k == nullptr || v == nullptr) return fail(KV_EINVAL, "k, v or rope is NULL");
+    if ((q == nullptr) != (q_out == nullptr)) return fail(KV_EINVAL, "q and q_out are given together or not at all");
+    if (type != KV_TYPE_BF16 && type != KV_TYPE_FP16 && type != KV_TYPE_FP32)
+        return fail(KV_EINVAL, "unknown type %d", int(type));
+    if (q != nullptr && q_out_type != type && q_out_type != KV_TYPE_BF16)
+        return fail(KV_EINVAL, "q_out's type must be q's or bf16");
+    if (q != nullptr && q_heads <= 0) return fail(KV_EINVAL, "q_heads must be > 0");
+    if (rope->rot < 0 || rope->rot % 2 != 0 || rope->rot > paged->head_dim || rope->rot > kMaxRot)
+        return fail(KV_EINVAL, "rot = %d must be even and within head_dim = %d and %d", rope->rot, paged->head_dim,
+                    kMaxRot);
+    if (rope->rot > 0 && rope->freqs == nullptr) return fail(KV_EINVAL, "freqs is NULL");
+    if (slots != nullptr) {
+        if (slots->weights == nullptr || slots->positions == nullptr)
+            return fail(KV_EINVAL, "slots: weights and positions must both be given");
+        if (slots->heads != 1 && slots->heads != paged->num_kv_heads)
+            return fail(KV_EINVAL, "slots: heads must be 1 or num_kv_heads (got %d)", slots->heads);
+        if (slots->cap < step->own.max_len)
+            return fail(KV_ERANGE, "slots: cap %lld below max_len %d", (long long)slots->cap, step->own.max_len);
+    }
+    if (step->n_rows == 0) return ok();
+    if (k->data == nullptr || v->data == nullptr || positions == nullptr || (q != nullptr && (q->data == nullptr || q_out->data == nullptr)))
+        return fail(KV_EINVAL, "q, k, v, q_out or positions is NULL");
+    const int64_t size = type == KV_TYPE_FP32 ? 4 : 2, out_size = q_out_type == KV_TYPE_FP32 ? 4 : 2;
+    // 16-byte vectors where every address, stride and the pairs' distance allow them, else element by element
+    const int dim = paged->head_dim, unit = rope->interleaved ? 8 : 16;
+    bool vectors = dim % 8 == 0 && rope->rot % unit == 0 && rows_vectors(*k, size) && rows_vectors(*v, size);
+    if (q != nullptr) vectors = vectors && rows_vectors(*q, size) && rows_vectors(*q_out, out_size);
+    for (const kv_rows* x : {k, v, q})
+        if (x != nullptr && misaligned(x->data, size)) return fail(KV_EINVAL, "q, k or v is not aligned to its type");
+    if (q != nullptr && misaligned(q_out->data, out_size)) return fail(KV_EINVAL, "q_out is not aligned to its type");
+    AppendArgs a{};
+    a.pool = pool_arg(paged, layer);
+    a.step = step_arg(step);
+    auto at = [](const kv_rows* x, uint64_t& data, int64_t& row, int64_t& head) {
+        if (x == nullptr) return;
+        data = reinterpret_cast<uint64_t>(x->data);
+        row = x->row_stride;
+        head = x->head_stride;
+    };
+    at(q, a.q, a.q_row, a.q_head);
+    at(k, a.k, a.k_row, a.k_head);
+    at(v, a.v, a.v_row, a.v_head);
+    at(q_out, a.q_out, a.o_row, a.o_head);
+    a.positions = reinterpret_cast<uint64_t>(positions);
+    a.freqs = reinterpret_cast<uint64_t>(rope->freqs);
+    if (slots != nullptr) {
+        a.weights = reinterpret_cast<uint64_t>(slots->weights);
+        a.slot_positions = reinterpret_cast<uint64_t>(slots->positions);
+        a.w_cap = slots->cap;
+        a.w_heads = slots->heads;
+    }
+    a.rot = rope->rot;
+    a.q_heads = q != nullptr ? q_heads : 0;
+    a.interleaved = rope->interleaved;
+    a.gain = rope->gain;
+    KernelFn f;
+    if (type == KV_TYPE_BF16)
+        f = append_kernel<__bf16, __bf16>(vectors);
+    else if (type == KV_TYPE_FP16)
+        f = q == nullptr || q_out_type == type ? append_kernel<_Float16, _Float16>(vectors)
+                                               : append_kernel<_Float16, __bf16>(vectors);
+    else
+        f = q == nullptr || q_out_type == type ? append_kernel<float, float>(vectors)
+                                               : append_kernel<float, __bf16>(vectors);
+    rc = launch(f, step->n_rows, kAppendBlock, &a, stream);
+    return rc == KV_OK ? ok() : rc;
+}
+
+// ---- attend
+
+// The launch of an attention: how many row tiles and pieces, from the bounds
+// that the host knows.
+struct AttendShape {
+    int32_t prefix_tiles, prefix_pieces, prefix_tokens;
+    int32_t own_tiles, own_pieces, own_tokens;
+    int32_t slots;
+    int64_t prefix_items, own_items;
+    int64_t ml_bytes, bytes;
+};
+
+int check_heads(const kv_paged* p, int32_t q_heads)
+{
+    if (q_heads <= 0 || q_heads % p->num_kv_heads != 0)
+        return fail(KV_EINVAL, "q_heads = %d must be a multiple of num_kv_heads = %d", q_heads, p->num_kv_heads);
+    if (p->head_dim % 8 != 0 || p->head_dim > 256)
+        return fail(KV_EINVAL, "head_dim = %d must be a multiple of 8 and at most 256 here", p->head_dim);
+    return KV_OK;
+}
+
+// Tokens of a piece: enough pieces that all pairs of (row tile, KV head)
+// together give about kItems workgroups, in whole rounds of a workgroup's
+// waves.
+void cut_tokens(int64_t pairs, int32_t max_len, int32_t* tokens, int32_t* pieces)
+{
+    constexpr int64_t kItems = 1024, kRound = kAttendWaves * kAttendTile;
+    const int64_t want = std::max<int64_t>(1, kItems / std::max<int64_t>(1, pairs));
+    int64_t t = ceil_div(ceil_div(std::max(max_len, 1), want), kRound) * kRound;
+    t = std::min<int64_t>(t, (INT32_MAX / kRound) * kRound);
+    *tokens = int32_t(t);
+    *pieces = int32_t(ceil_div(max_len, t));
+}
+
+int attend_shape(const kv_paged* p, const kv_step* s, int32_t q_heads, AttendShape* out)
+{
+    const int64_t heads = p->num_kv_heads, rep = q_heads / heads;
+    AttendShape a{};
+    const int64_t pt = ceil_div(int64_t(s->max_group_rows) * rep, kAttendRows);
+    const int64_t ot = ceil_div(int64_t(s->max_new) * rep, kAttendRows);
+    if (pt > INT32_MAX || ot > INT32_MAX) return fail(KV_EINVAL, "too many rows for one launch");
+    a.prefix_tiles = int32_t(pt);
+    a.own_tiles = int32_t(ot);
+    const int64_t pre = s->prefix.n * heads * pt, own = s->own.n * heads * ot;
+    cut_tokens(pre, s->prefix.n > 0 ? s->prefix.max_len : 0, &a.prefix_tokens, &a.prefix_pieces);
+    cut_tokens(own, s->own.n > 0 ? s->own.max_len : 0, &a.own_tokens, &a.own_pieces);
+    a.slots = std::max(1, a.prefix_pieces + a.own_pieces);
+    const int64_t most = max_blocks(kAttendBlock);
+    if (pre > most || own > most || pre * a.prefix_pieces + own * a.own_pieces > most)
+        return fail(KV_EINVAL, "too many row tiles and pieces for one launch");
+    a.prefix_items = pre * a.prefix_pieces;
+    a.own_items = own * a.own_pieces;
+    const int64_t parts = int64_t(s->n_rows) * q_heads;
+    if (parts > (int64_t(1) << 31) / 8) return fail(KV_EINVAL, "too many rows for one launch");
+    a.ml_bytes = ceil_div(parts * a.slots * 8, 256) * 256;
+    a.bytes = a.ml_bytes + ceil_div(parts * a.slots * p->head_dim * 4, 256) * 256;
+    *out = a;
+    return KV_OK;
+}
+
+int attend_checks(const kv_paged* paged, const kv_step* step, int32_t layer, int32_t q_heads)
+{
+    int rc = check_step_pool(paged, layer, layer + 1);
+    if (rc == KV_OK) rc = check_step(paged, step);
+    if (rc == KV_OK) rc = check_heads(paged, q_heads);
+    return rc;
+}
+
+int check_q(const kv_rows* q, float scale)
+{
+    if (q == nullptr || q->data == nullptr) return fail(KV_EINVAL, "q is NULL");
+    if (!rows_vectors(*q, 2)) return fail(KV_EINVAL, "q's address and strides must be multiples of 16 bytes");
+    if (!(scale > 0.0f) || scale > 1e30f) return fail(KV_EINVAL, "scale must be finite and > 0");
+    return KV_OK;
+}
+
+int attend(const kv_paged* paged, const kv_step* step, int32_t layer, const kv_rows* q, int32_t q_heads, float scale,
+           const kv_rows* out, float* lse, void* workspace, size_t workspace_bytes, hipStream_t stream)
+{
+    int rc = attend_checks(paged, step, layer, q_heads);
+    if (rc != KV_OK) return rc;
+    AttendShape sh;
+    rc = attend_shape(paged, step, q_heads, &sh);
+    if (rc != KV_OK) return rc;
+    if (step->n_rows == 0 || step->own.n == 0) return ok();
+    rc = check_q(q, scale);
+    if (rc != KV_OK) return rc;
+    if (out == nullptr || out->data == nullptr || lse == nullptr) return fail(KV_EINVAL, "out or lse is NULL");
+    if (misaligned(out->data, 8) || out->row_stride % 4 != 0 || out->head_stride % 4 != 0)
+        return fail(KV_EINVAL, "out's address and strides must be multiples of 8 bytes");
+    if (workspace == nullptr || workspace_bytes < size_t(sh.bytes) || misaligned(workspace, 256))
+        return fail(KV_EINVAL, "workspace of %lld bytes, 256-byte aligned, needed (got %zu at %p)",
+                    (long long)sh.bytes, workspace_bytes, workspace);
+    AttendArgs a{};
+    a.pool = pool_arg(paged, layer);
+    a.step = step_arg(step);
+    a.q = reinterpret_cast<uint64_t>(q->data);
+    a.q_row = q->row_stride;
+    a.q_head = q->head_stride;
+    a.out = reinterpret_cast<uint64_t>(out->data);
+    a.o_row = out->row_stride;
+    a.o_head = out->head_stride;
+    a.lse = reinterpret_cast<uint64_t>(lse);
+    a.part_ml = reinterpret_cast<uint64_t>(workspace);
+    a.part_acc = a.part_ml + uint64_t(sh.ml_bytes);
+    a.q_heads = q_heads;
+    a.rep = q_heads / paged->num_kv_heads;
+    a.scale_log2 = float(double(scale) * 1.4426950408889634);
+    a.prefix_tiles = sh.prefix_tiles;
+    a.prefix_pieces = sh.prefix_pieces;
+    a.prefix_tokens = sh.prefix_tokens;
+    a.own_tiles = sh.own_tiles;
+    a.own_pieces = sh.own_pieces;
+    a.own_tokens = sh.own_tokens;
+    a.slots = sh.slots;
+    a.prefix_items = uint32_t(sh.prefix_items);
+    const int dim = paged->head_dim;
+    KernelFn pieces = dim <= 64    ? reinterpret_cast<KernelFn>(&attend_pieces<64>)
+                      : dim <= 128 ? reinterpret_cast<KernelFn>(&attend_pieces<128>)
+                                   : reinterpret_cast<KernelFn>(&attend_pieces<256>);
+    KernelFn join = dim <= 64    ? reinterpret_cast<KernelFn>(&attend_join<64>)
+                    : dim <= 128 ? reinterpret_cast<KernelFn>(&attend_join<128>)
+                                 : reinterpret_cast<KernelFn>(&attend_join<256>);
+    rc = launch(pieces, sh.prefix_items + sh.own_items, kAttendBlock, &a, stream);
+    if (rc == KV_OK) rc = launch(join, int64_t(step->n_rows) * q_heads, 256, &a, stream);
+    return rc == KV_OK ? ok() : rc;
+}
+
+// ---- weights
+
+int add_weights_call(const kv_paged* paged, const kv_step* step, int32_t layer, const kv_rows* q, const float* lse,
+                     int32_t q_heads, float scale, const kv_sums* own, const kv_sums* prefix, hipStream_t stream)
+{
+    int rc = attend_checks(paged, step, layer, q_heads);
+    if (rc != KV_OK) return rc;
+    if (own == nullptr && prefix == nullptr) return fail(KV_EINVAL, "own or prefix sums are needed");
+    if (own != nullptr && (own->out == nullptr || own->cap < step->own.max_len))
+        return fail(own->out == nullptr ? KV_EINVAL : KV_ERANGE, "own sums: out is NULL or cap below max_len %d",
+                    step->own.max_len);
+    if (prefix != nullptr && (prefix->out == nullptr || prefix->cap < step->prefix.max_len))
+        return fail(prefix->out == nullptr ? KV_EINVAL : KV_ERANGE, "prefix sums: out is NULL or cap below max_len %d",
+                    step->prefix.max_len);
+    if (step->n_rows > 0) {
+        rc = check_q(q, scale);
+        if (rc != KV_OK) return rc;
+        if (lse == nullptr) return fail(KV_EINVAL, "lse is NULL");
+    }
+    WeightsArgs a{};
+    a.pool = pool_arg(paged, layer);
+    a.step = step_arg(step);
+    if (q != nullptr) {
+        a.q = reinterpret_cast<uint64_t>(q->data);
+        a.q_row = q->row_stride;
+        a.q_head = q->head_stride;
+    }
+    a.lse = reinterpret_cast<uint64_t>(lse);
+    a.q_heads = q_heads;
+    a.rep = q_heads / paged->num_kv_heads;
+    a.scale_log2 = float(double(scale) * 1.4426950408889634);
+    int64_t own_items = 0, prefix_items = 0;
+    if (own != nullptr) {
+        a.own_in = reinterpret_cast<uint64_t>(own->in);
+        a.own_out = reinterpret_cast<uint64_t>(own->out);
+        a.own_cap = own->cap;
+        a.own_blocks = int32_t(ceil_div(step->own.max_len, kWeightsTokens));
+        own_items = int64_t(step->own.n) * paged->num_kv_heads * a.own_blocks;
+    }
+    if (prefix != nullptr) {
+        a.prefix_in = reinterpret_cast<uint64_t>(prefix->in);
+        a.prefix_out = reinterpret_cast<uint64_t>(prefix->out);
+        a.prefix_cap = prefix->cap;
+        a.prefix_blocks = int32_t(ceil_div(step->prefix.max_len, kWeightsTokens));
+        prefix_items = int64_t(step->prefix.n) * paged->num_kv_heads * a.prefix_blocks;
+    }
+    const int64_t most = max_blocks(kAttendBlock);
+    if (own_items > most || prefix_items > most) return fail(KV_EINVAL, "too many tokens for one launch");
+    a.prefix_items = uint32_t(prefix_items);
+    const int dim = paged->head_dim;
+    KernelFn f = dim <= 64    ? reinterpret_cast<KernelFn>(&add_weights<64>)
+                 : dim <= 128 ? reinterpret_cast<KernelFn>(&add_weights<128>)
+                              : reinterpret_cast<KernelFn>(&add_weights<256>);
+    rc = launch(f, prefix_items + own_items, kAttendBlock, &a, stream);
+    return rc == KV_OK ? ok() : rc;
+}
+
+// ---- evict
+
+struct EvictShape {
+    int64_t jobs, max_moves, count_bytes, bytes;
+};
+
+int evict_shape(const kv_paged* p, const kv_tables* t, int32_t n_layers, int32_t heads, int32_t keep, EvictShape* out)
+{
+    if (t == nullptr) return fail(KV_EINVAL, "tables is NULL");
+    int rc = check_tables(p, t, "tables");
+    if (rc != KV_OK) return rc;
+    if (heads != 1 && heads != p->num_kv_heads)
+        return fail(KV_EINVAL, "heads must be 1 or num_kv_heads (got %d)", heads);
+    if (int64_t(p->num_kv_heads) * p->head_dim / heads % 8 != 0)
+        return fail(KV_EINVAL, "head_dim = %d must be a multiple of 8 to evict by head", p->head_dim);
+    if (keep < 0) return fail(KV_EINVAL, "keep < 0");
+    out->jobs = int64_t(n_layers) * t->n * heads;
+    if (out->jobs > max_blocks(kSelectBlock)) return fail(KV_EINVAL, "too many (layer, sequence, head) for one launch");
+    out->max_moves = std::min<int64_t>(keep, std::max(0, t->max_len - keep));
+    out->count_bytes = ceil_div(out->jobs * 4, 256) * 256;
+    out->bytes = out->count_bytes + ceil_div(out->jobs * out->max_moves * 8, 256) * 256;
+    return KV_OK;
+}
+
+int evict(const kv_paged* paged, const kv_tables* tables, int32_t layer_begin, int32_t layer_end, const kv_slots* in,
+          const kv_slots* out, int32_t keep, int32_t recent, int32_t* out_lens, void* workspace,
+          size_t workspace_bytes, hipStream_t stream)
+{
+    int rc = check_step_pool(paged, layer_begin, layer_end);
+    if (rc != KV_OK) return rc;
+    if (in == nullptr || out == nullptr) return fail(KV_EINVAL, "in or out is NULL");
+    EvictShape sh;
+    rc = evict_shape(paged, tables, layer_end - layer_begin, in->heads, keep, &sh);
+    if (rc != KV_OK) return rc;
+    if (recent < 0 || recent > keep) return fail(KV_EINVAL, "need 0 <= recent <= keep (got %d, %d)", recent, keep);
+    if (out->heads != in->heads) return fail(KV_EINVAL, "in and out must have the same heads");
+    if (tables->n == 0) return ok();
+    if (in->weights == nullptr || in->positions == nullptr || out->weights == nullptr || out->positions == nullptr ||
+        out_lens == nullptr)
+        return fail(KV_EINVAL, "weights, positions or out_lens is NULL");
+    if (out_lens == tables->lens) return fail(KV_EINVAL, "out_lens must not be the lengths that are read");
+    if ((in->weights == out->weights) != (in->positions == out->positions))
+        return fail(KV_EINVAL, "weights and positions are both updated in place or both written elsewhere");
+    if (in->weights == out->weights && in->cap != out->cap)
+        return fail(KV_EINVAL, "in place, in and out must have the same cap");
+    if (in->cap < tables->max_len)
+        return fail(KV_ERANGE, "cap %lld below max_len %d", (long long)in->cap, tables->max_len);
+    if (out->cap < std::min(keep, tables->max_len))
+        return fail(KV_ERANGE, "out's cap %lld below the %d slots kept", (long long)out->cap,
+                    std::min(keep, tables->max_len));
+    if (workspace == nullptr || workspace_bytes < size_t(sh.bytes) || misaligned(workspace, 256))
+        return fail(KV_EINVAL, "workspace of %lld bytes, 256-byte aligned, needed (got %zu at %p)",
+                    (long long)sh.bytes, workspace_bytes, workspace);
+    EvictArgs a{};
+    a.pool = pool_arg(paged, layer_begin);
+    a.tab = tables_arg(tables);
+    a.weights = reinterpret_cast<uint64_t>(in->weights);
+    a.positions = reinterpret_cast<uint64_t>(in->positions);
+    a.out_weights = reinterpret_cast<uint64_t>(out->weights);
+    a.out_positions = reinterpret_cast<uint64_t>(out->positions);
+    a.cap = in->cap;
+    a.out_cap = out->cap;
+    a.out_lens = reinterpret_cast<uint64_t>(out_lens);
+    a.counts = reinterpret_cast<uint64_t>(workspace);
+    a.moves = a.counts + uint64_t(sh.count_bytes);
+    a.heads = in->heads;
+    a.n_layers = layer_end - layer_begin;
+    a.keep = keep;
+    a.recent = recent;
+    a.max_moves = int32_t(sh.max_moves);
+    rc = launch(reinterpret_cast<KernelFn>(&evict_select), sh.jobs, kSelectBlock, &a, stream);
+    if (rc == KV_OK && sh.max_moves > 0) {
+        const int64_t vecs = int64_t(paged->num_kv_heads) * paged->head_dim / in->heads / 8;
+        const int64_t shares = ceil_div(sh.max_moves * vecs, kMoveRowsBlock * kMoveRowsPer);
+        rc = launch(reinterpret_cast<KernelFn>(&evict_move), sh.jobs, kMoveRowsBlock, &a, stream,
+                    unsigned(std::min<int64_t>(shares, 256)));
+    }
+    return rc == KV_OK ? ok() : rc;
+}
+
+}  // namespace
+
+extern "C" {
+
+int kv_append(const kv_paged* paged, const kv_step* step, int32_t layer, const kv_rows* q, const kv_rows* k,
+              const kv_rows* v, const kv_rows* q_out, int32_t q_heads, kv_type type, kv_type q_out_type,
+              const int32_t* positions, const kv_rope* rope, const kv_slots* slots, hipStream_t stream)
+{
+    return append(paged, step, layer, q, k, v, q_out, q_heads, type, q_out_type, positions, rope, slots, stream);
+}
+
+size_t kv_attend_workspace_bytes(const kv_paged* paged, const kv_step* step, int32_t q_heads)
+{
+    AttendShape sh;
+    if (attend_checks(paged, step, 0, q_heads) != KV_OK || attend_shape(paged, step, q_heads, &sh) != KV_OK) return 0;
+    ok();
+    return size_t(std::max<int64_t>(sh.bytes, 256));
+}
+
+int kv_attend(const kv_paged* paged, const kv_step* step, int32_t layer, const kv_rows* q, int32_t q_heads,
+              float scale, const kv_rows* out, float* lse, void* workspace, size_t workspace_bytes,
+              hipStream_t stream)
+{
+    return attend(paged, step, layer, q, q_heads, scale, out, lse, workspace, workspace_bytes, stream);
+}
+
+int kv_add_weights(const kv_paged* paged, const kv_step* step, int32_t layer, const kv_rows* q, const float* lse,
+                   int32_t q_heads, float scale, const kv_sums* own, const kv_sums* prefix, hipStream_t stream)
+{
+    return add_weights_call(paged, step, layer, q, lse, q_heads, scale, own, prefix, stream);
+}
+
+size_t kv_evict_workspace_bytes(const kv_paged* paged, const kv_tables* tables, int32_t n_layers, int32_t heads,
+                                int32_t keep)
+{
+    EvictShape sh;
+    if (check_paged(paged) != KV_OK) return 0;
+    if (n_layers <= 0 || n_layers > paged->num_layers) {
+        fail(KV_EINVAL, "n_layers = %d outside [1, %d]", n_layers, paged->num_layers);
+        return 0;
+    }
+    if (evict_shape(paged, tables, n_layers, heads, keep, &sh) != KV_OK) return 0;
+    ok();
+    return size_t(std::max<int64_t>(sh.bytes, 256));
+}
+
+int kv_evict(const kv_paged* paged, const kv_tables* tables, int32_t layer_begin, int32_t layer_end,
+             const kv_slots* in, const kv_slots* out, int32_t keep, int32_t recent, int32_t* out_lens,
+             void* workspace, size_t workspace_bytes, hipStream_t stream)
+{
+    return evict(paged, tables, layer_begin, layer_end, in, out, keep, recent, out_lens, workspace, workspace_bytes,
+                 stream);
+}
+
+}  // extern "C"

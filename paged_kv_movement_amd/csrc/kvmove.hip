@@ -15,11 +15,15 @@
 #include <mutex>
 #include <string>
 
+#include "kv_append.hpp"
+#include "kv_attend.hpp"
 #include "kv_cachegen.hpp"
 #include "kv_copy.hpp"
+#include "kv_evict.hpp"
 #include "kv_fp8.hpp"
 #include "kv_move_bf16.hpp"
 #include "kv_order.hpp"
+#include "kv_weights.hpp"
 
 namespace {
 
@@ -1123,3 +1127,5 @@ int kv_retrieve_chunks_cachegen(const kv_paged* paged, const kv_seq* seqs, const
 }
 
 }  // extern "C"
+
+#include "kv_step_entry.hpp"
