@@ -658,7 +658,7 @@ class Tables:
               "table must be an int32 device tensor [sequences, entries], entries contiguous")
         _need(lens.dtype == torch.int32 and lens.is_contiguous() and lens.is_cuda
               and tuple(lens.shape) == (table.size(0),), "lens must be a contiguous int32 device tensor [sequences]")
-        _need(0 <= max_len < 1 << 31, "max_len must be in [0, 2^31)")
+        _need(0 <= max_len <= 1 << 30, "max_len must be in [0, 2^30]")
         self.table, self.lens, self.max_len, self.n = table, lens, int(max_len), table.size(0)
         # rows further apart than their entries (a view) are reached through the stride
         _need(table.size(0) <= 1 or table.stride(0) >= table.size(1), "table's rows must not overlap")

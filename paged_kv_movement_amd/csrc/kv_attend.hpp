@@ -28,8 +28,8 @@ namespace kvmove {
 
 constexpr int kAttendWaves = 4;
 constexpr int kAttendBlock = kAttendWaves * 64;
-constexpr int kAttendTile = 32;        // tokens a wave takes at a time
-constexpr int kAttendRows = 16;        // rows of a tile: columns of one matrix product
+constexpr int kAttendTile = 32;        // tokens a wave of the narrow form takes at a time
+constexpr int kAttendRows = 16;        // columns of one matrix product: the narrow form's rows
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -47,6 +47,8 @@ struct AttendArgs {
     int32_t own_tiles, own_pieces, own_tokens;
     int32_t slots;                 // prefix_pieces + own_pieces
     uint32_t prefix_items;         // workgroups [0, prefix_items) take prefix pieces
+    int32_t prefix_wide, own_wide; // which form a piece takes
+    int32_t direct;                // one slot in all: out and lse are written at once, nothing is left to join
 };
 
 // What one workgroup does: rows [row0, row0 + n_rows) of the flattened (new
@@ -62,7 +64,7 @@ struct AttendItem {
     int32_t slot;
 };
 
-__device__ __forceinline__ AttendItem attend_item(const AttendArgs& a, uint32_t b, int tile_rows)
+__device__ __forceinline__ AttendItem attend_item(const AttendArgs& a, uint32_t b, int wide_rows)
 {
     AttendItem it;
     it.prefix = b < a.prefix_items;
@@ -77,8 +79,10 @@ __device__ __forceinline__ AttendItem attend_item(const AttendArgs& a, uint32_t 
     b /= tiles;
     const int32_t piece = b % pieces;
     it.table_row = b / pieces;
-    it.rows = it.prefix ? group_rows(a.step, it.table_row) : seq_rows(a.step, it.table_row);
-    it.len = table_len(it.prefix ? a.step.prefix : a.step.own, it.table_row);
+    const Rows rows = it.prefix ? group_rows(a.step, it.table_row) : seq_rows(a.step, it.table_row);
+    it.rows = {__builtin_amdgcn_readfirstlane(rows.first), __builtin_amdgcn_readfirstlane(rows.count)};
+    it.len = __builtin_amdgcn_readfirstlane(table_len(it.prefix ? a.step.prefix : a.step.own, it.table_row));
+    const int32_t tile_rows = (it.prefix ? a.prefix_wide : a.own_wide) ? wide_rows : kAttendRows;
     it.flat0 = tile * tile_rows;
     it.flat_n = it.rows.count * a.rep - it.flat0;
     it.flat_n = it.flat_n < tile_rows ? it.flat_n : tile_rows;
@@ -96,17 +100,27 @@ __device__ __forceinline__ int32_t visible_end(const AttendArgs& a, const Attend
     return clamp_i32(it.len - it.rows.count + (it.flat0 + f) / a.rep + 1, 0, it.len);
 }
 
-// Row of a layer's [num_pages * page_size] that token t is in, or -1 for a
-// bad page id.
-__device__ __forceinline__ int32_t token_row(const PoolArg& p, const TablesArg& t, int32_t table_row, int32_t tok)
+// Page id of token tok; the load is started here, what waits for it is
+// row_in_page.
+__device__ __forceinline__ int32_t token_page(const PoolArg& p, const TablesArg& t, int32_t table_row, int32_t tok)
 {
-    const uint32_t pi = page_of(p, uint32_t(tok));
-    const int32_t page = gptr<const gi32>(t.table)[table_row * t.stride + pi];
-    if (page < 0 || uint32_t(page) >= p.num_pages) {
+    return gptr<const gi32>(t.table)[table_row * t.stride + page_of(p, uint32_t(tok))];
+}
+
+// Row of a layer's [num_pages * page_size] that token tok, on that page, is
+// in; -1 for a page outside the pool.
+__device__ __forceinline__ int32_t row_in_page(const PoolArg& p, int32_t page, int32_t tok)
+{
+    if (uint32_t(page) >= p.num_pages) {
         raise_fault_lane(kFaultPage);
         return -1;
     }
-    return page * int32_t(p.page_size) + int32_t(uint32_t(tok) - pi * p.page_size);
+    return page * int32_t(p.page_size) + int32_t(uint32_t(tok) - page_of(p, uint32_t(tok)) * p.page_size);
+}
+
+__device__ __forceinline__ int32_t token_row(const PoolArg& p, const TablesArg& t, int32_t table_row, int32_t tok)
+{
+    return row_in_page(p, token_page(p, t, table_row, tok), tok);
 }
 
 // Two float32 -> two bf16 in one word, and the two bf16 of what that rounding
@@ -118,15 +132,38 @@ __device__ __forceinline__ void split_bf16(float a, float b, uint32_t& hi, uint3
     lo = bf16x2_rne(a - ra, b - rb);
 }
 
+// x, formed anew where this stands: what is made of it is not kept in registers over a loop.
+__device__ __forceinline__ int anew(int x)
+{
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
 __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c)
 {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
                                                    0, 0);
 }
 
-__device__ __forceinline__ bool has_nonfinite(uint32_t x)
+__device__ __forceinline__ float max3(float a, float b, float c)
 {
-    return (x & 0x7F800000u) == 0x7F800000u || (x & 0x7F80u) == 0x7F80u;
+    float r;
+    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+    return r;
+}
+
+// Maximum over the four lanes l % 16, + 16, + 32, + 48, without LDS: a swap of
+// a value with itself leaves the two halves side by side in every lane.
+__device__ __forceinline__ float max_over_groups(float x)
+{
+    const uint32_t u = __builtin_bit_cast(uint32_t, x);
+    const auto p = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    const uint32_t p0 = p[0], p1 = p[1];
+    const float y = max3(__builtin_bit_cast(float, p0), __builtin_bit_cast(float, p1), __builtin_bit_cast(float, p1));
+    const uint32_t w = __builtin_bit_cast(uint32_t, y);
+    const auto q = __builtin_amdgcn_permlane16_swap(w, w, false, false);
+    const uint32_t q0 = q[0], q1 = q[1];
+    return max3(__builtin_bit_cast(float, q0), __builtin_bit_cast(float, q1), __builtin_bit_cast(float, q1));
 }
 
 // A wave's registers of the online softmax over 16 rows (matrix columns):
@@ -134,186 +171,294 @@ __device__ __forceinline__ bool has_nonfinite(uint32_t x)
 // 4 * (l / 16).
 template <int DP>
 struct RowState {
-    static constexpr int E = DP / 16;
-    f32x4 acc[E];          // acc[m][i]: element d = (4 * (l / 16) + i) * E + m
-    float m, l;            // maximum (log2 units); this lane's share of the sum
+    f32x4 acc[DP / 16];    // acc[m][i]: element acc_element(4 * (l / 16) + i, m)
+    float m, l;            // the exponents' base (log2 units); this lane's share of the sum
 };
 
-// One tile of 32 tokens.  k[i][j]: token 16 i + l % 16, elements 32 j + 8 (l / 16) ..+8.
-// v[4 i + n]: token 16 i + 4 (l / 16) + n, elements (l % 16) * E ..+E.  The
-// tile's matrix rows are the tokens in their order, so P^T comes out of the
-// first product in the layout that the second one takes, and the second one's
-// left operand is v transposed in registers, two elements an instruction.
-// With kMasked, token t + x counts for this lane's row if t + x < vis and bit
-// x of valid is set.
-template <int DP, bool kMasked>
-__device__ __forceinline__ void tile_step(RowState<DP>& st, const u32x4 (&q)[DP / 32], const u32x4 (&k)[2][DP / 32],
-                                          const uint32_t (&v)[8][DP / 32], float c, int32_t t, int32_t vis,
-                                          uint32_t valid)
+template <int DP>
+__device__ __forceinline__ void clear(RowState<DP>& st)
 {
-    constexpr int E = DP / 16;
+    st.m = -__builtin_inff();
+    st.l = 0.0f;
+#pragma unroll
+    for (int m = 0; m < DP / 16; ++m) st.acc[m] = f32x4{0, 0, 0, 0};
+}
+
+// Elements of a token's V that lane r of 16 holds: 8 from 8 r, and for
+// 256-wide heads 8 more from 128 + 8 r; for 64-wide ones 4 from 4 r.
+template <int DP>
+__device__ __forceinline__ constexpr int acc_element(int r, int m)
+{
+    return DP == 64 ? r * 4 + m : (m / 8) * 128 + r * 8 + m % 8;
+}
+
+// How far the running maximum may lag behind: exponentials stay below 2^8,
+// and the accumulators are rescaled only when a row's maximum rises by more.
+constexpr float kLag = 8.0f;
+
+// Softmax weights of 32 tokens for one block of rows, as two bf16 parts in the
+// layout of the next product's right operand; the state's maximum, sum and
+// accumulators follow.  If masked (the same in every lane), token t + x counts
+// for this lane's row if t + x < vis and bit x of valid is set.
+template <int DP>
+__device__ __forceinline__ void softmax_block(RowState<DP>& st, f32x4 (&s)[2], u32x4& ph, u32x4& pl, float c,
+                                              bool masked, int32_t t, int32_t vis, uint32_t valid)
+{
     const int g = (threadIdx.x & 63) >> 4;
-    f32x4 s[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        s[i] = f32x4{0, 0, 0, 0};
-#pragma unroll
-        for (int j = 0; j < DP / 32; ++j) s[i] = mfma16(k[i][j], q[j], s[i]);
-    }
-    if (kMasked) {
+    if (masked) {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int n = 0; n < 4; ++n)
-                if (t + 16 * i + 4 * g + n >= vis || !((valid >> (16 * i + 4 * g + n)) & 1))
-                    s[i][n] = -__builtin_inff();
+            for (int n = 0; n < 4; ++n) {
+                const int x = 16 * i + 4 * g + n;
+                if (t + x >= vis || !((valid >> x) & 1)) s[i][n] = -__builtin_inff();
+            }
     }
-    float mx = -__builtin_inff();
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int n = 0; n < 4; ++n) mx = __builtin_fmaxf(mx, s[i][n]);
-    mx = __builtin_fmaxf(mx, __shfl_xor(mx, 16));
-    mx = __builtin_fmaxf(mx, __shfl_xor(mx, 32));
-    const float m_new = __builtin_fmaxf(st.m, mx * c);
-    const float base = m_new == -__builtin_inff() ? 0.0f : m_new;     // a row that has seen nothing yet
-    if (__any(m_new > st.m)) {
-        const float alpha = __builtin_amdgcn_exp2f(st.m - base);
+    const float mx = max3(max3(max3(s[0][0], s[0][1], s[0][2]), s[0][3], s[1][0]), max3(s[1][1], s[1][2], s[1][3]),
+                          s[1][3]);
+    const float top = max_over_groups(mx) * c;
+    if (__any(top > st.m + kLag)) {
+        const float m_new = __builtin_fmaxf(st.m, top);
+        const float alpha = m_new == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(st.m - m_new);
         st.l *= alpha;
 #pragma unroll
-        for (int m = 0; m < E; ++m) st.acc[m] *= alpha;
+        for (int m = 0; m < DP / 16; ++m) st.acc[m] *= alpha;
         st.m = m_new;
     }
-    u32x4 ph, pl;
+    const float base = st.m == -__builtin_inff() ? 0.0f : st.m;       // a row that has seen nothing yet
+    float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int n = 0; n < 4; n += 2) {
             const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i][n], c, -base));
             const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i][n + 1], c, -base));
-            st.l += p0 + p1;
+            sum += p0 + p1;
             uint32_t hi, lo;
             split_bf16(p0, p1, hi, lo);
             ph[2 * i + n / 2] = hi;
             pl[2 * i + n / 2] = lo;
         }
-    bool odd = false;
-    if (kMasked) {
-        // a token that some rows do not see must not reach them through 0 * inf or 0 * NaN
+    st.l += sum;
+}
+
+// Left operand of O^T = V^T P^T for accumulator m: the lane's element m of
+// its eight tokens (v[x]: token 16 (x / 4) + 4 (l / 16) + x % 4), two tokens
+// an instruction.
+template <int DP>
+__device__ __forceinline__ u32x4 v_column(const uint32_t (&v)[8][DP / 32], int m)
+{
+    u32x4 vt;
 #pragma unroll
-        for (int x = 0; x < 8; ++x)
+    for (int w = 0; w < 4; ++w)
+        vt[w] = __builtin_amdgcn_perm(v[2 * w + 1][m / 2], v[2 * w][m / 2], m % 2 ? 0x07060302u : 0x05040100u);
+    return vt;
+}
+
+// Adds 32 tokens' weighted V to NB blocks of rows.
+template <int DP, int NB>
+__device__ __forceinline__ void add_v(RowState<DP> (&st)[NB], const uint32_t (&v)[8][DP / 32], const u32x4 (&ph)[NB],
+                                      const u32x4 (&pl)[NB])
+{
 #pragma unroll
-            for (int y = 0; y < DP / 32; ++y) odd |= has_nonfinite(v[x][y]);
-    }
-    if (kMasked && __any(odd)) {
-        // token by token, each row taking only what it sees
-#pragma unroll 1
-        for (int x = 0; x < 32; ++x) {
-            const bool mine = g == ((x & 15) >> 2);
-            const int word = 2 * (x >> 4) + ((x & 3) >> 1);
-            u32x4 keep;
+    for (int m = 0; m < DP / 16; ++m) {
+        const u32x4 vt = v_column<DP>(v, m);
 #pragma unroll
-            for (int w = 0; w < 4; ++w) keep[w] = mine && w == word ? ((x & 1) ? 0xFFFF0000u : 0xFFFFu) : 0u;
-            const bool sees = t + x < vis && ((valid >> x) & 1);
+        for (int b = 0; b < NB; ++b) st[b].acc[m] = mfma16(vt, ph[b], st[b].acc[m]);
 #pragma unroll
-            for (int m = 0; m < E; ++m) {
-                u32x4 vt;
-#pragma unroll
-                for (int w = 0; w < 4; ++w)
-                    vt[w] = __builtin_amdgcn_perm(v[2 * w + 1][m / 2], v[2 * w][m / 2],
-                                                  m % 2 ? 0x07060302u : 0x05040100u) & keep[w];
-                f32x4 o = mfma16(vt, ph & keep, f32x4{0, 0, 0, 0});
-                o = mfma16(vt, pl & keep, o);
-                if (sees) st.acc[m] += o;
-            }
-        }
-        return;
-    }
-#pragma unroll
-    for (int m = 0; m < E; ++m) {
-        u32x4 vt;
-#pragma unroll
-        for (int w = 0; w < 4; ++w)
-            vt[w] = __builtin_amdgcn_perm(v[2 * w + 1][m / 2], v[2 * w][m / 2], m % 2 ? 0x07060302u : 0x05040100u);
-        st.acc[m] = mfma16(vt, ph, st.acc[m]);
-        st.acc[m] = mfma16(vt, pl, st.acc[m]);
+        for (int b = 0; b < NB; ++b) st[b].acc[m] = mfma16(vt, pl[b], st[b].acc[m]);
     }
 }
 
-// Elements [d, d + 8) of a row at `base` (byte address), 0 at and past dim.
+// A V that is not finite does not go through add_v: 0 times it is NaN, for a
+// row that does not see its token and for the second part of a weight alike.
+// A piece is therefore done without a thought of it, and if a result is not
+// finite it is done again with care: take_nonfinite sets such elements to 0
+// for add_v, add_nonfinite adds them as the formula has it, token by token,
+// each row what it sees.
 template <int DP>
+__device__ __forceinline__ void take_nonfinite(uint32_t (&v)[8][DP / 32])
+{
+#pragma unroll
+    for (int x = 0; x < 8; ++x)
+#pragma unroll
+        for (int y = 0; y < DP / 32; ++y) {
+            uint32_t u = v[x][y];
+            if ((u & 0x7F80u) == 0x7F80u) u &= 0xFFFF0000u;
+            if ((u & 0x7F800000u) == 0x7F800000u) u &= 0x0000FFFFu;
+            v[x][y] = u;
+        }
+}
+
+// row_of(x): LDS address of the 32 tokens' V row x, as it came from the pool;
+// at(d): where its elements [d, d + 4) are in the row, in bf16 elements.
+template <int DP, class RowOf, class At>
+__device__ __forceinline__ void add_nonfinite(RowState<DP>& st, u32x4 ph, u32x4 pl, int32_t t, int32_t vis,
+                                              uint32_t valid, RowOf&& row_of, At&& at)
+{
+    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+#pragma unroll 1
+    for (int x = 0; x < 32; ++x) {
+        const int word = 2 * (x >> 4) + ((x & 3) >> 1), shift = (x & 1) ? 0 : 16;
+        const uint32_t hi = word == 0 ? ph[0] : word == 1 ? ph[1] : word == 2 ? ph[2] : ph[3];
+        const uint32_t lo = word == 0 ? pl[0] : word == 1 ? pl[1] : word == 2 ? pl[2] : pl[3];
+        const int from = ((x & 15) >> 2) * 16 + r;                   // the lane that holds this weight
+        const uint32_t h = uint32_t(__shfl(int(hi), from)) << shift, l = uint32_t(__shfl(int(lo), from)) << shift;
+        const float p = __builtin_bit_cast(float, h & 0xFFFF0000u) + __builtin_bit_cast(float, l & 0xFFFF0000u);
+        if (t + x >= vis || !((valid >> x) & 1)) continue;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int m = 0; m < DP / 16; m += 4) {
+                const u32x2 w = *reinterpret_cast<const u32x2*>(row_of(x) + at(x, acc_element<DP>(4 * g + i, m)));
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t bits = e % 2 ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16;
+                    if ((bits & 0x7F800000u) == 0x7F800000u) st.acc[m + e][i] += p * __builtin_bit_cast(float, bits);
+                }
+            }
+    }
+}
+
+template <int DP>
+__device__ __forceinline__ bool all_finite(const RowState<DP>& st)
+{
+    float sum = 0.0f;                     // x - x is 0 for what is finite, else NaN
+#pragma unroll
+    for (int m = 0; m < DP / 16; ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum += st.acc[m][i] - st.acc[m][i];
+    return sum == 0.0f;
+}
+
+// Elements [d, d + 8) of a row at `base` (byte address), 0 at and past dim.
 __device__ __forceinline__ u32x4 load_k8(uint64_t base, int d, int dim)
 {
     if (d < dim) return *gptr<const gvec4>(base + d * 2);
     return u32x4{0, 0, 0, 0};
 }
 
-// Elements [r * E, r * E + E) of a row at `base`, 0 at and past dim.
+// Lane r's elements of a V row at `base`, 0 at and past dim.
 template <int DP>
 __device__ __forceinline__ void load_v(uint32_t (&v)[DP / 32], uint64_t base, int r, int dim)
 {
-    constexpr int E = DP / 16;
-    if constexpr (E == 4) {
+    if constexpr (DP == 64) {
         u32x2 x = {0, 0};
-        if (r * E < dim) x = *gptr<const gvec2>(base + r * E * 2);
+        if (r * 4 < dim) x = *gptr<const gvec2>(base + r * 8);
         v[0] = x[0];
         v[1] = x[1];
     } else {
 #pragma unroll
-        for (int y = 0; y < E / 8; ++y) {
-            const u32x4 x = load_k8<DP>(base, r * E + 8 * y, dim);
+        for (int y = 0; y < DP / 128; ++y) {
+            const u32x4 x = load_k8(base, y * 128 + r * 8, dim);
 #pragma unroll
             for (int w = 0; w < 4; ++w) v[4 * y + w] = x[w];
         }
     }
 }
 
+// q of one block of 16 rows in the layout of the first product's right
+// operand: column r, elements 32 j + 8 g ..+8.
 template <int DP>
-__global__ __launch_bounds__(kAttendBlock) void attend_pieces(AttendArgs a)
+__device__ __forceinline__ void load_q(u32x4 (&q)[DP / 32], const AttendArgs& a, const AttendItem& it, int32_t f,
+                                       bool live)
 {
-    constexpr int E = DP / 16, J = DP / 32;
-    __shared__ float sm[kAttendWaves][kAttendRows], sl[kAttendWaves][kAttendRows];
-    __shared__ float sacc[kAttendWaves][kAttendRows][DP + 4];
-    const AttendItem it = attend_item(a, blockIdx.x, kAttendRows);
-    if (it.flat_n <= 0) return;
-    // the last row sees the most: no later token is needed
-    const int32_t end_all = visible_end(a, it, it.flat_n - 1);
-    if (it.t0 >= (it.t1 < end_all ? it.t1 : end_all)) return;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
-    const int dim = a.pool.dim, heads = a.pool.heads;
-    const uint64_t kb = wave_uniform(gptr<const gu64>(a.pool.k_pages)[a.pool.layer]);
-    const uint64_t vb = wave_uniform(gptr<const gu64>(a.pool.v_pages)[a.pool.layer]);
-    const bool pool_ok = !bad_addr(kb) && !bad_addr(vb);
-    if (!pool_ok) raise_fault(kFaultPool);
+    const int g = (threadIdx.x & 63) >> 4;
+    const int32_t flat = it.flat0 + (live ? f : 0);
+    const int64_t row = it.rows.first + flat / a.rep, head = it.h * a.rep + flat % a.rep;
+    const uint64_t qb = a.q + (row * a.q_row + head * a.q_head) * 2;
+#pragma unroll
+    for (int j = 0; j < DP / 32; ++j) {
+        q[j] = u32x4{0, 0, 0, 0};
+        if (live) q[j] = load_k8(qb, j * 32 + g * 8, a.pool.dim);
+    }
+}
 
-    const int32_t t1 = pool_ok ? (it.t1 < end_all ? it.t1 : end_all) : it.t0;
+__device__ __forceinline__ float log_sum(float m, float l) { return (m + __builtin_amdgcn_logf(l)) * kLn2; }
+
+// 1 / l; 0 for a row that saw nothing, NaN stays.
+__device__ __forceinline__ float inverse_sum(float l) { return l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l); }
+
+// Where row f of a piece goes: its part of the workspace, or with `direct`
+// the result itself.
+struct RowSink {
+    uint64_t at;           // bf16 out or float32 acc
+    float inv;             // 1 / l with `direct`
+};
+
+// The sink of row f; `first` (one lane of the row) writes its maximum and sum, or its lse.
+__device__ __forceinline__ RowSink open_row(const AttendArgs& a, const AttendItem& it, int32_t f, float m, float l,
+                                            bool first)
+{
+    const int32_t flat = it.flat0 + f, i = flat / a.rep;
+    const int64_t row = it.rows.first + i, head = it.h * a.rep + (flat - i * a.rep);
+    if (a.direct) {
+        if (first) gptr<gf32>(a.lse)[row * a.q_heads + head] = log_sum(m, l);
+        return {a.out + (row * a.o_row + head * a.o_head) * 2, inverse_sum(l)};
+    }
+    const int64_t part = (row * a.q_heads + head) * a.slots + it.slot;
+    if (first) {
+        gptr<gf32>(a.part_ml)[2 * part] = m;
+        gptr<gf32>(a.part_ml)[2 * part + 1] = l;
+    }
+    return {a.part_acc + part * a.pool.dim * 4, 1.0f};
+}
+
+__device__ __forceinline__ void put4(const AttendArgs& a, const RowSink& to, int d, f32x4 o)
+{
+    if (a.direct) {
+        const u32x2 y = {bf16x2_rne(o[0] * to.inv, o[1] * to.inv), bf16x2_rne(o[2] * to.inv, o[3] * to.inv)};
+        *gptr<gvec2>(to.at + d * 2) = y;
+    } else {
+        *gptr<gf32x4>(to.at + d * 4) = o;
+    }
+}
+
+template <int DP>
+struct NarrowShared {
+    float m[kAttendWaves][kAttendRows], l[kAttendWaves][kAttendRows];
+    union {
+        float acc[kAttendWaves][kAttendRows][DP + 4];
+        u32x2 v[kAttendWaves][kAttendTile][DP / 4];          // a wave's V, for add_nonfinite
+    };
+};
+
+// A piece with at most 16 rows: the waves take its tokens in turn, 32 at a
+// time, each with K and V straight from memory in its registers (K rows as
+// they lie are the first product's left operand), and join at the end.
+//
+// Bound: the read of K and V.  16 KiB a wave are in flight, two waves a SIMD.
+template <int DP>
+__device__ __forceinline__ void narrow_piece(const AttendArgs& a, const AttendItem& it, uint64_t kb, uint64_t vb,
+                                             int32_t t1, NarrowShared<DP>& sh)
+{
+    constexpr int J = DP / 32;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
+    const int dim = a.pool.dim;
     const int32_t all_see = visible_end(a, it, 0);          // tokens below it are seen by every row
     const bool live = r < it.flat_n;
-    const int32_t vis = live ? visible_end(a, it, r) : 0;
-
-    const int32_t f = it.flat0 + (live ? r : 0);
-    const int32_t q_row = it.rows.first + f / a.rep, head = it.h * a.rep + f % a.rep;
+    const int32_t vis[1] = {live ? visible_end(a, it, r) : 0};
     u32x4 q[J];
-    const uint64_t qb = a.q + (q_row * a.q_row + head * a.q_head) * 2;
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-        q[j] = u32x4{0, 0, 0, 0};
-        if (live) q[j] = load_k8<DP>(qb, j * 32 + g * 8, dim);
-    }
-
-    RowState<DP> st;
-    st.m = -__builtin_inff();
-    st.l = 0.0f;
-#pragma unroll
-    for (int m = 0; m < E; ++m) st.acc[m] = f32x4{0, 0, 0, 0};
+    load_q<DP>(q, a, it, r, live);
+    RowState<DP> st[1];
 
     const TablesArg& tab = it.prefix ? a.step.prefix : a.step.own;
-    const int64_t row_bytes = int64_t(heads) * dim * 2;
+    const uint32_t row_bytes = a.pool.heads * dim * 2;
     const uint64_t kh = kb + uint64_t(it.h) * dim * 2, vh = vb + uint64_t(it.h) * dim * 2;
-    for (int32_t t = it.t0 + wave * kAttendTile; t < t1; t += kAttendWaves * kAttendTile) {
-        // lane l < 32 looks up token t + l; the others take it from there
-        int32_t row = -1;
-        if (lane < kAttendTile && t + lane < t1) row = token_row(a.pool, tab, it.table_row, t + lane);
+    // lane l < 32 looks up token t + l, its page a round ahead; the others take it from there
+    auto mine = [&](int32_t t) { return lane < kAttendTile && lane < t1 - t; };
+    auto page_at = [&](int32_t t) {                // of the last token where there is no such one: no branch to wait at
+        return token_page(a.pool, tab, it.table_row, lane < t1 - t ? t + lane : t1 - 1);
+    };
+    const int32_t first = it.t0 + wave * kAttendTile;
+    bool care = false;
+  again:
+    clear<DP>(st[0]);
+    int32_t page = it.t0 < t1 ? page_at(first) : -1;
+#pragma unroll 1
+    for (int32_t t = first; t < t1; t += kAttendWaves * kAttendTile) {
+        const int32_t row = mine(t) ? row_in_page(a.pool, page, t + lane) : -1;
+        page = page_at(t + kAttendWaves * kAttendTile);
         const uint32_t valid = uint32_t(__ballot(row >= 0));
         u32x4 k[2][J];
         uint32_t v[8][J];
@@ -323,58 +468,314 @@ __global__ __launch_bounds__(kAttendBlock) void attend_pieces(AttendArgs a)
 #pragma unroll
             for (int j = 0; j < J; ++j) {
                 k[i][j] = u32x4{0, 0, 0, 0};
-                if (kr >= 0) k[i][j] = load_k8<DP>(kh + kr * row_bytes, j * 32 + g * 8, dim);
+                if (kr >= 0) k[i][j] = load_k8(kh + uint64_t(uint32_t(kr)) * row_bytes, j * 32 + g * 8, dim);
             }
         }
 #pragma unroll
         for (int x = 0; x < 8; ++x) {
             const int32_t vr = __shfl(row, 16 * (x / 4) + 4 * g + x % 4);
-            if (vr >= 0) {
-                load_v<DP>(v[x], vh + vr * row_bytes, r, dim);
-            } else {
 #pragma unroll
-                for (int y = 0; y < J; ++y) v[x][y] = 0;
-            }
+            for (int y = 0; y < J; ++y) v[x][y] = 0;
+            if (vr >= 0) load_v<DP>(v[x], vh + uint64_t(uint32_t(vr)) * row_bytes, r, dim);
         }
-        if (valid == ~0u && t + kAttendTile <= all_see)
-            tile_step<DP, false>(st, q, k, v, a.scale_log2, t, vis, valid);
-        else
-            tile_step<DP, true>(st, q, k, v, a.scale_log2, t, vis, valid);
+        f32x4 s[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            s[i] = f32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int j = 0; j < J; ++j) s[i] = mfma16(k[i][j], q[j], s[i]);
+        }
+        u32x4 ph[1], pl[1];
+        const bool masked = valid != ~0u || t + kAttendTile > all_see;
+        softmax_block<DP>(st[0], s, ph[0], pl[0], a.scale_log2, masked, t, vis[0], valid);
+        if (care) {
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+#pragma unroll
+                for (int y = 0; y < J / 2; ++y) {
+                    const int chunk = DP == 64 ? r : (y / 2) * 32 + 2 * r + y % 2;
+                    sh.v[wave][16 * (x / 4) + 4 * g + x % 4][chunk] = u32x2{v[x][2 * y], v[x][2 * y + 1]};
+                }
+            __builtin_amdgcn_s_waitcnt(0);
+            __builtin_amdgcn_wave_barrier();
+            take_nonfinite<DP>(v);
+            add_nonfinite<DP>(st[0], ph[0], pl[0], t, vis[0], valid,
+                              [&](int x) { return reinterpret_cast<const uint16_t*>(&sh.v[wave][x][0]); },
+                              [](int, int d) { return d; });
+            __builtin_amdgcn_wave_barrier();
+        }
+        add_v<DP, 1>(st, v, ph, pl);
     }
-    st.l += __shfl_xor(st.l, 16);
-    st.l += __shfl_xor(st.l, 32);
+    if (!care && __any(!all_finite<DP>(st[0]))) {
+        care = true;
+        goto again;
+    }
+    __syncthreads();                       // sh.v and sh.acc are one memory
+    st[0].l += __shfl_xor(st[0].l, 16);
+    st[0].l += __shfl_xor(st[0].l, 32);
 
-    // the waves' pieces joined
+    // the waves' shares joined
     if (g == 0) {
-        sm[wave][r] = st.m;
-        sl[wave][r] = st.l;
+        sh.m[wave][r] = st[0].m;
+        sh.l[wave][r] = st[0].l;
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int m = 0; m < E; ++m) sacc[wave][r][(4 * g + i) * E + m] = st.acc[m][i];
+        for (int m = 0; m < DP / 16; ++m) sh.acc[wave][r][acc_element<DP>(4 * g + i, m)] = st[0].acc[m][i];
     __syncthreads();
     for (int x = threadIdx.x; x < it.flat_n * (dim / 4); x += kAttendBlock) {
         const int row = x / (dim / 4), d = 4 * (x - row * (dim / 4));
-        float m = sm[0][row];
+        float m = sh.m[0][row];
 #pragma unroll
-        for (int w = 1; w < kAttendWaves; ++w) m = __builtin_fmaxf(m, sm[w][row]);
+        for (int w = 1; w < kAttendWaves; ++w) m = __builtin_fmaxf(m, sh.m[w][row]);
         const float base = m == -__builtin_inff() ? 0.0f : m;
         float l = 0.0f;
         f32x4 o = {0, 0, 0, 0};
 #pragma unroll
         for (int w = 0; w < kAttendWaves; ++w) {
-            const float e = __builtin_amdgcn_exp2f(sm[w][row] - base);
-            l += e * sl[w][row];
-            o += *reinterpret_cast<const f32x4*>(&sacc[w][row][d]) * e;
+            const float e = __builtin_amdgcn_exp2f(sh.m[w][row] - base);
+            l += e * sh.l[w][row];
+            o += *reinterpret_cast<const f32x4*>(&sh.acc[w][row][d]) * e;
         }
-        const int32_t fr = it.flat0 + row;
-        const int64_t at = (int64_t(it.rows.first + fr / a.rep) * a.q_heads + it.h * a.rep + fr % a.rep) * a.slots + it.slot;
-        *gptr<gf32x4>(a.part_acc + (at * dim + d) * 4) = o;
-        if (d == 0) {
-            gptr<gf32>(a.part_ml)[2 * at] = m;
-            gptr<gf32>(a.part_ml)[2 * at + 1] = l;
+        put4(a, open_row(a, it, row, m, l, d == 0), d, o);
+    }
+}
+
+// Zeros in device memory: where a lane of a direct-to-LDS load has no token or
+// no element to fetch, it fetches these.
+__device__ u32x4 g_zero_vector;
+
+template <int DP>
+constexpr int kWideTile = DP <= 128 ? 64 : 32;       // tokens of a tile
+
+template <int DP>
+struct WideTile {
+    u32x4 k[kWideTile<DP> * DP / 8];
+    u32x4 v[kWideTile<DP> * DP / 8];
+};
+
+// Vectors of a token's row are stored at chunk ^ wide_swizzle(token): the 16
+// tokens that a K operand reads at one chunk then lie in different banks.
+template <int DP>
+__device__ __forceinline__ int wide_swizzle(int token)
+{
+    return DP == 64 ? (token >> 1) & 7 : token & 15;
+}
+
+// One tile of tokens into LDS, this wave's share of it.  rows: lane x's is the
+// pool row of the tile's token x (-1: none).
+template <int DP>
+__device__ __forceinline__ void wide_load(uint64_t kh, uint64_t vh, uint32_t row_bytes, int dim, int32_t rows,
+                                          WideTile<DP>& tile)
+{
+    constexpr int V = DP / 8, kPer = 64 / V;                             // vectors of a row, rows of a load
+    constexpr int kLoads = kWideTile<DP> / kPer / kAttendWaves;
+    const int lane = anew(threadIdx.x & 63), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint64_t zero = reinterpret_cast<uint64_t>(&g_zero_vector);
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+        const int first = (wave * kLoads + i) * kPer;
+        const int tok = first + lane / V, chunk = lane % V ^ wide_swizzle<DP>(tok);
+        const int32_t row = __shfl(rows, tok);
+        const bool there = row >= 0 && chunk * 8 < dim;
+        const uint64_t at = uint64_t(uint32_t(row)) * row_bytes + chunk * 16;
+        __builtin_amdgcn_global_load_lds(gptr<const gvec4>(there ? kh + at : zero),
+                                         (__attribute__((address_space(3))) void*)&tile.k[first * V], 16, 0, 0);
+        __builtin_amdgcn_global_load_lds(gptr<const gvec4>(there ? vh + at : zero),
+                                         (__attribute__((address_space(3))) void*)&tile.v[first * V], 16, 0, 0);
+    }
+}
+
+// The products and the softmax of 32 tokens (half h of a tile) for this wave's
+// NB blocks of rows.
+template <int DP, int NB>
+__device__ __forceinline__ void wide_half(RowState<DP> (&st)[NB], const u32x4 (&q)[NB][DP / 32],
+                                          const WideTile<DP>& tile, int h, float c, bool masked, int32_t t,
+                                          const int32_t (&vis)[NB], uint32_t valid, bool care)
+{
+    constexpr int V = DP / 8, J = DP / 32;
+    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+    f32x4 s[NB][2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b) s[b][i] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const u32x4 k = tile.k[(32 * h + 16 * i + r) * V + ((4 * j + g) ^ wide_swizzle<DP>(r))];
+#pragma unroll
+            for (int b = 0; b < NB; ++b) s[b][i] = mfma16(k, q[b][j], s[b][i]);
         }
+    }
+    u32x4 ph[NB], pl[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) softmax_block<DP>(st[b], s[b], ph[b], pl[b], c, masked, t, vis[b], valid);
+    if (care)                                     // before V takes its registers
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+            add_nonfinite<DP>(
+                st[b], ph[b], pl[b], t, vis[b], valid,
+                [&](int x) { return reinterpret_cast<const uint16_t*>(&tile.v[(32 * h + x) * V]); },
+                [](int x, int d) { return ((d / 8) ^ wide_swizzle<DP>(x)) * 8 + d % 8; });
+    uint32_t v[8][J];
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+        const int tok = 32 * h + 16 * (x / 4) + 4 * g + x % 4, swz = wide_swizzle<DP>(4 * g + x % 4);
+        if constexpr (DP == 64) {
+            const u32x2 y = reinterpret_cast<const u32x2*>(&tile.v[tok * V + (r / 2 ^ swz)])[r & 1];
+            v[x][0] = y[0];
+            v[x][1] = y[1];
+        } else {
+#pragma unroll
+            for (int y = 0; y < DP / 128; ++y) {
+                const u32x4 z = tile.v[tok * V + ((16 * y + r) ^ swz)];
+#pragma unroll
+                for (int w = 0; w < 4; ++w) v[x][4 * y + w] = z[w];
+            }
+        }
+    }
+    if (care) take_nonfinite<DP>(v);
+    add_v<DP, NB>(st, v, ph, pl);
+}
+
+// A piece with many rows: each wave has 16 NB rows, and all of them go through
+// the tokens together, kWideTile at a time, K and V brought into LDS once for
+// the four waves while the tile before is computed.
+template <int DP, int NB>
+__device__ __forceinline__ void wide_piece(const AttendArgs& a, const AttendItem& it, uint64_t kb, uint64_t vb,
+                                           int32_t t1, WideTile<DP>& tile0, WideTile<DP>& tile1)
+{
+    constexpr int T = kWideTile<DP>;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15,
+              g = lane >> 4;
+    const int dim = a.pool.dim;
+    const TablesArg& tab = it.prefix ? a.step.prefix : a.step.own;
+    const uint32_t row_bytes = a.pool.heads * dim * 2;
+    const uint64_t kh = kb + uint64_t(it.h) * dim * 2, vh = vb + uint64_t(it.h) * dim * 2;
+    // lane x looks up token x of a tile, its page two tiles ahead
+    auto page_at = [&](int32_t t) {                // of the last token where there is no such one: no branch to wait at
+        const int x = anew(lane);
+        return token_page(a.pool, tab, it.table_row, x < t1 - t ? t + x : t1 - 1);
+    };
+    auto row_at = [&](int32_t t, int32_t page) {
+        const int x = anew(lane);
+        return x < T && x < t1 - t ? row_in_page(a.pool, page, t + x) : -1;
+    };
+
+    const int32_t f0 = wave * 16 * NB;                       // the wave's first row in the tile
+    u32x4 q[NB][DP / 32];
+    RowState<DP> st[NB];
+    int32_t vis[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        const int32_t f = f0 + 16 * b + r;
+        vis[b] = f < it.flat_n ? visible_end(a, it, f) : 0;
+        load_q<DP>(q[b], a, it, f, f < it.flat_n);
+    }
+    const bool busy = f0 < it.flat_n;
+    const int32_t all_see = busy ? visible_end(a, it, f0) : 0;
+    const int32_t last = f0 + 16 * NB < it.flat_n ? f0 + 16 * NB - 1 : it.flat_n - 1;
+    const int32_t end = busy ? visible_end(a, it, last) : 0; // the wave's rows see nothing from here on
+
+    bool care = false;
+  again:
+#pragma unroll
+    for (int b = 0; b < NB; ++b) clear<DP>(st[b]);
+    int32_t page = -1, rows = -1;
+    uint64_t valid = 0;
+    if (it.t0 < t1) {
+        page = page_at(it.t0);
+        rows = row_at(it.t0, page);
+        page = page_at(it.t0 + T);
+        wide_load<DP>(kh, vh, row_bytes, dim, rows, tile0);
+        valid = __ballot(rows >= 0);
+        rows = row_at(it.t0 + T, page);
+        page = page_at(it.t0 + 2 * T);
+    }
+    // the loads of a tile are waited for one tile after they were issued; the barrier says both that every wave's share
+    // has landed and that the other tile is free again
+    auto one = [&](int32_t t, WideTile<DP>& now, WideTile<DP>& next) {
+        __builtin_amdgcn_s_waitcnt(0);
+        __syncthreads();
+        const uint64_t seen = valid;
+        if (t + T < t1) {
+            wide_load<DP>(kh, vh, row_bytes, dim, rows, next);
+            valid = __ballot(rows >= 0);
+        }
+        rows = row_at(t + 2 * T, page);
+        page = page_at(t + 3 * T);
+#pragma unroll 1
+        for (int h = 0; h < T / 32; ++h) {
+            const int32_t th = t + 32 * h;
+            if (th >= end) break;
+            const uint32_t half = uint32_t(seen >> (32 * h));
+            wide_half<DP, NB>(st, q, now, h, a.scale_log2, half != ~0u || th + 32 > all_see, th, vis, half, care);
+        }
+    };
+    // two tiles by name: with an index between them the reads of one would wait for the loads of the other
+#pragma unroll 1
+    for (int32_t t = it.t0; t < t1; t += 2 * T) {
+        one(t, tile0, tile1);
+        if (t + T >= t1) break;
+        one(t + T, tile1, tile0);
+    }
+    bool finite = true;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) finite = finite && all_finite<DP>(st[b]);
+    if (__syncthreads_or(!finite) && !care) {
+        care = true;
+        goto again;
+    }
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        float l = st[b].l;
+        l += __shfl_xor(l, 16);
+        l += __shfl_xor(l, 32);
+        const int32_t f = f0 + 16 * b + anew(r);
+        if (f >= it.flat_n) continue;
+        const RowSink to = open_row(a, it, f, st[b].m, l, g == 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int m = 0; m < DP / 16; m += 4) {
+                const int d = acc_element<DP>(4 * g + i, m);
+                if (d < dim)
+                    put4(a, to, d,
+                         f32x4{st[b].acc[m][i], st[b].acc[m + 1][i], st[b].acc[m + 2][i], st[b].acc[m + 3][i]});
+            }
+    }
+}
+
+// NB: blocks of 16 rows a wave of the wide form takes; 0: only the narrow form.
+template <int DP, int NB>
+__global__ __launch_bounds__(kAttendBlock, DP <= 128 ? 2 : 1) void attend_pieces(AttendArgs a)
+{
+    const AttendItem it = attend_item(a, blockIdx.x, kAttendWaves * 16 * NB);
+    if (it.flat_n <= 0) return;
+    // the last row sees the most: no later token is needed
+    const int32_t end_all = visible_end(a, it, it.flat_n - 1);
+    int32_t t1 = it.t1 < end_all ? it.t1 : end_all;
+    if (it.t0 >= t1) {
+        if (!a.direct) return;                              // nothing seen: the join takes no such piece
+        t1 = it.t0;
+    }
+    const uint64_t kb = wave_uniform(gptr<const gu64>(a.pool.k_pages)[a.pool.layer]);
+    const uint64_t vb = wave_uniform(gptr<const gu64>(a.pool.v_pages)[a.pool.layer]);
+    if (bad_addr(kb) || bad_addr(vb)) {
+        raise_fault(kFaultPool);
+        t1 = it.t0;
+    }
+    if constexpr (NB > 0) {
+        __shared__ union { WideTile<DP> tile; NarrowShared<DP> narrow; } sh;
+        __shared__ WideTile<DP> other;
+        if (it.prefix ? a.prefix_wide : a.own_wide)
+            wide_piece<DP, NB>(a, it, kb, vb, t1, sh.tile, other);
+        else
+            narrow_piece<DP>(a, it, kb, vb, t1, sh.narrow);
+    } else {
+        __shared__ NarrowShared<DP> sh;
+        narrow_piece<DP>(a, it, kb, vb, t1, sh);
     }
 }
 
@@ -433,10 +834,10 @@ __global__ __launch_bounds__(256) void attend_join(AttendArgs a)
     if (grp == 0 && c * 4 < dim) {
 #pragma unroll
         for (int x = 1; x < G; ++x) o += so[x][c];
-        const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);       // NaN stays
+        const float inv = inverse_sum(l);
         const u32x2 y = {bf16x2_rne(o[0] * inv, o[1] * inv), bf16x2_rne(o[2] * inv, o[3] * inv)};
         *gptr<gvec2>(a.out + (r * a.o_row + head * a.o_head + c * 4) * 2) = y;
-        if (c == 0) gptr<gf32>(a.lse)[int64_t(r) * a.q_heads + head] = (m + __builtin_amdgcn_logf(l)) * kLn2;
+        if (c == 0) gptr<gf32>(a.lse)[int64_t(r) * a.q_heads + head] = log_sum(m, l);
     }
 }
 

@@ -9,7 +9,8 @@ namespace {
 int check_tables(const kv_paged* p, const kv_tables* t, const char* what)
 {
     if (t->n < 0 || t->n > (1 << 24)) return fail(KV_EINVAL, "%s: %d sequences outside [0, 2^24]", what, t->n);
-    if (t->max_len < 0) return fail(KV_EINVAL, "%s: max_len < 0", what);
+    if (t->max_len < 0 || t->max_len > (1 << 30))
+        return fail(KV_EINVAL, "%s: max_len %d outside [0, 2^30]", what, t->max_len);
     if (t->n == 0) return KV_OK;
     if (t->lens == nullptr) return fail(KV_EINVAL, "%s: lens is NULL", what);
     if (t->max_len > 0 && t->table == nullptr) return fail(KV_EINVAL, "%s: table is NULL", what);
@@ -193,6 +194,8 @@ struct AttendShape {
     int32_t prefix_tiles, prefix_pieces, prefix_tokens;
     int32_t own_tiles, own_pieces, own_tokens;
     int32_t slots;
+    int32_t blocks;                // blocks of 16 rows of a wave of the wide form, 0: narrow only
+    bool prefix_wide, own_wide, direct;
     int64_t prefix_items, own_items;
     int64_t ml_bytes, bytes;
 };
@@ -223,15 +226,22 @@ int attend_shape(const kv_paged* p, const kv_step* s, int32_t q_heads, AttendSha
 {
     const int64_t heads = p->num_kv_heads, rep = q_heads / heads;
     AttendShape a{};
-    const int64_t pt = ceil_div(int64_t(s->max_group_rows) * rep, kAttendRows);
-    const int64_t ot = ceil_div(int64_t(s->max_new) * rep, kAttendRows);
+    const int64_t pr = s->prefix.n > 0 ? int64_t(s->max_group_rows) * rep : 0, orows = int64_t(s->max_new) * rep;
+    a.prefix_wide = pr > kAttendRows;
+    a.own_wide = orows > kAttendRows;
+    if (a.prefix_wide || a.own_wide) a.blocks = std::max(pr, orows) > 64 && p->head_dim <= 128 ? 2 : 1;
+    const int64_t wide_rows = kAttendWaves * 16 * a.blocks;
+    const int64_t pt = ceil_div(pr, a.prefix_wide ? wide_rows : kAttendRows);
+    const int64_t ot = ceil_div(orows, a.own_wide ? wide_rows : kAttendRows);
     if (pt > INT32_MAX || ot > INT32_MAX) return fail(KV_EINVAL, "too many rows for one launch");
     a.prefix_tiles = int32_t(pt);
     a.own_tiles = int32_t(ot);
     const int64_t pre = s->prefix.n * heads * pt, own = s->own.n * heads * ot;
     cut_tokens(pre, s->prefix.n > 0 ? s->prefix.max_len : 0, &a.prefix_tokens, &a.prefix_pieces);
     cut_tokens(own, s->own.n > 0 ? s->own.max_len : 0, &a.own_tokens, &a.own_pieces);
-    a.slots = std::max(1, a.prefix_pieces + a.own_pieces);
+    a.own_pieces = std::max(1, a.own_pieces);
+    a.slots = a.prefix_pieces + a.own_pieces;
+    a.direct = a.slots == 1;
     const int64_t most = max_blocks(kAttendBlock);
     if (pre > most || own > most || pre * a.prefix_pieces + own * a.own_pieces > most)
         return fail(KV_EINVAL, "too many row tiles and pieces for one launch");
@@ -259,6 +269,15 @@ int check_q(const kv_rows* q, float scale)
     if (!rows_vectors(*q, 2)) return fail(KV_EINVAL, "q's address and strides must be multiples of 16 bytes");
     if (!(scale > 0.0f) || scale > 1e30f) return fail(KV_EINVAL, "scale must be finite and > 0");
     return KV_OK;
+}
+
+template <int DP>
+KernelFn attend_kernel(int blocks)
+{
+    if constexpr (DP <= 128)
+        if (blocks == 2) return reinterpret_cast<KernelFn>(&attend_pieces<DP, 2>);
+    return blocks == 0 ? reinterpret_cast<KernelFn>(&attend_pieces<DP, 0>)
+                       : reinterpret_cast<KernelFn>(&attend_pieces<DP, 1>);
 }
 
 int attend(const kv_paged* paged, const kv_step* step, int32_t layer, const kv_rows* q, int32_t q_heads, float scale,
@@ -301,15 +320,18 @@ int attend(const kv_paged* paged, const kv_step* step, int32_t layer, const kv_r
     a.own_tokens = sh.own_tokens;
     a.slots = sh.slots;
     a.prefix_items = uint32_t(sh.prefix_items);
+    a.prefix_wide = sh.prefix_wide;
+    a.own_wide = sh.own_wide;
+    a.direct = sh.direct;
     const int dim = paged->head_dim;
-    KernelFn pieces = dim <= 64    ? reinterpret_cast<KernelFn>(&attend_pieces<64>)
-                      : dim <= 128 ? reinterpret_cast<KernelFn>(&attend_pieces<128>)
-                                   : reinterpret_cast<KernelFn>(&attend_pieces<256>);
+    KernelFn pieces = dim <= 64    ? attend_kernel<64>(sh.blocks)
+                      : dim <= 128 ? attend_kernel<128>(sh.blocks)
+                                   : attend_kernel<256>(sh.blocks);
     KernelFn join = dim <= 64    ? reinterpret_cast<KernelFn>(&attend_join<64>)
                     : dim <= 128 ? reinterpret_cast<KernelFn>(&attend_join<128>)
                                  : reinterpret_cast<KernelFn>(&attend_join<256>);
     rc = launch(pieces, sh.prefix_items + sh.own_items, kAttendBlock, &a, stream);
-    if (rc == KV_OK) rc = launch(join, int64_t(step->n_rows) * q_heads, 256, &a, stream);
+    if (rc == KV_OK && !sh.direct) rc = launch(join, int64_t(step->n_rows) * q_heads, 256, &a, stream);
     return rc == KV_OK ? ok() : rc;
 }
 

@@ -67,7 +67,7 @@ __global__ __launch_bounds__(kAttendBlock) void add_weights(WeightsArgs a)
 #pragma unroll
         for (int j = 0; j < J; ++j) {
             k[i][j] = u32x4{0, 0, 0, 0};
-            if (kr >= 0) k[i][j] = load_k8<DP>(kh + kr * row_bytes, j * 32 + g * 8, dim);
+            if (kr >= 0) k[i][j] = load_k8(kh + kr * row_bytes, j * 32 + g * 8, dim);
         }
     }
     f32x4 sum[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
@@ -90,7 +90,7 @@ __global__ __launch_bounds__(kAttendBlock) void add_weights(WeightsArgs a)
 #pragma unroll
         for (int j = 0; j < J; ++j) {
             u32x4 q = {0, 0, 0, 0};
-            if (live) q = load_k8<DP>(a.q + (qr * a.q_row + head * a.q_head) * 2, j * 32 + g * 8, dim);
+            if (live) q = load_k8(a.q + (qr * a.q_row + head * a.q_head) * 2, j * 32 + g * 8, dim);
             s[0] = mfma16(k[0][j], q, s[0]);
             s[1] = mfma16(k[1][j], q, s[1]);
         }
