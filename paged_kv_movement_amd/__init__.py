@@ -630,13 +630,25 @@ def copy_blocks(dst, src, nbytes: int, block_bytes: int, permute: int, stream=No
 
 # ---- a model step on the paged pool: append, attend, add_weights, evict
 
-def _here(*tensors) -> None:
-    """Every tensor on the current device (the calls launch there)."""
-    import torch
-    cur = torch.cuda.current_device()
+_torch = None
+
+
+def _t():
+    """torch, imported on the first use and kept: a step's calls are made every few microseconds."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
+def _here(*tensors) -> int:
+    """The current device; every tensor must be on it (the calls launch there)."""
+    cur = _t().cuda.current_device()
     for t in tensors:
-        if t is not None and not (t.is_cuda and t.device.index == cur):
+        if t is not None and t.get_device() != cur:
             raise KvError(KV_EINVAL, f"every tensor must be on the current device (cuda:{cur}), got {t.device}")
+    return cur
 
 
 def _ref(struct):
@@ -725,7 +737,9 @@ class Step:
         if prefix is not None:
             self._tensors += [prefix.table, prefix.lens]
         self._on_streams = set()
-        _here(*self._tensors)
+        self._dim = paged.head_dim
+        self._device = _here(*self._tensors)
+        self._ref = ctypes.byref(self.c)
 
     def attend_workspace_bytes(self, q_heads: int) -> int:
         """Device bytes attend needs (kv_attend_workspace_bytes)."""
@@ -740,22 +754,31 @@ class Step:
         return torch.empty(self.attend_workspace_bytes(q_heads), dtype=torch.uint8, device=self.own.table.device)
 
     def _rows(self, t, heads, what, types):
-        """(kv_rows of a tensor [n_rows, heads, head_dim], its type)."""
-        _need(t.dtype in types, f"{what} has type {t.dtype}")
-        _need(tuple(t.shape) == (self.n_rows, heads, self.paged.head_dim),
-              f"{what} must be [{self.n_rows}, {heads}, {self.paged.head_dim}], got {list(t.shape)}")
+        """kv_rows of a tensor [n_rows, heads, head_dim] of one of the types."""
+        if t.dtype not in types:
+            raise KvError(KV_EINVAL, f"{what} has type {t.dtype}")
+        if t.shape != (self.n_rows, heads, self._dim):
+            raise KvError(KV_EINVAL, f"{what} must be [{self.n_rows}, {heads}, {self._dim}], got {list(t.shape)}")
         row, head, last = t.stride()
-        _need(last == 1 or self.paged.head_dim == 1, f"{what}: the last dimension must be contiguous")
+        if last != 1 and self._dim != 1:
+            raise KvError(KV_EINVAL, f"{what}: the last dimension must be contiguous")
         return _KvRows(t.data_ptr(), row, head)
 
     def _call(self, paged, stream, *tensors) -> int | None:
-        _need(paged is self.paged or paged.c.page_size == self.paged.c.page_size
-              and paged.head_dim == self.paged.head_dim and paged.num_kv_heads == self.paged.num_kv_heads,
-              "the step was made for a pool of another shape")
-        _here(*self._tensors, *tensors)
-        if stream is not None:
-            _used_on(stream, self._tensors, self._on_streams)
-            _used_on(stream, tensors)
+        """Checks of every call; the handle of its stream (None: the current one)."""
+        if paged is not self.paged and (paged.page_size, paged.head_dim, paged.num_kv_heads) != \
+                (self.paged.page_size, self._dim, self.paged.num_kv_heads):
+            raise KvError(KV_EINVAL, "the step was made for a pool of another shape")
+        if _here(*tensors) != self._device:
+            raise KvError(KV_EINVAL, f"the step's tables are on cuda:{self._device}, not on the current device")
+        if paged is not self.paged:
+            _here(paged.k_addrs)
+        if stream is None:
+            return _t()._C._cuda_getCurrentRawStream(self._device) or None
+        _used_on(stream, self._tensors, self._on_streams)
+        if paged is not self.paged:
+            _used_on(stream, (paged.k_addrs, paged.v_addrs))
+        _used_on(stream, tensors)
         return _stream_handle(stream)
 
 
@@ -812,19 +835,25 @@ class Rope:
         return f, gain
 
 
+_type_codes = None
+
+
 def _types():
-    import torch
-    return {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+    global _type_codes
+    if _type_codes is None:
+        _type_codes = {_t().bfloat16: 0, _t().float16: 1, _t().float32: 2}
+    return _type_codes
 
 
 def _slots(weights, positions, shape, what):
     """kv_slots of contiguous [*shape, heads, cap] tensors."""
-    import torch
+    torch = _t()
     for t, dt, name in ((weights, torch.float32, "weights"), (positions, torch.int32, "positions")):
-        _need(t is not None and t.dtype == dt and t.is_contiguous() and t.dim() == len(shape) + 2
-              and tuple(t.shape[:len(shape)]) == tuple(shape),
-              f"{what} {name} must be a contiguous {dt} device tensor {list(shape)} + [heads, slots]")
-    _need(weights.shape == positions.shape, f"{what} weights and positions must have one shape")
+        if t is None or t.dtype != dt or not t.is_contiguous() or t.dim() != len(shape) + 2 or t.shape[:-2] != shape:
+            raise KvError(KV_EINVAL,
+                          f"{what} {name} must be a contiguous {dt} device tensor {list(shape)} + [heads, slots]")
+    if weights.shape != positions.shape:
+        raise KvError(KV_EINVAL, f"{what} weights and positions must have one shape")
     return _KvSlots(weights.data_ptr(), positions.data_ptr(), weights.shape[-2], weights.shape[-1])
 
 
@@ -838,14 +867,15 @@ def append(paged: Paged, step: Step, layer: int, q, k, v, positions, rope: Rope,
     ``weights`` / ``slot_positions`` [sequences, H or 1, slots]: this layer's
     eviction state; the new slots' weights become 0 and their positions the
     tokens'.  Returns the rotated q."""
-    import torch
+    torch = _t()
     types = _types()
     st = step
     H = paged.num_kv_heads
     ck, cv = st._rows(k, H, "k", types), st._rows(v, H, "v", types)
-    _need(k.dtype == v.dtype and (q is None or q.dtype == k.dtype), "q, k and v must have one type")
-    _need(positions.dtype == torch.int32 and positions.is_contiguous() and tuple(positions.shape) == (st.n_rows,),
-          f"positions must be a contiguous int32 device tensor [{st.n_rows}]")
+    if k.dtype != v.dtype or (q is not None and q.dtype != k.dtype):
+        raise KvError(KV_EINVAL, "q, k and v must have one type")
+    if positions.dtype != torch.int32 or not positions.is_contiguous() or positions.shape != (st.n_rows,):
+        raise KvError(KV_EINVAL, f"positions must be a contiguous int32 device tensor [{st.n_rows}]")
     cq = co = None
     q_heads, out_type = 0, types[k.dtype]
     if q is not None:
@@ -862,14 +892,16 @@ def append(paged: Paged, step: Step, layer: int, q, k, v, positions, rope: Rope,
     if weights is not None or slot_positions is not None:
         cs = _slots(weights, slot_positions, (st.own.n,), "append:")
     h = st._call(paged, stream, q, k, v, positions, rope.freqs, q_out, weights, slot_positions)
-    _check(load().kv_append(ctypes.byref(paged.c), ctypes.byref(st.c), layer, _ref(cq), ctypes.byref(ck),
-                            ctypes.byref(cv), _ref(co), q_heads, types[k.dtype], out_type, positions.data_ptr(),
-                            ctypes.byref(rope.c), _ref(cs), h))
+    rc = load().kv_append(ctypes.byref(paged.c), st._ref, layer, _ref(cq), ctypes.byref(ck), ctypes.byref(cv),
+                          _ref(co), q_heads, types[k.dtype], out_type, positions.data_ptr(), ctypes.byref(rope.c),
+                          _ref(cs), h)
+    if rc != KV_OK:
+        _check(rc)
     return q_out
 
 
 def _q(paged, step, q):
-    import torch
+    torch = _t()
     _need(q.dim() == 3, "q must be [rows, q_heads, head_dim]")
     return step._rows(q, q.shape[1], "q", (torch.bfloat16,)), q.shape[1]
 
@@ -884,34 +916,37 @@ def attend(paged: Paged, step: Step, layer: int, q, scale=None, out=None, lse=No
     ``scale``: 1/sqrt(D) unless given.  ``workspace``: a device uint8 tensor of
     step.attend_workspace_bytes(q_heads) (None: one is allocated for the call).
     Returns (out bf16 like q, lse float32 [rows, q_heads])."""
-    import torch
+    torch = _t()
     cq, heads = _q(paged, step, q)
     if out is None:
         out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     if lse is None:
         lse = torch.empty((step.n_rows, heads), dtype=torch.float32, device=q.device)
     co = step._rows(out, heads, "out", (torch.bfloat16,))
-    _need(lse.dtype == torch.float32 and lse.is_contiguous() and tuple(lse.shape) == (step.n_rows, heads),
-          f"lse must be a contiguous float32 device tensor [{step.n_rows}, {heads}]")
+    if lse.dtype != torch.float32 or not lse.is_contiguous() or lse.shape != (step.n_rows, heads):
+        raise KvError(KV_EINVAL, f"lse must be a contiguous float32 device tensor [{step.n_rows}, {heads}]")
     if workspace is None:
         workspace = step.new_attend_workspace(heads)
     ws, n_ws = _workspace(workspace)
     h = step._call(paged, stream, q, out, lse, workspace)
-    _check(load().kv_attend(ctypes.byref(paged.c), ctypes.byref(step.c), layer, ctypes.byref(cq), heads,
-                            _scale(paged, scale), ctypes.byref(co), lse.data_ptr(), ws, n_ws, h))
+    rc = load().kv_attend(ctypes.byref(paged.c), step._ref, layer, ctypes.byref(cq), heads, _scale(paged, scale),
+                          ctypes.byref(co), lse.data_ptr(), ws, n_ws, h)
+    if rc != KV_OK:
+        _check(rc)
     return out, lse
 
 
 def _sums(inp, out, n, heads, what):
-    import torch
+    torch = _t()
     if out is None:
         out = inp
     if out is None:
         return None, None
     for t in (inp, out):
-        _need(t is None or (t.dtype == torch.float32 and t.is_contiguous() and t.dim() == 3
-                            and tuple(t.shape[:2]) == (n, heads) and t.shape == out.shape),
-              f"{what} must be contiguous float32 device tensors [{n}, {heads}, slots] of one shape")
+        if t is not None and (t.dtype != torch.float32 or not t.is_contiguous() or t.dim() != 3
+                              or t.shape[:2] != (n, heads) or t.shape != out.shape):
+            raise KvError(KV_EINVAL,
+                          f"{what} must be contiguous float32 device tensors [{n}, {heads}, slots] of one shape")
     return _KvSums(inp.data_ptr() if inp is not None else None, out.data_ptr(), out.shape[2]), out
 
 
@@ -923,16 +958,18 @@ def add_weights(paged: Paged, step: Step, layer: int, q, lse, weights=None, pref
     (either may be None: not computed), in place, or into ``out`` /
     ``prefix_out`` (with weights None: from zero).  ``lse``: what attend
     returned.  Returns (own sums, prefix sums)."""
-    import torch
+    torch = _t()
     cq, heads = _q(paged, step, q)
-    _need(lse.dtype == torch.float32 and lse.is_contiguous() and tuple(lse.shape) == (step.n_rows, heads),
-          f"lse must be a contiguous float32 device tensor [{step.n_rows}, {heads}]")
+    if lse.dtype != torch.float32 or not lse.is_contiguous() or lse.shape != (step.n_rows, heads):
+        raise KvError(KV_EINVAL, f"lse must be a contiguous float32 device tensor [{step.n_rows}, {heads}]")
     co, out = _sums(weights, out, step.own.n, paged.num_kv_heads, "weights")
     cp, prefix_out = _sums(prefix_weights, prefix_out, step.prefix.n if step.prefix is not None else 0,
                            paged.num_kv_heads, "prefix weights")
     h = step._call(paged, stream, q, lse, weights, prefix_weights, out, prefix_out)
-    _check(load().kv_add_weights(ctypes.byref(paged.c), ctypes.byref(step.c), layer, ctypes.byref(cq),
-                                 lse.data_ptr(), heads, _scale(paged, scale), _ref(co), _ref(cp), h))
+    rc = load().kv_add_weights(ctypes.byref(paged.c), step._ref, layer, ctypes.byref(cq), lse.data_ptr(), heads,
+                               _scale(paged, scale), _ref(co), _ref(cp), h)
+    if rc != KV_OK:
+        _check(rc)
     return out, prefix_out
 
 
@@ -945,7 +982,7 @@ def evict(paged: Paged, tables: Tables, layer_begin: int, layer_end: int, weight
     [layers, sequences, H or 1, >= keep] are given.  ``workspace``: a device
     uint8 tensor of tables.evict_workspace_bytes(...) (None: allocated for the
     call).  Returns the new lengths, an int32 tensor [sequences]."""
-    import torch
+    torch = _t()
     shape = (layer_end - layer_begin, tables.n)
     ci = _slots(weights, positions, shape, "evict:")
     if out_weights is None and out_positions is None:
@@ -955,15 +992,21 @@ def evict(paged: Paged, tables: Tables, layer_begin: int, layer_end: int, weight
     tables._check(paged)
     if out_lens is None:
         out_lens = torch.empty((tables.n,), dtype=torch.int32, device=tables.table.device)
-    _need(out_lens.dtype == torch.int32 and out_lens.is_contiguous() and tuple(out_lens.shape) == (tables.n,),
-          f"out_lens must be a contiguous int32 device tensor [{tables.n}]")
+    if out_lens.dtype != torch.int32 or not out_lens.is_contiguous() or out_lens.shape != (tables.n,):
+        raise KvError(KV_EINVAL, f"out_lens must be a contiguous int32 device tensor [{tables.n}]")
     if workspace is None:
         workspace = tables.new_evict_workspace(paged, shape[0], ci.heads, keep)
     ws, n_ws = _workspace(workspace)
     used = (paged.k_addrs, paged.v_addrs, tables.table, tables.lens, weights, positions, out_weights, out_positions,
             out_lens, workspace)
-    _here(*used)
-    _used_on(stream, used)
-    _check(load().kv_evict(ctypes.byref(paged.c), ctypes.byref(tables.c), layer_begin, layer_end, ctypes.byref(ci),
-                           ctypes.byref(co), keep, recent, out_lens.data_ptr(), ws, n_ws, _stream_handle(stream)))
+    dev = _here(*used)
+    if stream is None:
+        h = torch._C._cuda_getCurrentRawStream(dev) or None
+    else:
+        _used_on(stream, used)
+        h = _stream_handle(stream)
+    rc = load().kv_evict(ctypes.byref(paged.c), ctypes.byref(tables.c), layer_begin, layer_end, ctypes.byref(ci),
+                         ctypes.byref(co), keep, recent, out_lens.data_ptr(), ws, n_ws, h)
+    if rc != KV_OK:
+        _check(rc)
     return out_lens
