@@ -779,65 +779,152 @@ __global__ __launch_bounds__(kAttendBlock, DP <= 128 ? 2 : 1) void attend_pieces
     }
 }
 
-// One workgroup per (row, query head): its valid pieces, prefix first.
+// What a join needs of row r: its tokens and how many pieces each side has.
+// One round of loads for up to 64 sequences and groups (lane i holds the i-th
+// of both; the row's own are taken from the lanes that hold them), and one
+// more only where a group may be larger than its bound.
+struct RowPieces {
+    int32_t prefix, own;       // pieces; own < 0: a row of no sequence
+};
+
+__device__ __forceinline__ RowPieces row_pieces(const AttendArgs& a, int32_t r)
+{
+    const StepArg& st = a.step;
+    const int32_t lane = threadIdx.x & 63;
+    int32_t s = -1, first = 0, count = 0, len = 0;
+    for (int32_t i0 = 0; i0 < st.own.n && s < 0; i0 += 64) {
+        const int32_t i = i0 + lane;
+        int32_t b = 0, e = 0, n = 0;
+        if (i < st.own.n) {
+            b = gptr<const gi32>(st.q_start)[i];
+            e = gptr<const gi32>(st.q_start)[i + 1];
+            n = table_len(st.own, i);
+        }
+        const uint64_t m = __ballot(b <= r && r < e);
+        if (m == 0) continue;
+        const int j = __builtin_ctzll(m);
+        s = i0 + j;
+        first = clamp_i32(__builtin_amdgcn_readlane(b, j), 0, st.n_rows);
+        count = clamp_i32(__builtin_amdgcn_readlane(e, j), first, st.n_rows) - first;
+        count = count < st.max_new ? count : st.max_new;
+        len = __builtin_amdgcn_readlane(n, j);
+    }
+    if (s < 0 || r - first >= count) return {0, -1};
+    int32_t prefix = 0;
+    for (int32_t i0 = 0; i0 < st.prefix.n; i0 += 64) {
+        const int32_t i = i0 + lane;
+        int32_t b = 0, e = 0, n = 0;
+        if (i < st.prefix.n) {
+            b = gptr<const gi32>(st.group_start)[i];
+            e = gptr<const gi32>(st.group_start)[i + 1];
+            n = table_len(st.prefix, i);
+        }
+        const uint64_t m = __ballot(b <= s && s < e);
+        if (m == 0) continue;
+        const int j = __builtin_ctzll(m);
+        prefix = __builtin_amdgcn_readlane(n, j);
+        if (st.max_group_rows < st.n_rows) {                   // else no group can be cut
+            const Rows gr = group_rows(st, i0 + j);
+            if (r - gr.first >= gr.count) prefix = 0;
+        }
+        break;
+    }
+    const int32_t own = clamp_i32(len - count + (r - first) + 1, 0, len);
+    return {int32_t((uint32_t(prefix) + a.prefix_tokens - 1) / uint32_t(a.prefix_tokens)),
+            int32_t((uint32_t(own) + a.own_tokens - 1) / uint32_t(a.own_tokens))};
+}
+
+// Joins the pieces of (row, query head), G lanes' worth of slots at a time:
+// lane group `grp` of `groups` takes pieces grp, grp + groups, ...  Returns
+// this lane's elements [4 c, 4 c + 4), summed over its own group only, and
+// the row's maximum and sum.
+template <int DP>
+__device__ __forceinline__ f32x4 join_row(const AttendArgs& a, int64_t at, RowPieces n, int c, int grp, int groups,
+                                          float& m, float& l)
+{
+    const int lane = threadIdx.x & 63, dim = a.pool.dim, total = n.prefix + n.own;
+    auto slot_of = [&](int x) { return x < n.prefix ? x : a.prefix_pieces + x - n.prefix; };
+    float pm = -__builtin_inff(), pl = 0.0f;                   // this lane's piece of the first 64
+    if (lane < total) {
+        const int64_t p = at + slot_of(lane);
+        pm = gptr<const gf32>(a.part_ml)[2 * p];
+        pl = gptr<const gf32>(a.part_ml)[2 * p + 1];
+    }
+    m = pm;
+    for (int x = lane + 64; x < total; x += 64)
+        m = __builtin_fmaxf(m, gptr<const gf32>(a.part_ml)[2 * (at + slot_of(x))]);
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) m = __builtin_fmaxf(m, __shfl_xor(m, d));
+    const float base = m == -__builtin_inff() ? 0.0f : m;
+    const float w = __builtin_amdgcn_exp2f(pm - base);         // weight of this lane's piece
+    l = lane < total ? w * pl : 0.0f;
+    for (int x = lane + 64; x < total; x += 64) {
+        const int64_t p = at + slot_of(x);
+        l += __builtin_amdgcn_exp2f(gptr<const gf32>(a.part_ml)[2 * p] - base) * gptr<const gf32>(a.part_ml)[2 * p + 1];
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) l += __shfl_xor(l, d);
+    f32x4 o = {0, 0, 0, 0};
+#pragma unroll 2
+    for (int x0 = 0; x0 < total; x0 += groups) {               // the same rounds in every lane
+        const int x = x0 + grp;
+        float e = __shfl(w, x & 63);
+        if (x >= 64 && x < total)
+            e = __builtin_amdgcn_exp2f(gptr<const gf32>(a.part_ml)[2 * (at + slot_of(x))] - base);
+        if (x < total && c * 4 < dim) o += *gptr<const gf32x4>(a.part_acc + ((at + slot_of(x)) * dim + c * 4) * 4) * e;
+    }
+    return o;
+}
+
+__device__ __forceinline__ void put_joined(const AttendArgs& a, int32_t r, int32_t head, int c, f32x4 o, float m,
+                                           float l)
+{
+    const float inv = inverse_sum(l);
+    const u32x2 y = {bf16x2_rne(o[0] * inv, o[1] * inv), bf16x2_rne(o[2] * inv, o[3] * inv)};
+    *gptr<gvec2>(a.out + (r * a.o_row + head * a.o_head + c * 4) * 2) = y;
+    if (c == 0) gptr<gf32>(a.lse)[int64_t(r) * a.q_heads + head] = log_sum(m, l);
+}
+
+// Few rows, many pieces: a workgroup per (row, query head).
 template <int DP>
 __global__ __launch_bounds__(256) void attend_join(AttendArgs a)
 {
     constexpr int L = DP / 4, G = 256 / L;
     __shared__ f32x4 so[G][L];
     const int32_t r = blockIdx.x / a.q_heads, head = blockIdx.x - r * a.q_heads;
-    const int32_t s = wave_find(a.step.q_start, a.step.own.n, r);
-    if (s < 0) return;
-    const Rows rows = seq_rows(a.step, s);
-    const int32_t i = r - rows.first;
-    if (i >= rows.count) return;
-    const int32_t len = table_len(a.step.own, s);
-    const int32_t own = clamp_i32(len - rows.count + i + 1, 0, len);
-    int32_t n_pre = 0;
-    if (a.step.prefix.n > 0) {
-        const int32_t g = wave_find(a.step.group_start, a.step.prefix.n, s);
-        if (g >= 0) {
-            const Rows gr = group_rows(a.step, g);
-            if (r - gr.first < gr.count)
-                n_pre = (table_len(a.step.prefix, g) + a.prefix_tokens - 1) / a.prefix_tokens;
-        }
-    }
-    const int32_t n_own = (own + a.own_tokens - 1) / a.own_tokens, n = n_pre + n_own;
-    const int64_t at = (int64_t(r) * a.q_heads + head) * a.slots;
-    const int lane = threadIdx.x & 63;
-    float m = -__builtin_inff();
-    for (int x = lane; x < n; x += 64) {
-        const int slot = x < n_pre ? x : a.prefix_pieces + x - n_pre;
-        m = __builtin_fmaxf(m, gptr<const gf32>(a.part_ml)[2 * (at + slot)]);
-    }
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) m = __builtin_fmaxf(m, __shfl_xor(m, d));
-    const float base = m == -__builtin_inff() ? 0.0f : m;
-    float l = 0.0f;
-    for (int x = lane; x < n; x += 64) {
-        const int slot = x < n_pre ? x : a.prefix_pieces + x - n_pre;
-        const float e = __builtin_amdgcn_exp2f(gptr<const gf32>(a.part_ml)[2 * (at + slot)] - base);
-        l += e * gptr<const gf32>(a.part_ml)[2 * (at + slot) + 1];
-    }
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) l += __shfl_xor(l, d);
-    const int dim = a.pool.dim, c = threadIdx.x % L, grp = threadIdx.x / L;
-    f32x4 o = {0, 0, 0, 0};
-    if (c * 4 < dim)
-        for (int x = grp; x < n; x += G) {
-            const int slot = x < n_pre ? x : a.prefix_pieces + x - n_pre;
-            const float e = __builtin_amdgcn_exp2f(gptr<const gf32>(a.part_ml)[2 * (at + slot)] - base);
-            o += *gptr<const gf32x4>(a.part_acc + ((at + slot) * dim + c * 4) * 4) * e;
-        }
+    const RowPieces n = row_pieces(a, r);
+    if (n.own < 0) return;
+    const int c = threadIdx.x % L, grp = threadIdx.x / L;
+    float m, l;
+    f32x4 o = join_row<DP>(a, (int64_t(r) * a.q_heads + head) * a.slots, n, c, grp, G, m, l);
     so[grp][c] = o;
     __syncthreads();
-    if (grp == 0 && c * 4 < dim) {
+    if (grp == 0 && c * 4 < int(a.pool.dim)) {
 #pragma unroll
         for (int x = 1; x < G; ++x) o += so[x][c];
-        const float inv = inverse_sum(l);
-        const u32x2 y = {bf16x2_rne(o[0] * inv, o[1] * inv), bf16x2_rne(o[2] * inv, o[3] * inv)};
-        *gptr<gvec2>(a.out + (r * a.o_row + head * a.o_head + c * 4) * 2) = y;
-        if (c == 0) gptr<gf32>(a.lse)[int64_t(r) * a.q_heads + head] = log_sum(m, l);
+        put_joined(a, r, head, c, o, m, l);
+    }
+}
+
+// Many rows: a workgroup per row, a wave per query head at a time, so that a
+// row's lookups are made once for its heads.
+template <int DP>
+__global__ __launch_bounds__(256) void attend_join_rows(AttendArgs a)
+{
+    constexpr int L = DP / 4, G = 64 / L;
+    const int32_t r = blockIdx.x;
+    const RowPieces n = row_pieces(a, r);
+    if (n.own < 0) return;
+    const int lane = threadIdx.x & 63, c = lane % L, grp = lane / L;
+#pragma unroll 1
+    for (int32_t head = threadIdx.x >> 6; head < a.q_heads; head += 4) {
+        float m, l;
+        f32x4 o = join_row<DP>(a, (int64_t(r) * a.q_heads + head) * a.slots, n, c, grp, G, m, l);
+#pragma unroll
+        for (int d = L; d < 64; d *= 2)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[e] += __shfl_xor(o[e], d);
+        if (grp == 0 && c * 4 < int(a.pool.dim)) put_joined(a, r, head, c, o, m, l);
     }
 }
 

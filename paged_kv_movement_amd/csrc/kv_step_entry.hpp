@@ -209,15 +209,13 @@ int check_heads(const kv_paged* p, int32_t q_heads)
     return KV_OK;
 }
 
-// Tokens of a piece: enough pieces that all pairs of (row tile, KV head)
-// together give about kItems workgroups, in whole rounds of a workgroup's
-// waves.
-void cut_tokens(int64_t pairs, int32_t max_len, int32_t* tokens, int32_t* pieces)
+// Tokens of a piece: as many pieces as make `items` workgroups of all pairs
+// of (row tile, KV head) together, in whole rounds of a workgroup's waves.
+void cut_tokens(int64_t pairs, int32_t max_len, int64_t items, int32_t* tokens, int32_t* pieces)
 {
-    constexpr int64_t kItems = 1024, kRound = kAttendWaves * kAttendTile;
-    const int64_t want = std::max<int64_t>(1, kItems / std::max<int64_t>(1, pairs));
-    int64_t t = ceil_div(ceil_div(std::max(max_len, 1), want), kRound) * kRound;
-    t = std::min<int64_t>(t, (INT32_MAX / kRound) * kRound);
+    constexpr int64_t kRound = kAttendWaves * kAttendTile;
+    const int64_t want = std::max<int64_t>(1, items / std::max<int64_t>(1, pairs));
+    const int64_t t = ceil_div(ceil_div(std::max(max_len, 1), want), kRound) * kRound;
     *tokens = int32_t(t);
     *pieces = int32_t(ceil_div(max_len, t));
 }
@@ -237,12 +235,22 @@ int attend_shape(const kv_paged* p, const kv_step* s, int32_t q_heads, AttendSha
     a.prefix_tiles = int32_t(pt);
     a.own_tiles = int32_t(ot);
     const int64_t pre = s->prefix.n * heads * pt, own = s->own.n * heads * ot;
-    cut_tokens(pre, s->prefix.n > 0 ? s->prefix.max_len : 0, &a.prefix_tokens, &a.prefix_pieces);
-    cut_tokens(own, s->own.n > 0 ? s->own.max_len : 0, &a.own_tokens, &a.own_pieces);
+    // Two workgroups fit a CU, so 512 pieces run at once: fewer leave CUs idle, more cost a round of set-up and twice the
+    // pieces to join (one 10000-token sequence: 18.6 us, with 1024 pieces 23.9).  A wide prefix beside narrow own pieces
+    // takes 256, one a CU: it waits for the matrix cores, they for memory, and each CU then holds both (64 sequences
+    // behind two 32768-token prefixes: 205 us, with 512 pieces 232) -- unless the own tokens are few beside it, a token
+    // of a narrow piece costing what one of a wide tile does.
+    const int64_t full = 512;
+    const int64_t prefix_work = s->prefix.n * pt * (s->prefix.n > 0 ? s->prefix.max_len : 0);
+    const int64_t own_work = int64_t(s->own.n) * s->own.max_len;
+    const bool beside = a.prefix_wide && !a.own_wide && 2 * own_work >= prefix_work;
+    cut_tokens(pre, s->prefix.n > 0 ? s->prefix.max_len : 0, beside ? full / 2 : full, &a.prefix_tokens,
+               &a.prefix_pieces);
+    cut_tokens(own, s->own.n > 0 ? s->own.max_len : 0, full, &a.own_tokens, &a.own_pieces);
     a.own_pieces = std::max(1, a.own_pieces);
     a.slots = a.prefix_pieces + a.own_pieces;
     a.direct = a.slots == 1;
-    const int64_t most = max_blocks(kAttendBlock);
+    const int64_t most = max_blocks(kAttendBlock) - 16;
     if (pre > most || own > most || pre * a.prefix_pieces + own * a.own_pieces > most)
         return fail(KV_EINVAL, "too many row tiles and pieces for one launch");
     a.prefix_items = pre * a.prefix_pieces;
@@ -278,6 +286,12 @@ KernelFn attend_kernel(int blocks)
         if (blocks == 2) return reinterpret_cast<KernelFn>(&attend_pieces<DP, 2>);
     return blocks == 0 ? reinterpret_cast<KernelFn>(&attend_pieces<DP, 0>)
                        : reinterpret_cast<KernelFn>(&attend_pieces<DP, 1>);
+}
+
+template <int DP>
+KernelFn join_kernel(bool by_row)
+{
+    return by_row ? reinterpret_cast<KernelFn>(&attend_join_rows<DP>) : reinterpret_cast<KernelFn>(&attend_join<DP>);
 }
 
 int attend(const kv_paged* paged, const kv_step* step, int32_t layer, const kv_rows* q, int32_t q_heads, float scale,
@@ -327,15 +341,26 @@ int attend(const kv_paged* paged, const kv_step* step, int32_t layer, const kv_r
     KernelFn pieces = dim <= 64    ? attend_kernel<64>(sh.blocks)
                       : dim <= 128 ? attend_kernel<128>(sh.blocks)
                                    : attend_kernel<256>(sh.blocks);
-    KernelFn join = dim <= 64    ? reinterpret_cast<KernelFn>(&attend_join<64>)
-                    : dim <= 128 ? reinterpret_cast<KernelFn>(&attend_join<128>)
-                                 : reinterpret_cast<KernelFn>(&attend_join<256>);
+    // rows enough to fill the GPU: a workgroup a row
+    const bool by_row = step->n_rows >= 1024;
+    KernelFn join = dim <= 64    ? join_kernel<64>(by_row)
+                    : dim <= 128 ? join_kernel<128>(by_row)
+                                 : join_kernel<256>(by_row);
     rc = launch(pieces, sh.prefix_items + sh.own_items, kAttendBlock, &a, stream);
-    if (rc == KV_OK && !sh.direct) rc = launch(join, int64_t(step->n_rows) * q_heads, 256, &a, stream);
+    if (rc == KV_OK && !sh.direct)
+        rc = launch(join, by_row ? step->n_rows : int64_t(step->n_rows) * q_heads, 256, &a, stream);
     return rc == KV_OK ? ok() : rc;
 }
 
 // ---- weights
+
+template <int DP>
+KernelFn weights_kernel(bool split_rows, int32_t* tokens)
+{
+    *tokens = split_rows ? kWeightsTokens<DP, true> : kWeightsTokens<DP, false>;
+    return split_rows ? reinterpret_cast<KernelFn>(&add_weights<DP, true>)
+                      : reinterpret_cast<KernelFn>(&add_weights<DP, false>);
+}
 
 int add_weights_call(const kv_paged* paged, const kv_step* step, int32_t layer, const kv_rows* q, const float* lse,
                      int32_t q_heads, float scale, const kv_sums* own, const kv_sums* prefix, hipStream_t stream)
@@ -366,28 +391,32 @@ int add_weights_call(const kv_paged* paged, const kv_step* step, int32_t layer, 
     a.q_heads = q_heads;
     a.rep = q_heads / paged->num_kv_heads;
     a.scale_log2 = float(double(scale) * 1.4426950408889634);
+    // many rows: the waves share a workgroup's tokens and split the rows
+    const int64_t rows = std::max(own != nullptr ? step->max_new : 0, prefix != nullptr ? step->max_group_rows : 0);
+    const bool split = rows * a.rep > 256;
+    const int dim = paged->head_dim;
+    int32_t tokens = 0;
+    KernelFn f = dim <= 64    ? weights_kernel<64>(split, &tokens)
+                 : dim <= 128 ? weights_kernel<128>(split, &tokens)
+                              : weights_kernel<256>(split, &tokens);
     int64_t own_items = 0, prefix_items = 0;
     if (own != nullptr) {
         a.own_in = reinterpret_cast<uint64_t>(own->in);
         a.own_out = reinterpret_cast<uint64_t>(own->out);
         a.own_cap = own->cap;
-        a.own_blocks = int32_t(ceil_div(step->own.max_len, kWeightsTokens));
+        a.own_blocks = int32_t(ceil_div(step->own.max_len, tokens));
         own_items = int64_t(step->own.n) * paged->num_kv_heads * a.own_blocks;
     }
     if (prefix != nullptr) {
         a.prefix_in = reinterpret_cast<uint64_t>(prefix->in);
         a.prefix_out = reinterpret_cast<uint64_t>(prefix->out);
         a.prefix_cap = prefix->cap;
-        a.prefix_blocks = int32_t(ceil_div(step->prefix.max_len, kWeightsTokens));
+        a.prefix_blocks = int32_t(ceil_div(step->prefix.max_len, tokens));
         prefix_items = int64_t(step->prefix.n) * paged->num_kv_heads * a.prefix_blocks;
     }
     const int64_t most = max_blocks(kAttendBlock);
     if (own_items > most || prefix_items > most) return fail(KV_EINVAL, "too many tokens for one launch");
     a.prefix_items = uint32_t(prefix_items);
-    const int dim = paged->head_dim;
-    KernelFn f = dim <= 64    ? reinterpret_cast<KernelFn>(&add_weights<64>)
-                 : dim <= 128 ? reinterpret_cast<KernelFn>(&add_weights<128>)
-                              : reinterpret_cast<KernelFn>(&add_weights<256>);
     rc = launch(f, prefix_items + own_items, kAttendBlock, &a, stream);
     return rc == KV_OK ? ok() : rc;
 }
