@@ -42,6 +42,7 @@ struct AttendArgs {
     uint64_t part_ml;              // float2 [n_rows * q_heads][slots]: maximum (log2 units) and sum of a piece
     uint64_t part_acc;             // float32 [n_rows * q_heads][slots][dim]
     int32_t q_heads, rep;          // rep = q_heads / KV heads
+    uint32_t rep_magic, rep_shift; // f / rep = (f * rep_magic) >> rep_shift for f < 2^31
     float scale_log2;              // scale * log2(e)
     int32_t prefix_tiles, prefix_pieces, prefix_tokens;   // row tiles of a group, pieces, tokens of a piece
     int32_t own_tiles, own_pieces, own_tokens;
@@ -92,12 +93,19 @@ __device__ __forceinline__ AttendItem attend_item(const AttendArgs& a, uint32_t 
     return it;
 }
 
+// New token of the flattened row f, counted from the first.
+template <class Args>
+__device__ __forceinline__ int32_t new_token(const Args& a, int32_t f)
+{
+    return int32_t((uint64_t(uint32_t(f)) * a.rep_magic) >> a.rep_shift);
+}
+
 // Tokens that the flattened row f sees of the table's row: all of a prefix,
 // own tokens up to itself.
 __device__ __forceinline__ int32_t visible_end(const AttendArgs& a, const AttendItem& it, int32_t f)
 {
     if (it.prefix) return it.len;
-    return clamp_i32(it.len - it.rows.count + (it.flat0 + f) / a.rep + 1, 0, it.len);
+    return clamp_i32(it.len - it.rows.count + new_token(a, it.flat0 + f) + 1, 0, it.len);
 }
 
 // Page id of token tok; the load is started here, what waits for it is
@@ -365,7 +373,8 @@ __device__ __forceinline__ void load_q(u32x4 (&q)[DP / 32], const AttendArgs& a,
 {
     const int g = (threadIdx.x & 63) >> 4;
     const int32_t flat = it.flat0 + (live ? f : 0);
-    const int64_t row = it.rows.first + flat / a.rep, head = it.h * a.rep + flat % a.rep;
+    const int32_t i = new_token(a, flat);
+    const int64_t row = it.rows.first + i, head = it.h * a.rep + (flat - i * a.rep);
     const uint64_t qb = a.q + (row * a.q_row + head * a.q_head) * 2;
 #pragma unroll
     for (int j = 0; j < DP / 32; ++j) {
@@ -390,7 +399,7 @@ struct RowSink {
 __device__ __forceinline__ RowSink open_row(const AttendArgs& a, const AttendItem& it, int32_t f, float m, float l,
                                             bool first)
 {
-    const int32_t flat = it.flat0 + f, i = flat / a.rep;
+    const int32_t flat = it.flat0 + f, i = new_token(a, flat);
     const int64_t row = it.rows.first + i, head = it.h * a.rep + (flat - i * a.rep);
     if (a.direct) {
         if (first) gptr<gf32>(a.lse)[row * a.q_heads + head] = log_sum(m, l);

@@ -58,6 +58,16 @@ bool rows_vectors(const kv_rows& x, int64_t size)
     return !misaligned(x.data, 16) && x.row_stride * size % 16 == 0 && x.head_stride * size % 16 == 0;
 }
 
+// x / d = (x * magic) >> shift for x < 2^31: with 2^s >= d, magic = floor(2^(31 + s) / d) + 1 is too large by at most
+// 2^s / 2^(31 + s) of itself, which stays below one over the whole range.
+void magic_of(int32_t d, uint32_t* magic, uint32_t* shift)
+{
+    uint32_t s = 0;
+    while ((int64_t(1) << s) < d) ++s;
+    *magic = uint32_t((uint64_t(1) << (31 + s)) / uint64_t(d) + 1);
+    *shift = 31 + s;
+}
+
 PoolArg pool_arg(const kv_paged* p, int32_t layer)
 {
     PoolArg a{};
@@ -65,11 +75,7 @@ PoolArg pool_arg(const kv_paged* p, int32_t layer)
     a.v_pages = reinterpret_cast<uint64_t>(p->v_pages);
     a.num_pages = uint32_t(p->num_pages);
     a.page_size = uint32_t(p->page_size);
-    // t / P for t < 2^31: with 2^s >= P, magic = floor(2^(31 + s) / P) + 1 is off by at most 2^s / 2^(31 + s)
-    uint32_t s = 0;
-    while ((int64_t(1) << s) < p->page_size) ++s;
-    a.page_magic = uint32_t((uint64_t(1) << (31 + s)) / uint64_t(p->page_size) + 1);
-    a.page_shift = 31 + s;
+    magic_of(p->page_size, &a.page_magic, &a.page_shift);
     a.heads = uint32_t(p->num_kv_heads);
     a.dim = uint32_t(p->head_dim);
     a.layer = layer;
@@ -325,6 +331,7 @@ int attend(const kv_paged* paged, const kv_step* step, int32_t layer, const kv_r
     a.part_acc = a.part_ml + uint64_t(sh.ml_bytes);
     a.q_heads = q_heads;
     a.rep = q_heads / paged->num_kv_heads;
+    magic_of(a.rep, &a.rep_magic, &a.rep_shift);
     a.scale_log2 = float(double(scale) * 1.4426950408889634);
     a.prefix_tiles = sh.prefix_tiles;
     a.prefix_pieces = sh.prefix_pieces;
@@ -390,6 +397,7 @@ int add_weights_call(const kv_paged* paged, const kv_step* step, int32_t layer, 
     a.lse = reinterpret_cast<uint64_t>(lse);
     a.q_heads = q_heads;
     a.rep = q_heads / paged->num_kv_heads;
+    magic_of(a.rep, &a.rep_magic, &a.rep_shift);
     a.scale_log2 = float(double(scale) * 1.4426950408889634);
     // many rows: the waves share a workgroup's tokens and split the rows
     const int64_t rows = std::max(own != nullptr ? step->max_new : 0, prefix != nullptr ? step->max_group_rows : 0);

@@ -29,6 +29,7 @@ struct WeightsArgs {
     uint64_t q, lse;               // bf16 rows with strides, float32 [n_rows][q_heads]
     int64_t q_row, q_head;
     int32_t q_heads, rep;
+    uint32_t rep_magic, rep_shift;
     float scale_log2;
     uint64_t own_in, own_out;      // float32 [own.n][heads][own_cap]; in may be 0 (zeros) or out
     uint64_t prefix_in, prefix_out;// float32 [prefix.n][heads][prefix_cap]
@@ -37,16 +38,18 @@ struct WeightsArgs {
     uint32_t prefix_items;
 };
 
-template <int DP>
-constexpr int kWeightsTiles = DP <= 128 ? 4 : 2;       // tiles of 16 tokens a wave holds
+// Tiles of 16 tokens a wave holds: four where many rows pass by, so that a
+// row's q serves more products; two otherwise, for more waves in flight.
+template <int DP, bool kSplitRows>
+constexpr int kWeightsTiles = DP <= 128 && kSplitRows ? 4 : 2;
 
 template <int DP, bool kSplitRows>
-constexpr int kWeightsTokens = 16 * kWeightsTiles<DP> * (kSplitRows ? 1 : kAttendWaves);   // of a workgroup
+constexpr int kWeightsTokens = 16 * kWeightsTiles<DP, kSplitRows> * (kSplitRows ? 1 : kAttendWaves);   // of a workgroup
 
 template <int DP, bool kSplitRows>
 __global__ __launch_bounds__(kAttendBlock) void add_weights(WeightsArgs a)
 {
-    constexpr int J = DP / 32, NT = kWeightsTiles<DP>;
+    constexpr int J = DP / 32, NT = kWeightsTiles<DP, kSplitRows>;
     __shared__ float part[kAttendWaves][16 * NT];
     uint32_t b = blockIdx.x;
     const bool prefix = b < a.prefix_items;
@@ -100,25 +103,23 @@ __global__ __launch_bounds__(kAttendBlock) void add_weights(WeightsArgs a)
     const int32_t skip = before > 0 ? before * a.rep / 16 : 0;
     constexpr int kStep = kSplitRows ? kAttendWaves : 1;
 
-    // column r of row block x: q, and -lse in log2 units (-infinity, so that nothing is added, for no row and for a
-    // row that saw nothing)
+    // column r of row block x: its q and lse (-infinity for no row)
     struct Column {
         u32x4 q[J];
-        float neg;
+        float lse;
         int32_t vis;
     };
     auto load_column = [&](int32_t x, Column& c) {
         const int32_t f = x * 16 + r;
         const bool live = f < flat_n;
-        const int32_t i = live ? f / a.rep : 0, head = h * a.rep + (live ? f - i * a.rep : 0);
+        const int32_t i = live ? new_token(a, f) : 0, head = h * a.rep + (live ? f - i * a.rep : 0);
         const int64_t qr = first_row + i;
         c.vis = prefix ? len : clamp_i32(len - count + i + 1, 0, len);
-        c.neg = -__builtin_inff();
+        c.lse = -__builtin_inff();
 #pragma unroll
         for (int j = 0; j < J; ++j) c.q[j] = u32x4{0, 0, 0, 0};
         if (!live) return;
-        const float lse = gptr<const gf32>(a.lse)[qr * a.q_heads + head];
-        c.neg = lse == -__builtin_inff() ? lse : -lse * kLog2e;
+        c.lse = gptr<const gf32>(a.lse)[qr * a.q_heads + head];
 #pragma unroll
         for (int j = 0; j < J; ++j)
             c.q[j] = load_k8(a.q + (qr * a.q_row + head * a.q_head) * 2, j * 32 + g * 8, dim);
@@ -138,14 +139,16 @@ __global__ __launch_bounds__(kAttendBlock) void add_weights(WeightsArgs a)
 #pragma unroll
             for (int j = 0; j < J; ++j) s[i] = mfma16(k[i][j], now.q[j], s[i]);
         }
+        // minus lse in log2 units; a row that saw nothing adds nothing: exp2(-infinity)
+        const float neg = now.lse == -__builtin_inff() ? now.lse : -now.lse * kLog2e;
         // the block's first row sees the least
-        const bool masked = !prefix && len - count + (x * 16) / a.rep + 1 < t + 16 * NT;
+        const bool masked = !prefix && len - count + new_token(a, x * 16) + 1 < t + 16 * NT;
         if (masked) {
 #pragma unroll
             for (int i = 0; i < NT; ++i)
 #pragma unroll
                 for (int n = 0; n < 4; ++n) {
-                    const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i][n], a.scale_log2, now.neg));
+                    const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i][n], a.scale_log2, neg));
                     sum[i][n] += t + 16 * i + 4 * g + n < now.vis ? p : 0.0f;
                 }
         } else {
@@ -153,7 +156,7 @@ __global__ __launch_bounds__(kAttendBlock) void add_weights(WeightsArgs a)
             for (int i = 0; i < NT; ++i)
 #pragma unroll
                 for (int n = 0; n < 4; ++n)
-                    sum[i][n] += __builtin_amdgcn_exp2f(__builtin_fmaf(s[i][n], a.scale_log2, now.neg));
+                    sum[i][n] += __builtin_amdgcn_exp2f(__builtin_fmaf(s[i][n], a.scale_log2, neg));
         }
         now = next;
     }
