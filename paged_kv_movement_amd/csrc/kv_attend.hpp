@@ -153,11 +153,12 @@ __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c)
                                                    0, 0);
 }
 
+// One instruction (v_maximum3_f32).  Not by inline assembly: the compiler does
+// not count the wait states that a product's result needs before it is read
+// there.
 __device__ __forceinline__ float max3(float a, float b, float c)
 {
-    float r;
-    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
-    return r;
+    return __builtin_elementwise_maximum(__builtin_elementwise_maximum(a, b), c);
 }
 
 // Maximum over the four lanes l % 16, + 16, + 32, + 48, without LDS: a swap of
@@ -346,19 +347,39 @@ __device__ __forceinline__ u32x4 load_k8(uint64_t base, int d, int dim)
     return u32x4{0, 0, 0, 0};
 }
 
-// Lane r's elements of a V row at `base`, 0 at and past dim.
+// A token's (or a row's) elements 32 j + 8 g ..+8, without a branch: past dim
+// the first ones are read instead, for clear_past to set to 0.
+template <int DP>
+__device__ __forceinline__ void load_row(u32x4 (&x)[DP / 32], uint64_t base, int g, int dim)
+{
+#pragma unroll
+    for (int j = 0; j < DP / 32; ++j) {
+        const int d = j * 32 + g * 8;
+        x[j] = *gptr<const gvec4>(base + (d < dim ? d : 0) * 2);
+    }
+}
+
+template <int DP>
+__device__ __forceinline__ void clear_past(u32x4 (&x)[DP / 32], int g, int dim)
+{
+#pragma unroll
+    for (int j = 0; j < DP / 32; ++j)
+        if (j * 32 + g * 8 >= dim) x[j] = u32x4{0, 0, 0, 0};
+}
+
+// Lane r's elements of a V row at `base`; past dim the first ones.
 template <int DP>
 __device__ __forceinline__ void load_v(uint32_t (&v)[DP / 32], uint64_t base, int r, int dim)
 {
     if constexpr (DP == 64) {
-        u32x2 x = {0, 0};
-        if (r * 4 < dim) x = *gptr<const gvec2>(base + r * 8);
+        const u32x2 x = *gptr<const gvec2>(base + (r * 4 < dim ? r * 8 : 0));
         v[0] = x[0];
         v[1] = x[1];
     } else {
 #pragma unroll
         for (int y = 0; y < DP / 128; ++y) {
-            const u32x4 x = load_k8(base, y * 128 + r * 8, dim);
+            const int d = y * 128 + r * 8;
+            const u32x4 x = *gptr<const gvec4>(base + (d < dim ? d : 0) * 2);
 #pragma unroll
             for (int w = 0; w < 4; ++w) v[4 * y + w] = x[w];
         }
@@ -471,21 +492,33 @@ __device__ __forceinline__ void narrow_piece(const AttendArgs& a, const AttendIt
         const uint32_t valid = uint32_t(__ballot(row >= 0));
         u32x4 k[2][J];
         uint32_t v[8][J];
+        // no load behind a branch (row 0 for a token that has none), so that the waits for K leave V in flight
+        const int32_t some = row < 0 ? 0 : row;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const int32_t kr = __shfl(row, 16 * i + r);
-#pragma unroll
-            for (int j = 0; j < J; ++j) {
-                k[i][j] = u32x4{0, 0, 0, 0};
-                if (kr >= 0) k[i][j] = load_k8(kh + uint64_t(uint32_t(kr)) * row_bytes, j * 32 + g * 8, dim);
-            }
+            const uint32_t kr = uint32_t(__shfl(some, 16 * i + r));
+            load_row<DP>(k[i], kh + uint64_t(kr) * row_bytes, g, dim);
         }
 #pragma unroll
         for (int x = 0; x < 8; ++x) {
-            const int32_t vr = __shfl(row, 16 * (x / 4) + 4 * g + x % 4);
+            const uint32_t vr = uint32_t(__shfl(some, 16 * (x / 4) + 4 * g + x % 4));
+            load_v<DP>(v[x], vh + uint64_t(vr) * row_bytes, r, dim);
+        }
+        if (dim < DP) {
 #pragma unroll
-            for (int y = 0; y < J; ++y) v[x][y] = 0;
-            if (vr >= 0) load_v<DP>(v[x], vh + uint64_t(uint32_t(vr)) * row_bytes, r, dim);
+            for (int i = 0; i < 2; ++i) clear_past<DP>(k[i], g, dim);
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+#pragma unroll
+                for (int y = 0; y < J; ++y)
+                    if (acc_element<DP>(r, DP == 64 ? 2 * y : 8 * (y / 4)) >= dim) v[x][y] = 0;
+        }
+        if (valid != ~0u) {               // a token that is not there weighs 0, and 0 times what was read may be NaN
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+#pragma unroll
+                for (int y = 0; y < J; ++y)
+                    if (!((valid >> (16 * (x / 4) + 4 * g + x % 4)) & 1)) v[x][y] = 0;
         }
         f32x4 s[2];
 #pragma unroll
@@ -874,7 +907,6 @@ __device__ __forceinline__ f32x4 join_row(const AttendArgs& a, int64_t at, RowPi
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) l += __shfl_xor(l, d);
     f32x4 o = {0, 0, 0, 0};
-#pragma unroll 2
     for (int x0 = 0; x0 < total; x0 += groups) {               // the same rounds in every lane
         const int x = x0 + grp;
         float e = __shfl(w, x & 63);
