@@ -605,15 +605,32 @@ __device__ __forceinline__ int wide_swizzle(int token)
     return DP == 64 ? (token >> 1) & 7 : token & 15;
 }
 
-// One tile of tokens into LDS, this wave's share of it.  rows: lane x's is the
-// pool row of the tile's token x (-1: none).
+// One tile of tokens into LDS, this wave's share of it: kWideTile / 4 tokens.
+// rows: lane x's is the pool row of the tile's token x (-1: none); valid: its
+// ballot.  `flat`: a wave's tokens always lie in one page and heads fill DP,
+// so that its rows follow one another and need one address.
 template <int DP>
-__device__ __forceinline__ void wide_load(uint64_t kh, uint64_t vh, uint32_t row_bytes, int dim, int32_t rows,
-                                          WideTile<DP>& tile)
+__device__ __forceinline__ void wide_load(uint64_t kh, uint64_t vh, uint32_t row_bytes, int dim, bool flat,
+                                          int32_t rows, uint64_t valid, WideTile<DP>& tile)
 {
     constexpr int V = DP / 8, kPer = 64 / V;                             // vectors of a row, rows of a load
-    constexpr int kLoads = kWideTile<DP> / kPer / kAttendWaves;
+    constexpr int kLoads = kWideTile<DP> / kPer / kAttendWaves, kTokens = kLoads * kPer;
     const int lane = anew(threadIdx.x & 63), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint64_t all = ((1ull << kTokens) - 1) << (wave * kTokens);
+    if (flat && (valid & all) == all) {
+        const uint64_t at = uint64_t(uint32_t(__builtin_amdgcn_readlane(rows, wave * kTokens))) * row_bytes;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int first = (wave * kLoads + i) * kPer;
+            const int chunk = lane % V ^ wide_swizzle<DP>(first + lane / V);
+            const uint32_t off = uint32_t(i * kPer + lane / V) * row_bytes + chunk * 16;
+            __builtin_amdgcn_global_load_lds(gptr<const gvec4>(kh + at + off),
+                                             (__attribute__((address_space(3))) void*)&tile.k[first * V], 16, 0, 0);
+            __builtin_amdgcn_global_load_lds(gptr<const gvec4>(vh + at + off),
+                                             (__attribute__((address_space(3))) void*)&tile.v[first * V], 16, 0, 0);
+        }
+        return;
+    }
     const uint64_t zero = reinterpret_cast<uint64_t>(&g_zero_vector);
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
@@ -720,6 +737,7 @@ __device__ __forceinline__ void wide_piece(const AttendArgs& a, const AttendItem
     const int32_t last = f0 + 16 * NB < it.flat_n ? f0 + 16 * NB - 1 : it.flat_n - 1;
     const int32_t end = busy ? visible_end(a, it, last) : 0; // the wave's rows see nothing from here on
 
+    const bool flat = dim == DP && a.pool.page_size % (T / kAttendWaves) == 0;
     bool care = false;
   again:
 #pragma unroll
@@ -730,8 +748,8 @@ __device__ __forceinline__ void wide_piece(const AttendArgs& a, const AttendItem
         page = page_at(it.t0);
         rows = row_at(it.t0, page);
         page = page_at(it.t0 + T);
-        wide_load<DP>(kh, vh, row_bytes, dim, rows, tile0);
         valid = __ballot(rows >= 0);
+        wide_load<DP>(kh, vh, row_bytes, dim, flat, rows, valid, tile0);
         rows = row_at(it.t0 + T, page);
         page = page_at(it.t0 + 2 * T);
     }
@@ -742,8 +760,8 @@ __device__ __forceinline__ void wide_piece(const AttendArgs& a, const AttendItem
         __syncthreads();
         const uint64_t seen = valid;
         if (t + T < t1) {
-            wide_load<DP>(kh, vh, row_bytes, dim, rows, next);
             valid = __ballot(rows >= 0);
+            wide_load<DP>(kh, vh, row_bytes, dim, flat, rows, valid, next);
         }
         rows = row_at(t + 2 * T, page);
         page = page_at(t + 3 * T);
