@@ -76,7 +76,8 @@ __device__ __forceinline__ AttendItem attend_item(const AttendArgs& a, uint32_t 
     const int32_t tiles = it.prefix ? a.prefix_tiles : a.own_tiles;
     const int32_t pieces = it.prefix ? a.prefix_pieces : a.own_pieces;
     const int32_t tokens = it.prefix ? a.prefix_tokens : a.own_tokens;
-    const int32_t tile = b % tiles;
+    // the last rows of a prompt see the most: they start first
+    const int32_t tile = it.prefix ? b % tiles : tiles - 1 - b % tiles;
     b /= tiles;
     const int32_t piece = b % pieces;
     it.table_row = b / pieces;

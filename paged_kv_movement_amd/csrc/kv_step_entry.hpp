@@ -215,12 +215,13 @@ int check_heads(const kv_paged* p, int32_t q_heads)
     return KV_OK;
 }
 
-// Tokens of a piece: as many pieces as make `items` workgroups of all pairs
-// of (row tile, KV head) together, in whole rounds of a workgroup's waves.
-void cut_tokens(int64_t pairs, int32_t max_len, int64_t items, int32_t* tokens, int32_t* pieces)
+// Tokens of a piece: as many pieces as make `room` workgroups (what runs at
+// once) of all pairs of (row tile, KV head) together, in whole rounds of a
+// workgroup's waves.
+void cut_tokens(int64_t pairs, int32_t max_len, int64_t room, int32_t* tokens, int32_t* pieces)
 {
     constexpr int64_t kRound = kAttendWaves * kAttendTile;
-    const int64_t want = std::max<int64_t>(1, items / std::max<int64_t>(1, pairs));
+    const int64_t want = std::max<int64_t>(1, room / std::max<int64_t>(1, pairs));
     const int64_t t = ceil_div(ceil_div(std::max(max_len, 1), want), kRound) * kRound;
     *tokens = int32_t(t);
     *pieces = int32_t(ceil_div(max_len, t));
