@@ -10,14 +10,21 @@
 // be moved, and since no slot is both read and written, all moves run at
 // once and in place.
 //
-// evict_select   one workgroup per (layer, sequence, head): the keep-th
-//                largest key by radix select (11, 11 and 10 bits, counts in
-//                LDS), then the list of moves by running counts over the
-//                slots; weights and positions go to their new slots;
-// evict_move     the K and V rows of the moves, 16 bytes a thread.
+// evict_select   one workgroup per (layer, sequence, head): the tokens' keys
+//                (weights as ordered integers) once into LDS, the keep-th
+//                largest by radix select (11, 11 and 10 bits, counts in LDS),
+//                then each thread takes a run of slots and two sums over the
+//                workgroup number the ties and the moves; weights and
+//                positions go to their new slots.  A few tokens too many
+//                (kFew, the steady state of decoding) are found one by one
+//                instead, as the smallest key each time.
+// evict_move     the K and V rows of the moves, 16 bytes a thread.  Where the
+//                host's bound says that a row has at most kFusedMoves of
+//                them, evict_select makes them itself.
 //
-// Bound: select reads 8 bytes a token (the weights again, from L2, for each
-// digit) and waits on LDS counts; move is a scattered copy of rows.
+// Bound: select, of latency: some twenty waits of a workgroup for loads, LDS
+// counts and each other; move, of memory: a scattered copy of rows of
+// head_dim elements.
 #pragma once
 
 #include "kv_order.hpp"
@@ -26,9 +33,12 @@
 namespace kvmove {
 
 constexpr int kSelectBlock = 1024;
+constexpr int kSelectWaves = kSelectBlock / 64;
 constexpr int kSelectBins = 2048;
 constexpr int kMoveRowsBlock = 256;
 constexpr int kMoveRowsPer = 4;        // moves of a thread in flight
+constexpr int kFusedMoves = 64;        // most moves of a row that evict_select makes itself
+constexpr int kFew = 4;                // tokens too many that are found one by one
 
 struct EvictArgs {
     PoolArg pool;                      // layer: first layer
@@ -43,6 +53,9 @@ struct EvictArgs {
     int32_t n_layers;
     int32_t keep, recent;
     int32_t max_moves;
+    uint32_t vecs;                     // 16-byte vectors of a moved row
+    uint32_t vec_magic, vec_shift;     // x / vecs
+    int32_t fused;
 };
 
 // Order of the weights as unsigned integers: larger key, larger weight; -0 as
@@ -71,7 +84,7 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* wave_sums, 
     uint32_t before = 0;
     total = 0;
 #pragma unroll
-    for (int w = 0; w < kSelectBlock / 64; ++w) {
+    for (int w = 0; w < kSelectWaves; ++w) {
         const uint32_t s = wave_sums[w];
         if (w < wave) before += s;
         total += s;
@@ -79,19 +92,85 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* wave_sums, 
     return before + v - x;
 }
 
+// Rows of a (layer, sequence, head): vectors [x, x + kMoveRowsPer * kThreads)
+// by kThreads threads of the workgroup's moves (to, from).
+struct RowMover {
+    const EvictArgs& a;
+    uint64_t kb, vb;
+    int32_t s, h;
+
+    __device__ __forceinline__ int64_t row_of(uint32_t slot) const
+    {
+        if (slot >= uint32_t(a.tab.max_len)) return -1;     // not from this call: see evict_move
+        const uint32_t pi = page_of(a.pool, slot);
+        const int32_t page = gptr<const gi32>(a.tab.table)[s * a.tab.stride + pi];
+        if (uint32_t(page) >= a.pool.num_pages) {
+            raise_fault_lane(kFaultPage);
+            return -1;
+        }
+        return int64_t(page) * a.pool.page_size + (slot - pi * a.pool.page_size);
+    }
+
+    template <int kThreads, class Moves>
+    __device__ __forceinline__ void run(Moves&& moves, uint32_t x0, uint32_t total) const
+    {
+        const uint64_t per_row = uint64_t(a.pool.heads) * a.pool.dim * 2, head = uint64_t(h) * a.vecs * 16;
+        u32x4 kx[kMoveRowsPer], vx[kMoveRowsPer];
+        uint64_t to[kMoveRowsPer], from[kMoveRowsPer];
+#pragma unroll
+        for (int u = 0; u < kMoveRowsPer; ++u) {
+            const uint32_t x = x0 + u * kThreads + threadIdx.x;
+            to[u] = from[u] = ~0ull;
+            if (x >= total) continue;
+            const uint32_t m = uint32_t((uint64_t(x) * a.vec_magic) >> a.vec_shift), v = x - m * a.vecs;
+            const int64_t rt = row_of(moves(2 * m)), rf = row_of(moves(2 * m + 1));
+            if (rt < 0 || rf < 0) continue;
+            to[u] = rt * per_row + head + v * 16;
+            from[u] = rf * per_row + head + v * 16;
+        }
+#pragma unroll
+        for (int u = 0; u < kMoveRowsPer; ++u)
+            if (from[u] != ~0ull) {
+                kx[u] = *gptr<const gvec4>(kb + from[u]);
+                vx[u] = *gptr<const gvec4>(vb + from[u]);
+            }
+#pragma unroll
+        for (int u = 0; u < kMoveRowsPer; ++u)
+            if (to[u] != ~0ull) {
+                *gptr<gvec4>(kb + to[u]) = kx[u];
+                *gptr<gvec4>(vb + to[u]) = vx[u];
+            }
+    }
+};
+
+__device__ __forceinline__ RowMover row_mover(const EvictArgs& a, int32_t job, bool& ok)
+{
+    const int32_t layer = a.pool.layer + job / a.heads / a.tab.n;
+    const uint64_t kb = gptr<const gu64>(a.pool.k_pages)[layer], vb = gptr<const gu64>(a.pool.v_pages)[layer];
+    ok = !bad_addr(kb) && !bad_addr(vb);
+    if (!ok) raise_fault(kFaultPool);
+    return {a, kb, vb, job / a.heads % a.tab.n, job % a.heads};
+}
+
+// kKeys: keys that fit the kernel's LDS; longer rows read weights and
+// positions again wherever a key is needed.
+template <int kKeys>
 __global__ __launch_bounds__(kSelectBlock) void evict_select(EvictArgs a)
 {
+    __shared__ uint32_t keys[kKeys];
     __shared__ uint32_t bins[kSelectBins];
-    __shared__ uint32_t wave_sums[kSelectBlock / 64];
+    __shared__ uint32_t wave_sums[kSelectWaves];
+    __shared__ uint64_t wave_least[kSelectWaves];
     __shared__ int32_t found[2];
-    const int32_t tid = threadIdx.x, job = blockIdx.x;
+    __shared__ uint32_t few[2 * kFusedMoves];
+    const int32_t tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, job = blockIdx.x;
     const int32_t s = job / a.heads % a.tab.n;
-    const int32_t n = table_len(a.tab, s), keep = a.keep;
     const gf32* w = gptr<const gf32>(a.weights) + job * a.cap;
     const gi32* p = gptr<const gi32>(a.positions) + job * a.cap;
     gf32* ow = gptr<gf32>(a.out_weights) + job * a.out_cap;
     gi32* op = gptr<gi32>(a.out_positions) + job * a.out_cap;
     const bool in_place = a.weights == a.out_weights;
+    const int32_t n = table_len(a.tab, s), keep = a.keep;
     if (tid == 0 && job / a.heads < a.tab.n && job % a.heads == 0)
         gptr<gi32>(a.out_lens)[s] = n < keep ? n : keep;
     if (n <= keep) {
@@ -103,7 +182,8 @@ __global__ __launch_bounds__(kSelectBlock) void evict_select(EvictArgs a)
         if (tid == 0) gptr<gu32>(a.counts)[job] = 0;
         return;
     }
-    // the newest position; 64-bit so that no `recent` wraps around
+    const bool in_lds = n <= kKeys;
+    // the newest position; compared in 64 bits, so that no `recent` wraps around
     int32_t newest = INT32_MIN;
     for (int32_t i = tid; i < n; i += kSelectBlock) newest = p[i] > newest ? p[i] : newest;
 #pragma unroll
@@ -111,80 +191,179 @@ __global__ __launch_bounds__(kSelectBlock) void evict_select(EvictArgs a)
         const int32_t y = __shfl_xor(newest, d);
         newest = y > newest ? y : newest;
     }
-    if ((tid & 63) == 0) wave_sums[tid >> 6] = uint32_t(newest);
+    if (lane == 0) wave_sums[wave] = uint32_t(newest);
     __syncthreads();
 #pragma unroll
-    for (int x = 0; x < kSelectBlock / 64; ++x) {
+    for (int x = 0; x < kSelectWaves; ++x) {
         const int32_t y = int32_t(wave_sums[x]);
         newest = y > newest ? y : newest;
     }
     const int64_t border = int64_t(newest) - a.recent;
-    auto key_of = [&](int32_t i) { return weight_key(w[i], int64_t(p[i]) > border); };
-
-    // the keep-th largest key: top 11 bits, then 11, then 10
-    uint32_t prefix = 0, mask = 0;
-    int32_t want = keep;                   // rank, from the largest, within what matches the prefix
-    for (int pass = 0; pass < 3; ++pass) {
-        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
-        __syncthreads();
-        for (int32_t x = tid; x < kSelectBins; x += kSelectBlock) bins[x] = 0;
-        __syncthreads();
-        for (int32_t i = tid; i < n; i += kSelectBlock) {
-            const uint32_t key = key_of(i);
-            if ((key & mask) == prefix) atomicAdd(&bins[(key >> shift) & ((1u << bits) - 1)], 1u);
-        }
-        __syncthreads();
-        // thread x holds bins from the top: 2047 - 2x and 2046 - 2x
-        const uint32_t c0 = bins[kSelectBins - 1 - 2 * tid], c1 = bins[kSelectBins - 2 - 2 * tid];
-        uint32_t total;
-        const uint32_t before = block_scan(c0 + c1, wave_sums, total);
-        if (before < uint32_t(want) && uint32_t(want) <= before + c0) {
-            found[0] = kSelectBins - 1 - 2 * tid;
-            found[1] = want - before;
-        } else if (before + c0 < uint32_t(want) && uint32_t(want) <= before + c0 + c1) {
-            found[0] = kSelectBins - 2 - 2 * tid;
-            found[1] = want - before - c0;
-        }
-        __syncthreads();
-        prefix |= uint32_t(found[0]) << shift;
-        mask |= ((1u << bits) - 1) << shift;
-        want = found[1];
-    }
-    const uint32_t border_key = prefix;    // `want` of the tokens with this very key stay, the first ones
-
-    // slots in order: what stays, and the moves
+    auto key_anew = [&](int32_t i) { return weight_key(w[i], int64_t(p[i]) > border); };
+    if (in_lds)
+        for (int32_t i = tid; i < n; i += kSelectBlock) keys[i] = key_anew(i);
+    auto key_of = [&](int32_t i) { return in_lds ? keys[i] : key_anew(i); };
     gu32* moves = gptr<gu32>(a.moves) + int64_t(job) * a.max_moves * 2;
-    uint32_t ties = 0, holes = 0, sources = 0;
-    for (int32_t i0 = 0; i0 < n; i0 += kSelectBlock) {
-        const int32_t i = i0 + tid;
-        const uint32_t key = i < n ? key_of(i) : 0;
-        const bool tie = i < n && key == border_key;
-        uint32_t n_tie, n_both;
-        const uint32_t tie_rank = ties + block_scan(tie, wave_sums, n_tie);
-        const bool stays = i < n && (key > border_key || (tie && tie_rank < uint32_t(want)));
-        const bool hole = i < keep && !stays, source = i >= keep && stays;
-        // both counts in one scan: at most 1024 each
-        const uint32_t rank = block_scan(uint32_t(hole) | uint32_t(source) << 16, wave_sums, n_both);
-        const uint32_t to = holes + (rank & 0xFFFFu), from = sources + (rank >> 16);
-        if (hole && to < uint32_t(a.max_moves)) moves[2 * to] = i;
-        if (source && from < uint32_t(a.max_moves)) moves[2 * from + 1] = i;
-        if (!in_place && i < keep && stays) {
-            ow[i] = w[i];
-            op[i] = p[i];
+    uint32_t n_moves;
+
+    if (n - keep <= kFew) {
+        // the tokens that go, one by one: least key, of equal ones the last slot
+        const int32_t gone_max = n - keep;
+        int32_t gone[kFew];
+        uint64_t above = 0;                    // what went before is below it
+#pragma unroll
+        for (int e = 0; e < kFew; ++e) {
+            gone[e] = n;
+            if (e >= gone_max) continue;
+            uint64_t least = ~0ull;
+            __syncthreads();
+            for (int32_t i = tid; i < n; i += kSelectBlock) {
+                const uint64_t x = uint64_t(key_of(i)) << 32 | uint32_t(n - 1 - i);
+                if ((e == 0 || x > above) && x < least) least = x;
+            }
+#pragma unroll
+            for (int d = 1; d < 64; d *= 2) {
+                const uint64_t y = __shfl_xor((unsigned long long)least, d);
+                least = y < least ? y : least;
+            }
+            if (lane == 0) wave_least[wave] = least;
+            __syncthreads();
+#pragma unroll
+            for (int x = 0; x < kSelectWaves; ++x) least = wave_least[x] < least ? wave_least[x] : least;
+            above = least;
+            gone[e] = n - 1 - int32_t(uint32_t(least));
         }
-        ties += n_tie;
-        holes += n_both & 0xFFFFu;
-        sources += n_both >> 16;
+        // free slots, and the kept ones behind `keep`, both ascending; the same in every thread
+        n_moves = 0;
+        int32_t last_to = -1, last_from = keep - 1;
+#pragma unroll
+        for (int e = 0; e < kFew; ++e) {
+            int32_t to = n, from = n;
+#pragma unroll
+            for (int x = 0; x < kFew; ++x)
+                if (gone[x] > last_to && gone[x] < to) to = gone[x];
+            if (to >= keep) break;
+            for (int32_t i = last_from + 1; i < n; ++i) {
+                bool stays = true;
+#pragma unroll
+                for (int x = 0; x < kFew; ++x) stays = stays && gone[x] != i;
+                if (stays) {
+                    from = i;
+                    break;
+                }
+            }
+            if (tid == 0) {
+                few[2 * e] = to;
+                few[2 * e + 1] = from;
+            }
+            last_to = to;
+            last_from = from;
+            ++n_moves;
+        }
+        n_moves = n_moves < uint32_t(a.max_moves) ? n_moves : uint32_t(a.max_moves);
+        __syncthreads();
+        if (!a.fused && tid < int32_t(2 * n_moves)) moves[tid] = few[tid];
+        if (!in_place)
+            for (int32_t i = tid; i < keep; i += kSelectBlock) {
+                uint32_t from = i;
+                for (uint32_t x = 0; x < n_moves; ++x)
+                    if (few[2 * x] == uint32_t(i)) from = few[2 * x + 1];
+                ow[i] = w[from];
+                op[i] = p[from];
+            }
+        else if (tid < int32_t(n_moves)) {
+            ow[few[2 * tid]] = w[few[2 * tid + 1]];
+            op[few[2 * tid]] = p[few[2 * tid + 1]];
+        }
+    } else {
+        // the keep-th largest key: top 11 bits, then 11, then 10
+        uint32_t prefix = 0, mask = 0;
+        int32_t want = keep;                   // rank, from the largest, within what matches the prefix
+        for (int pass = 0; pass < 3; ++pass) {
+            const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
+            __syncthreads();
+            for (int32_t x = tid; x < kSelectBins; x += kSelectBlock) bins[x] = 0;
+            __syncthreads();
+            for (int32_t i = tid; i < n; i += kSelectBlock) {
+                const uint32_t key = key_of(i);
+                if ((key & mask) == prefix) atomicAdd(&bins[(key >> shift) & ((1u << bits) - 1)], 1u);
+            }
+            __syncthreads();
+            // thread x holds bins from the top: 2047 - 2x and 2046 - 2x
+            const uint32_t c0 = bins[kSelectBins - 1 - 2 * tid], c1 = bins[kSelectBins - 2 - 2 * tid];
+            uint32_t total;
+            const uint32_t before = block_scan(c0 + c1, wave_sums, total);
+            if (before < uint32_t(want) && uint32_t(want) <= before + c0) {
+                found[0] = kSelectBins - 1 - 2 * tid;
+                found[1] = want - before;
+            } else if (before + c0 < uint32_t(want) && uint32_t(want) <= before + c0 + c1) {
+                found[0] = kSelectBins - 2 - 2 * tid;
+                found[1] = want - before - c0;
+            }
+            __syncthreads();
+            prefix |= uint32_t(found[0]) << shift;
+            mask |= ((1u << bits) - 1) << shift;
+            want = found[1];
+        }
+        const uint32_t border_key = prefix;    // `want` of the tokens with this very key stay, the first ones
+
+        // a run of slots a thread (an odd number of them: its keys lie in other banks than its neighbours'); what stays,
+        // and the moves by rank
+        const int32_t run = ((n + kSelectBlock - 1) / kSelectBlock) | 1;
+        const int32_t i0 = tid * run < n ? tid * run : n, i1 = i0 + run < n ? i0 + run : n;
+        uint32_t my_ties = 0;
+        for (int32_t i = i0; i < i1; ++i) my_ties += key_of(i) == border_key;
+        uint32_t total;
+        const uint32_t ties0 = block_scan(my_ties, wave_sums, total);
+        auto stays_from = [&](int32_t i, uint32_t& ties) {
+            const uint32_t key = key_of(i);
+            const bool tie = key == border_key, stays = key > border_key || (tie && ties < uint32_t(want));
+            ties += tie;
+            return stays;
+        };
+        uint32_t holes = 0, sources = 0, ties = ties0;
+        for (int32_t i = i0; i < i1; ++i) {
+            const bool stays = stays_from(i, ties);
+            holes += i < keep && !stays;
+            sources += i >= keep && stays;
+        }
+        uint32_t to = block_scan(holes, wave_sums, n_moves), from = block_scan(sources, wave_sums, total);
+        n_moves = n_moves < uint32_t(a.max_moves) ? n_moves : uint32_t(a.max_moves);
+        ties = ties0;
+        for (int32_t i = i0; i < i1; ++i) {
+            const bool stays = stays_from(i, ties);
+            if (i < keep && !stays && to < n_moves) {
+                moves[2 * to++] = i;
+                if (to <= kFusedMoves) few[2 * to - 2] = i;
+            }
+            if (i >= keep && stays && from < n_moves) {
+                moves[2 * from++ + 1] = i;
+                if (from <= kFusedMoves) few[2 * from - 1] = i;
+            }
+        }
+        if (!in_place)                         // every slot; those that fall free are overwritten after the barrier
+            for (int32_t i = tid; i < keep; i += kSelectBlock) {
+                ow[i] = w[i];
+                op[i] = p[i];
+            }
+        __threadfence_block();
+        __syncthreads();
+        for (uint32_t x = tid; x < n_moves; x += kSelectBlock) {
+            const uint32_t t = moves[2 * x], f = moves[2 * x + 1];
+            ow[t] = w[f];
+            op[t] = p[f];
+        }
     }
-    __threadfence_block();
-    __syncthreads();
-    holes = holes < uint32_t(a.max_moves) ? holes : uint32_t(a.max_moves);
-    for (uint32_t x = tid; x < holes; x += kSelectBlock) {
-        const uint32_t to = moves[2 * x], from = moves[2 * x + 1];
-        ow[to] = w[from];
-        op[to] = p[from];
+    if (!a.fused) {
+        if (tid == 0) gptr<gu32>(a.counts)[job] = n_moves;
+        return;
     }
-    if (tid == 0) gptr<gu32>(a.counts)[job] = holes;
+    bool ok;
+    const RowMover mover = row_mover(a, job, ok);
+    const uint32_t total = n_moves * a.vecs;
+    if (ok)
+        for (uint32_t x = 0; x < total; x += kSelectBlock * kMoveRowsPer)
+            mover.run<kSelectBlock>([&](uint32_t i) { return few[i]; }, x, total);
 }
 
 // blockIdx.x: (layer, sequence, head); blockIdx.y: a share of its moves.
@@ -195,52 +374,15 @@ __global__ __launch_bounds__(kMoveRowsBlock) void evict_move(EvictArgs a)
     // cannot send an access outside
     uint32_t n = gptr<const gu32>(a.counts)[job];
     n = n < uint32_t(a.max_moves) ? n : uint32_t(a.max_moves);
-    const int32_t h = job % a.heads, s = job / a.heads % a.tab.n, layer = a.pool.layer + job / a.heads / a.tab.n;
-    const uint32_t width = a.pool.heads * a.pool.dim / a.heads;        // elements of a move
-    const uint32_t vecs = width / 8;
-    const uint64_t kb = gptr<const gu64>(a.pool.k_pages)[layer], vb = gptr<const gu64>(a.pool.v_pages)[layer];
     const gu32* moves = gptr<const gu32>(a.moves) + int64_t(job) * a.max_moves * 2;
     if (n == 0) return;
-    if (bad_addr(kb) || bad_addr(vb)) {
-        raise_fault(kFaultPool);
-        return;
-    }
-    const uint64_t per_row = uint64_t(a.pool.heads) * a.pool.dim * 2;
-    const uint64_t total = uint64_t(n) * vecs;
-    auto row_of = [&](uint32_t slot) -> int64_t {
-        if (slot >= uint32_t(a.tab.max_len)) return -1;
-        const uint32_t pi = page_of(a.pool, slot);
-        const int32_t page = gptr<const gi32>(a.tab.table)[s * a.tab.stride + pi];
-        if (page < 0 || uint32_t(page) >= a.pool.num_pages) {
-            raise_fault_lane(kFaultPage);
-            return -1;
-        }
-        return int64_t(page) * a.pool.page_size + (slot - pi * a.pool.page_size);
-    };
-    for (uint64_t x0 = uint64_t(blockIdx.y) * kMoveRowsBlock * kMoveRowsPer; x0 < total;
-         x0 += uint64_t(gridDim.y) * kMoveRowsBlock * kMoveRowsPer) {
-        u32x4 kx[kMoveRowsPer], vx[kMoveRowsPer];
-        uint64_t to[kMoveRowsPer];
-#pragma unroll
-        for (int u = 0; u < kMoveRowsPer; ++u) {
-            const uint64_t x = x0 + u * kMoveRowsBlock + threadIdx.x;
-            to[u] = ~0ull;
-            if (x >= total) continue;
-            const uint32_t m = uint32_t(x / vecs), v = uint32_t(x - uint64_t(m) * vecs);
-            const int64_t rt = row_of(moves[2 * m]), rf = row_of(moves[2 * m + 1]);
-            if (rt < 0 || rf < 0) continue;
-            const uint64_t in_row = (uint64_t(h) * width + v * 8) * 2;
-            to[u] = rt * per_row + in_row;
-            kx[u] = *gptr<const gvec4>(kb + rf * per_row + in_row);
-            vx[u] = *gptr<const gvec4>(vb + rf * per_row + in_row);
-        }
-#pragma unroll
-        for (int u = 0; u < kMoveRowsPer; ++u)
-            if (to[u] != ~0ull) {
-                *gptr<gvec4>(kb + to[u]) = kx[u];
-                *gptr<gvec4>(vb + to[u]) = vx[u];
-            }
-    }
+    bool ok;
+    const RowMover mover = row_mover(a, job, ok);
+    if (!ok) return;
+    const uint32_t total = n * a.vecs;
+    for (uint32_t x = blockIdx.y * kMoveRowsBlock * kMoveRowsPer; x < total;
+         x += gridDim.y * kMoveRowsBlock * kMoveRowsPer)
+        mover.run<kMoveRowsBlock>([&](uint32_t i) { return moves[i]; }, x, total);
 }
 
 }  // namespace kvmove

@@ -449,6 +449,11 @@ int evict_shape(const kv_paged* p, const kv_tables* t, int32_t n_layers, int32_t
     out->jobs = int64_t(n_layers) * t->n * heads;
     if (out->jobs > max_blocks(kSelectBlock)) return fail(KV_EINVAL, "too many (layer, sequence, head) for one launch");
     out->max_moves = std::min<int64_t>(keep, std::max(0, t->max_len - keep));
+    // vectors of a row's moves are numbered in 31 bits
+    const int64_t vecs = int64_t(p->num_kv_heads) * p->head_dim / heads / 8;
+    if (out->max_moves * vecs > INT32_MAX - kSelectBlock * kMoveRowsPer)
+        return fail(KV_EINVAL, "%lld moves of %lld bytes: too many for one call", (long long)out->max_moves,
+                    (long long)(vecs * 16));
     out->count_bytes = ceil_div(out->jobs * 4, 256) * 256;
     out->bytes = out->count_bytes + ceil_div(out->jobs * out->max_moves * 8, 256) * 256;
     return KV_OK;
@@ -500,10 +505,17 @@ int evict(const kv_paged* paged, const kv_tables* tables, int32_t layer_begin, i
     a.keep = keep;
     a.recent = recent;
     a.max_moves = int32_t(sh.max_moves);
-    rc = launch(reinterpret_cast<KernelFn>(&evict_select), sh.jobs, kSelectBlock, &a, stream);
-    if (rc == KV_OK && sh.max_moves > 0) {
-        const int64_t vecs = int64_t(paged->num_kv_heads) * paged->head_dim / in->heads / 8;
-        const int64_t shares = ceil_div(sh.max_moves * vecs, kMoveRowsBlock * kMoveRowsPer);
+    a.vecs = uint32_t(int64_t(paged->num_kv_heads) * paged->head_dim / in->heads / 8);
+    magic_of(int32_t(a.vecs), &a.vec_magic, &a.vec_shift);
+    a.fused = sh.max_moves <= kFusedMoves;
+    // keys in LDS: as little of it as the bound needs, so that several workgroups fit a CU
+    const int32_t len = tables->max_len;
+    const KernelFn select = len <= 4096    ? reinterpret_cast<KernelFn>(&evict_select<4096>)
+                            : len <= 12288 ? reinterpret_cast<KernelFn>(&evict_select<12288>)
+                                           : reinterpret_cast<KernelFn>(&evict_select<32768>);
+    rc = launch(select, sh.jobs, kSelectBlock, &a, stream);
+    if (rc == KV_OK && sh.max_moves > 0 && !a.fused) {
+        const int64_t shares = ceil_div(sh.max_moves * a.vecs, kMoveRowsBlock * kMoveRowsPer);
         rc = launch(reinterpret_cast<KernelFn>(&evict_move), sh.jobs, kMoveRowsBlock, &a, stream,
                     unsigned(std::min<int64_t>(shares, 256)));
     }

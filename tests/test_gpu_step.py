@@ -297,6 +297,10 @@ EVICT = [
     (4, True, 128, 16, [1025, 3000], 1024, 100, 1),
     (2, True, 64, 16, [33], 0, 0, 1),                     # nothing stays
     (1, True, 64, 8, [9], 1, 1, 2),
+    (2, True, 64, 16, [70, 71, 72, 73, 74, 75], 70, 0, 1),     # a few too many
+    (1, False, 16, 16, [40000, 33000], 20000, 500, 1),   # more keys than LDS takes
+    (1, True, 8, 256, [33000], 32997, 3, 1),
+    (1, True, 128, 16, [13000], 12000, 1, 1),
 ]
 
 
@@ -306,9 +310,11 @@ EVICT = [
 def test_evict(case, in_place, kind):
     H, by_head, D, P, lens, keep, recent, layers = case
     say("evict", case, in_place, kind)
-    b = su.Batch(7, H, D, P, lens, [0] * len(lens), layers=layers + 1)
-    pool, paged, step = device(b)
-    hs, cap = (H if by_head else 1), max(lens) + 5
+    b = su.Batch(7, H, D, P, lens, [0] * len(lens), layers=layers + 1, table_room=0 if in_place else 8)
+    # a bound above the lengths takes other kernels than one that says how few moves there can be
+    room = b.own_table.shape[1] * P
+    pool, paged, step = device(b, max_len=max(lens) if in_place else min(room, max(lens) + 300))
+    hs, cap = (H if by_head else 1), max(lens) + 305
     w = torch.rand((layers, len(lens), hs, cap), generator=b.g)
     if kind == "ties":
         w = torch.randint(0, 3, w.shape, generator=b.g).float()
