@@ -34,168 +34,184 @@ struct AppendArgs {
     int64_t w_cap;
     int32_t w_heads;
     int32_t rot;
+    int32_t units;                     // units of a head of q or k
+    uint32_t unit_magic, unit_shift;   // i / units
+    uint32_t vec_magic, vec_shift;     // i / (vectors of a head)
     int32_t q_heads;
     int32_t interleaved;
     float gain;
 };
-
-template <class T>
-__device__ __forceinline__ float to_float(T x)
-{
-    return float(x);
-}
 
 template <class T, int N>
 struct alignas(sizeof(T) * N > 16 ? 16 : sizeof(T) * N) Vec {
     T x[N];
 };
 
-template <class T>
-__device__ __forceinline__ T from_float(float x)
-{
-    return T(x);
-}
+// A token's heads are cut into units of one or two vectors of kVec elements:
+// two halves of kVec pairs (half layout; interleaved pairs element by element
+// for kVec = 1), one vector of interleaved pairs, or one vector that passes.
+enum : int { kUnitPairs = 0, kUnitInterleaved = 1, kUnitPass = 2 };
 
-// One head's unit u of kVec-wide vectors, rotated or passed on.  Units of a
-// head: half layout, rot / (2 kVec) pairs of vectors, then the vectors behind
-// the rotated part; interleaved, dim / kVec vectors (pairs of elements for
-// kVec = 1).
-template <class TI, class TO, int kVec>
-__device__ __forceinline__ void rotate_unit(const TI* src, TO* dst, int u, int rot, bool interleaved,
-                                            const float2* cs)
+struct Unit {
+    int kind;
+    int d0, d1;           // elements of the head where its vectors begin
+    int pair;             // first pair's angle
+};
+
+template <int kVec>
+__device__ __forceinline__ Unit head_unit(int u, int rot, bool interleaved)
 {
-    using VI = Vec<TI, kVec>;
-    using VO = Vec<TO, kVec>;
-    if (!interleaved) {
-        const int half = rot / 2, pairs = half / kVec;
-        if (u < pairs) {
-            const int d = u * kVec;
-            const VI x = *reinterpret_cast<const VI*>(src + d), y = *reinterpret_cast<const VI*>(src + half + d);
-            VO ox, oy;
-#pragma unroll
-            for (int i = 0; i < kVec; ++i) {
-                const float2 c = cs[d + i];
-                const float a = to_float(x.x[i]), b = to_float(y.x[i]);
-                ox.x[i] = from_float<TO>(__builtin_fmaf(a, c.x, -(b * c.y)));
-                oy.x[i] = from_float<TO>(__builtin_fmaf(b, c.x, a * c.y));
-            }
-            *reinterpret_cast<VO*>(dst + d) = ox;
-            *reinterpret_cast<VO*>(dst + half + d) = oy;
-            return;
+    if (interleaved) {
+        if (kVec == 1) {
+            if (u < rot / 2) return {kUnitPairs, 2 * u, 2 * u + 1, u};
+            return {kUnitPass, u + rot / 2, u + rot / 2, 0};
         }
-        const int d = rot + (u - pairs) * kVec;
-        const VI x = *reinterpret_cast<const VI*>(src + d);
-        VO o;
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) o.x[i] = from_float<TO>(to_float(x.x[i]));
-        *reinterpret_cast<VO*>(dst + d) = o;
-        return;
-    }
-    if constexpr (kVec == 1) {
-        if (u < rot / 2) {
-            const float a = to_float(src[2 * u]), b = to_float(src[2 * u + 1]);
-            const float2 c = cs[u];
-            dst[2 * u] = from_float<TO>(__builtin_fmaf(a, c.x, -(b * c.y)));
-            dst[2 * u + 1] = from_float<TO>(__builtin_fmaf(b, c.x, a * c.y));
-        } else {
-            const int d = u + rot / 2;
-            dst[d] = from_float<TO>(to_float(src[d]));
-        }
-    } else {
         const int d = u * kVec;
-        const VI x = *reinterpret_cast<const VI*>(src + d);
-        VO o;
-#pragma unroll
-        for (int i = 0; i < kVec; i += 2) {
-            float a = to_float(x.x[i]), b = to_float(x.x[i + 1]);
-            if (d < rot) {
-                const float2 c = cs[(d + i) / 2];
-                const float r = __builtin_fmaf(a, c.x, -(b * c.y));
-                b = __builtin_fmaf(b, c.x, a * c.y);
-                a = r;
-            }
-            o.x[i] = from_float<TO>(a);
-            o.x[i + 1] = from_float<TO>(b);
-        }
-        *reinterpret_cast<VO*>(dst + d) = o;
+        return {d < rot ? kUnitInterleaved : kUnitPass, d, d, d / 2};
     }
+    const int pairs = rot / (2 * kVec);
+    if (u < pairs) return {kUnitPairs, u * kVec, rot / 2 + u * kVec, u * kVec};
+    const int d = rot + (u - pairs) * kVec;
+    return {kUnitPass, d, d, 0};
 }
 
-// Units a head has under rotate_unit.
-__device__ __forceinline__ int head_units(int rot, int dim, bool interleaved, int vec)
+// Units a head has.
+__host__ __device__ __forceinline__ int head_units(int rot, int dim, bool interleaved, int vec)
 {
     if (!interleaved) return rot / (2 * vec) + (dim - rot) / vec;
     return vec == 1 ? rot / 2 + (dim - rot) : dim / vec;
 }
 
+// Writes a unit: x and y are its vectors, cs the token's cosines and sines.
+template <class TI, class TO, int kVec>
+__device__ __forceinline__ void put_unit(const Unit& u, const Vec<TI, kVec>& x, const Vec<TI, kVec>& y, TO* dst,
+                                         const float2* cs)
+{
+    Vec<TO, kVec> ox, oy;
+    if (u.kind == kUnitPairs) {
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+            const float2 c = cs[u.pair + i];
+            const float a = float(x.x[i]), b = float(y.x[i]);
+            ox.x[i] = TO(__builtin_fmaf(a, c.x, -(b * c.y)));
+            oy.x[i] = TO(__builtin_fmaf(b, c.x, a * c.y));
+        }
+        *reinterpret_cast<Vec<TO, kVec>*>(dst + u.d1) = oy;
+    } else if (kVec > 1 && u.kind == kUnitInterleaved) {
+#pragma unroll
+        for (int i = 0; i + 1 < kVec; i += 2) {
+            const float2 c = cs[u.pair + i / 2];
+            const float a = float(x.x[i]), b = float(x.x[i + 1]);
+            ox.x[i] = TO(__builtin_fmaf(a, c.x, -(b * c.y)));
+            ox.x[i + 1] = TO(__builtin_fmaf(b, c.x, a * c.y));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) ox.x[i] = TO(float(x.x[i]));
+    }
+    *reinterpret_cast<Vec<TO, kVec>*>(dst + u.d0) = ox;
+}
+
+// Unit i of a token: of q's heads, then k's, then v's.
+template <class TI, int kVec>
+struct TokenUnit {
+    Vec<TI, kVec> x, y;
+    Unit u;
+    int head;             // of its array
+    int array;            // 0: q, 1: k, 2: v
+};
+
+template <class TI, int kVec>
+__device__ __forceinline__ void load_unit(const AppendArgs& a, int32_t r, int i, TokenUnit<TI, kVec>& t)
+{
+    const int nq = a.q_heads * a.units, nk = a.pool.heads * a.units;
+    const bool v = i >= nq + nk;
+    t.array = v ? 2 : i >= nq ? 1 : 0;
+    i -= v ? nq + nk : t.array == 1 ? nq : 0;
+    int u;
+    if (v) {
+        const int per = a.pool.dim / kVec;
+        t.head = int((uint64_t(uint32_t(i)) * a.vec_magic) >> a.vec_shift);
+        u = i - t.head * per;
+        t.u = {kUnitPass, u * kVec, u * kVec, 0};
+    } else {
+        t.head = int((uint64_t(uint32_t(i)) * a.unit_magic) >> a.unit_shift);
+        u = i - t.head * a.units;
+        t.u = head_unit<kVec>(u, a.rot, a.interleaved != 0);
+    }
+    const uint64_t base = t.array == 0 ? a.q : t.array == 1 ? a.k : a.v;
+    const int64_t row = t.array == 0 ? a.q_row : t.array == 1 ? a.k_row : a.v_row;
+    const int64_t head = t.array == 0 ? a.q_head : t.array == 1 ? a.k_head : a.v_head;
+    const TI* src = reinterpret_cast<const TI*>(base) + r * row + t.head * head;
+    t.x = *reinterpret_cast<const Vec<TI, kVec>*>(src + t.u.d0);
+    if (t.u.kind == kUnitPairs) t.y = *reinterpret_cast<const Vec<TI, kVec>*>(src + t.u.d1);
+}
+
+// One workgroup per token.  What does not depend on each other is asked for
+// at once: the first units' values, the token's owner and length, the
+// frequencies; the angles are formed while these are on their way.
 template <class TI, class TO, int kVec>
 __global__ __launch_bounds__(kAppendBlock) void append_rows(AppendArgs a)
 {
+    constexpr int kUnits = kVec == 1 ? 4 : 2;      // units of a thread in flight
     __shared__ float2 cs[kMaxRot / 2];
     const int32_t r = blockIdx.x, tid = threadIdx.x;
+    const int dim = a.pool.dim, kv_heads = a.pool.heads;
+    const int total = (a.q_heads + kv_heads) * a.units + kv_heads * (dim / kVec);
+    TokenUnit<TI, kVec> t[kUnits];
+#pragma unroll
+    for (int x = 0; x < kUnits; ++x)
+        if (tid + x * kAppendBlock < total) load_unit<TI, kVec>(a, r, tid + x * kAppendBlock, t[x]);
     const int32_t pos = gptr<const gi32>(a.positions)[r];
+    const uint64_t kb = gptr<const gu64>(a.pool.k_pages)[a.pool.layer];
+    const uint64_t vb = gptr<const gu64>(a.pool.v_pages)[a.pool.layer];
+    const RowOwner o = row_owner(a.step, r);
     const double turns_per_radian = 0.15915494309189533577;
     for (int j = tid; j < a.rot / 2; j += kAppendBlock) {
         const double f = gptr<const __attribute__((address_space(1))) double>(a.freqs)[j];
-        const double t = double(pos) * (f * turns_per_radian);
-        const float frac = float(t - __builtin_rint(t));
+        const double turns = double(pos) * (f * turns_per_radian);
+        const float frac = float(turns - __builtin_rint(turns));
         float sn, cn;
         sincospif(2.0f * frac, &sn, &cn);
         cs[j] = {cn * a.gain, sn * a.gain};
     }
-    const int32_t s = wave_find(a.step.q_start, a.step.own.n, r);
-
-    const int dim = a.pool.dim, rot = a.rot;
-    const bool il = a.interleaved != 0;
-    const int per = head_units(rot, dim, il, kVec);
-    const int vper = dim / kVec;
-    const int kv_heads = a.pool.heads;
-    __syncthreads();
-    if (a.q != 0) {
-        const TI* q = reinterpret_cast<const TI*>(a.q) + int64_t(r) * a.q_row;
-        TO* o = reinterpret_cast<TO*>(a.q_out) + int64_t(r) * a.o_row;
-        for (int i = tid; i < a.q_heads * per; i += kAppendBlock) {
-            const int h = i / per, u = i - h * per;
-            rotate_unit<TI, TO, kVec>(q + h * a.q_head, o + h * a.o_head, u, rot, il, cs);
+    // where k and v go; 0: nowhere (a row of no sequence, no slot left, a bad page)
+    uint64_t kd = 0, vd = 0;
+    const int32_t slot = o.len - o.count + (r - o.first);
+    if (o.s >= 0 && slot >= 0) {
+        const uint32_t pi = page_of(a.pool, uint32_t(slot));
+        const int32_t page = gptr<const gi32>(a.step.own.table)[o.s * a.step.own.stride + pi];
+        if (uint32_t(page) >= a.pool.num_pages) {
+            raise_fault(kFaultPage);
+        } else if (bad_addr(kb) || bad_addr(vb)) {
+            raise_fault(kFaultPool);
+        } else {
+            const int64_t row = int64_t(page) * a.pool.page_size + (uint32_t(slot) - pi * a.pool.page_size);
+            kd = kb + uint64_t(row) * kv_heads * dim * 2;
+            vd = vb + uint64_t(row) * kv_heads * dim * 2;
         }
     }
-    if (s < 0) return;                             // a row of no sequence: nothing is cached
-    const Rows rows = seq_rows(a.step, s);
-    const int32_t i = r - rows.first;
-    const int32_t slot = table_len(a.step.own, s) - rows.count + i;
-    if (i >= rows.count || slot < 0) return;
-    const uint32_t pi = page_of(a.pool, uint32_t(slot));
-    const int32_t page = gptr<const gi32>(a.step.own.table)[s * a.step.own.stride + pi];
-    const uint64_t kb = gptr<const gu64>(a.pool.k_pages)[a.pool.layer];
-    const uint64_t vb = gptr<const gu64>(a.pool.v_pages)[a.pool.layer];
-    if (page < 0 || uint32_t(page) >= a.pool.num_pages) {
-        raise_fault(kFaultPage);
-        return;
-    }
-    if (bad_addr(kb) || bad_addr(vb)) {
-        raise_fault(kFaultPool);
-        return;
-    }
-    const int64_t row = int64_t(page) * a.pool.page_size + (uint32_t(slot) - pi * a.pool.page_size);
-    __bf16* kd = reinterpret_cast<__bf16*>(kb) + row * kv_heads * dim;
-    __bf16* vd = reinterpret_cast<__bf16*>(vb) + row * kv_heads * dim;
-    const TI* k = reinterpret_cast<const TI*>(a.k) + int64_t(r) * a.k_row;
-    const TI* v = reinterpret_cast<const TI*>(a.v) + int64_t(r) * a.v_row;
-    for (int i = tid; i < kv_heads * per; i += kAppendBlock) {
-        const int h = i / per, u = i - h * per;
-        rotate_unit<TI, __bf16, kVec>(k + h * a.k_head, kd + h * dim, u, rot, il, cs);
-    }
-    for (int i = tid; i < kv_heads * vper; i += kAppendBlock) {
-        const int h = i / vper, u = i - h * vper;
-        const Vec<TI, kVec> x = *reinterpret_cast<const Vec<TI, kVec>*>(v + h * a.v_head + u * kVec);
-        Vec<__bf16, kVec> o;
+    __syncthreads();
+    for (int i = tid; i < total; i += kUnits * kAppendBlock) {
+        if (i != tid)
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) o.x[e] = from_float<__bf16>(to_float(x.x[e]));
-        *reinterpret_cast<Vec<__bf16, kVec>*>(vd + h * dim + u * kVec) = o;
+            for (int x = 0; x < kUnits; ++x)
+                if (i + x * kAppendBlock < total) load_unit<TI, kVec>(a, r, i + x * kAppendBlock, t[x]);
+#pragma unroll
+        for (int x = 0; x < kUnits; ++x) {
+            if (i + x * kAppendBlock >= total) continue;
+            if (t[x].array == 0) {
+                TO* dst = reinterpret_cast<TO*>(a.q_out) + r * a.o_row + t[x].head * a.o_head;
+                put_unit<TI, TO, kVec>(t[x].u, t[x].x, t[x].y, dst, cs);
+            } else if (kd != 0) {
+                __bf16* dst = reinterpret_cast<__bf16*>(t[x].array == 1 ? kd : vd) + t[x].head * dim;
+                put_unit<TI, __bf16, kVec>(t[x].u, t[x].x, t[x].y, dst, cs);
+            }
+        }
     }
-    if (a.weights != 0)
+    if (a.weights != 0 && kd != 0)
         for (int h = tid; h < a.w_heads; h += kAppendBlock) {
-            const int64_t at = (int64_t(s) * a.w_heads + h) * a.w_cap + slot;
+            const int64_t at = (int64_t(o.s) * a.w_heads + h) * a.w_cap + slot;
             gptr<gf32>(a.weights)[at] = 0.0f;
             gptr<gi32>(a.slot_positions)[at] = pos;
         }

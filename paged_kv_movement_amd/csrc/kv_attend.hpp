@@ -840,10 +840,9 @@ __global__ __launch_bounds__(kAttendBlock, DP <= 128 ? 2 : 1) void attend_pieces
     }
 }
 
-// What a join needs of row r: its tokens and how many pieces each side has.
-// One round of loads for up to 64 sequences and groups (lane i holds the i-th
-// of both; the row's own are taken from the lanes that hold them), and one
-// more only where a group may be larger than its bound.
+// What a join needs of row r: how many pieces each side has.  One round of
+// loads for its sequence and one for its group, and one more only where a
+// group may be larger than its bound.
 struct RowPieces {
     int32_t prefix, own;       // pieces; own < 0: a row of no sequence
 };
@@ -852,25 +851,8 @@ __device__ __forceinline__ RowPieces row_pieces(const AttendArgs& a, int32_t r)
 {
     const StepArg& st = a.step;
     const int32_t lane = threadIdx.x & 63;
-    int32_t s = -1, first = 0, count = 0, len = 0;
-    for (int32_t i0 = 0; i0 < st.own.n && s < 0; i0 += 64) {
-        const int32_t i = i0 + lane;
-        int32_t b = 0, e = 0, n = 0;
-        if (i < st.own.n) {
-            b = gptr<const gi32>(st.q_start)[i];
-            e = gptr<const gi32>(st.q_start)[i + 1];
-            n = table_len(st.own, i);
-        }
-        const uint64_t m = __ballot(b <= r && r < e);
-        if (m == 0) continue;
-        const int j = __builtin_ctzll(m);
-        s = i0 + j;
-        first = clamp_i32(__builtin_amdgcn_readlane(b, j), 0, st.n_rows);
-        count = clamp_i32(__builtin_amdgcn_readlane(e, j), first, st.n_rows) - first;
-        count = count < st.max_new ? count : st.max_new;
-        len = __builtin_amdgcn_readlane(n, j);
-    }
-    if (s < 0 || r - first >= count) return {0, -1};
+    const RowOwner o = row_owner(st, r);
+    if (o.s < 0) return {0, -1};
     int32_t prefix = 0;
     for (int32_t i0 = 0; i0 < st.prefix.n; i0 += 64) {
         const int32_t i = i0 + lane;
@@ -880,7 +862,7 @@ __device__ __forceinline__ RowPieces row_pieces(const AttendArgs& a, int32_t r)
             e = gptr<const gi32>(st.group_start)[i + 1];
             n = table_len(st.prefix, i);
         }
-        const uint64_t m = __ballot(b <= s && s < e);
+        const uint64_t m = __ballot(b <= o.s && o.s < e);
         if (m == 0) continue;
         const int j = __builtin_ctzll(m);
         prefix = __builtin_amdgcn_readlane(n, j);
@@ -890,7 +872,7 @@ __device__ __forceinline__ RowPieces row_pieces(const AttendArgs& a, int32_t r)
         }
         break;
     }
-    const int32_t own = clamp_i32(len - count + (r - first) + 1, 0, len);
+    const int32_t own = clamp_i32(o.len - o.count + (r - o.first) + 1, 0, o.len);
     return {int32_t((uint32_t(prefix) + a.prefix_tokens - 1) / uint32_t(a.prefix_tokens)),
             int32_t((uint32_t(own) + a.own_tokens - 1) / uint32_t(a.own_tokens))};
 }

@@ -82,19 +82,37 @@ __device__ __forceinline__ uint32_t page_of(const PoolArg& p, uint32_t t)
     return uint32_t((uint64_t(t) * p.page_magic) >> p.page_shift);
 }
 
-// Index of the interval [start[i], start[i + 1]) that holds x, or -1; every
-// lane of the wave gets it.  One load per 64 intervals and no dependent chain.
-__device__ __forceinline__ int32_t wave_find(uint64_t start, int32_t n, int32_t x)
+// The sequence that new-token row r belongs to, from one round of loads for up
+// to 64 sequences (lane i holds the i-th; the row's own is taken from the lane
+// that holds it).  s < 0: none.
+struct RowOwner {
+    int32_t s, first, count, len;
+};
+
+__device__ __forceinline__ RowOwner row_owner(const StepArg& a, int32_t r)
 {
     const int32_t lane = threadIdx.x & 63;
-    for (int32_t i0 = 0; i0 < n; i0 += 64) {
+    for (int32_t i0 = 0; i0 < a.own.n; i0 += 64) {
         const int32_t i = i0 + lane;
-        bool here = false;
-        if (i < n) here = gptr<const gi32>(start)[i] <= x && x < gptr<const gi32>(start)[i + 1];
-        const uint64_t m = __ballot(here);
-        if (m != 0) return i0 + __builtin_ctzll(m);
+        int32_t b = 0, e = 0, n = 0;
+        if (i < a.own.n) {
+            b = gptr<const gi32>(a.q_start)[i];
+            e = gptr<const gi32>(a.q_start)[i + 1];
+            n = table_len(a.own, i);
+        }
+        const uint64_t m = __ballot(b <= r && r < e);
+        if (m == 0) continue;
+        const int j = __builtin_ctzll(m);
+        RowOwner o;
+        o.s = i0 + j;
+        o.first = clamp_i32(__builtin_amdgcn_readlane(b, j), 0, a.n_rows);
+        o.count = clamp_i32(__builtin_amdgcn_readlane(e, j), o.first, a.n_rows) - o.first;
+        o.count = o.count < a.max_new ? o.count : a.max_new;
+        o.len = __builtin_amdgcn_readlane(n, j);
+        if (r - o.first >= o.count) o.s = -1;
+        return o;
     }
-    return -1;
+    return {-1, 0, 0, 0};
 }
 
 __device__ __forceinline__ void raise_fault_lane(unsigned bit) { atomicOr(&g_kv_faults, bit); }

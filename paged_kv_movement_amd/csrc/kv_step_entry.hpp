@@ -178,6 +178,12 @@ int append(const kv_paged* paged, const kv_step* step, int32_t layer, const kv_r
     a.rot = rope->rot;
     a.q_heads = q != nullptr ? q_heads : 0;
     a.interleaved = rope->interleaved;
+    const int vec = vectors ? 8 : 1;
+    a.units = head_units(a.rot, dim, a.interleaved != 0, vec);
+    magic_of(a.units, &a.unit_magic, &a.unit_shift);
+    magic_of(dim / vec, &a.vec_magic, &a.vec_shift);
+    if (int64_t(a.q_heads + 2 * int64_t(paged->num_kv_heads)) * dim > INT32_MAX / 2)
+        return fail(KV_EINVAL, "a token's heads are too large for one workgroup");
     a.gain = rope->gain;
     KernelFn f;
     if (type == KV_TYPE_BF16)
