@@ -73,9 +73,9 @@ __device__ __forceinline__ AttendItem attend_item(const AttendArgs& a, uint32_t 
     const uint32_t heads = a.pool.heads;
     it.h = b % heads;
     b /= heads;
+    const int32_t tokens = it.prefix ? a.prefix_tokens : a.own_tokens;
     const int32_t tiles = it.prefix ? a.prefix_tiles : a.own_tiles;
     const int32_t pieces = it.prefix ? a.prefix_pieces : a.own_pieces;
-    const int32_t tokens = it.prefix ? a.prefix_tokens : a.own_tokens;
     // the last rows of a prompt see the most: they start first
     const int32_t tile = it.prefix ? b % tiles : tiles - 1 - b % tiles;
     b /= tiles;

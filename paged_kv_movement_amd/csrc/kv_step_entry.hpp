@@ -369,11 +369,11 @@ int attend(const kv_paged* paged, const kv_step* step, int32_t layer, const kv_r
 // ---- weights
 
 template <int DP>
-KernelFn weights_kernel(bool split_rows, int32_t* tokens)
+KernelFn weights_kernel(bool rows, int32_t* tokens, int* block)
 {
-    *tokens = split_rows ? kWeightsTokens<DP, true> : kWeightsTokens<DP, false>;
-    return split_rows ? reinterpret_cast<KernelFn>(&add_weights<DP, true>)
-                      : reinterpret_cast<KernelFn>(&add_weights<DP, false>);
+    *tokens = rows ? kRowsTokens<DP> : kWeightsTokens;
+    *block = rows ? kRowsWaves * 64 : kAttendBlock;
+    return rows ? reinterpret_cast<KernelFn>(&add_weights_rows<DP>) : reinterpret_cast<KernelFn>(&add_weights<DP>);
 }
 
 int add_weights_call(const kv_paged* paged, const kv_step* step, int32_t layer, const kv_rows* q, const float* lse,
@@ -411,9 +411,10 @@ int add_weights_call(const kv_paged* paged, const kv_step* step, int32_t layer, 
     const bool split = rows * a.rep > 256;
     const int dim = paged->head_dim;
     int32_t tokens = 0;
-    KernelFn f = dim <= 64    ? weights_kernel<64>(split, &tokens)
-                 : dim <= 128 ? weights_kernel<128>(split, &tokens)
-                              : weights_kernel<256>(split, &tokens);
+    int block = 0;
+    KernelFn f = dim <= 64    ? weights_kernel<64>(split, &tokens, &block)
+                 : dim <= 128 ? weights_kernel<128>(split, &tokens, &block)
+                              : weights_kernel<256>(split, &tokens, &block);
     int64_t own_items = 0, prefix_items = 0;
     if (own != nullptr) {
         a.own_in = reinterpret_cast<uint64_t>(own->in);
@@ -429,10 +430,10 @@ int add_weights_call(const kv_paged* paged, const kv_step* step, int32_t layer, 
         a.prefix_blocks = int32_t(ceil_div(step->prefix.max_len, tokens));
         prefix_items = int64_t(step->prefix.n) * paged->num_kv_heads * a.prefix_blocks;
     }
-    const int64_t most = max_blocks(kAttendBlock);
+    const int64_t most = max_blocks(block);
     if (own_items > most || prefix_items > most) return fail(KV_EINVAL, "too many tokens for one launch");
     a.prefix_items = uint32_t(prefix_items);
-    rc = launch(f, prefix_items + own_items, kAttendBlock, &a, stream);
+    rc = launch(f, prefix_items + own_items, block, &a, stream);
     return rc == KV_OK ? ok() : rc;
 }
 

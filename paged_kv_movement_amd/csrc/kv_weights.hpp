@@ -6,10 +6,14 @@
 //
 // with the lse of a finished attention, so no maximum is searched.  A wave
 // keeps its tokens' K in registers as the left operand of S^T = K Q^T and
-// walks the rows, 16 at a time, the next ones' q already on its way: K is
-// read once whatever the number of rows.  With few rows the four waves of a
-// workgroup take different tokens; with many rows they take the same tokens
-// and every fourth block of rows (kSplitRows), and their sums meet in LDS.
+// walks the rows, 16 at a time: K is read once whatever the number of rows.
+//
+// add_weights        few rows: each of a workgroup's four waves has its own
+//                    tokens, and the next rows' q on its way to registers;
+// add_weights_rows   many rows: eight waves, two groups of tokens by four
+//                    shares of the rows, whose q comes through LDS for all of
+//                    them, a stage ahead; the four sums of a token meet there.
+//
 // Each token's sum has one owner and one order, so the same call gives the
 // same bits.
 //
@@ -38,13 +42,17 @@ struct WeightsArgs {
     uint32_t prefix_items;
 };
 
-// Tiles of 16 tokens a wave holds: four where many rows pass by, so that a
-// row's q serves more products; two otherwise, for more waves in flight.
-template <int DP, bool kSplitRows>
-constexpr int kWeightsTiles = DP <= 128 && kSplitRows ? 4 : 2;
-
-template <int DP, bool kSplitRows>
-constexpr int kWeightsTokens = 16 * kWeightsTiles<DP, kSplitRows> * (kSplitRows ? 1 : kAttendWaves);   // of a workgroup
+// Tiles of 16 tokens a wave holds: two with few rows, for more waves in
+// flight; four where many rows pass by, so that a row's q serves more products.
+constexpr int kWeightsTiles = 2;
+constexpr int kWeightsTokens = 16 * kWeightsTiles * kAttendWaves;       // of a workgroup
+template <int DP>
+constexpr int kRowsTiles = DP <= 128 ? 4 : 2;
+constexpr int kRowsGroups = 2, kRowsShares = 4, kRowsWaves = kRowsGroups * kRowsShares;
+template <int DP>
+constexpr int kRowsTokens = 16 * kRowsTiles<DP> * kRowsGroups;
+template <int DP>
+constexpr int kStageRows = DP <= 128 ? 128 : 64;                        // rows whose q is in LDS at a time
 
 struct WeightsPiece {
     uint64_t kh;                   // this KV head's K pool
@@ -89,11 +97,13 @@ __device__ __forceinline__ void add_block(const WeightsArgs& a, const WeightsPie
     if (int(a.pool.dim) < DP) clear_past<DP>(c.q, g, a.pool.dim);
     f32x4 s[NT];
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-        s[i] = f32x4{0, 0, 0, 0};
+    for (int i = 0; i < NT; ++i) s[i] = f32x4{0, 0, 0, 0};
+    // the sums in turn: a product waits for the one before it on the same sum
 #pragma unroll
-        for (int j = 0; j < DP / 32; ++j) s[i] = mfma16(k[i][j], c.q[j], s[i]);
-    }
+    for (int j = 0; j < DP / 32; ++j)
+#pragma unroll
+        for (int i = 0; i < NT; ++i) s[i] = mfma16(k[i][j], c.q[j], s[i]);
+    __builtin_amdgcn_sched_group_barrier(0x008, NT * (DP / 32), 0);
     // minus lse in log2 units; a row that saw nothing adds nothing: exp2(-infinity)
     const float neg = !c.live || c.lse == -__builtin_inff() ? -__builtin_inff() : -c.lse * kLog2e;
     // the block's first row sees the least
@@ -151,55 +161,6 @@ __device__ __forceinline__ void fold_columns(const f32x4 (&sum)[NT], float* part
         }
 }
 
-// Many rows: the four waves hold the same tokens [t, t + 16 NT) and take every
-// fourth block of rows, the q of the next two on their way.
-template <int DP>
-__device__ __forceinline__ void weights_by_rows(const WeightsArgs& a, const WeightsPiece& w, int32_t t, bool pool_ok,
-                                                float (&part)[kAttendWaves][64])
-{
-    constexpr int NT = kWeightsTiles<DP, true>;
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const bool here = pool_ok && lane < 16 * NT && lane < w.len - t;
-    const int32_t row = here ? token_row(a.pool, w.tab, w.table_row, t + lane) : -1;
-    u32x4 k[NT][DP / 32];
-    if (pool_ok) load_keys<DP, NT>(a, w, row, k);
-    f32x4 sum[NT];
-#pragma unroll
-    for (int i = 0; i < NT; ++i) sum[i] = f32x4{0, 0, 0, 0};
-    // token t is first seen by new token t - (len - count): blocks of rows before it see none of these tokens
-    const int32_t before = w.prefix ? 0 : t - (w.len - w.count);
-    const int32_t n_blocks = (w.count * a.rep + 15) / 16;
-    int32_t x = (before > 0 ? before * a.rep / 16 : 0) + wave;
-    WeightsColumn<DP> c0, c1, c2;
-    if (!pool_ok) x = n_blocks;
-    if (x < n_blocks) {
-        load_column<DP>(a, w, x, c0);
-        load_column<DP>(a, w, x + kAttendWaves, c1);
-    }
-    // three columns by name: to move one on would wait for its loads
-#pragma unroll 1
-    while (x < n_blocks) {
-        load_column<DP>(a, w, x + 2 * kAttendWaves, c2);
-        add_block<DP, NT>(a, w, x, t, k, c0, sum);
-        if ((x += kAttendWaves) >= n_blocks) break;
-        load_column<DP>(a, w, x + 2 * kAttendWaves, c0);
-        add_block<DP, NT>(a, w, x, t, k, c1, sum);
-        if ((x += kAttendWaves) >= n_blocks) break;
-        load_column<DP>(a, w, x + 2 * kAttendWaves, c1);
-        add_block<DP, NT>(a, w, x, t, k, c2, sum);
-        x += kAttendWaves;
-    }
-    fold_columns<NT>(sum, part[wave]);
-    __syncthreads();
-    if (wave == 0 && lane < 16 * NT && lane < w.len - t) {
-        float v = part[0][lane];
-#pragma unroll
-        for (int y = 1; y < kAttendWaves; ++y) v += part[y][lane];
-        const float old = w.in != 0 ? gptr<const gf32>(w.in)[t + lane] : 0.0f;
-        gptr<gf32>(w.out)[t + lane] = old + (row >= 0 ? v : 0.0f);
-    }
-}
-
 // Few rows: each wave has its own tokens [t, t + 16 NT), one group of them:
 // many short waves hide their three rounds of loads (lengths and pages; K and
 // q; the sums out) behind each other, which measured better than fewer waves
@@ -209,7 +170,7 @@ template <int DP>
 __device__ __forceinline__ void weights_by_tokens(const WeightsArgs& a, const WeightsPiece& w, int32_t t, int32_t page,
                                                   float old, bool pool_ok, float (&part)[kAttendWaves][64])
 {
-    constexpr int NT = kWeightsTiles<DP, false>, T = 16 * NT;
+    constexpr int NT = kWeightsTiles, T = 16 * NT;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const bool here = pool_ok && lane < T && lane < w.len - t;
     const int32_t row = here ? row_in_page(a.pool, page, t + lane) : -1;
@@ -237,45 +198,194 @@ __device__ __forceinline__ void weights_by_tokens(const WeightsArgs& a, const We
     if (lane < T && lane < w.len - t) gptr<gf32>(w.out)[t + lane] = old + (row >= 0 ? part[wave][lane] : 0.0f);
 }
 
-template <int DP, bool kSplitRows>
-__global__ __launch_bounds__(kAttendBlock, kSplitRows || DP > 128 ? 2 : 4) void add_weights(WeightsArgs a)
+// What the workgroup at b works on; tokens: of a workgroup.
+struct WeightsItem {
+    bool prefix;
+    int32_t h, table_row, t0;
+    int64_t at;            // first sum of (table row, KV head)
+    uint64_t in, out;
+};
+
+template <bool kByTokens>
+__device__ __forceinline__ WeightsItem weights_item(const WeightsArgs& a, uint32_t b, int tokens)
+{
+    WeightsItem it;
+    it.prefix = b < a.prefix_items;
+    if (!it.prefix) b -= a.prefix_items;
+    it.h = b % a.pool.heads;
+    b /= a.pool.heads;
+    if (kByTokens) {
+        // every sequence's first tokens, which the most rows see, before the later ones
+        const int32_t n = it.prefix ? a.step.prefix.n : a.step.own.n;
+        it.t0 = b / n * tokens;
+        it.table_row = b % n;
+    } else {
+        const int32_t blocks = it.prefix ? a.prefix_blocks : a.own_blocks;
+        it.table_row = b / blocks;
+        it.t0 = (b - it.table_row * blocks) * tokens;
+    }
+    it.at = (int64_t(it.table_row) * a.pool.heads + it.h) * (it.prefix ? a.prefix_cap : a.own_cap);
+    it.in = it.prefix ? a.prefix_in : a.own_in;
+    it.out = it.prefix ? a.prefix_out : a.own_out;
+    return it;
+}
+
+__device__ __forceinline__ WeightsPiece weights_piece(const WeightsArgs& a, const WeightsItem& it, uint64_t kb,
+                                                      int32_t len)
+{
+    const Rows rows = it.prefix ? group_rows(a.step, it.table_row) : seq_rows(a.step, it.table_row);
+    return {kb + uint64_t(it.h) * a.pool.dim * 2,
+            it.in != 0 ? it.in + it.at * 4 : 0,
+            it.out + it.at * 4,
+            it.prefix ? a.step.prefix : a.step.own,
+            it.table_row,
+            it.h,
+            len,
+            __builtin_amdgcn_readfirstlane(rows.first),
+            __builtin_amdgcn_readfirstlane(rows.count),
+            it.prefix};
+}
+
+template <int DP>
+__global__ __launch_bounds__(kAttendBlock, DP > 128 ? 2 : 4) void add_weights(WeightsArgs a)
 {
     __shared__ float part[kAttendWaves][64];
-    uint32_t b = blockIdx.x;
-    const bool prefix = b < a.prefix_items;
-    if (!prefix) b -= a.prefix_items;
-    const int32_t heads = a.pool.heads;
-    const int32_t h = b % heads;
-    b /= heads;
-    const int32_t blocks = prefix ? a.prefix_blocks : a.own_blocks;
-    const int32_t table_row = b / blocks, t0 = (b - table_row * blocks) * kWeightsTokens<DP, kSplitRows>;
-    const TablesArg& tab = prefix ? a.step.prefix : a.step.own;
-    const int64_t cap = prefix ? a.prefix_cap : a.own_cap, at = (int64_t(table_row) * heads + h) * cap;
-    const uint64_t in = prefix ? a.prefix_in : a.own_in, out = prefix ? a.prefix_out : a.own_out;
-    // page ids and old sums are asked for together with the lengths: within the bounds, and not used behind the end
-    const int32_t t = t0 + (kSplitRows ? 0 : int(threadIdx.x >> 6) * 16 * kWeightsTiles<DP, false>);
+    const WeightsItem it = weights_item<false>(a, blockIdx.x, kWeightsTokens);
+    const TablesArg& tab = it.prefix ? a.step.prefix : a.step.own;
     const int lane = threadIdx.x & 63;
-    int32_t page = -1;
+    const int32_t t = it.t0 + int(threadIdx.x >> 6) * 16 * kWeightsTiles;
+    if (t >= tab.max_len) return;
+    // page ids and old sums are asked for together with the lengths: within the bounds, and not used behind the end
+    const int32_t tok = lane < tab.max_len - t ? t + lane : tab.max_len - 1;
+    const int32_t page = token_page(a.pool, tab, it.table_row, tok);
     float old = 0.0f;
-    if constexpr (!kSplitRows) {
-        if (t >= tab.max_len) return;
-        const int32_t tok = lane < tab.max_len - t ? t + lane : tab.max_len - 1;
-        page = token_page(a.pool, tab, table_row, tok);
-        if (in != 0) old = gptr<const gf32>(in)[at + tok];
-    }
+    if (it.in != 0) old = gptr<const gf32>(it.in)[it.at + tok];
     const uint64_t kb = wave_uniform(gptr<const gu64>(a.pool.k_pages)[a.pool.layer]);
-    const int32_t len = __builtin_amdgcn_readfirstlane(table_len(tab, table_row));
-    const Rows rows = prefix ? group_rows(a.step, table_row) : seq_rows(a.step, table_row);
+    const int32_t len = __builtin_amdgcn_readfirstlane(table_len(tab, it.table_row));
+    const WeightsPiece w = weights_piece(a, it, kb, len);
     if (t >= len) return;
-    const WeightsPiece w = {kb + uint64_t(h) * a.pool.dim * 2, in != 0 ? in + at * 4 : 0, out + at * 4, tab, table_row,
-                            h, len, __builtin_amdgcn_readfirstlane(rows.first),
-                            __builtin_amdgcn_readfirstlane(rows.count), prefix};
     const bool pool_ok = !bad_addr(kb);
     if (!pool_ok && lane == 0) raise_fault_lane(kFaultPool);
-    if constexpr (kSplitRows)
-        weights_by_rows<DP>(a, w, t, pool_ok, part);
-    else
-        weights_by_tokens<DP>(a, w, __builtin_amdgcn_readfirstlane(t), page, old, pool_ok, part);
+    weights_by_tokens<DP>(a, w, __builtin_amdgcn_readfirstlane(t), page, old, pool_ok, part);
+}
+
+// q of kStageRows rows from flattened row f0 into LDS, this wave's share.  A
+// row's vectors are at chunk ^ wide_swizzle(row), as in the attention's tiles;
+// rows past the last one repeat it, elements past dim are 0.
+template <int DP>
+__device__ __forceinline__ void load_stage(const WeightsArgs& a, const WeightsPiece& w, int32_t f0, u32x4* stage)
+{
+    constexpr int V = DP / 8, kPer = 64 / V, kLoads = kStageRows<DP> / kPer / kRowsWaves;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int32_t n = w.count * a.rep;
+    const uint64_t zero = reinterpret_cast<uint64_t>(&g_zero_vector);
+#pragma unroll
+    for (int x = 0; x < kLoads; ++x) {
+        const int first = (wave * kLoads + x) * kPer, y = first + lane / V;
+        const int chunk = lane % V ^ wide_swizzle<DP>(y);
+        const int32_t f = f0 + y < n ? f0 + y : n - 1;
+        const int32_t i = new_token(a, f), head = w.h * a.rep + (f - i * a.rep);
+        const uint64_t at = a.q + (int64_t(w.first_row + i) * a.q_row + head * a.q_head) * 2 + chunk * 16;
+        __builtin_amdgcn_global_load_lds(gptr<const gvec4>(chunk * 8 < int(a.pool.dim) ? at : zero),
+                                         (__attribute__((address_space(3))) void*)&stage[first * V], 16, 0, 0);
+    }
+}
+
+// The blocks of rows that this wave has in a stage.
+template <int DP>
+__device__ __forceinline__ void add_stage(const WeightsArgs& a, const WeightsPiece& w, int32_t f0, int32_t t,
+                                          const u32x4* stage, const float (&lse)[kStageRows<DP> / 64],
+                                          const u32x4 (&k)[kRowsTiles<DP>][DP / 32], f32x4 (&sum)[kRowsTiles<DP>])
+{
+    constexpr int V = DP / 8, NT = kRowsTiles<DP>;
+    const int lane = threadIdx.x & 63, share = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % kRowsShares,
+              r = lane & 15, g = lane >> 4;
+    const int32_t n = w.count * a.rep;
+#pragma unroll 1
+    for (int y = 0; y < kStageRows<DP> / 64; ++y) {
+        const int block = y * kRowsShares + share;
+        const int32_t f = f0 + block * 16 + r;
+        if (f0 + block * 16 >= n) break;
+        WeightsColumn<DP> c;
+        c.live = f < n;
+        c.vis = w.prefix ? w.len : clamp_i32(w.len - w.count + new_token(a, c.live ? f : n - 1) + 1, 0, w.len);
+        c.lse = y == 0 ? lse[0] : lse[kStageRows<DP> / 64 - 1];
+#pragma unroll
+        for (int j = 0; j < DP / 32; ++j)
+            c.q[j] = stage[(block * 16 + r) * V + ((4 * j + g) ^ wide_swizzle<DP>(r))];
+        add_block<DP, NT>(a, w, f0 / 16 + block, t, k, c, sum);
+    }
+}
+
+template <int DP>
+__global__ __launch_bounds__(kRowsWaves * 64, 2) void add_weights_rows(WeightsArgs a)
+{
+    constexpr int NT = kRowsTiles<DP>, V = DP / 8, S = kStageRows<DP>, Y = S / 64;
+    __shared__ u32x4 stage0[S * V];
+    __shared__ u32x4 stage1[S * V];
+    __shared__ float part[kRowsWaves][64];
+    const WeightsItem it = weights_item<true>(a, blockIdx.x, kRowsTokens<DP>);
+    const TablesArg& tab = it.prefix ? a.step.prefix : a.step.own;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6),
+              share = wave % kRowsShares, r = lane & 15;
+    const uint64_t kb = wave_uniform(gptr<const gu64>(a.pool.k_pages)[a.pool.layer]);
+    const int32_t len = __builtin_amdgcn_readfirstlane(table_len(tab, it.table_row));
+    const WeightsPiece w = weights_piece(a, it, kb, len);
+    if (it.t0 >= len) return;
+    const bool pool_ok = !bad_addr(kb);
+    if (!pool_ok) raise_fault(kFaultPool);
+    const int32_t t = it.t0 + wave / kRowsShares * 16 * NT;
+    const bool here = pool_ok && lane < 16 * NT && lane < len - t;
+    const int32_t row = here ? token_row(a.pool, tab, it.table_row, t + lane) : -1;
+    u32x4 k[NT][DP / 32];
+    if (pool_ok) load_keys<DP, NT>(a, w, row, k);
+    f32x4 sum[NT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) sum[i] = f32x4{0, 0, 0, 0};
+    // token t0 is first seen by new token t0 - (len - count): stages of rows before it see none of these tokens
+    const int32_t before = w.prefix ? 0 : it.t0 - (len - w.count), n = pool_ok ? w.count * a.rep : 0;
+    int32_t f0 = before > 0 ? before * a.rep / S * S : 0;
+    // the lse of this lane's rows of a stage, asked for when its q is
+    auto load_lse = [&](int32_t f0, float (&lse)[Y]) {
+#pragma unroll
+        for (int y = 0; y < Y; ++y) {
+            const int32_t f = f0 + (y * kRowsShares + share) * 16 + r, g = f < n ? f : n - 1;
+            const int32_t i = new_token(a, g);
+            lse[y] = gptr<const gf32>(a.lse)[int64_t(w.first_row + i) * a.q_heads + w.h * a.rep + (g - i * a.rep)];
+        }
+    };
+    float lse0[Y], lse1[Y];
+    if (f0 < n) {
+        load_lse(f0, lse0);
+        load_stage<DP>(a, w, f0, stage0);
+    }
+#pragma unroll 1
+    for (; f0 < n; f0 += 2 * S) {
+        __builtin_amdgcn_s_waitcnt(0);
+        __syncthreads();
+        if (f0 + S < n) {
+            load_lse(f0 + S, lse1);
+            load_stage<DP>(a, w, f0 + S, stage1);
+        }
+        add_stage<DP>(a, w, f0, t, stage0, lse0, k, sum);
+        if (f0 + S >= n) break;
+        __builtin_amdgcn_s_waitcnt(0);
+        __syncthreads();
+        if (f0 + 2 * S < n) {
+            load_lse(f0 + 2 * S, lse0);
+            load_stage<DP>(a, w, f0 + 2 * S, stage0);
+        }
+        add_stage<DP>(a, w, f0 + S, t, stage1, lse1, k, sum);
+    }
+    fold_columns<NT>(sum, part[wave]);
+    __syncthreads();
+    if (share == 0 && lane < 16 * NT && lane < len - t) {
+        float v = part[wave][lane];
+#pragma unroll
+        for (int y = 1; y < kRowsShares; ++y) v += part[wave + y][lane];
+        const float old = w.in != 0 ? gptr<const gf32>(w.in)[t + lane] : 0.0f;
+        gptr<gf32>(w.out)[t + lane] = old + (row >= 0 ? v : 0.0f);
+    }
 }
 
 }  // namespace kvmove
