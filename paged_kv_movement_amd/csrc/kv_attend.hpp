@@ -206,27 +206,30 @@ __device__ __forceinline__ constexpr int acc_element(int r, int m)
 // and the accumulators are rescaled only when a row's maximum rises by more.
 constexpr float kLag = 8.0f;
 
-// Softmax weights of 32 tokens for one block of rows, as two bf16 parts in the
-// layout of the next product's right operand; the state's maximum, sum and
-// accumulators follow.  If masked (the same in every lane), token t + x counts
-// for this lane's row if t + x < vis and bit x of valid is set.
-template <int DP>
-__device__ __forceinline__ void softmax_block(RowState<DP>& st, f32x4 (&s)[2], u32x4& ph, u32x4& pl, float c,
-                                              bool masked, int32_t t, int32_t vis, uint32_t valid)
+// Scores of 32 tokens that this lane's row does not see to -infinity: token
+// t + x counts if t + x < vis and bit x of valid is set.
+__device__ __forceinline__ void mask_scores(f32x4 (&s)[2], int32_t t, int32_t vis, uint32_t valid)
 {
     const int g = (threadIdx.x & 63) >> 4;
-    if (masked) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                const int x = 16 * i + 4 * g + n;
-                if (t + x >= vis || !((valid >> x) & 1)) s[i][n] = -__builtin_inff();
-            }
-    }
-    const float mx = max3(max3(max3(s[0][0], s[0][1], s[0][2]), s[0][3], s[1][0]), max3(s[1][1], s[1][2], s[1][3]),
-                          s[1][3]);
-    const float top = max_over_groups(mx) * c;
+        for (int n = 0; n < 4; ++n) {
+            const int x = 16 * i + 4 * g + n;
+            if (t + x >= vis || !((valid >> x) & 1)) s[i][n] = -__builtin_inff();
+        }
+}
+
+__device__ __forceinline__ float max_of(const f32x4 (&s)[2])
+{
+    return max3(max3(max3(s[0][0], s[0][1], s[0][2]), s[0][3], s[1][0]), max3(s[1][1], s[1][2], s[1][3]), s[1][3]);
+}
+
+// Raises the state's base to a row's new maximum `top` (log2 units) where it
+// has risen by more than kLag, and what it holds with it.
+template <int DP>
+__device__ __forceinline__ void raise_base(RowState<DP>& st, float top)
+{
     if (__any(top > st.m + kLag)) {
         const float m_new = __builtin_fmaxf(st.m, top);
         const float alpha = m_new == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(st.m - m_new);
@@ -235,6 +238,13 @@ __device__ __forceinline__ void softmax_block(RowState<DP>& st, f32x4 (&s)[2], u
         for (int m = 0; m < DP / 16; ++m) st.acc[m] *= alpha;
         st.m = m_new;
     }
+}
+
+// Softmax weights of 32 tokens for one block of rows, as two bf16 parts in the
+// layout of the next product's right operand; their sum goes to the state.
+template <int DP>
+__device__ __forceinline__ void weights_of(RowState<DP>& st, const f32x4 (&s)[2], u32x4& ph, u32x4& pl, float c)
+{
     const float base = st.m == -__builtin_inff() ? 0.0f : st.m;       // a row that has seen nothing yet
     float sum = 0.0f;
 #pragma unroll
@@ -530,7 +540,9 @@ __device__ __forceinline__ void narrow_piece(const AttendArgs& a, const AttendIt
         }
         u32x4 ph[1], pl[1];
         const bool masked = valid != ~0u || t + kAttendTile > all_see;
-        softmax_block<DP>(st[0], s, ph[0], pl[0], a.scale_log2, masked, t, vis[0], valid);
+        if (masked) mask_scores(s, t, vis[0], valid);
+        raise_base<DP>(st[0], max_over_groups(max_of(s)) * a.scale_log2);
+        weights_of<DP>(st[0], s, ph[0], pl[0], a.scale_log2);
         if (care) {
 #pragma unroll
             for (int x = 0; x < 8; ++x)
@@ -647,38 +659,33 @@ __device__ __forceinline__ void wide_load(uint64_t kh, uint64_t vh, uint32_t row
     }
 }
 
-// The products and the softmax of 32 tokens (half h of a tile) for this wave's
-// NB blocks of rows.
+// Scores of 32 tokens (half h of a tile) for this wave's NB blocks of rows.
 template <int DP, int NB>
-__device__ __forceinline__ void wide_half(RowState<DP> (&st)[NB], const u32x4 (&q)[NB][DP / 32],
-                                          const WideTile<DP>& tile, int h, float c, bool masked, int32_t t,
-                                          const int32_t (&vis)[NB], uint32_t valid, bool care)
+__device__ __forceinline__ void wide_scores(f32x4 (&s)[NB][2], const u32x4 (&q)[NB][DP / 32],
+                                            const WideTile<DP>& tile, int h)
 {
-    constexpr int V = DP / 8, J = DP / 32;
+    constexpr int V = DP / 8;
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
-    f32x4 s[NB][2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int b = 0; b < NB; ++b) s[b][i] = f32x4{0, 0, 0, 0};
 #pragma unroll
-        for (int j = 0; j < J; ++j) {
+    for (int j = 0; j < DP / 32; ++j)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
             const u32x4 k = tile.k[(32 * h + 16 * i + r) * V + ((4 * j + g) ^ wide_swizzle<DP>(r))];
 #pragma unroll
             for (int b = 0; b < NB; ++b) s[b][i] = mfma16(k, q[b][j], s[b][i]);
         }
-    }
-    u32x4 ph[NB], pl[NB];
-#pragma unroll
-    for (int b = 0; b < NB; ++b) softmax_block<DP>(st[b], s[b], ph[b], pl[b], c, masked, t, vis[b], valid);
-    if (care)                                     // before V takes its registers
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-            add_nonfinite<DP>(
-                st[b], ph[b], pl[b], t, vis[b], valid,
-                [&](int x) { return reinterpret_cast<const uint16_t*>(&tile.v[(32 * h + x) * V]); },
-                [](int x, int d) { return ((d / 8) ^ wide_swizzle<DP>(x)) * 8 + d % 8; });
-    uint32_t v[8][J];
+}
+
+// V of those tokens as add_v takes it.
+template <int DP>
+__device__ __forceinline__ void wide_values(uint32_t (&v)[8][DP / 32], const WideTile<DP>& tile, int h)
+{
+    constexpr int V = DP / 8;
+    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
 #pragma unroll
     for (int x = 0; x < 8; ++x) {
         const int tok = 32 * h + 16 * (x / 4) + 4 * g + x % 4, swz = wide_swizzle<DP>(4 * g + x % 4);
@@ -695,7 +702,73 @@ __device__ __forceinline__ void wide_half(RowState<DP> (&st)[NB], const u32x4 (&
             }
         }
     }
-    if (care) take_nonfinite<DP>(v);
+}
+
+// The products and the softmax of a tile for this wave's NB blocks of rows.
+// One maximum and one look at the base for the whole tile; the first half's
+// second product runs beside the second half's exponentials.
+template <int DP, int NB>
+__device__ __forceinline__ void wide_tile(RowState<DP> (&st)[NB], const u32x4 (&q)[NB][DP / 32],
+                                          const WideTile<DP>& tile, float c, bool masked, int32_t t,
+                                          const int32_t (&vis)[NB], uint64_t valid)
+{
+    constexpr int H = kWideTile<DP> / 32;
+    f32x4 s[H][NB][2];
+#pragma unroll
+    for (int h = 0; h < H; ++h) wide_scores<DP, NB>(s[h], q, tile, h);
+    if (masked)
+#pragma unroll
+        for (int h = 0; h < H; ++h)
+#pragma unroll
+            for (int b = 0; b < NB; ++b) mask_scores(s[h][b], t + 32 * h, vis[b], uint32_t(valid >> (32 * h)));
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        float mx = max_of(s[0][b]);
+        if (H > 1) {
+            const float m1 = max_of(s[H - 1][b]);
+            mx = max3(mx, m1, m1);
+        }
+        raise_base<DP>(st[b], max_over_groups(mx) * c);
+    }
+    u32x4 ph[NB], pl[NB];
+    uint32_t v[8][DP / 32];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) weights_of<DP>(st[b], s[0][b], ph[b], pl[b], c);
+    wide_values<DP>(v, tile, 0);
+    if (H > 1) {
+        u32x4 ph1[NB], pl1[NB];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) weights_of<DP>(st[b], s[H - 1][b], ph1[b], pl1[b], c);
+        add_v<DP, NB>(st, v, ph, pl);
+        wide_values<DP>(v, tile, H - 1);
+        add_v<DP, NB>(st, v, ph1, pl1);
+    } else {
+        add_v<DP, NB>(st, v, ph, pl);
+    }
+}
+
+// The same for a piece that is done again with care: half by half.
+template <int DP, int NB>
+__device__ __forceinline__ void wide_half_with_care(RowState<DP> (&st)[NB], const u32x4 (&q)[NB][DP / 32],
+                                                    const WideTile<DP>& tile, int h, float c, int32_t t,
+                                                    const int32_t (&vis)[NB], uint32_t valid)
+{
+    f32x4 s[NB][2];
+    u32x4 ph[NB], pl[NB];
+    wide_scores<DP, NB>(s, q, tile, h);
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        mask_scores(s[b], t, vis[b], valid);
+        raise_base<DP>(st[b], max_over_groups(max_of(s[b])) * c);
+        weights_of<DP>(st[b], s[b], ph[b], pl[b], c);
+        add_nonfinite<DP>(
+            st[b], ph[b], pl[b], t, vis[b], valid,
+            [&](int x) { return reinterpret_cast<const uint16_t*>(&tile.v[(32 * h + x) * (DP / 8)]); },
+            [](int x, int d) { return ((d / 8) ^ wide_swizzle<DP>(x)) * 8 + d % 8; });
+    }
+    uint32_t v[8][DP / 32];
+    wide_values<DP>(v, tile, h);
+    take_nonfinite<DP>(v);
     add_v<DP, NB>(st, v, ph, pl);
 }
 
@@ -739,8 +812,6 @@ __device__ __forceinline__ void wide_piece(const AttendArgs& a, const AttendItem
     const int32_t end = busy ? visible_end(a, it, last) : 0; // the wave's rows see nothing from here on
 
     const bool flat = dim == DP && a.pool.page_size % (T / kAttendWaves) == 0;
-    bool care = false;
-  again:
 #pragma unroll
     for (int b = 0; b < NB; ++b) clear<DP>(st[b]);
     int32_t page = -1, rows = -1;
@@ -754,6 +825,7 @@ __device__ __forceinline__ void wide_piece(const AttendArgs& a, const AttendItem
         rows = row_at(it.t0 + T, page);
         page = page_at(it.t0 + 2 * T);
     }
+    constexpr uint64_t full = T == 64 ? ~0ull : (1ull << (T & 63)) - 1;
     // the loads of a tile are waited for one tile after they were issued; the barrier says both that every wave's share
     // has landed and that the other tile is free again
     auto one = [&](int32_t t, WideTile<DP>& now, WideTile<DP>& next) {
@@ -766,13 +838,8 @@ __device__ __forceinline__ void wide_piece(const AttendArgs& a, const AttendItem
         }
         rows = row_at(t + 2 * T, page);
         page = page_at(t + 3 * T);
-#pragma unroll 1
-        for (int h = 0; h < T / 32; ++h) {
-            const int32_t th = t + 32 * h;
-            if (th >= end) break;
-            const uint32_t half = uint32_t(seen >> (32 * h));
-            wide_half<DP, NB>(st, q, now, h, a.scale_log2, half != ~0u || th + 32 > all_see, th, vis, half, care);
-        }
+        if (t < end)
+            wide_tile<DP, NB>(st, q, now, a.scale_log2, seen != full || t + T > all_see, t, vis, seen);
     };
     // two tiles by name: with an index between them the reads of one would wait for the loads of the other
 #pragma unroll 1
@@ -784,9 +851,23 @@ __device__ __forceinline__ void wide_piece(const AttendArgs& a, const AttendItem
     bool finite = true;
 #pragma unroll
     for (int b = 0; b < NB; ++b) finite = finite && all_finite<DP>(st[b]);
-    if (__syncthreads_or(!finite) && !care) {
-        care = true;
-        goto again;
+    if (__syncthreads_or(!finite)) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b) clear<DP>(st[b]);
+#pragma unroll 1
+        for (int32_t t = it.t0; t < t1; t += T) {
+            rows = row_at(t, page_at(t));
+            valid = __ballot(rows >= 0);
+            __syncthreads();                               // the tile before is done with
+            wide_load<DP>(kh, vh, row_bytes, dim, flat, rows, valid, tile0);
+            __builtin_amdgcn_s_waitcnt(0);
+            __syncthreads();
+#pragma unroll 1
+            for (int h = 0; h < T / 32; ++h)
+                if (t + 32 * h < end)
+                    wide_half_with_care<DP, NB>(st, q, tile0, h, a.scale_log2, t + 32 * h, vis,
+                                                uint32_t(valid >> (32 * h)));
+        }
     }
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
