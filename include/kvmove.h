@@ -362,8 +362,8 @@ int kv_retrieve_chunks_cachegen(const kv_paged* paged, const kv_seq* seqs, const
 typedef struct {
     int32_t n;            /* sequences (rows of the table), at most 2^24 */
     int32_t max_len;      /* bound of lens; <= stride * page_size and <= 2^30 */
-    const int32_t* table; /* DEVICE int32[n][stride]: page id of tokens [P*i, P*(i+1)); only the entries of the
-                             first lens tokens are read */
+    const int32_t* table; /* DEVICE int32[n][stride]: page id of tokens [P*i, P*(i+1)); entries past lens may hold
+                             anything */
     int64_t stride;       /* entries of a row */
     const int32_t* lens;  /* DEVICE int32[n]: tokens cached */
 } kv_tables;

@@ -244,27 +244,33 @@ int attend_shape(const kv_paged* p, const kv_step* s, int32_t q_heads, AttendSha
     const int64_t wide_rows = kAttendWaves * 16 * a.blocks;
     const int64_t pt = ceil_div(pr, a.prefix_wide ? wide_rows : kAttendRows);
     const int64_t ot = ceil_div(orows, a.own_wide ? wide_rows : kAttendRows);
-    if (pt > INT32_MAX || ot > INT32_MAX) return fail(KV_EINVAL, "too many rows for one launch");
+    const int64_t most = max_blocks(kAttendBlock);
+    if (pt > most || ot > most || s->prefix.n * heads > most || s->own.n * heads > most ||
+        s->prefix.n * heads * pt > most || s->own.n * heads * ot > most)
+        return fail(KV_EINVAL, "too many row tiles for one launch");
     a.prefix_tiles = int32_t(pt);
     a.own_tiles = int32_t(ot);
     const int64_t pre = s->prefix.n * heads * pt, own = s->own.n * heads * ot;
     // Two workgroups fit a CU, so 512 pieces run at once: fewer leave CUs idle, more cost a round of set-up and twice the
     // pieces to join (one 10000-token sequence: 18.6 us, with 1024 pieces 23.9).  A wide prefix beside narrow own pieces
-    // takes 256, one a CU: it waits for the matrix cores, they for memory, and each CU then holds both (64 sequences
-    // behind two 32768-token prefixes: 205 us, with 512 pieces 232) -- unless the own tokens are few beside it, a token
-    // of a narrow piece costing what one of a wide tile does.
-    const int64_t full = 512;
-    const int64_t prefix_work = s->prefix.n * pt * (s->prefix.n > 0 ? s->prefix.max_len : 0);
-    const int64_t own_work = int64_t(s->own.n) * s->own.max_len;
-    const bool beside = a.prefix_wide && !a.own_wide && 2 * own_work >= prefix_work;
-    cut_tokens(pre, s->prefix.n > 0 ? s->prefix.max_len : 0, beside ? full / 2 : full, &a.prefix_tokens,
-               &a.prefix_pieces);
-    cut_tokens(own, s->own.n > 0 ? s->own.max_len : 0, full, &a.own_tokens, &a.own_pieces);
+    // takes its share of them, so that its pieces, which start first, last as long as the own ones take on the rest of
+    // the GPU: the ones wait for the matrix cores, the others for memory.  A token of a narrow piece costs what one of a
+    // wide tile does; the own lengths are taken to be a little over half their bound.  (32 sequences behind an
+    // 8192-token prefix: 46 us, with 256 wide pieces 52, with 512 63; 64 behind two 32768-token ones: 201, 213, 220.)  The
+    // own pieces are then cut once more, as sequences of different lengths end at different times (24 ragged ones: 109 us,
+    // not cut 121).
+    const int64_t room = 512;
+    const int64_t prefix_work = pre * s->prefix.max_len, own_work = own * s->own.max_len * 6 / 10;
+    const bool beside = a.prefix_wide && !a.own_wide && prefix_work > 0 && own_work > 0;
+    const int64_t wide_room =
+        beside ? std::max<int64_t>(room / 8, int64_t(double(room) * prefix_work / (double(prefix_work) + own_work)))
+               : room;
+    cut_tokens(pre, s->prefix.n > 0 ? s->prefix.max_len : 0, wide_room, &a.prefix_tokens, &a.prefix_pieces);
+    cut_tokens(own, s->own.n > 0 ? s->own.max_len : 0, beside ? 2 * room : room, &a.own_tokens, &a.own_pieces);
     a.own_pieces = std::max(1, a.own_pieces);
     a.slots = a.prefix_pieces + a.own_pieces;
     a.direct = a.slots == 1;
-    const int64_t most = max_blocks(kAttendBlock) - 16;
-    if (pre > most || own > most || pre * a.prefix_pieces + own * a.own_pieces > most)
+    if (pre * a.prefix_pieces + own * a.own_pieces > most)
         return fail(KV_EINVAL, "too many row tiles and pieces for one launch");
     a.prefix_items = pre * a.prefix_pieces;
     a.own_items = own * a.own_pieces;
