@@ -377,7 +377,7 @@ int attend(const kv_paged* paged, const kv_step* step, int32_t layer, const kv_r
 template <int DP>
 KernelFn weights_kernel(bool rows, int32_t* tokens, int* block)
 {
-    *tokens = rows ? kRowsTokens<DP> : kWeightsTokens;
+    *tokens = rows ? kRowsTokens : kWeightsTokens;
     *block = rows ? kRowsWaves * 64 : kAttendBlock;
     return rows ? reinterpret_cast<KernelFn>(&add_weights_rows<DP>) : reinterpret_cast<KernelFn>(&add_weights<DP>);
 }

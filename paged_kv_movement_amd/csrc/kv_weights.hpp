@@ -42,17 +42,16 @@ struct WeightsArgs {
     uint32_t prefix_items;
 };
 
-// Tiles of 16 tokens a wave holds: two with few rows, for more waves in
-// flight; four where many rows pass by, so that a row's q serves more products.
-constexpr int kWeightsTiles = 2;
+constexpr int kWeightsTiles = 2;                                        // tiles of 16 tokens a wave holds
 constexpr int kWeightsTokens = 16 * kWeightsTiles * kAttendWaves;       // of a workgroup
-template <int DP>
-constexpr int kRowsTiles = DP <= 128 ? 4 : 2;
+// add_weights_rows: groups of tokens by shares of the rows, and the rows whose
+// q is in LDS at a time.  Two tiles a wave and short stages leave room for two
+// workgroups a CU, which counts for more than a q read by fewer of them (four
+// prompts of 1100 to 1300 tokens: 90 us, with four tiles and 128 rows 97).
 constexpr int kRowsGroups = 2, kRowsShares = 4, kRowsWaves = kRowsGroups * kRowsShares;
-template <int DP>
-constexpr int kRowsTokens = 16 * kRowsTiles<DP> * kRowsGroups;
-template <int DP>
-constexpr int kStageRows = DP <= 128 ? 128 : 64;                        // rows whose q is in LDS at a time
+constexpr int kRowsTokens = 16 * kWeightsTiles * kRowsGroups;
+constexpr int kStageRows = 64;
+constexpr int kStageBlocks = kStageRows / 16 / kRowsShares;             // blocks of 16 rows of a wave in a stage
 
 struct WeightsPiece {
     uint64_t kh;                   // this KV head's K pool
@@ -67,8 +66,8 @@ template <int DP>
 struct WeightsColumn {
     u32x4 q[DP / 32];
     float lse;
-    int32_t vis;
-    bool live;
+    int32_t f;             // flattened row
+    bool live;             // else it repeats the last one and adds nothing
 };
 
 // No load stands behind a branch, so that the compiler counts which of them a
@@ -81,7 +80,7 @@ __device__ __forceinline__ void load_column(const WeightsArgs& a, const WeightsP
     const int32_t n = w.count * a.rep, f = x * 16 + r < n ? x * 16 + r : n - 1;
     const int32_t i = new_token(a, f), head = w.h * a.rep + (f - i * a.rep);
     const int64_t qr = w.first_row + i;
-    c.vis = w.prefix ? w.len : clamp_i32(w.len - w.count + i + 1, 0, w.len);
+    c.f = f;
     c.live = x * 16 + r < n;
     c.lse = gptr<const gf32>(a.lse)[qr * a.q_heads + head];
     load_row<DP>(c.q, a.q + (qr * a.q_row + head * a.q_head) * 2, g, dim);
@@ -108,12 +107,13 @@ __device__ __forceinline__ void add_block(const WeightsArgs& a, const WeightsPie
     const float neg = !c.live || c.lse == -__builtin_inff() ? -__builtin_inff() : -c.lse * kLog2e;
     // the block's first row sees the least
     if (!w.prefix && w.len - w.count + new_token(a, x * 16) + 1 < t + 16 * NT) {
+        const int32_t vis = w.len - w.count + new_token(a, c.f) + 1;
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
                 const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i][n], a.scale_log2, neg));
-                sum[i][n] += t + 16 * i + 4 * g + n < c.vis ? p : 0.0f;
+                sum[i][n] += t + 16 * i + 4 * g + n < vis ? p : 0.0f;
             }
     } else {
 #pragma unroll
@@ -143,22 +143,33 @@ __device__ __forceinline__ void load_keys(const WeightsArgs& a, const WeightsPie
         for (int i = 0; i < NT; ++i) clear_past<DP>(k[i], g, dim);
 }
 
-// The sums over the 16 columns, token y's to part[y].
+// The sums over the 16 columns, token y's to part[y].  Each step adds across a
+// distance and halves what a lane still holds: 4 NT - 1 exchanges, not 16 NT.
 template <int NT>
 __device__ __forceinline__ void fold_columns(const f32x4 (&sum)[NT], float* part)
 {
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+    float v[4 * NT];
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
+    for (int x = 0; x < 4 * NT; ++x) v[x] = sum[x / 4][x % 4];
+    int which = 0;                       // the value that this lane ends with
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-            float v = sum[i][n];
-            v += __shfl_xor(v, 1);
-            v += __shfl_xor(v, 2);
-            v += __shfl_xor(v, 4);
-            v += __shfl_xor(v, 8);
-            if (r == 0) part[16 * i + 4 * g + n] = v;
+    for (int n = 4 * NT, d = 8; d > 0; d /= 2) {
+        const bool up = (r & d) != 0;
+        if (n > 1) {
+            n /= 2;
+#pragma unroll
+            for (int x = 0; x < n; ++x) {
+                const float mine = up ? v[x + n] : v[x], other = up ? v[x] : v[x + n];
+                v[x] = mine + __shfl_xor(other, d);
+            }
+            which += up ? n : 0;
+        } else {
+            v[0] += __shfl_xor(v[0], d);
         }
+    }
+    const bool first = (4 * NT == 16) || (r & 1) == 0;
+    if (first) part[16 * (which / 4) + 4 * g + which % 4] = v[0];
 }
 
 // Few rows: each wave has its own tokens [t, t + 16 NT), one group of them:
@@ -269,47 +280,81 @@ __global__ __launch_bounds__(kAttendBlock, DP > 128 ? 2 : 4) void add_weights(We
     weights_by_tokens<DP>(a, w, __builtin_amdgcn_readfirstlane(t), page, old, pool_ok, part);
 }
 
-// q of kStageRows rows from flattened row f0 into LDS, this wave's share.  A
-// row's vectors are at chunk ^ wide_swizzle(row), as in the attention's tiles;
-// rows past the last one repeat it, elements past dim are 0.
+// Where a lane's share of a stage is in memory: the q vectors that it brings
+// into LDS (a row's at chunk ^ wide_swizzle(row), as in the attention's tiles;
+// rows past the last one repeat it, elements past dim are 0) and the lse of
+// its columns.  Where a stage holds whole tokens, the next stage's addresses
+// follow by a step; they are worked out anew for the last stage, and
+// everywhere for other numbers of heads.
 template <int DP>
-__device__ __forceinline__ void load_stage(const WeightsArgs& a, const WeightsPiece& w, int32_t f0, u32x4* stage)
-{
-    constexpr int V = DP / 8, kPer = 64 / V, kLoads = kStageRows<DP> / kPer / kRowsWaves;
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int32_t n = w.count * a.rep;
-    const uint64_t zero = reinterpret_cast<uint64_t>(&g_zero_vector);
+struct StageCursor {
+    static constexpr int V = DP / 8, kPer = 64 / V, kLoads = kStageRows / kPer / kRowsWaves;
+    static constexpr int Y = kStageBlocks;
+    uint64_t q[kLoads], lse[Y];
+
+    __device__ __forceinline__ void place(const WeightsArgs& a, const WeightsPiece& w, int32_t f0)
+    {
+        const int lane = anew(threadIdx.x & 63), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        const int32_t n = w.count * a.rep;
+        const uint64_t zero = reinterpret_cast<uint64_t>(&g_zero_vector);
 #pragma unroll
-    for (int x = 0; x < kLoads; ++x) {
-        const int first = (wave * kLoads + x) * kPer, y = first + lane / V;
-        const int chunk = lane % V ^ wide_swizzle<DP>(y);
-        const int32_t f = f0 + y < n ? f0 + y : n - 1;
-        const int32_t i = new_token(a, f), head = w.h * a.rep + (f - i * a.rep);
-        const uint64_t at = a.q + (int64_t(w.first_row + i) * a.q_row + head * a.q_head) * 2 + chunk * 16;
-        __builtin_amdgcn_global_load_lds(gptr<const gvec4>(chunk * 8 < int(a.pool.dim) ? at : zero),
-                                         (__attribute__((address_space(3))) void*)&stage[first * V], 16, 0, 0);
+        for (int x = 0; x < kLoads; ++x) {
+            const int y = (wave * kLoads + x) * kPer + lane / V;
+            const int chunk = lane % V ^ wide_swizzle<DP>(y);
+            const int32_t f = f0 + y < n ? f0 + y : n - 1;
+            const int32_t i = new_token(a, f), head = w.h * a.rep + (f - i * a.rep);
+            const uint64_t at = a.q + (int64_t(w.first_row + i) * a.q_row + head * a.q_head) * 2 + chunk * 16;
+            q[x] = chunk * 8 < int(a.pool.dim) ? at : zero;
+        }
+#pragma unroll
+        for (int y = 0; y < Y; ++y) {
+            const int32_t g = f0 + (y * kRowsShares + wave % kRowsShares) * 16 + lane % 16, f = g < n ? g : n - 1;
+            const int32_t i = new_token(a, f);
+            lse[y] = a.lse + (int64_t(w.first_row + i) * a.q_heads + w.h * a.rep + (f - i * a.rep)) * 4;
+        }
     }
-}
+
+    // The stage from flattened row f0 on, and the cursor to the next one.
+    __device__ __forceinline__ void load(const WeightsArgs& a, const WeightsPiece& w, int32_t f0, bool steps,
+                                         u32x4* stage, float (&to)[Y])
+    {
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        if (!steps || f0 + kStageRows > w.count * a.rep) place(a, w, f0);
+        const int64_t tokens = kStageRows / a.rep;
+#pragma unroll
+        for (int y = 0; y < Y; ++y) {
+            to[y] = *gptr<const gf32>(lse[y]);
+            lse[y] += tokens * a.q_heads * 4;
+        }
+#pragma unroll
+        for (int x = 0; x < kLoads; ++x) {
+            __builtin_amdgcn_global_load_lds(gptr<const gvec4>(q[x]),
+                                             (__attribute__((address_space(3))) void*)&stage[(wave * kLoads + x) * 64],
+                                             16, 0, 0);
+            q[x] += tokens * a.q_row * 2;
+        }
+    }
+};
 
 // The blocks of rows that this wave has in a stage.
 template <int DP>
 __device__ __forceinline__ void add_stage(const WeightsArgs& a, const WeightsPiece& w, int32_t f0, int32_t t,
-                                          const u32x4* stage, const float (&lse)[kStageRows<DP> / 64],
-                                          const u32x4 (&k)[kRowsTiles<DP>][DP / 32], f32x4 (&sum)[kRowsTiles<DP>])
+                                          const u32x4* stage, const float (&lse)[kStageBlocks],
+                                          const u32x4 (&k)[kWeightsTiles][DP / 32], f32x4 (&sum)[kWeightsTiles])
 {
-    constexpr int V = DP / 8, NT = kRowsTiles<DP>;
+    constexpr int V = DP / 8, NT = kWeightsTiles;
     const int lane = threadIdx.x & 63, share = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % kRowsShares,
               r = lane & 15, g = lane >> 4;
     const int32_t n = w.count * a.rep;
-#pragma unroll 1
-    for (int y = 0; y < kStageRows<DP> / 64; ++y) {
+#pragma unroll
+    for (int y = 0; y < kStageBlocks; ++y) {
         const int block = y * kRowsShares + share;
         const int32_t f = f0 + block * 16 + r;
         if (f0 + block * 16 >= n) break;
         WeightsColumn<DP> c;
         c.live = f < n;
-        c.vis = w.prefix ? w.len : clamp_i32(w.len - w.count + new_token(a, c.live ? f : n - 1) + 1, 0, w.len);
-        c.lse = y == 0 ? lse[0] : lse[kStageRows<DP> / 64 - 1];
+        c.f = c.live ? f : n - 1;
+        c.lse = lse[y];
 #pragma unroll
         for (int j = 0; j < DP / 32; ++j)
             c.q[j] = stage[(block * 16 + r) * V + ((4 * j + g) ^ wide_swizzle<DP>(r))];
@@ -318,16 +363,16 @@ __device__ __forceinline__ void add_stage(const WeightsArgs& a, const WeightsPie
 }
 
 template <int DP>
-__global__ __launch_bounds__(kRowsWaves * 64, 2) void add_weights_rows(WeightsArgs a)
+__global__ __launch_bounds__(kRowsWaves * 64, DP > 128 ? 2 : 4) void add_weights_rows(WeightsArgs a)
 {
-    constexpr int NT = kRowsTiles<DP>, V = DP / 8, S = kStageRows<DP>, Y = S / 64;
+    constexpr int NT = kWeightsTiles, V = DP / 8, S = kStageRows;
     __shared__ u32x4 stage0[S * V];
     __shared__ u32x4 stage1[S * V];
     __shared__ float part[kRowsWaves][64];
-    const WeightsItem it = weights_item<true>(a, blockIdx.x, kRowsTokens<DP>);
+    const WeightsItem it = weights_item<true>(a, blockIdx.x, kRowsTokens);
     const TablesArg& tab = it.prefix ? a.step.prefix : a.step.own;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6),
-              share = wave % kRowsShares, r = lane & 15;
+              share = wave % kRowsShares;
     const uint64_t kb = wave_uniform(gptr<const gu64>(a.pool.k_pages)[a.pool.layer]);
     const int32_t len = __builtin_amdgcn_readfirstlane(table_len(tab, it.table_row));
     const WeightsPiece w = weights_piece(a, it, kb, len);
@@ -345,36 +390,23 @@ __global__ __launch_bounds__(kRowsWaves * 64, 2) void add_weights_rows(WeightsAr
     // token t0 is first seen by new token t0 - (len - count): stages of rows before it see none of these tokens
     const int32_t before = w.prefix ? 0 : it.t0 - (len - w.count), n = pool_ok ? w.count * a.rep : 0;
     int32_t f0 = before > 0 ? before * a.rep / S * S : 0;
-    // the lse of this lane's rows of a stage, asked for when its q is
-    auto load_lse = [&](int32_t f0, float (&lse)[Y]) {
-#pragma unroll
-        for (int y = 0; y < Y; ++y) {
-            const int32_t f = f0 + (y * kRowsShares + share) * 16 + r, g = f < n ? f : n - 1;
-            const int32_t i = new_token(a, g);
-            lse[y] = gptr<const gf32>(a.lse)[int64_t(w.first_row + i) * a.q_heads + w.h * a.rep + (g - i * a.rep)];
-        }
-    };
-    float lse0[Y], lse1[Y];
+    const bool steps = S % a.rep == 0 && int(a.pool.dim) == DP;
+    StageCursor<DP> cursor;
+    float lse0[kStageBlocks], lse1[kStageBlocks];
     if (f0 < n) {
-        load_lse(f0, lse0);
-        load_stage<DP>(a, w, f0, stage0);
+        cursor.place(a, w, f0);
+        cursor.load(a, w, f0, steps, stage0, lse0);
     }
 #pragma unroll 1
     for (; f0 < n; f0 += 2 * S) {
         __builtin_amdgcn_s_waitcnt(0);
         __syncthreads();
-        if (f0 + S < n) {
-            load_lse(f0 + S, lse1);
-            load_stage<DP>(a, w, f0 + S, stage1);
-        }
+        if (f0 + S < n) cursor.load(a, w, f0 + S, steps, stage1, lse1);
         add_stage<DP>(a, w, f0, t, stage0, lse0, k, sum);
         if (f0 + S >= n) break;
         __builtin_amdgcn_s_waitcnt(0);
         __syncthreads();
-        if (f0 + 2 * S < n) {
-            load_lse(f0 + 2 * S, lse0);
-            load_stage<DP>(a, w, f0 + 2 * S, stage0);
-        }
+        if (f0 + 2 * S < n) cursor.load(a, w, f0 + 2 * S, steps, stage0, lse0);
         add_stage<DP>(a, w, f0 + S, t, stage1, lse1, k, sum);
     }
     fold_columns<NT>(sum, part[wave]);
