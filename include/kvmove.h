@@ -357,8 +357,9 @@ int kv_retrieve_chunks_cachegen(const kv_paged* paged, const kv_seq* seqs, const
  * A page id outside the pool leaves its tokens out (not written, not seen)
  * and sets fault bit 1.  Limits: num_pages * page_size < 2^31; attention and
  * weights need head_dim % 8 == 0 and head_dim <= 256.  Every call works on
- * the current device; workspaces are DEVICE memory, 256-byte aligned, whose
- * contents on entry do not matter, and calls that share one must be ordered. */
+ * the current device, where its stream must be; workspaces are DEVICE memory,
+ * 256-byte aligned, whose contents on entry do not matter, and calls that
+ * share one must be ordered. */
 typedef struct {
     int32_t n;            /* sequences (rows of the table), at most 2^24 */
     int32_t max_len;      /* bound of lens; <= stride * page_size and <= 2^30 */
@@ -435,7 +436,7 @@ int kv_append(const kv_paged* paged, const kv_step* step, int32_t layer, const k
  * out 0 and lse -infinity; rows of no sequence are left as they were.  What a
  * row does not see never reaches it, NaN and infinities included.  A group's
  * prefix is read once for all its sequences.  scale > 0; q needs 16-byte
- * aligned address and strides, out 8-byte aligned ones.
+ * aligned address and strides, out 8-byte aligned ones; out must not overlap q.
  * kv_attend_workspace_bytes depends on the bounds only; 0 on a malformed
  * argument. */
 size_t kv_attend_workspace_bytes(const kv_paged* paged, const kv_step* step, int32_t q_heads);
@@ -446,10 +447,11 @@ int kv_attend(const kv_paged* paged, const kv_step* step, int32_t layer, const k
 /* Add to every cached token's sum the attention weight that the new tokens
  * give it: sums->out[s][h][t] = in[s][h][t] + sum over the rows that see token
  * t and the query heads of KV head h of exp(scale * q.k_t - lse[row]), with
- * the lse of kv_attend (a row whose lse is -infinity adds nothing).  prefix:
- * the same per group over all its sequences' rows.  Either may be NULL: then
- * those sums are not computed.  Entries at and past lens are left as they
- * were.  No atomics: the same call gives the same bits. */
+ * the lse of kv_attend (a row whose lse is -infinity adds nothing where its
+ * scores are numbers).  prefix: the same per group over all its sequences'
+ * rows.  Either may be NULL: then those sums are not computed.  Entries at and
+ * past lens are left as they were.  No atomics: the same call gives the same
+ * bits. */
 int kv_add_weights(const kv_paged* paged, const kv_step* step, int32_t layer, const kv_rows* q, const float* lse,
                    int32_t q_heads, float scale, const kv_sums* own, const kv_sums* prefix, hipStream_t stream);
 

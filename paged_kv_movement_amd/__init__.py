@@ -762,7 +762,8 @@ class Step:
         row, head, last = t.stride()
         if last != 1 and self._dim != 1:
             raise KvError(KV_EINVAL, f"{what}: the last dimension must be contiguous")
-        return _KvRows(t.data_ptr(), row, head)
+        # the stride of a dimension of one is never used, and torch may give any
+        return _KvRows(t.data_ptr(), row if self.n_rows > 1 else 0, head if heads > 1 else 0)
 
     def _call(self, paged, stream, *tensors) -> int | None:
         """Checks of every call; the handle of its stream (None: the current one)."""
@@ -838,6 +839,17 @@ class Rope:
 _type_codes = None
 
 
+def _empty(shape, dtype, device, stream):
+    """A new device tensor for a call on ``stream``, allocated for that stream
+    (the caching allocator then orders its memory's earlier use before it)."""
+    if stream is None:
+        return _t().empty(shape, dtype=dtype, device=device)
+    if not hasattr(stream, "cuda_stream"):
+        raise KvError(KV_EINVAL, "a call on a raw stream handle needs its outputs and workspace given")
+    with _t().cuda.stream(stream):
+        return _t().empty(shape, dtype=dtype, device=device)
+
+
 def _types():
     global _type_codes
     if _type_codes is None:
@@ -883,7 +895,7 @@ def append(paged: Paged, step: Step, layer: int, q, k, v, positions, rope: Rope,
         q_heads = q.shape[1]
         cq = st._rows(q, q_heads, "q", types)
         if q_out is None:
-            q_out = torch.empty((st.n_rows, q_heads, paged.head_dim), dtype=q.dtype, device=q.device)
+            q_out = _empty((st.n_rows, q_heads, paged.head_dim), q.dtype, q.device, stream)
         co = st._rows(q_out, q_heads, "q_out", (q.dtype, torch.bfloat16))
         out_type = types[q_out.dtype]
     else:
@@ -919,14 +931,14 @@ def attend(paged: Paged, step: Step, layer: int, q, scale=None, out=None, lse=No
     torch = _t()
     cq, heads = _q(paged, step, q)
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out = _empty(q.shape, q.dtype, q.device, stream)
     if lse is None:
-        lse = torch.empty((step.n_rows, heads), dtype=torch.float32, device=q.device)
+        lse = _empty((step.n_rows, heads), torch.float32, q.device, stream)
     co = step._rows(out, heads, "out", (torch.bfloat16,))
     if lse.dtype != torch.float32 or not lse.is_contiguous() or lse.shape != (step.n_rows, heads):
         raise KvError(KV_EINVAL, f"lse must be a contiguous float32 device tensor [{step.n_rows}, {heads}]")
     if workspace is None:
-        workspace = step.new_attend_workspace(heads)
+        workspace = _empty(step.attend_workspace_bytes(heads), torch.uint8, q.device, stream)
     ws, n_ws = _workspace(workspace)
     h = step._call(paged, stream, q, out, lse, workspace)
     rc = load().kv_attend(ctypes.byref(paged.c), step._ref, layer, ctypes.byref(cq), heads, _scale(paged, scale),
@@ -991,11 +1003,12 @@ def evict(paged: Paged, tables: Tables, layer_begin: int, layer_end: int, weight
         co = _slots(out_weights, out_positions, shape, "evict: out")
     tables._check(paged)
     if out_lens is None:
-        out_lens = torch.empty((tables.n,), dtype=torch.int32, device=tables.table.device)
+        out_lens = _empty((tables.n,), torch.int32, tables.table.device, stream)
     if out_lens.dtype != torch.int32 or not out_lens.is_contiguous() or out_lens.shape != (tables.n,):
         raise KvError(KV_EINVAL, f"out_lens must be a contiguous int32 device tensor [{tables.n}]")
     if workspace is None:
-        workspace = tables.new_evict_workspace(paged, shape[0], ci.heads, keep)
+        workspace = _empty(tables.evict_workspace_bytes(paged, shape[0], ci.heads, keep), torch.uint8,
+                           tables.table.device, stream)
     ws, n_ws = _workspace(workspace)
     used = (paged.k_addrs, paged.v_addrs, tables.table, tables.lens, weights, positions, out_weights, out_positions,
             out_lens, workspace)

@@ -935,8 +935,8 @@ __device__ __forceinline__ RowPieces row_pieces(const AttendArgs& a, int32_t r)
     const RowOwner o = row_owner(st, r);
     if (o.s < 0) return {0, -1};
     int32_t prefix = 0;
-    for (int32_t i0 = 0; i0 < st.prefix.n; i0 += 64) {
-        const int32_t i = i0 + lane;
+    if (st.prefix.n > 0) {
+        const int32_t i0 = ranges_around(st.group_start, st.prefix.n, o.s), i = i0 + lane;
         int32_t b = 0, e = 0, n = 0;
         if (i < st.prefix.n) {
             b = gptr<const gi32>(st.group_start)[i];
@@ -944,14 +944,14 @@ __device__ __forceinline__ RowPieces row_pieces(const AttendArgs& a, int32_t r)
             n = table_len(st.prefix, i);
         }
         const uint64_t m = __ballot(b <= o.s && o.s < e);
-        if (m == 0) continue;
-        const int j = __builtin_ctzll(m);
-        prefix = __builtin_amdgcn_readlane(n, j);
-        if (st.max_group_rows < st.n_rows) {                   // else no group can be cut
-            const Rows gr = group_rows(st, i0 + j);
-            if (r - gr.first >= gr.count) prefix = 0;
+        if (m != 0) {
+            const int j = __builtin_ctzll(m);
+            prefix = __builtin_amdgcn_readlane(n, j);
+            if (st.max_group_rows < st.n_rows) {               // else no group can be cut
+                const Rows gr = group_rows(st, i0 + j);
+                if (r - gr.first >= gr.count) prefix = 0;
+            }
         }
-        break;
     }
     const int32_t own = clamp_i32(o.len - o.count + (r - o.first) + 1, 0, o.len);
     return {int32_t((uint32_t(prefix) + a.prefix_tokens - 1) / uint32_t(a.prefix_tokens)),

@@ -174,8 +174,8 @@ __global__ __launch_bounds__(kSelectBlock) void evict_select(EvictArgs a)
     const int32_t n = table_len(a.tab, s), keep = a.keep;
     if (tid == 0 && job / a.heads < a.tab.n && job % a.heads == 0)
         gptr<gi32>(a.out_lens)[s] = n < keep ? n : keep;
-    if (n <= keep) {
-        if (!in_place)
+    if (n <= keep || keep == 0) {              // all stay, or none
+        if (!in_place && keep > 0)
             for (int32_t i = tid; i < n; i += kSelectBlock) {
                 ow[i] = w[i];
                 op[i] = p[i];

@@ -82,8 +82,27 @@ __device__ __forceinline__ uint32_t page_of(const PoolArg& p, uint32_t t)
     return uint32_t((uint64_t(t) * p.page_magic) >> p.page_shift);
 }
 
-// The sequence that new-token row r belongs to, from one round of loads for up
-// to 64 sequences (lane i holds the i-th; the row's own is taken from the lane
+// First of the 64 neighbouring ranges [starts[i], starts[i + 1]), i < n, one of
+// which holds x if any does.  Every round of loads leaves a 64th of them: none
+// for up to 64 ranges, one for up to 4096.
+__device__ __forceinline__ int32_t ranges_around(uint64_t starts, int32_t n, int32_t x)
+{
+    const int32_t lane = threadIdx.x & 63;
+    int32_t lo = 0, span = n;
+    while (span > 64) {
+        const int32_t step = (span + 63) / 64, i = lane * step;
+        const int32_t b = gptr<const gi32>(starts)[lo + (i < span ? i : 0)];
+        const uint64_t m = __ballot(i < span && b <= x);
+        if (m == 0) break;
+        const int32_t at = (63 - __builtin_clzll(m)) * step;
+        lo += at;
+        span = span - at < step ? span - at : step;
+    }
+    return lo;
+}
+
+// The sequence that new-token row r belongs to, from one round of loads after
+// ranges_around (lane i holds the i-th; the row's own is taken from the lane
 // that holds it).  s < 0: none.
 struct RowOwner {
     int32_t s, first, count, len;
@@ -91,28 +110,24 @@ struct RowOwner {
 
 __device__ __forceinline__ RowOwner row_owner(const StepArg& a, int32_t r)
 {
-    const int32_t lane = threadIdx.x & 63;
-    for (int32_t i0 = 0; i0 < a.own.n; i0 += 64) {
-        const int32_t i = i0 + lane;
-        int32_t b = 0, e = 0, n = 0;
-        if (i < a.own.n) {
-            b = gptr<const gi32>(a.q_start)[i];
-            e = gptr<const gi32>(a.q_start)[i + 1];
-            n = table_len(a.own, i);
-        }
-        const uint64_t m = __ballot(b <= r && r < e);
-        if (m == 0) continue;
-        const int j = __builtin_ctzll(m);
-        RowOwner o;
-        o.s = i0 + j;
-        o.first = clamp_i32(__builtin_amdgcn_readlane(b, j), 0, a.n_rows);
-        o.count = clamp_i32(__builtin_amdgcn_readlane(e, j), o.first, a.n_rows) - o.first;
-        o.count = o.count < a.max_new ? o.count : a.max_new;
-        o.len = __builtin_amdgcn_readlane(n, j);
-        if (r - o.first >= o.count) o.s = -1;
-        return o;
+    const int32_t i0 = ranges_around(a.q_start, a.own.n, r), i = i0 + int32_t(threadIdx.x & 63);
+    int32_t b = 0, e = 0, n = 0;
+    if (i < a.own.n) {
+        b = gptr<const gi32>(a.q_start)[i];
+        e = gptr<const gi32>(a.q_start)[i + 1];
+        n = table_len(a.own, i);
     }
-    return {-1, 0, 0, 0};
+    const uint64_t m = __ballot(b <= r && r < e);
+    if (m == 0) return {-1, 0, 0, 0};
+    const int j = __builtin_ctzll(m);
+    RowOwner o;
+    o.s = i0 + j;
+    o.first = clamp_i32(__builtin_amdgcn_readlane(b, j), 0, a.n_rows);
+    o.count = clamp_i32(__builtin_amdgcn_readlane(e, j), o.first, a.n_rows) - o.first;
+    o.count = o.count < a.max_new ? o.count : a.max_new;
+    o.len = __builtin_amdgcn_readlane(n, j);
+    if (r - o.first >= o.count) o.s = -1;
+    return o;
 }
 
 __device__ __forceinline__ void raise_fault_lane(unsigned bit) { atomicOr(&g_kv_faults, bit); }

@@ -49,6 +49,18 @@ int check_step(const kv_paged* p, const kv_step* s)
     return KV_OK;
 }
 
+// The calls launch on the current device, and so must their stream.
+int check_stream(hipStream_t stream)
+{
+    if (stream == nullptr) return KV_OK;
+    int dev = -1, sdev = -1;
+    hipError_t e = hipGetDevice(&dev);
+    if (e == hipSuccess) e = hipStreamGetDevice(stream, &sdev);
+    if (e != hipSuccess) return fail(KV_EHIP, "reading the device failed: %s", hipGetErrorString(e));
+    if (sdev != dev) return fail(KV_EINVAL, "the stream belongs to device %d, the current device is %d", sdev, dev);
+    return KV_OK;
+}
+
 bool misaligned(const void* p, uintptr_t to) { return reinterpret_cast<uintptr_t>(p) % to != 0; }
 
 // [n_rows][heads][dim] with strides in elements of `size` bytes: vectors of
@@ -154,6 +166,8 @@ int append(const kv_paged* paged, const kv_step* step, int32_t layer, const kv_r
     for (const kv_rows* x : {k, v, q})
         if (x != nullptr && misaligned(x->data, size)) return fail(KV_EINVAL, "q, k or v is not aligned to its type");
     if (q != nullptr && misaligned(q_out->data, out_size)) return fail(KV_EINVAL, "q_out is not aligned to its type");
+    rc = check_stream(stream);
+    if (rc != KV_OK) return rc;
     AppendArgs a{};
     a.pool = pool_arg(paged, layer);
     a.step = step_arg(step);
@@ -330,6 +344,9 @@ int attend(const kv_paged* paged, const kv_step* step, int32_t layer, const kv_r
     if (workspace == nullptr || workspace_bytes < size_t(sh.bytes) || misaligned(workspace, 256))
         return fail(KV_EINVAL, "workspace of %lld bytes, 256-byte aligned, needed (got %zu at %p)",
                     (long long)sh.bytes, workspace_bytes, workspace);
+    if (out->data == q->data) return fail(KV_EINVAL, "out must not be q");
+    rc = check_stream(stream);
+    if (rc != KV_OK) return rc;
     AttendArgs a{};
     a.pool = pool_arg(paged, layer);
     a.step = step_arg(step);
@@ -399,6 +416,8 @@ int add_weights_call(const kv_paged* paged, const kv_step* step, int32_t layer, 
         if (rc != KV_OK) return rc;
         if (lse == nullptr) return fail(KV_EINVAL, "lse is NULL");
     }
+    rc = check_stream(stream);
+    if (rc != KV_OK) return rc;
     WeightsArgs a{};
     a.pool = pool_arg(paged, layer);
     a.step = step_arg(step);
@@ -414,6 +433,7 @@ int add_weights_call(const kv_paged* paged, const kv_step* step, int32_t layer, 
     a.scale_log2 = float(double(scale) * 1.4426950408889634);
     // many rows: the waves share a workgroup's tokens and split the rows
     const int64_t rows = std::max(own != nullptr ? step->max_new : 0, prefix != nullptr ? step->max_group_rows : 0);
+    if (rows * a.rep > INT32_MAX - 2 * kStageRows) return fail(KV_EINVAL, "too many rows for one launch");
     const bool split = rows * a.rep > 256;
     const int dim = paged->head_dim;
     int32_t tokens = 0;
@@ -501,6 +521,8 @@ int evict(const kv_paged* paged, const kv_tables* tables, int32_t layer_begin, i
     if (workspace == nullptr || workspace_bytes < size_t(sh.bytes) || misaligned(workspace, 256))
         return fail(KV_EINVAL, "workspace of %lld bytes, 256-byte aligned, needed (got %zu at %p)",
                     (long long)sh.bytes, workspace_bytes, workspace);
+    rc = check_stream(stream);
+    if (rc != KV_OK) return rc;
     EvictArgs a{};
     a.pool = pool_arg(paged, layer_begin);
     a.tab = tables_arg(tables);

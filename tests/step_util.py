@@ -39,6 +39,7 @@ class Batch:
         self.q_start = [0]
         for m in self.new:
             self.q_start.append(self.q_start[-1] + m)
+        self.groups = [g for g, n in enumerate(self.sizes) for _ in range(n)]
 
     def flat(self):
         return self.pool.view(self.layers, 2, -1, self.heads, self.dim)
@@ -51,12 +52,7 @@ class Batch:
         return (torch.randn(shape, generator=self.g) * gain).to(dtype)
 
     def group(self, s):
-        at = 0
-        for g, n in enumerate(self.sizes):
-            if at <= s < at + n:
-                return g
-            at += n
-        return None
+        return self.groups[s] if s < len(self.groups) else None
 
     def cached(self, which, s, layer=0):
         """64-bit K (0) or V (1) [tokens, heads, dim] that sequence s sees: prefix, then own."""
@@ -115,11 +111,14 @@ def weights64(b, q, lse, scale, own, prefix=None, layer=0):
     own, eo = own.double().clone(), torch.zeros_like(own, dtype=torch.float64)
     pre = prefix.double().clone() if prefix is not None else None
     ep = torch.zeros_like(pre) if pre is not None else None
+    group_new = [0] * len(b.sizes)
+    for g, m in zip(b.groups, b.new):
+        group_new[g] += m
     for s, (n, m) in enumerate(zip(b.lens, b.new)):
         k = b.cached(0, s, layer)
         np_ = k.shape[0] - n
         g = b.group(s)
-        count = m * rep if g is None else rep * sum(mm for x, mm in enumerate(b.new) if b.group(x) == g)
+        count = rep * (m if g is None else group_new[g])
         for i in range(m):
             r = b.q_start[s] + i
             see = np_ + max(0, n - m + i + 1)

@@ -151,6 +151,13 @@ ATTEND = [
     (1, 1, 128, 16, [20] * 70, [1] * 70, [90], [70]),                       # more sequences than a wave has lanes
     (2, 4, 128, 16, [12] * 20, [1] * 20, [2000, 900], [11, 9]),
     (1, 3, 128, 48, [600, 90], [300, 2], [1100], [2]),
+    (1, 4, 256, 16, [150, 9], [75, 9], [40], [2]),                          # many rows of the widest heads
+    (1, 5, 192, 32, [130], [60], [], []),
+    (1, 1, 64, 16, [1100, 20], [1100, 3], [130], [2]),                      # rows enough for a join by rows
+    (2, 1, 16, 16, [1, 40], [1030, 20], [70], [2]),                         # most rows see nothing of their own
+    (1, 2, 128, 16, [3, 3, 3], [1, 1, 1], [5, 0], [1, 1]),                  # an empty prefix, and a sequence of no group
+    (1, 2, 16, 4, [9, 5] * 100, [1, 2] * 100, [6, 11] * 35, [3, 2] * 35),   # more groups than a wave has lanes
+    (1, 1, 8, 1, [2, 0, 3] * 1400, [1, 1, 0] * 1400, [1] * 4200, [1] * 4200),   # more of both than 64 times its lanes
 ]
 
 
@@ -494,6 +501,55 @@ def test_step_captured_in_a_graph_follows_the_lengths():
     assert kvm.take_faults() == 0
 
 
+def test_rows_of_one_token_with_any_stride():
+    """Dimensions of one may have any stride: q of one row and one head cut out of odd places."""
+    b, q = _attend_case((1, 1, 64, 16, [30], [1], [], []))
+    pool, paged, step = device(b)
+    wide = torch.zeros((3, 5, 72), dtype=torch.bfloat16, device="cuda")
+    odd = wide.as_strided((1, 1, 64), (77, 13, 1), 0)
+    odd.copy_(q)
+    out, lse = kvm.attend(paged, step, 1, odd)
+    ref, ref_lse = kvm.attend(paged, step, 1, q.cuda())
+    assert torch.equal(out, ref) and torch.equal(lse, ref_lse)
+
+
+def test_python_refusals():
+    b, q = _attend_case((2, 2, 64, 16, [30, 17], [3, 2], [21], [1]))
+    pool, paged, step = device(b)
+    qd, lse = q.cuda(), torch.zeros((5, 4), device="cuda")
+    rope, pos = kvm.Rope(64), torch.zeros(5, dtype=torch.int32, device="cuda")
+    k = torch.zeros((5, 2, 64), dtype=torch.bfloat16, device="cuda")
+    raw = torch.cuda.current_stream().cuda_stream or 1
+    w = torch.zeros((2, 2, 30), device="cuda")
+    sp = torch.zeros((2, 2, 30), dtype=torch.int32, device="cuda")
+    for call in (lambda: kvm.attend(paged, step, 1, qd.float()), lambda: kvm.attend(paged, step, 1, qd[:4]),
+                 lambda: kvm.attend(paged, step, 1, qd[:, :3]), lambda: kvm.attend(paged, step, 2, qd),
+                 lambda: kvm.attend(paged, step, 1, qd, scale=0.0), lambda: kvm.attend(paged, step, 1, q),
+                 lambda: kvm.attend(paged, step, 1, qd.transpose(1, 2).contiguous().transpose(1, 2)),
+                 lambda: kvm.attend(paged, step, 1, qd, lse=lse.half()), lambda: kvm.attend(paged, step, 1, qd, stream=raw),
+                 lambda: kvm.attend(paged, step, 1, qd, workspace=torch.zeros(64, dtype=torch.uint8, device="cuda")),
+                 lambda: kvm.append(paged, step, 0, qd, k, k, pos.long(), rope), lambda: kvm.append(paged, step, 0, qd, k, k.half(), pos, rope),
+                 lambda: kvm.append(paged, step, 0, qd, k, k, pos[:4], rope), lambda: kvm.append(paged, step, 0, None, k, k, pos, rope, q_out=qd),
+                 lambda: kvm.append(paged, step, 0, qd, k, k, pos, kvm.Rope(66)), lambda: kvm.append(paged, step, 0, qd, k, k, pos, rope, weights=w),
+                 lambda: kvm.append(paged, step, 0, qd, k, k, pos, rope, weights=w[:, :, :20], slot_positions=sp[:, :, :20]),
+                 lambda: kvm.add_weights(paged, step, 0, qd, lse, w[:1]), lambda: kvm.add_weights(paged, step, 0, qd, lse),
+                 lambda: kvm.add_weights(paged, step, 0, qd, lse, w[:, :, :29].contiguous()),
+                 lambda: kvm.evict(paged, step.own, 0, 1, w[None], sp[None], 40, recent=41),
+                 lambda: kvm.evict(paged, step.own, 0, 2, w[None], sp[None], 10),
+                 lambda: kvm.evict(paged, step.own, 0, 1, w[None], sp[None].float(), 10),
+                 lambda: kvm.evict(paged, step.own, 0, 1, w[None], sp[None], 10, out_lens=step.own.lens),
+                 lambda: kvm.evict(paged, step.own, 0, 1, w[None], sp[None], 10, out_weights=w[None]),
+                 lambda: kvm.Step(paged, step.own, [1]), lambda: kvm.Step(paged, step.own, [1, 1], group_sizes=[1]),
+                 lambda: kvm.Step(paged, step.own, [1, 1], prefix=step.prefix, group_sizes=[3]),
+                 lambda: kvm.Step(paged, kvm.Tables(step.own.table, step.own.lens, 1000), [1, 1]),
+                 lambda: kvm.Tables(step.own.table.long(), step.own.lens, 10), lambda: kvm.Tables(step.own.table, step.own.lens[:1], 10),
+                 lambda: kvm.Tables(step.own.table.cpu(), step.own.lens, 10)):
+        with pytest.raises(kvm.KvError):
+            call()
+    torch.cuda.synchronize()
+    assert torch.equal(pool.cpu().view(torch.int16), b.pool.view(torch.int16)) and kvm.take_faults() == 0
+
+
 def test_calls_on_a_side_stream():
     """Two streams at once, each with its own workspace, ordered after the current stream's work."""
     b, q = _attend_case((2, 4, 128, 16, [300, 170], [1, 1], [400], [2]))
@@ -506,6 +562,7 @@ def test_calls_on_a_side_stream():
         st.wait_stream(torch.cuda.current_stream())
         ws = step.new_attend_workspace(8)
         outs.append(kvm.attend(paged, step, 1, qd, workspace=ws, stream=st))
+        outs.append(kvm.attend(paged, step, 1, qd, stream=st))       # allocates for that stream
     torch.cuda.synchronize()
     for o, l in outs:
         assert torch.equal(o, ref[0]) and torch.equal(l, ref[1])
