@@ -958,6 +958,8 @@ __device__ __forceinline__ RowPieces row_pieces(const AttendArgs& a, int32_t r)
             int32_t((uint32_t(own) + a.own_tokens - 1) / uint32_t(a.own_tokens))};
 }
 
+constexpr int kJoinAhead = 4;      // pieces of a lane whose sums are on their way at once
+
 // Joins the pieces of (row, query head), G lanes' worth of slots at a time:
 // lane group `grp` of `groups` takes pieces grp, grp + groups, ...  Returns
 // this lane's elements [4 c, 4 c + 4), summed over its own group only, and
@@ -968,6 +970,16 @@ __device__ __forceinline__ f32x4 join_row(const AttendArgs& a, int64_t at, RowPi
 {
     const int lane = threadIdx.x & 63, dim = a.pool.dim, total = n.prefix + n.own;
     auto slot_of = [&](int x) { return x < n.prefix ? x : a.prefix_pieces + x - n.prefix; };
+    m = -__builtin_inff();
+    l = 0.0f;
+    if (total == 0) return f32x4{0, 0, 0, 0};
+    auto part_of = [&](int x) {
+        return *gptr<const gf32x4>(a.part_acc + ((at + slot_of(x)) * dim + (c * 4 < dim ? c * 4 : 0)) * 4);
+    };
+    // the first pieces' sums are asked for together with their maxima: the last piece again where there are fewer
+    f32x4 first[kJoinAhead];
+#pragma unroll
+    for (int u = 0; u < kJoinAhead; ++u) first[u] = part_of(grp + u * groups < total ? grp + u * groups : total - 1);
     float pm = -__builtin_inff(), pl = 0.0f;                   // this lane's piece of the first 64
     if (lane < total) {
         const int64_t p = at + slot_of(lane);
@@ -989,12 +1001,18 @@ __device__ __forceinline__ f32x4 join_row(const AttendArgs& a, int64_t at, RowPi
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) l += __shfl_xor(l, d);
     f32x4 o = {0, 0, 0, 0};
-    for (int x0 = 0; x0 < total; x0 += groups) {               // the same rounds in every lane
+#pragma unroll
+    for (int u = 0; u < kJoinAhead; ++u) {
+        const int x = grp + u * groups;                        // below 64
+        const float e = __shfl(w, x);
+        if (x < total) o += first[u] * e;
+    }
+    for (int x0 = kJoinAhead * groups; x0 < total; x0 += groups) {   // the same rounds in every lane
         const int x = x0 + grp;
         float e = __shfl(w, x & 63);
         if (x >= 64 && x < total)
             e = __builtin_amdgcn_exp2f(gptr<const gf32>(a.part_ml)[2 * (at + slot_of(x))] - base);
-        if (x < total && c * 4 < dim) o += *gptr<const gf32x4>(a.part_acc + ((at + slot_of(x)) * dim + c * 4) * 4) * e;
+        if (x < total) o += part_of(x) * e;
     }
     return o;
 }
@@ -1040,7 +1058,7 @@ __global__ __launch_bounds__(256) void attend_join_rows(AttendArgs a)
     if (n.own < 0) return;
     const int lane = threadIdx.x & 63, c = lane % L, grp = lane / L;
 #pragma unroll 1
-    for (int32_t head = threadIdx.x >> 6; head < a.q_heads; head += 4) {
+    for (int32_t head = blockIdx.y * 4 + (threadIdx.x >> 6); head < a.q_heads; head += 4 * gridDim.y) {
         float m, l;
         f32x4 o = join_row<DP>(a, (int64_t(r) * a.q_heads + head) * a.slots, n, c, grp, G, m, l);
 #pragma unroll

@@ -247,6 +247,68 @@ void cut_tokens(int64_t pairs, int32_t max_len, int64_t room, int32_t* tokens, i
     *pieces = int32_t(ceil_div(max_len, t));
 }
 
+// Cuts of a table's tokens into pieces of whole tiles that cut_wide chooses
+// from: each number of pieces up to eight, then every half as many more.
+struct WideCuts {
+    static constexpr int kMost = 24;
+    int32_t pieces[kMost], tokens[kMost];
+    int n = 0;
+
+    WideCuts(int64_t pairs, int32_t len)
+    {
+        constexpr int32_t kTile = 64;
+        if (len == 0) {
+            pieces[0] = 0;
+            tokens[0] = kTile;
+            n = 1;
+        }
+        // no more than four rounds of 512 items
+        for (int32_t x = 1; len > 0 && n < kMost && (x == 1 || pairs * x <= 2048); x += x < 8 ? 1 : x / 2) {
+            const int32_t t = int32_t(ceil_div(ceil_div(len, x), kTile) * kTile);
+            if (n > 0 && tokens[n - 1] == t) continue;
+            tokens[n] = t;
+            pieces[n++] = int32_t(ceil_div(len, t));
+        }
+    }
+};
+
+// Pieces of a prefix and of own pages that both go through the wide form: the
+// cheapest numbers of them by what an item and a join cost, in us for heads of
+// 128 elements.  An item costs 8 and, for every 64 tokens, 2.0 where it has a
+// CU to itself and 2.9 beside another; 512 run at once.  With more than one
+// piece a row there is a join: 6, and the parts' way to memory and back.
+// As many pieces as fill the GPU, whatever they cost to join, measured longer:
+// 512 new tokens behind 2048 (32 query heads) 108 us, so 56; 1024 new ones 108
+// and 90; 700 and no prefix 57 and 30; 512 at the end of 16384 own ones 226 and
+// 212.
+void cut_wide(const kv_paged* p, const kv_step* s, int32_t q_heads, int64_t pre, int64_t own, AttendShape* a)
+{
+    const double wide = std::max(1.0, p->head_dim / 128.0), tile = wide / 64;
+    const int32_t pl = s->prefix.n > 0 ? s->prefix.max_len : 0, ol = std::max(s->own.max_len, 1);
+    const double seen = std::max(ol - s->max_new / 2.0, ol / 2.0) / ol;      // of the own tokens, by a row on average
+    const WideCuts pc(pre, pl), oc(own, ol);
+    double best = 0;
+    for (int x = 0; x < pc.n; ++x)
+        for (int y = 0; y < oc.n; ++y) {
+            const int32_t pp = pc.pieces[x], op = oc.pieces[y];
+            const double live = std::min<double>(op, std::max(1.0, op * seen + 0.5));   // own pieces of a tile
+            const double pi = double(pre) * pp, oi = double(own) * live;
+            const double sum = (8 * (pi + oi) + 2.9 * tile * (double(pre) * pl + double(own) * seen * ol)) / 512;
+            // the longest items: beside one another where there are more of them than CUs
+            const double last = 8 + tile * std::max((pi > 256 ? 2.9 : 2.0) * (pp > 0 ? pc.tokens[x] : 0),
+                                                    (oi * seen > 256 ? 2.9 : 2.0) * oc.tokens[y]);
+            double cost = pi + oi <= 512 ? std::max(last, sum) : std::max(last, sum + 0.15 * last);
+            if (pp + op > 1) cost += 6 + 2.5e-4 * wide * double(s->n_rows) * q_heads * (pp + op);
+            if (best == 0 || cost < best) {
+                best = cost;
+                a->prefix_pieces = pp;
+                a->prefix_tokens = pc.tokens[x];
+                a->own_pieces = op;
+                a->own_tokens = oc.tokens[y];
+            }
+        }
+}
+
 int attend_shape(const kv_paged* p, const kv_step* s, int32_t q_heads, AttendShape* out)
 {
     const int64_t heads = p->num_kv_heads, rep = q_heads / heads;
@@ -275,12 +337,14 @@ int attend_shape(const kv_paged* p, const kv_step* s, int32_t q_heads, AttendSha
     // not cut 121).
     const int64_t room = 512;
     const int64_t prefix_work = pre * s->prefix.max_len, own_work = own * s->own.max_len * 6 / 10;
+    const bool wide = a.own_wide && (a.prefix_wide || prefix_work == 0);
     const bool beside = a.prefix_wide && !a.own_wide && prefix_work > 0 && own_work > 0;
     const int64_t wide_room =
         beside ? std::max<int64_t>(room / 8, int64_t(double(room) * prefix_work / (double(prefix_work) + own_work)))
                : room;
     cut_tokens(pre, s->prefix.n > 0 ? s->prefix.max_len : 0, wide_room, &a.prefix_tokens, &a.prefix_pieces);
     cut_tokens(own, s->own.n > 0 ? s->own.max_len : 0, beside ? 2 * room : room, &a.own_tokens, &a.own_pieces);
+    if (wide) cut_wide(p, s, q_heads, pre, own, &a);
     a.own_pieces = std::max(1, a.own_pieces);
     a.slots = a.prefix_pieces + a.own_pieces;
     a.direct = a.slots == 1;
@@ -378,14 +442,16 @@ int attend(const kv_paged* paged, const kv_step* step, int32_t layer, const kv_r
     KernelFn pieces = dim <= 64    ? attend_kernel<64>(sh.blocks)
                       : dim <= 128 ? attend_kernel<128>(sh.blocks)
                                    : attend_kernel<256>(sh.blocks);
-    // rows enough to fill the GPU: a workgroup a row
-    const bool by_row = step->n_rows >= 1024;
+    // Rows enough to fill the GPU: a workgroup a row and some of its heads, so that 4096 of them make up for the
+    // shared look-ups' wait.  (512 new tokens behind 2048: by row 56 us, by row and head 75; one token over 10000: 23 and 17.)
+    const bool by_row = step->n_rows >= 128;
     KernelFn join = dim <= 64    ? join_kernel<64>(by_row)
                     : dim <= 128 ? join_kernel<128>(by_row)
                                  : join_kernel<256>(by_row);
     rc = launch(pieces, sh.prefix_items + sh.own_items, kAttendBlock, &a, stream);
     if (rc == KV_OK && !sh.direct)
-        rc = launch(join, by_row ? step->n_rows : int64_t(step->n_rows) * q_heads, 256, &a, stream);
+        rc = launch(join, by_row ? step->n_rows : int64_t(step->n_rows) * q_heads, 256, &a, stream,
+                    by_row ? unsigned(std::clamp<int64_t>(4096 / step->n_rows, 1, ceil_div(q_heads, 4))) : 1u);
     return rc == KV_OK ? ok() : rc;
 }
 
@@ -431,10 +497,11 @@ int add_weights_call(const kv_paged* paged, const kv_step* step, int32_t layer, 
     a.rep = q_heads / paged->num_kv_heads;
     magic_of(a.rep, &a.rep_magic, &a.rep_shift);
     a.scale_log2 = float(double(scale) * 1.4426950408889634);
-    // many rows: the waves share a workgroup's tokens and split the rows
+    // Many rows: the waves share a workgroup's tokens and split the rows.  (4 sequences of 4000 tokens, 4 heads a KV
+    // head: 32 new tokens 25 us, split 32; 64 new ones 40 and 36; 256 127 and 70.)
     const int64_t rows = std::max(own != nullptr ? step->max_new : 0, prefix != nullptr ? step->max_group_rows : 0);
     if (rows * a.rep > INT32_MAX - 2 * kStageRows) return fail(KV_EINVAL, "too many rows for one launch");
-    const bool split = rows * a.rep > 256;
+    const bool split = rows * a.rep > 192;
     const int dim = paged->head_dim;
     int32_t tokens = 0;
     int block = 0;
