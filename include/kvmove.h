@@ -11,7 +11,10 @@
  *   retrieve (scatter) chunk buffers -> pages, for the leading hit chunks;
  *   store / retrieve one layer, then record an event, so compute on another
  *            stream overlaps the movement of the neighbouring layer;
- *   optional fp8 serde: quantise to e4m3 on store, dequantise on retrieve.
+ *   optional fp8 serde: quantise to e4m3 on store, dequantise on retrieve;
+ *   a model step on the same pool: append new tokens with rotary positions,
+ *            attend to shared prefixes and own pages, add up the attention
+ *            weight of every cached token, evict by it.
  *
  * Sources (web pages, cited by title and section):
  *   [paper]  "LMCache: An Efficient KV Cache Layer for Enterprise-Scale LLM

@@ -9,8 +9,13 @@
 // before it becomes a float: in 32 bits a position of 10^6 would already be
 // off by 0.03 rad.  The rotation is float32 and each result is rounded once.
 //
-// Bound: memory, q, k and v read once, q', k', v' written once; one workgroup
-// per token, so that the R/2 angles are formed once for all its heads.
+// Bound: memory, q, k and v read once, q', k', v' written once.  One workgroup
+// per token, so that the R/2 angles are formed once for all its heads, and two
+// units a thread in flight before anything is waited for.  45116 tokens of 32
+// query heads and 8 KV heads of 128 (1.1 GB): 200 us, 5.5 TB/s, where a plain
+// copy reaches 6.8; with the units asked for after the angles 237, and no
+// better with 128 or 512 threads, four units or streaming loads.  One token:
+// 3.8 us, 64 tokens 5.3, the wait for owner, page and stores in turn.
 #pragma once
 
 #include "kv_step.hpp"

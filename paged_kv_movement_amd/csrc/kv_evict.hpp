@@ -23,9 +23,11 @@
 //                them, evict_select makes them itself.
 //
 // Bound: select, of latency: some twenty waits of a workgroup for loads, LDS
-// counts and each other; move, of memory: a scattered copy of rows of
-// head_dim elements, past the caches (each is read or written once: 134 us
-// with the streaming policy, 147 without).
+// counts and each other; 8.3 us for rows of 2049 with their moves, 26 for 256
+// rows of up to 10000.  Move, of memory: a scattered copy of rows of head_dim
+// elements, past the caches (each is read or written once: both kernels 134 us
+// with the streaming policy, 147 without): 105 us for 440 MB of 256-byte rows,
+// 4.2 TB/s.
 #pragma once
 
 #include "kv_order.hpp"
