@@ -420,8 +420,9 @@ typedef struct {
 /* Rotate the new tokens' q into q_out and write their rotated k and their v
  * into layer `layer`'s pages, in one launch.  q, k and v have one type; q_out
  * has it too, or is bf16; q and q_out may both be NULL (then q_heads and
- * q_out_type are not looked at), and q_out may be q itself.  The arithmetic
- * is float32 with angles formed in 64 bits, each result rounded once.
+ * q_out_type are not looked at), and q_out may be q itself (same type and
+ * strides; else they must not overlap).  The arithmetic is float32 with angles
+ * formed in 64 bits, each result rounded once.
  * positions: DEVICE int32[n_rows], any value.  A row of no sequence gets its
  * q_out and is not cached; tokens that a too small lens[s] leaves no slot for
  * are not cached either.  slots (NULL: none): one layer's weights of the new
@@ -468,8 +469,8 @@ int kv_add_weights(const kv_paged* paged, const kv_step* step, int32_t layer, co
  * out_lens[s] (DEVICE, not `lens` itself) = min(lens[s], keep): the lengths
  * for the next step; pages past them are the caller's to reuse.  out's first
  * min(n, keep) slots of each row are written; out may be in (both of its
- * arrays), then only moved slots are.  The pages of one call must be
- * distinct.  Shared prefixes are evicted by passing their table. */
+ * arrays), then only moved slots are; else they must not overlap.  The pages
+ * of one call must be distinct.  Shared prefixes are evicted by passing their table. */
 size_t kv_evict_workspace_bytes(const kv_paged* paged, const kv_tables* tables, int32_t n_layers, int32_t heads,
                                 int32_t keep);
 int kv_evict(const kv_paged* paged, const kv_tables* tables, int32_t layer_begin, int32_t layer_end,

@@ -840,14 +840,18 @@ _type_codes = None
 
 
 def _empty(shape, dtype, device, stream):
-    """A new device tensor for a call on ``stream``, allocated for that stream
-    (the caching allocator then orders its memory's earlier use before it)."""
+    """A new device tensor for a call on ``stream``: allocated for that stream
+    (the caching allocator then orders its memory's earlier use before it) and
+    free to be used on the current one."""
     if stream is None:
         return _t().empty(shape, dtype=dtype, device=device)
     if not hasattr(stream, "cuda_stream"):
         raise KvError(KV_EINVAL, "a call on a raw stream handle needs its outputs and workspace given")
     with _t().cuda.stream(stream):
-        return _t().empty(shape, dtype=dtype, device=device)
+        t = _t().empty(shape, dtype=dtype, device=device)
+    if t.is_cuda:
+        t.record_stream(_t().cuda.current_stream(t.device))
+    return t
 
 
 def _types():

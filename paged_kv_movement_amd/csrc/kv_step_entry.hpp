@@ -262,12 +262,14 @@ struct WideCuts {
             tokens[0] = kTile;
             n = 1;
         }
-        // no more than four rounds of 512 items
+        // no more than four rounds of 512 items, none below a tile
         for (int32_t x = 1; len > 0 && n < kMost && (x == 1 || pairs * x <= 2048); x += x < 8 ? 1 : x / 2) {
             const int32_t t = int32_t(ceil_div(ceil_div(len, x), kTile) * kTile);
-            if (n > 0 && tokens[n - 1] == t) continue;
-            tokens[n] = t;
-            pieces[n++] = int32_t(ceil_div(len, t));
+            if (n == 0 || tokens[n - 1] != t) {
+                tokens[n] = t;
+                pieces[n++] = int32_t(ceil_div(len, t));
+            }
+            if (t == kTile) break;
         }
     }
 };

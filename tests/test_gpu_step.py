@@ -156,6 +156,7 @@ ATTEND = [
     (1, 1, 64, 16, [1100, 20], [1100, 3], [130], [2]),                      # rows enough for a join by rows
     (2, 1, 16, 16, [1, 40], [1030, 20], [70], [2]),                         # most rows see nothing of their own
     (1, 2, 128, 16, [3, 3, 3], [1, 1, 1], [5, 0], [1, 1]),                  # an empty prefix, and a sequence of no group
+    (1, 5, 32, 16, [796, 322], [9, 7], [40], [0]),                          # a prefix of a group without sequences
     (1, 2, 16, 4, [9, 5] * 100, [1, 2] * 100, [6, 11] * 35, [3, 2] * 35),   # more groups than a wave has lanes
     (1, 1, 8, 1, [2, 0, 3] * 1400, [1, 1, 0] * 1400, [1] * 4200, [1] * 4200),   # more of both than 64 times its lanes
 ]

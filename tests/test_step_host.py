@@ -80,6 +80,22 @@ def test_attend_workspace_grows_with_the_bounds_only():
     assert b"multiple" in L.kv_last_error()
 
 
+@pytest.mark.timeout(60, method="signal")
+@pytest.mark.parametrize("group_rows", [0, 1, 5, 700, 1 << 20])
+@pytest.mark.parametrize("new", [0, 1, 5, 700, 1 << 20])
+def test_attend_workspace_of_any_bounds(group_rows, new):
+    """A size, or a refusal with its reason, in bounded time: empty groups, groups of few rows over one token, long tables."""
+    L = _lib()
+    for own_len in (0, 1, 64, 65, 5000, 1 << 30):
+        for prefix_len in (None, 0, 1, 40, 64, 65, 100000, 1 << 30):
+            for dim in (8, 128, 256):
+                own = tables(n=3, max_len=own_len, stride=1 << 26)
+                prefix = None if prefix_len is None else tables(n=2, max_len=prefix_len, stride=1 << 26)
+                s = step(own=own, prefix=prefix, n_rows=min(3 * new, 1 << 20), max_new=new, max_group_rows=group_rows)
+                size = L.kv_attend_workspace_bytes(ref(_paged(D=dim)), ref(s), 32)
+                assert size % 256 == 0 and (size > 0 or b"too many" in L.kv_last_error())
+
+
 def append(p=None, s=None, layer=0, q=1, k=1, v=1, o=1, heads=32, t=0, ot=0, pos=A, rope=1, slots=None):
     def r(x):
         return ref(rows()) if x == 1 else ref(x)
