@@ -469,9 +469,9 @@ struct NarrowShared {
 // they lie are the first product's left operand), and join at the end.
 //
 // Bound: the read of K and V.  16 KiB a wave are in flight, two waves a SIMD:
-// 64 sequences of 9000 to 10000 tokens, 8 KV heads of 128, in 451 us, 5.5 TB/s.
-// One such sequence is 80 pieces a head and a wait from page to page id to K to
-// V and the waves' join: 12.8 us for 41 MB.
+// 64 sequences of 9000 to 10000 tokens, 8 KV heads of 128, in 442 us, 5.6 TB/s.
+// One such sequence is 27 pieces a head and the waits from page id to K and V,
+// three rounds of them, and the waves' join: 11.6 us for 41 MB.
 template <int DP>
 __device__ __forceinline__ void narrow_piece(const AttendArgs& a, const AttendItem& it, uint64_t kb, uint64_t vb,
                                              int32_t t1, NarrowShared<DP>& sh)
@@ -969,8 +969,8 @@ __device__ __forceinline__ RowPieces row_pieces(const AttendArgs& a, int32_t r)
 }
 
 // Bound: a row's waits -- its sequence, its group, its parts -- and for many
-// rows the read of the parts: 4.4 us for 32 rows, 28 us for 2862 tokens of 32
-// heads and two pieces each (119 MB, 4.2 TB/s).
+// rows the read of the parts: 4.0 us for 32 rows, 30 us for 2862 tokens of 32
+// heads and two pieces each (119 MB, 4.0 TB/s).
 constexpr int kJoinAhead = 4;      // pieces of a lane whose sums are on their way at once
 
 // Joins the pieces of (row, query head), G lanes' worth of slots at a time:

@@ -329,15 +329,16 @@ int attend_shape(const kv_paged* p, const kv_step* s, int32_t q_heads, AttendSha
     a.prefix_tiles = int32_t(pt);
     a.own_tiles = int32_t(ot);
     const int64_t pre = s->prefix.n * heads * pt, own = s->own.n * heads * ot;
-    // Two workgroups fit a CU, so 512 pieces run at once: fewer leave CUs idle, more cost a round of set-up and twice the
-    // pieces to join (one 10000-token sequence: 18.6 us, with 1024 pieces 23.9).  A wide prefix beside narrow own pieces
+    // Two workgroups fit a CU, so 512 pieces run at once.  Narrow own pieces alone are cut into 256: a CU's loads in
+    // flight are enough from one of them, and there is half as much to join (one 10000-token sequence: 15.6 us, with 128
+    // pieces 17.6, with 512 17.1; 24 of them 180, 180, 201).  A wide prefix beside narrow own pieces
     // takes its share of them, so that its pieces, which start first, last as long as the own ones take on the rest of
     // the GPU: the ones wait for the matrix cores, the others for memory.  A token of a narrow piece costs what one of a
     // wide tile does; the own lengths are taken to be a little over half their bound.  (32 sequences behind an
     // 8192-token prefix: 46 us, with 256 wide pieces 52, with 512 63; 64 behind two 32768-token ones: 201, 213, 220.)  The
     // own pieces are then cut once more, as sequences of different lengths end at different times (24 ragged ones: 109 us,
     // not cut 121).
-    const int64_t room = 512;
+    const int64_t room = 512, narrow_room = 256;
     const int64_t prefix_work = pre * s->prefix.max_len, own_work = own * s->own.max_len * 6 / 10;
     const bool wide = a.own_wide && (a.prefix_wide || prefix_work == 0);
     const bool beside = a.prefix_wide && !a.own_wide && prefix_work > 0 && own_work > 0;
@@ -345,7 +346,7 @@ int attend_shape(const kv_paged* p, const kv_step* s, int32_t q_heads, AttendSha
         beside ? std::max<int64_t>(room / 8, int64_t(double(room) * prefix_work / (double(prefix_work) + own_work)))
                : room;
     cut_tokens(pre, s->prefix.n > 0 ? s->prefix.max_len : 0, wide_room, &a.prefix_tokens, &a.prefix_pieces);
-    cut_tokens(own, s->own.n > 0 ? s->own.max_len : 0, beside ? 2 * room : room, &a.own_tokens, &a.own_pieces);
+    cut_tokens(own, s->own.n > 0 ? s->own.max_len : 0, beside ? 2 * room : narrow_room, &a.own_tokens, &a.own_pieces);
     if (wide) cut_wide(p, s, q_heads, pre, own, &a);
     a.own_pieces = std::max(1, a.own_pieces);
     a.slots = a.prefix_pieces + a.own_pieces;

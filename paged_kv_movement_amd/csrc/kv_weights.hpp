@@ -58,8 +58,7 @@ constexpr int kStageBlocks = kStageRows / 16 / kRowsShares;             // block
 struct WeightsPiece {
     uint64_t kh;                   // this KV head's K pool
     uint64_t in, out;              // sums of (table row, KV head)
-    const TablesArg& tab;
-    int32_t table_row, h, len, first_row, count;
+    int32_t h, len, first_row, count;
     bool prefix;
 };
 
@@ -250,8 +249,6 @@ __device__ __forceinline__ WeightsPiece weights_piece(const WeightsArgs& a, cons
     return {kb + uint64_t(it.h) * a.pool.dim * 2,
             it.in != 0 ? it.in + it.at * 4 : 0,
             it.out + it.at * 4,
-            it.prefix ? a.step.prefix : a.step.own,
-            it.table_row,
             it.h,
             len,
             __builtin_amdgcn_readfirstlane(rows.first),
