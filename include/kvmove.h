@@ -436,9 +436,11 @@ int kv_append(const kv_paged* paged, const kv_step* step, int32_t layer, const k
  * multiple of num_kv_heads, consecutive query heads share a KV head): each row
  * sees the whole prefix of its sequence's group and the own tokens up to
  * itself.  out (bf16) = softmax(scale * q.k) v; lse (DEVICE float32
- * [n_rows][q_heads]) = log sum exp(scale * q.k).  A row that sees nothing gets
- * out 0 and lse -infinity; rows of no sequence are left as they were.  What a
- * row does not see never reaches it, NaN and infinities included.  A group's
+ * [n_rows][q_heads]) = log sum exp(scale * q.k).  A row that sees nothing, or
+ * nothing but scores of -infinity, gets out 0 and lse -infinity; one with a
+ * score of +infinity gets out NaN and lse +infinity; a NaN score makes both
+ * NaN.  Rows of no sequence are left as they were.  What a row does not see
+ * never reaches it, NaN and infinities included.  A group's
  * prefix is read once for all its sequences.  scale > 0; q needs 16-byte
  * aligned address and strides, out 8-byte aligned ones; out must not overlap q.
  * kv_attend_workspace_bytes depends on the bounds only; 0 on a malformed

@@ -226,12 +226,16 @@ __device__ __forceinline__ float max_of(const f32x4 (&s)[2])
 }
 
 // Raises the state's base to a row's new maximum `top` (log2 units) where it
-// has risen by more than kLag, and what it holds with it.
+// has risen by more than kLag, and what it holds with it.  The base stays
+// finite: a score of +infinity then weighs infinity, l is infinite and so is
+// the lse (less an infinite base it would be NaN), and a NaN beside it still
+// makes l NaN; the row's out is NaN, its weights' second part being
+// infinity less infinity.
 template <int DP>
 __device__ __forceinline__ void raise_base(RowState<DP>& st, float top)
 {
     if (__any(top > st.m + kLag)) {
-        const float m_new = __builtin_fmaxf(st.m, top);
+        const float m_new = __builtin_fminf(__builtin_fmaxf(st.m, top), __FLT_MAX__);
         const float alpha = m_new == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(st.m - m_new);
         st.l *= alpha;
 #pragma unroll

@@ -1,0 +1,113 @@
+"""append, attend, add_weights and evict where they can go wrong at the edges: values that are not finite in every form of
+the attention, rows of many pieces, several streams.  Against plain 64-bit implementations; every pool row that no token
+is in holds NaN."""
+import math
+
+import pytest
+import torch
+
+import paged_kv_movement_amd as kvm
+import step_util as su
+from gpu_util import say
+from test_gpu_step import device, within
+
+pytestmark = pytest.mark.gpu
+
+INF, NAN = float("inf"), float("nan")
+U = 2.0 ** -24
+
+
+def attend64(b, q, scale, layer=0):
+    """step_util.attend64 for caches whose scores may be infinite: an infinite score has no error of its own, so the
+    bounds are those of the finite ones (the same count of roundings); a row whose scores are all -infinity weighs
+    nothing and gets 0."""
+    rows, hq, D = q.shape
+    rep = hq // b.heads
+    out = torch.full((rows, hq, D), NAN, dtype=torch.float64)
+    lse = torch.full((rows, hq), NAN, dtype=torch.float64)
+    eo, el = torch.zeros_like(out), torch.zeros_like(lse)
+    for s, (n, m) in enumerate(zip(b.lens, b.new)):
+        k, v = b.cached(0, s, layer), b.cached(1, s, layer)
+        pre = k.shape[0] - n
+        for i in range(m):
+            r, see = b.q_start[s] + i, pre + max(0, n - m + i + 1)
+            for h in range(hq):
+                kk, vv, x = k[:see, h // rep], v[:see, h // rep], q[r, h].double()
+                sc = (kk @ x) * scale
+                lse[r, h] = torch.logsumexp(sc, 0) if see else -INF
+                if float(lse[r, h]) == -INF:
+                    out[r, h] = 0.0
+                    continue
+                p = torch.exp(sc - lse[r, h])
+                out[r, h] = p @ vv
+                size = ((kk.abs() @ x.abs()) * scale)[torch.isfinite(sc)]
+                if math.isfinite(float(lse[r, h])):
+                    S = float(size.max())
+                    rel = (D + 4) * U * S + (see + 12) * U
+                    el[r, h] = rel + 4 * U * (abs(float(lse[r, h])) + S)
+                    eo[r, h] = ((2 * rel + 2.0 ** -16) * (p @ vv.abs())) * (1 + 2.0 ** -8) + 2.0 ** -8 * out[r, h].abs() + 2.0 ** -133
+    return out, lse, eo, el
+
+
+# Each form of the attention and each of its layouts (a narrow piece has at most 16 rows, a wide one 16 or 32 a wave):
+# heads, rep, dim, page, lens, new, prefix, sizes, own token of sequence 0 and token of prefix 0 that is not finite
+FORMS = {
+    "narrow 128": (2, 4, 128, 16, [300, 170], [1, 1], [400], [1], 210, 333),
+    "narrow 64": (1, 2, 64, 16, [150, 40], [1, 1], [260], [1], 149, 5),
+    "narrow 80": (1, 4, 80, 12, [130, 33], [2, 1], [140], [1], 129, 139),
+    "narrow 256": (1, 3, 256, 16, [90, 20], [2, 1], [70], [1], 88, 40),
+    "one piece": (1, 1, 64, 16, [20, 9], [1, 1], [], [], 3, None),
+    "prefix wide, own narrow": (1, 4, 128, 16, [70] + [30, 9] * 4, [1] * 9, [300], [8], 60, 250),
+    "prefix wide of two blocks, own narrow": (1, 8, 128, 16, [70] + [30, 9] * 6, [1] * 13, [300], [12], 60, 250),
+    "prefix wide 256, own narrow": (1, 4, 256, 16, [70] + [30, 9] * 4, [1] * 9, [130], [8], 60, 77),
+    "wide 64": (1, 2, 64, 16, [120, 20], [20, 9], [90], [1], 110, 17),
+    "wide 64 of two blocks": (1, 2, 64, 16, [140, 20], [70, 9], [90], [1], 100, 17),
+    "wide 80": (1, 2, 80, 16, [120, 20], [20, 9], [90], [1], 110, 17),
+    "wide 80 of two blocks": (1, 2, 80, 12, [140, 20], [70, 9], [90], [1], 100, 17),
+    "wide 128 of two blocks": (2, 2, 128, 16, [240, 20], [70, 9], [90], [1], 200, 89),
+    "wide 256": (1, 2, 256, 16, [90, 20], [40, 9], [60], [1], 70, 17),
+}
+VALUES = [INF, -INF, NAN]
+
+
+def _form(name, place, where, value):
+    H, rep, D, P, lens, new, prefix, sizes, own_tok, pre_tok = FORMS[name]
+    b = su.Batch(21, H, D, P, lens, new, prefix, sizes, layers=2)
+    q = b.normal(b.q_start[-1], H * rep, D)
+    table, tok = (b.own_table, own_tok) if place == "own" else (b.prefix_table, pre_tok)
+    b.flat()[1, where, b.rows(table, 0, tok + 1, tok)[0], 0, 3] = value
+    return b, q
+
+
+PLACES = [(f, p) for f in FORMS for p in ("own", "prefix") if p == "own" or FORMS[f][9] is not None]
+
+
+@pytest.mark.parametrize("value", VALUES)
+@pytest.mark.parametrize("where", [0, 1], ids=["k", "v"])
+@pytest.mark.parametrize("form,place", PLACES)
+def test_attend_follows_the_formula_where_a_value_is_not_finite(form, place, where, value):
+    """Rows that see it follow the formula (an infinite lse included), the others stay as they are without it."""
+    say("not finite", form, place, where, value)
+    b, q = _form(form, place, where, value)
+    pool, paged, step = device(b)
+    out, lse = kvm.attend(paged, step, 1, q.cuda())
+    torch.cuda.synchronize()
+    assert kvm.take_faults() == 0
+    wo, wl, eo, el = attend64(b, q, b.dim ** -0.5, layer=1)
+    assert not torch.isfinite(b.cached(where, 0, layer=1)).all()
+    within(lse, wl, el, "lse")
+    within(out, wo, eo, "out")
+
+
+def test_a_row_whose_scores_are_all_minus_infinity_weighs_nothing():
+    b = su.Batch(22, 1, 64, 16, [1, 30], [1, 1], layers=2)
+    q = b.normal(2, 2, 64)
+    q[0, :, 3] = q[0, :, 3].abs() + 1
+    b.flat()[1, 0, b.rows(b.own_table, 0, 1)[0], 0, 3] = -INF
+    pool, paged, step = device(b)
+    out, lse = kvm.attend(paged, step, 1, q.cuda())
+    assert torch.all(out[0] == 0) and torch.all(lse[0] == -INF)
+    assert torch.isfinite(lse[1]).all()
+    w = torch.zeros((2, 1, 30), device="cuda")
+    kvm.add_weights(paged, step, 1, q.cuda(), lse, w)
+    assert torch.all(w[0] == 0) and torch.isfinite(w[1]).all()
