@@ -68,11 +68,11 @@ struct WeightsColumn {
     u32x4 q[DP / 32];
     float lse;
     int32_t f;             // flattened row
-    bool live;             // else it repeats the last one and adds nothing
+    bool live;             // else it repeats the last one and sees nothing
 };
 
 // No load stands behind a branch, so that the compiler counts which of them a
-// wait is for: columns past the last row read it again and add nothing.
+// wait is for: columns past the last row read it again and see nothing.
 template <int DP>
 __device__ __forceinline__ void load_column(const WeightsArgs& a, const WeightsPiece& w, int32_t x,
                                             WeightsColumn<DP>& c)
@@ -105,10 +105,11 @@ __device__ __forceinline__ void add_block(const WeightsArgs& a, const WeightsPie
         for (int i = 0; i < NT; ++i) s[i] = mfma16(k[i][j], c.q[j], s[i]);
     __builtin_amdgcn_sched_group_barrier(0x008, NT * (DP / 32), 0);
     // minus lse in log2 units; a row that saw nothing adds nothing: exp2(-infinity)
-    const float neg = !c.live || c.lse == -__builtin_inff() ? -__builtin_inff() : -c.lse * kLog2e;
-    // the block's first row sees the least
-    if (!w.prefix && w.len - w.count + new_token(a, x * 16) + 1 < t + 16 * NT) {
-        const int32_t vis = w.len - w.count + new_token(a, c.f) + 1;
+    const float neg = c.lse == -__builtin_inff() ? -__builtin_inff() : -c.lse * kLog2e;
+    // the block's first row sees the least; a column past the last row sees nothing
+    const bool whole = (x + 1) * 16 <= w.count * a.rep;
+    if (!whole || (!w.prefix && w.len - w.count + new_token(a, x * 16) + 1 < t + 16 * NT)) {
+        const int32_t vis = !c.live ? 0 : w.prefix ? w.len : w.len - w.count + new_token(a, c.f) + 1;
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll

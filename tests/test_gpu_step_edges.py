@@ -49,6 +49,37 @@ def attend64(b, q, scale, layer=0):
     return out, lse, eo, el
 
 
+def weights64(b, q, lse, scale, layer=0):
+    """(own, prefix) sums from zero and their bounds, step_util.weights64's count of roundings, infinite scores as above;
+    a row whose lse is -infinity adds nothing."""
+    rows, hq, D = q.shape
+    rep = hq // b.heads
+    own = torch.zeros((len(b.lens), b.heads, max(b.lens)), dtype=torch.float64)
+    pre = torch.zeros((len(b.prefix), b.heads, max(b.prefix, default=0)), dtype=torch.float64)
+    eo, ep = torch.zeros_like(own), torch.zeros_like(pre)
+    count = rep * sum(b.new)
+    for s, (n, m) in enumerate(zip(b.lens, b.new)):
+        k, g = b.cached(0, s, layer), b.group(s)
+        np_ = k.shape[0] - n
+        for i in range(m):
+            r, see = b.q_start[s] + i, np_ + max(0, n - m + i + 1)
+            for h in range(hq):
+                L = float(lse[r, h])
+                if L == -INF or see == 0:
+                    continue
+                kk, x = k[:see, h // rep], q[r, h].double()
+                sc = (kk @ x) * scale
+                p = torch.exp(sc - L)
+                S = torch.where(torch.isfinite(sc), (kk.abs() @ x.abs()) * scale, 0.0)
+                e = p * ((D + 4) * U * S + 4 * U * (S + (abs(L) if math.isfinite(L) else 0.0)) + (4 + count) * U)
+                if g is not None:
+                    pre[g, h // rep, :np_] += p[:np_]
+                    ep[g, h // rep, :np_] += e[:np_]
+                own[s, h // rep, :see - np_] += p[np_:]
+                eo[s, h // rep, :see - np_] += e[np_:]
+    return own, pre, eo, ep
+
+
 # Each form of the attention and each of its layouts (a narrow piece has at most 16 rows, a wide one 16 or 32 a wave):
 # heads, rep, dim, page, lens, new, prefix, sizes, own token of sequence 0 and token of prefix 0 that is not finite
 FORMS = {
@@ -97,6 +128,27 @@ def test_attend_follows_the_formula_where_a_value_is_not_finite(form, place, whe
     assert not torch.isfinite(b.cached(where, 0, layer=1)).all()
     within(lse, wl, el, "lse")
     within(out, wo, eo, "out")
+
+
+@pytest.mark.parametrize("lse_of", ["its own", "another cache"])
+@pytest.mark.parametrize("value", VALUES)
+@pytest.mark.parametrize("form,place", PLACES)
+def test_weights_follow_the_formula_where_a_key_is_not_finite(form, place, value, lse_of):
+    """With the lse of the same cache, and with a finite one (of the cache before the key was overwritten)."""
+    say("weights not finite", form, place, value, lse_of)
+    b, q = _form(form, place, 0, value)
+    clean = _form(form, place, 0, 0.5)[0] if lse_of == "another cache" else b
+    lse = attend64(clean, q, b.dim ** -0.5, layer=1)[1].float()
+    pool, paged, step = device(b)
+    o = torch.zeros((len(b.lens), b.heads, max(b.lens)), device="cuda")
+    p = torch.zeros((len(b.prefix), b.heads, max(b.prefix)), device="cuda") if b.prefix else None
+    kvm.add_weights(paged, step, 1, q.cuda(), lse.cuda(), o, p)
+    torch.cuda.synchronize()
+    assert kvm.take_faults() == 0
+    wo, wp, eo, ep = weights64(b, q, lse, b.dim ** -0.5, layer=1)
+    within(o, wo, eo, "own")
+    if b.prefix:
+        within(p, wp, ep, "prefix")
 
 
 def test_a_row_whose_scores_are_all_minus_infinity_weighs_nothing():
