@@ -44,7 +44,8 @@ int check_step(const kv_paged* p, const kv_step* s)
     if (rc != KV_OK) return rc;
     if (s->n_rows < 0 || s->max_new < 0 || s->max_group_rows < 0)
         return fail(KV_EINVAL, "n_rows, max_new and max_group_rows must be >= 0");
-    if (s->own.n > 0 && s->q_start == nullptr) return fail(KV_EINVAL, "q_start is NULL");
+    // a group of no sequences reads q_start[0]
+    if ((s->own.n > 0 || s->prefix.n > 0) && s->q_start == nullptr) return fail(KV_EINVAL, "q_start is NULL");
     if (s->prefix.n > 0 && s->group_start == nullptr) return fail(KV_EINVAL, "group_start is NULL");
     return KV_OK;
 }

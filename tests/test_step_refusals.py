@@ -1,0 +1,31 @@
+"""Calls of a model step that the host refuses, or answers without a launch, before any HIP call (no GPU needed)."""
+import ctypes
+
+import pytest
+
+import paged_kv_movement_amd as kvm
+from test_abi_host import _lib, _paged
+from test_step_host import A, EINVAL, append, attend, ref, rows, step, tables
+
+
+def add_weights(s=None, q=None, lse=A, own=None, prefix=None):
+    return _lib().kv_add_weights(ref(_paged()), ref(s or step()), 0, ref(q or rows()), lse, 32, 0.1, ref(own), ref(prefix),
+                                 None)
+
+
+def last_error():
+    return _lib().kv_last_error().decode()
+
+
+# ---- q_start is read for every group too
+
+NO_ROWS = dict(own=tables(n=0), prefix=tables(n=1), q_start=None)
+
+
+def test_groups_of_no_sequences_still_need_q_start():
+    """With prefixes but no sequences the kernels read q_start[0]."""
+    assert add_weights(s=step(**NO_ROWS), prefix=kvm._KvSums(None, A, 100)) == EINVAL
+    assert "q_start" in last_error()
+    assert append(s=step(**NO_ROWS)) == EINVAL and "q_start" in last_error()
+    assert attend(s=step(**NO_ROWS)) == EINVAL and "q_start" in last_error()
+    assert attend(s=step(own=tables(n=0), q_start=None, group_start=None)) == kvm.KV_OK     # neither: nothing reads it
