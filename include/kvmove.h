@@ -360,7 +360,8 @@ int kv_retrieve_chunks_cachegen(const kv_paged* paged, const kv_seq* seqs, const
  * A page id outside the pool leaves its tokens out (not written, not seen)
  * and sets fault bit 1.  Limits: num_pages * page_size < 2^31; attention and
  * weights need head_dim % 8 == 0 and head_dim <= 256.  Every call works on
- * the current device, where its stream must be; workspaces are DEVICE memory,
+ * the current device, where its stream must be; arrays that nothing is read
+ * from or written to (no sequences, no slots) may be NULL; workspaces are DEVICE memory,
  * 256-byte aligned, whose contents on entry do not matter, and calls that
  * share one must be ordered. */
 typedef struct {

@@ -22,6 +22,9 @@ int check_tables(const kv_paged* p, const kv_tables* t, const char* what)
     return KV_OK;
 }
 
+// No slot is ever read or written: then its arrays may be NULL, as an empty tensor's address is.
+bool holds_nothing(const kv_tables& t) { return t.n == 0 || t.max_len == 0; }
+
 // The pool as the step kernels take it: rows of a layer are numbered in 31 bits.
 int check_step_pool(const kv_paged* p, int32_t layer_begin, int32_t layer_end)
 {
@@ -149,7 +152,7 @@ int append(const kv_paged* paged, const kv_step* step, int32_t layer, const kv_r
                     kMaxRot);
     if (rope->rot > 0 && rope->freqs == nullptr) return fail(KV_EINVAL, "freqs is NULL");
     if (slots != nullptr) {
-        if (slots->weights == nullptr || slots->positions == nullptr)
+        if ((slots->weights == nullptr || slots->positions == nullptr) && !holds_nothing(step->own))
             return fail(KV_EINVAL, "slots: weights and positions must both be given");
         if (slots->heads != 1 && slots->heads != paged->num_kv_heads)
             return fail(KV_EINVAL, "slots: heads must be 1 or num_kv_heads (got %d)", slots->heads);
@@ -475,12 +478,17 @@ int add_weights_call(const kv_paged* paged, const kv_step* step, int32_t layer, 
     int rc = attend_checks(paged, step, layer, q_heads);
     if (rc != KV_OK) return rc;
     if (own == nullptr && prefix == nullptr) return fail(KV_EINVAL, "own or prefix sums are needed");
-    if (own != nullptr && (own->out == nullptr || own->cap < step->own.max_len))
-        return fail(own->out == nullptr ? KV_EINVAL : KV_ERANGE, "own sums: out is NULL or cap below max_len %d",
-                    step->own.max_len);
-    if (prefix != nullptr && (prefix->out == nullptr || prefix->cap < step->prefix.max_len))
-        return fail(prefix->out == nullptr ? KV_EINVAL : KV_ERANGE, "prefix sums: out is NULL or cap below max_len %d",
-                    step->prefix.max_len);
+    auto check_sums = [](const kv_sums* x, const kv_tables& t, bool may_be_null, const char* what) {
+        if (x == nullptr) return int(KV_OK);
+        if (x->out == nullptr && !may_be_null) return fail(KV_EINVAL, "%s sums: out is NULL", what);
+        if (x->cap < t.max_len)
+            return fail(KV_ERANGE, "%s sums: cap %lld below max_len %d", what, (long long)x->cap, t.max_len);
+        return int(KV_OK);
+    };
+    rc = check_sums(own, step->own, holds_nothing(step->own), "own");
+    // prefix sums of a step without prefixes stay a mistake
+    if (rc == KV_OK) rc = check_sums(prefix, step->prefix, step->prefix.n > 0 && step->prefix.max_len == 0, "prefix");
+    if (rc != KV_OK) return rc;
     if (step->n_rows > 0) {
         rc = check_q(q, scale);
         if (rc != KV_OK) return rc;
@@ -576,8 +584,9 @@ int evict(const kv_paged* paged, const kv_tables* tables, int32_t layer_begin, i
     if (recent < 0 || recent > keep) return fail(KV_EINVAL, "need 0 <= recent <= keep (got %d, %d)", recent, keep);
     if (out->heads != in->heads) return fail(KV_EINVAL, "in and out must have the same heads");
     if (tables->n == 0) return ok();
-    if (in->weights == nullptr || in->positions == nullptr || out->weights == nullptr || out->positions == nullptr ||
-        out_lens == nullptr)
+    const int32_t kept = std::min(keep, tables->max_len);
+    if (out_lens == nullptr || (tables->max_len > 0 && (in->weights == nullptr || in->positions == nullptr)) ||
+        (kept > 0 && (out->weights == nullptr || out->positions == nullptr)))
         return fail(KV_EINVAL, "weights, positions or out_lens is NULL");
     if (out_lens == tables->lens) return fail(KV_EINVAL, "out_lens must not be the lengths that are read");
     if ((in->weights == out->weights) != (in->positions == out->positions))
@@ -586,9 +595,8 @@ int evict(const kv_paged* paged, const kv_tables* tables, int32_t layer_begin, i
         return fail(KV_EINVAL, "in place, in and out must have the same cap");
     if (in->cap < tables->max_len)
         return fail(KV_ERANGE, "cap %lld below max_len %d", (long long)in->cap, tables->max_len);
-    if (out->cap < std::min(keep, tables->max_len))
-        return fail(KV_ERANGE, "out's cap %lld below the %d slots kept", (long long)out->cap,
-                    std::min(keep, tables->max_len));
+    if (out->cap < kept)
+        return fail(KV_ERANGE, "out's cap %lld below the %d slots kept", (long long)out->cap, kept);
     if (workspace == nullptr || workspace_bytes < size_t(sh.bytes) || misaligned(workspace, 256))
         return fail(KV_EINVAL, "workspace of %lld bytes, 256-byte aligned, needed (got %zu at %p)",
                     (long long)sh.bytes, workspace_bytes, workspace);

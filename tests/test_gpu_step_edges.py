@@ -163,3 +163,34 @@ def test_a_row_whose_scores_are_all_minus_infinity_weighs_nothing():
     w = torch.zeros((2, 1, 30), device="cuda")
     kvm.add_weights(paged, step, 1, q.cuda(), lse, w)
     assert torch.all(w[0] == 0) and torch.isfinite(w[1]).all()
+
+
+@pytest.mark.parametrize("lens", [[], [0, 0]], ids=["no sequences", "nothing cached"])
+def test_a_batch_of_nothing(lens):
+    """Every call takes a step without sequences, and one whose sequences hold nothing, and leaves all as it was."""
+    H, D = 2, 64
+    b = su.Batch(23, H, D, 16, lens, [0] * len(lens), layers=1)
+    pool, paged, step = device(b)
+    q, k = (torch.zeros((0, h, D), dtype=torch.bfloat16, device="cuda") for h in (4, H))
+    w = torch.zeros((len(lens), H, 0 if lens else 5), device="cuda")
+    p = torch.zeros(w.shape, dtype=torch.int32, device="cuda")
+    pos = torch.zeros(0, dtype=torch.int32, device="cuda")
+    assert kvm.append(paged, step, 0, q, k, k, pos, kvm.Rope(D), weights=w, slot_positions=p).shape == q.shape
+    out, lse = kvm.attend(paged, step, 0, q)
+    assert out.shape == q.shape and lse.shape == (0, 4)
+    assert kvm.add_weights(paged, step, 0, q, lse, w)[0] is w
+    assert kvm.evict(paged, step.own, 0, 1, w[None], p[None], 3).tolist() == lens
+    assert kvm.evict(paged, step.own, 0, 1, w[None], p[None], 0, out_weights=w[None, :, :, :0].contiguous(),
+                     out_positions=p[None, :, :, :0].contiguous()).tolist() == lens
+    torch.cuda.synchronize()
+    assert kvm.take_faults() == 0 and torch.equal(pool.cpu().view(torch.int16), b.pool.view(torch.int16))
+
+
+def test_evict_to_nothing_into_empty_tensors():
+    b = su.Batch(24, 2, 64, 16, [9, 3], [0, 0], layers=1)
+    pool, paged, step = device(b)
+    w = torch.rand((1, 2, 2, 9), generator=b.g).cuda()
+    p = torch.zeros(w.shape, dtype=torch.int32, device="cuda")
+    empty = {"out_weights": torch.empty((1, 2, 2, 0), device="cuda"),
+             "out_positions": torch.empty((1, 2, 2, 0), dtype=torch.int32, device="cuda")}
+    assert kvm.evict(paged, step.own, 0, 1, w, p, 0, **empty).tolist() == [0, 0]

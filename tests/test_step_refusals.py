@@ -29,3 +29,20 @@ def test_groups_of_no_sequences_still_need_q_start():
     assert append(s=step(**NO_ROWS)) == EINVAL and "q_start" in last_error()
     assert attend(s=step(**NO_ROWS)) == EINVAL and "q_start" in last_error()
     assert attend(s=step(own=tables(n=0), q_start=None, group_start=None)) == kvm.KV_OK     # neither: nothing reads it
+
+
+# ---- nothing cached, nothing asked
+
+def test_batches_of_nothing_may_have_no_memory():
+    """An empty tensor's address is NULL: sequences that hold nothing, or none at all, are no error."""
+    empty = step(own=tables(n=0), n_rows=0)
+    none = kvm._KvSums(None, None, 0)
+    assert add_weights(s=empty, own=kvm._KvSums(None, None, 100)) == kvm.KV_OK
+    assert add_weights(s=step(own=tables(max_len=0), n_rows=0), own=none) == kvm.KV_OK
+    assert add_weights(s=step(own=tables(max_len=0), prefix=tables(n=1, max_len=0), n_rows=0), own=none, prefix=none) == kvm.KV_OK
+    assert append(s=empty, slots=kvm._KvSlots(None, None, 8, 100)) == kvm.KV_OK
+    assert append(s=step(own=tables(max_len=0), n_rows=0), slots=kvm._KvSlots(None, None, 8, 0)) == kvm.KV_OK
+    # where there is something to write, NULL stays refused
+    assert add_weights(own=kvm._KvSums(None, None, 100)) == EINVAL and "own" in last_error()
+    assert add_weights(s=step(prefix=tables(n=1)), prefix=kvm._KvSums(None, None, 100)) == EINVAL
+    assert append(slots=kvm._KvSlots(None, None, 8, 100)) == EINVAL and "slots" in last_error()
