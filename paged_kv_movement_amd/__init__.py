@@ -642,6 +642,13 @@ def _t():
     return _torch
 
 
+def _int32(what: str, *numbers) -> None:
+    """Refuse what a C int32 does not hold: ctypes would pass its low bits."""
+    for x in numbers:
+        if not -0x80000000 <= x <= 0x7FFFFFFF:
+            raise KvError(KV_EINVAL, f"{what} = {x} does not fit 32 bits")
+
+
 def _here(*tensors) -> int:
     """The current device; every tensor must be on it (the calls launch there)."""
     cur = _t().cuda.current_device()
@@ -685,6 +692,7 @@ class Tables:
 
     def evict_workspace_bytes(self, paged: Paged, n_layers: int, heads: int, keep: int) -> int:
         """Device bytes evict needs (kv_evict_workspace_bytes)."""
+        _int32("n_layers, heads or keep", n_layers, heads, keep)
         n = load().kv_evict_workspace_bytes(ctypes.byref(paged.c), ctypes.byref(self.c), n_layers, heads, keep)
         if n == 0:
             _check(KV_EINVAL)
@@ -743,6 +751,7 @@ class Step:
 
     def attend_workspace_bytes(self, q_heads: int) -> int:
         """Device bytes attend needs (kv_attend_workspace_bytes)."""
+        _int32("q_heads", q_heads)
         n = load().kv_attend_workspace_bytes(ctypes.byref(self.paged.c), ctypes.byref(self.c), q_heads)
         if n == 0:
             _check(KV_EINVAL)
@@ -883,6 +892,7 @@ def append(paged: Paged, step: Step, layer: int, q, k, v, positions, rope: Rope,
     ``weights`` / ``slot_positions`` [sequences, H or 1, slots]: this layer's
     eviction state; the new slots' weights become 0 and their positions the
     tokens'.  Returns the rotated q."""
+    _int32("layer", layer)
     torch = _t()
     types = _types()
     st = step
@@ -932,6 +942,7 @@ def attend(paged: Paged, step: Step, layer: int, q, scale=None, out=None, lse=No
     ``scale``: 1/sqrt(D) unless given.  ``workspace``: a device uint8 tensor of
     step.attend_workspace_bytes(q_heads) (None: one is allocated for the call).
     Returns (out bf16 like q, lse float32 [rows, q_heads])."""
+    _int32("layer", layer)
     torch = _t()
     cq, heads = _q(paged, step, q)
     if out is None:
@@ -974,6 +985,7 @@ def add_weights(paged: Paged, step: Step, layer: int, q, lse, weights=None, pref
     (either may be None: not computed), in place, or into ``out`` /
     ``prefix_out`` (with weights None: from zero).  ``lse``: what attend
     returned.  Returns (own sums, prefix sums)."""
+    _int32("layer", layer)
     torch = _t()
     cq, heads = _q(paged, step, q)
     if lse.dtype != torch.float32 or not lse.is_contiguous() or lse.shape != (step.n_rows, heads):
@@ -998,6 +1010,8 @@ def evict(paged: Paged, tables: Tables, layer_begin: int, layer_end: int, weight
     [layers, sequences, H or 1, >= keep] are given.  ``workspace``: a device
     uint8 tensor of tables.evict_workspace_bytes(...) (None: allocated for the
     call).  Returns the new lengths, an int32 tensor [sequences]."""
+    _int32("layer", layer_begin, layer_end)
+    _int32("keep or recent", keep, recent)
     torch = _t()
     shape = (layer_end - layer_begin, tables.n)
     ci = _slots(weights, positions, shape, "evict:")

@@ -46,3 +46,37 @@ def test_batches_of_nothing_may_have_no_memory():
     assert add_weights(own=kvm._KvSums(None, None, 100)) == EINVAL and "own" in last_error()
     assert add_weights(s=step(prefix=tables(n=1)), prefix=kvm._KvSums(None, None, 100)) == EINVAL
     assert append(slots=kvm._KvSlots(None, None, 8, 100)) == EINVAL and "slots" in last_error()
+
+
+# ---- numbers that a C int does not hold
+
+class Stub:
+    """Stands where a call must not get to."""
+    def __getattr__(self, name):
+        raise AssertionError(f"{name} was looked at")
+
+
+@pytest.mark.parametrize("wrong", [1 << 32, (1 << 32) + 7, 1 << 31, -(1 << 31) - 1, 1 << 63])
+def test_numbers_past_32_bits_are_refused_not_cut(wrong):
+    """ctypes cuts an integer to its low bits: keep = 2^32 would evict everything, layer = 2^32 write into layer 0."""
+    x = Stub()
+    for call in (lambda: kvm.evict(x, x, 0, 1, x, x, wrong), lambda: kvm.evict(x, x, 0, 1, x, x, 5, recent=wrong),
+                 lambda: kvm.evict(x, x, wrong, wrong + 1, x, x, 5), lambda: kvm.evict(x, x, 0, wrong, x, x, 5),
+                 lambda: kvm.append(x, x, wrong, x, x, x, x, x), lambda: kvm.attend(x, x, wrong, x),
+                 lambda: kvm.add_weights(x, x, wrong, x, x)):
+        with pytest.raises(kvm.KvError, match="32 bits"):
+            call()
+
+
+@pytest.mark.parametrize("keep", [1 << 32, (1 << 32) + 50])
+def test_sizes_past_32_bits_are_refused_not_cut(keep):
+    t = object.__new__(kvm.Tables)
+    t.c = tables()
+    p = Stub()
+    for args in ((p, 1, 8, keep), (p, 1 << 32, 8, 50), (p, 1, 1 << 32, 50)):
+        with pytest.raises(kvm.KvError, match="32 bits"):
+            t.evict_workspace_bytes(*args)
+    s = object.__new__(kvm.Step)
+    s.paged = Stub()
+    with pytest.raises(kvm.KvError, match="32 bits"):
+        s.attend_workspace_bytes(keep)
