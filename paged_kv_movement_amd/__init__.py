@@ -194,8 +194,9 @@ def _used_on(stream, tensors, seen=None) -> None:
     made inline; without this, freeing them while the side stream still runs
     could hand their memory to new work too early.  With ``seen`` (a set kept
     by the owner of the tensors, which keeps them alive) each (tensor, stream)
-    is recorded once.  Nothing is done for stream=None (the current stream)
-    or a raw stream handle (the caller then keeps the tensors alive)."""
+    is recorded once.  Nothing is done for stream=None (the current stream,
+    see _used_on_current) or a raw stream handle (the caller then keeps the
+    tensors alive)."""
     if stream is None or not hasattr(stream, "cuda_stream"):
         return
     for t in tensors:
@@ -208,6 +209,20 @@ def _used_on(stream, tensors, seen=None) -> None:
         if key not in seen:
             t.record_stream(stream)
             seen.add(key)
+
+
+def _used_on_current(tensors, seen) -> None:
+    """_used_on for the current stream, of device tensors that the binding made
+    and the caller does not see: made on one stream and used under
+    ``torch.cuda.stream`` of another, they may be dropped before the kernels
+    have run.  Once per stream (its handle goes into ``seen``)."""
+    if not getattr(tensors[0], "is_cuda", False):
+        return
+    dev = tensors[0].get_device()
+    h = _t()._C._cuda_getCurrentRawStream(dev)
+    if h not in seen:
+        _used_on(_t().cuda.current_stream(dev), tensors, seen)
+        seen.add(h)
 
 
 class Paged:
@@ -225,6 +240,7 @@ class Paged:
         self.page_size, self.chunk_size, self.num_pages = page_size, chunk_size, num_pages
         self.c = _KvPaged(num_layers, num_kv_heads, head_dim, page_size, chunk_size, num_pages,
                           k_addrs.data_ptr(), v_addrs.data_ptr())
+        self._on_streams = set()        # streams that calls without a Batch or Step of their own were made on
 
     @classmethod
     def from_pool(cls, pool, chunk_size: int = 256) -> "Paged":
@@ -407,7 +423,10 @@ def _batch(paged, seqs, fmt, stream, *extra) -> Batch:
     tensors the call reads marked as used on stream."""
     b = seqs if isinstance(seqs, Batch) else Batch(paged, seqs)
     b.check_chunks(fmt)
-    b.used_on(stream, *extra)
+    if stream is None:
+        _used_on_current(b._dev_tensors, b._on_streams)
+    else:
+        b.used_on(stream, *extra)
     return b
 
 
@@ -784,7 +803,12 @@ class Step:
         if paged is not self.paged:
             _here(paged.k_addrs)
         if stream is None:
-            return _t()._C._cuda_getCurrentRawStream(self._device) or None
+            h = _t()._C._cuda_getCurrentRawStream(self._device)
+            if h not in self._on_streams:
+                _used_on_current(self._tensors, self._on_streams)
+            if paged is not self.paged and h not in paged._on_streams:
+                _used_on_current((paged.k_addrs, paged.v_addrs), paged._on_streams)
+            return h or None
         _used_on(stream, self._tensors, self._on_streams)
         if paged is not self.paged:
             _used_on(stream, (paged.k_addrs, paged.v_addrs))
@@ -811,6 +835,7 @@ class Rope:
         self.rot, self.interleaved = int(rot), bool(interleaved)
         self.gain = float(g if gain is None else gain)
         self.freqs = torch.tensor(f, dtype=torch.float64).to(device)
+        self._on_streams = set()
         self.c = _KvRope(self.freqs.data_ptr(), self.rot, int(self.interleaved), self.gain)
 
     @staticmethod
@@ -918,6 +943,8 @@ def append(paged: Paged, step: Step, layer: int, q, k, v, positions, rope: Rope,
     if weights is not None or slot_positions is not None:
         cs = _slots(weights, slot_positions, (st.own.n,), "append:")
     h = st._call(paged, stream, q, k, v, positions, rope.freqs, q_out, weights, slot_positions)
+    if stream is None and (h or 0) not in rope._on_streams:
+        _used_on_current((rope.freqs,), rope._on_streams)
     rc = load().kv_append(ctypes.byref(paged.c), st._ref, layer, _ref(cq), ctypes.byref(ck), ctypes.byref(cv),
                           _ref(co), q_heads, types[k.dtype], out_type, positions.data_ptr(), ctypes.byref(rope.c),
                           _ref(cs), h)
@@ -1033,6 +1060,8 @@ def evict(paged: Paged, tables: Tables, layer_begin: int, layer_end: int, weight
     dev = _here(*used)
     if stream is None:
         h = torch._C._cuda_getCurrentRawStream(dev) or None
+        if (h or 0) not in paged._on_streams:
+            _used_on_current((paged.k_addrs, paged.v_addrs), paged._on_streams)
     else:
         _used_on(stream, used)
         h = _stream_handle(stream)

@@ -194,3 +194,50 @@ def test_evict_to_nothing_into_empty_tensors():
     empty = {"out_weights": torch.empty((1, 2, 2, 0), device="cuda"),
              "out_positions": torch.empty((1, 2, 2, 0), dtype=torch.int32, device="cuda")}
     assert kvm.evict(paged, step.own, 0, 1, w, p, 0, **empty).tolist() == [0, 0]
+
+
+@pytest.mark.parametrize("what", ["append", "attend", "evict", "store"])
+def test_what_the_binding_made_outlives_calls_on_another_current_stream(what):
+    """Made on the default stream, used under another one and dropped while that one is still busy: their memory goes
+    to nobody else before the calls have run."""
+    b = su.Batch(25, 2, 64, 16, [40, 20], [1, 1], [50], [2], layers=2)
+    q, k = b.normal(2, 4, 64).cuda(), b.normal(2, 2, 64).cuda()
+    pos = torch.tensor([39, 19], dtype=torch.int32, device="cuda")
+    w = torch.rand((1, 2, 2, 48), device="cuda")
+    p = torch.arange(48, dtype=torch.int32, device="cuda").expand(1, 2, 2, 48).contiguous()
+    chunk = torch.zeros(1 << 20, dtype=torch.uint8, device="cuda")
+    busy = torch.randn((8192, 8192), device="cuda").bfloat16()
+    side, done = torch.cuda.Stream(), torch.cuda.Event()
+    pool, paged, step = device(b)
+    table, rope = step.own.table, kvm.Rope(64)
+    ws, es = step.new_attend_workspace(4), step.own.new_evict_workspace(paged, 1, 2, 10)
+    batch = kvm.Batch(paged, [kvm.Seq(table[0].contiguous(), 0, 40, [chunk] * 3)])
+
+    def call():
+        if what == "append":
+            return kvm.append(paged, step, 1, q, k, k, pos, rope)
+        if what == "attend":
+            return kvm.attend(paged, step, 1, q, workspace=ws)
+        if what == "evict":
+            return kvm.evict(paged, step.own, 0, 1, w, p, 10, workspace=es)
+        return kvm.store(paged, batch)
+    hidden = {"append": [step.q_start, step.group_start, paged.k_addrs, paged.v_addrs, rope.freqs],
+              "attend": [step.q_start, step.group_start, paged.k_addrs, paged.v_addrs],
+              "evict": [paged.k_addrs, paged.v_addrs],
+              "store": [paged.k_addrs, paged.v_addrs, batch.seqs[0].chunk_addrs]}[what]
+    held = {t.data_ptr() for t in hidden}
+    call()                                        # loads the code
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for _ in range(40):
+            busy @ busy
+        call()
+        done.record()
+    del hidden, step, rope, paged, batch, call
+    new = [torch.empty(n, dtype=torch.int32, device="cuda") for n in (2, 3, 4, 16, 64) for _ in range(300)]
+    taken = {t.data_ptr() for t in new} & held
+    pending = not done.query()
+    torch.cuda.synchronize()
+    assert pending, "the stream was not busy for long enough to tell"
+    assert not taken
+    assert kvm.take_faults() == 0

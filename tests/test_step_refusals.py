@@ -80,3 +80,67 @@ def test_sizes_past_32_bits_are_refused_not_cut(keep):
     s.paged = Stub()
     with pytest.raises(kvm.KvError, match="32 bits"):
         s.attend_workspace_bytes(keep)
+
+
+# ---- what the binding made itself stays while a kernel on the current stream reads it
+
+class Recorded:
+    """A device tensor that notes the streams it is said to be used on."""
+    is_cuda = True
+
+    def __init__(self):
+        self.streams = []
+
+    def get_device(self):
+        return 0
+
+    device = "cuda:0"
+
+    def record_stream(self, stream):
+        self.streams.append(stream.cuda_stream)
+
+
+class FakeTorch:
+    """Two streams of one device, by handle; ``current`` is the one that calls without a stream go to."""
+    current = 7
+
+    def __init__(self):
+        outer = self
+
+        class Stream:
+            def __init__(self, handle):
+                self.cuda_stream = handle
+
+        class C:
+            _cuda_getCurrentRawStream = staticmethod(lambda device: outer.current)
+
+        class Cuda:
+            current_device = staticmethod(lambda: 0)
+            current_stream = staticmethod(lambda device=None: Stream(outer.current))
+        self._C, self.cuda = C, Cuda
+
+
+@pytest.fixture
+def fake_torch(monkeypatch):
+    t = FakeTorch()
+    monkeypatch.setattr(kvm, "_t", lambda: t)
+    return t
+
+
+def test_a_step_is_recorded_on_the_current_stream(fake_torch):
+    p = Stub()
+    s = object.__new__(kvm.Step)
+    s.paged, s._dim, s._device, s._tensors, s._on_streams = p, 64, 0, [Recorded(), Recorded()], set()
+    for current, expect in ((7, [7]), (7, [7]), (9, [7, 9]), (7, [7, 9])):          # once per stream
+        fake_torch.current = current
+        assert s._call(p, None, Recorded()) == current
+        assert all(t.streams == expect for t in s._tensors)
+
+
+def test_a_batch_is_recorded_on_the_current_stream(fake_torch):
+    b = object.__new__(kvm.Batch)
+    b._dev_tensors, b._on_streams, b._checked_fmts = [Recorded(), Recorded()], set(), {kvm.FMT_BF16}
+    for current, expect in ((7, [7]), (7, [7]), (9, [7, 9]), (7, [7, 9])):
+        fake_torch.current = current
+        assert kvm._batch(None, b, kvm.FMT_BF16, None) is b
+        assert all(t.streams == expect for t in b._dev_tensors)
