@@ -241,3 +241,97 @@ def test_what_the_binding_made_outlives_calls_on_another_current_stream(what):
     assert pending, "the stream was not busy for long enough to tell"
     assert not taken
     assert kvm.take_faults() == 0
+
+
+def test_side_streams_with_inputs_of_their_own():
+    """Three streams at once, each with its own pool, inputs and workspaces, in every call; each result equals the one
+    of the same call alone on the current stream, bit for bit."""
+    H, rep, D = 2, 4, 128
+    rope = kvm.Rope(D)
+
+    def batch(i):
+        b = su.Batch(30 + i, H, D, 16, [600 - 90 * i, 170 + i], [1, 1], [400 + 37 * i], [2], layers=1, table_room=1)
+        d = dict(zip(("pool", "paged", "step"), device(b)))
+        d.update(q=b.normal(2, H * rep, D).cuda(), k=b.normal(2, H, D).cuda(), v=b.normal(2, H, D).cuda(),
+                 pos=torch.tensor([1000 + i, 50 * i], dtype=torch.int32).cuda(),
+                 w=torch.rand((1, 2, H, 640), generator=b.g).cuda(), pw=torch.rand((1, H, 500), generator=b.g).cuda(),
+                 p=torch.arange(640, dtype=torch.int32, device="cuda").expand(1, 2, H, 640).contiguous())
+        d["sp"] = d["p"].clone()
+        return d
+
+    def steps(d, stream):
+        d["qr"] = kvm.append(d["paged"], d["step"], 0, d["q"], d["k"], d["v"], d["pos"], rope, weights=d["w"][0],
+                             slot_positions=d["sp"][0], stream=stream)
+        for _ in range(4):
+            d["out"], d["lse"] = kvm.attend(d["paged"], d["step"], 0, d["qr"], stream=stream)
+            kvm.add_weights(d["paged"], d["step"], 0, d["qr"], d["lse"], d["w"][0], d["pw"], stream=stream)
+        d["new"] = kvm.evict(d["paged"], d["step"].own, 0, 1, d["w"], d["sp"], 150, recent=9, stream=stream)
+
+    alone, beside = [batch(i) for i in range(3)], [batch(i) for i in range(3)]
+    for d in alone:
+        steps(d, None)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in beside]
+    for st in streams:
+        st.wait_stream(torch.cuda.current_stream())
+    for d, st in zip(beside, streams):
+        steps(d, st)
+    torch.cuda.synchronize()
+    assert kvm.take_faults() == 0
+    for i, (x, y) in enumerate(zip(alone, beside)):
+        for name in ("pool", "qr", "out", "lse", "w", "pw", "sp", "new"):
+            a, c = x[name], y[name]
+            if a.dtype == torch.bfloat16:
+                a, c = a.view(torch.int16), c.view(torch.int16)
+            assert torch.equal(a, c), (i, name)
+    for name in ("out", "lse"):
+        assert not torch.equal(alone[0][name], alone[1][name])
+
+
+# Rows of many pieces: heads, rep, dim, page, lens, new, prefix, sizes, pieces a row has (of 128 tokens each)
+MANY = [
+    (1, 1, 64, 16, [63 * 128], [1], [], [], 63),
+    (1, 4, 128, 16, [64 * 128], [1], [], [], 64),
+    (1, 4, 128, 16, [64 * 128 + 1], [1], [], [], 65),
+    (1, 2, 80, 16, [10200], [1], [], [], 80),
+    (1, 1, 256, 256, [10001], [1], [], [], 79),
+    (1, 4, 128, 16, [900], [1], [20000], [1], 157 + 8),                     # 157 of the prefix, 8 of its own
+    (1, 4, 64, 16, [70] + [20, 9] * 4, [1] * 9, [20000], [9], 64),          # a wide prefix beside own pieces
+    (1, 1, 64, 16, [30, 20] * 65, [1] * 130, [17000], [130], 64),           # rows enough for a join by rows
+]
+
+
+@pytest.mark.parametrize("case", MANY, ids=[str(i) for i in range(len(MANY))])
+@pytest.mark.parametrize("value", [None, INF, NAN], ids=["finite", "inf", "nan"])
+def test_attend_rows_of_many_pieces(case, value):
+    """Joins of more pieces than a wave has lanes; with a value that is not finite in the last but one token, too."""
+    H, rep, D, P, lens, new, prefix, sizes, pieces = case
+    say("many pieces", case, value)
+    b = su.Batch(26, H, D, P, lens, new, prefix, sizes, layers=2)
+    q = b.normal(b.q_start[-1], H * rep, D, gain=3.0)
+    if value is not None:
+        b.flat()[1, 0, b.rows(b.own_table, 0, lens[0] - 1, lens[0] - 2)[0], 0, 3] = value
+    pool, paged, step = device(b)
+    # the workspace has a float32 pair and a float32 row for each (row, head, piece)
+    assert step.attend_workspace_bytes(H * rep) // (b.q_start[-1] * H * rep * (8 + 4 * D)) >= pieces
+    out, lse = kvm.attend(paged, step, 1, q.cuda(), workspace=step.new_attend_workspace(H * rep).fill_(0xFF))
+    torch.cuda.synchronize()
+    assert kvm.take_faults() == 0
+    wo, wl, eo, el = attend64(b, q, D ** -0.5, layer=1)
+    within(lse, wl, el, "lse")
+    within(out, wo, eo, "out")
+
+
+@pytest.mark.parametrize("bound", [1, 64, 1000, 8191])
+def test_attend_short_rows_under_a_long_bound(bound):
+    """A capacity as the bound, as in a captured graph: rows of one token to a full one under pieces cut for 8192."""
+    lens = [bound, max(1, bound // 3), 1]
+    b = su.Batch(27, 1, 64, 16, lens, [1, 1, 1], [bound], [2], layers=2, table_room=512)
+    q = b.normal(3, 2, 64, gain=3.0)
+    pool, paged, step = device(b, max_len=8192, prefix_max=8192)
+    out, lse = kvm.attend(paged, step, 1, q.cuda(), workspace=step.new_attend_workspace(2).fill_(0xFF))
+    torch.cuda.synchronize()
+    assert kvm.take_faults() == 0
+    wo, wl, eo, el = attend64(b, q, 64 ** -0.5, layer=1)
+    within(lse, wl, el, "lse")
+    within(out, wo, eo, "out")
