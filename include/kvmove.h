@@ -387,7 +387,8 @@ typedef struct {
 typedef enum { KV_TYPE_BF16 = 0, KV_TYPE_FP16 = 1, KV_TYPE_FP32 = 2 } kv_type;
 
 /* [n_rows][heads][head_dim] on the DEVICE, the last dimension contiguous,
- * strides in elements (so q, k and v can be parts of one projection's rows). */
+ * strides in elements (so q, k and v can be parts of one projection's rows);
+ * rows that are written must not overlap one another. */
 typedef struct {
     void* data;
     int64_t row_stride, head_stride;

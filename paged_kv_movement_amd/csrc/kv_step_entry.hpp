@@ -74,6 +74,24 @@ bool rows_vectors(const kv_rows& x, int64_t size)
     return !misaligned(x.data, 16) && x.row_stride * size % 16 == 0 && x.head_stride * size % 16 == 0;
 }
 
+// Two of the [n_rows][heads] runs of dim elements have an element in common.
+bool rows_overlap(const kv_rows& x, int64_t n_rows, int64_t heads, int64_t dim)
+{
+    using Wide = __int128;
+    const Wide row = x.row_stride < 0 ? -Wide(x.row_stride) : x.row_stride;
+    const Wide head = x.head_stride < 0 ? -Wide(x.head_stride) : x.head_stride;
+    if ((n_rows > 1 && row < dim) || (heads > 1 && head < dim)) return true;
+    if (n_rows <= 1 || heads <= 1) return false;
+    // one dimension lies wholly within a step of the other: nearly every layout
+    if (row >= (heads - 1) * head + dim || head >= (n_rows - 1) * row + dim) return false;
+    for (int64_t h = 1; h < heads; ++h)        // the two rows nearest to h heads on (signs do not matter: all h and rows)
+        for (Wide r = h * head / row; r <= h * head / row + 1; ++r) {
+            const Wide apart = h * head - r * row;
+            if (r >= 1 && r < n_rows && (apart < 0 ? -apart : apart) < dim) return true;
+        }
+    return false;
+}
+
 // x / d = (x * magic) >> shift for x < 2^31: with 2^s >= d, magic = floor(2^(31 + s) / d) + 1 is too large by at most
 // 2^s / 2^(31 + s) of itself, which stays below one over the whole range.
 void magic_of(int32_t d, uint32_t* magic, uint32_t* shift)
@@ -160,6 +178,8 @@ int append(const kv_paged* paged, const kv_step* step, int32_t layer, const kv_r
             return fail(KV_ERANGE, "slots: cap %lld below max_len %d", (long long)slots->cap, step->own.max_len);
     }
     if (step->n_rows == 0) return ok();
+    if (q_out != nullptr && rows_overlap(*q_out, step->n_rows, q_heads, paged->head_dim))
+        return fail(KV_EINVAL, "q_out's rows overlap");
     if (k->data == nullptr || v->data == nullptr || positions == nullptr || (q != nullptr && (q->data == nullptr || q_out->data == nullptr)))
         return fail(KV_EINVAL, "q, k, v, q_out or positions is NULL");
     const int64_t size = type == KV_TYPE_FP32 ? 4 : 2, out_size = q_out_type == KV_TYPE_FP32 ? 4 : 2;
@@ -412,6 +432,7 @@ int attend(const kv_paged* paged, const kv_step* step, int32_t layer, const kv_r
     if (out == nullptr || out->data == nullptr || lse == nullptr) return fail(KV_EINVAL, "out or lse is NULL");
     if (misaligned(out->data, 8) || out->row_stride % 4 != 0 || out->head_stride % 4 != 0)
         return fail(KV_EINVAL, "out's address and strides must be multiples of 8 bytes");
+    if (rows_overlap(*out, step->n_rows, q_heads, paged->head_dim)) return fail(KV_EINVAL, "out's rows overlap");
     if (workspace == nullptr || workspace_bytes < size_t(sh.bytes) || misaligned(workspace, 256))
         return fail(KV_EINVAL, "workspace of %lld bytes, 256-byte aligned, needed (got %zu at %p)",
                     (long long)sh.bytes, workspace_bytes, workspace);

@@ -144,3 +144,25 @@ def test_a_batch_is_recorded_on_the_current_stream(fake_torch):
         fake_torch.current = current
         assert kvm._batch(None, b, kvm.FMT_BF16, None) is b
         assert all(t.streams == expect for t in b._dev_tensors)
+
+
+# ---- outputs whose rows lie on one another
+
+@pytest.mark.parametrize("n,heads,row,head,overlap", [
+    (2, 32, 32 * 128, 128, False), (2, 32, 0, 128, True), (2, 32, 32 * 128, 0, True), (2, 32, 32 * 128, 64, True),
+    (2, 32, 128, 128, True),                    # row 1 is row 0's second head
+    (2, 32, 31 * 128, 128, True),               # its first head is row 0's last
+    (2, 32, 128, 256, False), (3, 32, 128, 256, True),         # heads outside, two or three rows in each
+    (32, 32, 128, 32 * 128, False), (33, 32, 128, 32 * 128, True),
+    (2, 32, -32 * 128, 128, False), (2, 32, -128, 128, True), (2, 32, 64, 1 << 40, True),
+    (1, 32, 0, 128, False), (1, 32, 0, 0, True), (9, 8, 1 << 62, 1 << 62, True), (9, 8, 1 << 62, 128, False),
+])
+def test_outputs_whose_rows_overlap_are_refused(n, heads, row, head, overlap):
+    """What two rows write into one place depends on their order: out and q_out of such strides are refused.  The calls
+    that are not refused end at the workspace or at k's address, before any HIP call."""
+    s = step(n_rows=n)
+    out = rows(row=row, head=head)
+    assert attend(s=s, heads=heads, out=out, ws=None) == EINVAL
+    assert ("overlap" in last_error()) == overlap
+    assert append(s=s, heads=heads, o=out, k=rows(data=A + 1)) == EINVAL
+    assert ("overlap" in last_error()) == overlap
