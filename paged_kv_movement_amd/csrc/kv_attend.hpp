@@ -18,8 +18,13 @@
 // Sums, maxima and accumulators are float32.  The products run on the matrix
 // cores with the cache's own bf16: S^T = K Q^T, exact products of bf16 in
 // float32 sums, and O^T = V^T P^T.  P is the one value that has to be bf16
-// there; it goes in as two bf16 (p and what rounding p left), so that the
-// output's error stays that of its own final rounding.
+// there; it goes in as two bf16, p and what rounding p left (at most 2^-8 of
+// it), so that at most 2^-16 of a weight is lost and the output's error stays
+// that of its own final rounding, at most 2^-8.  Over 10000 tokens: 1.1e-6
+// before that rounding, float32 weights 0.5e-6, and 1.677e-3 after it either
+// way; one bf16 output in a thousand differs from that of float32 sums in
+// another order, by its last bit, and one in two thousand does with float32
+// weights.  A third part would keep all 24 bits for a third more products.
 #pragma once
 
 #include "kv_step.hpp"
@@ -473,9 +478,9 @@ struct NarrowShared {
 // they lie are the first product's left operand), and join at the end.
 //
 // Bound: the read of K and V.  16 KiB a wave are in flight, two waves a SIMD:
-// 64 sequences of 9000 to 10000 tokens, 8 KV heads of 128, in 442 us, 5.6 TB/s.
+// 64 sequences of 9000 to 10000 tokens, 8 KV heads of 128, in 442 to 452 us, 5.6 TB/s.
 // One such sequence is 27 pieces a head and the waits from page id to K and V,
-// three rounds of them, and the waves' join: 11.6 us for 41 MB.
+// three rounds of them, and the waves' join: 11.8 us for 41 MB.
 template <int DP>
 __device__ __forceinline__ void narrow_piece(const AttendArgs& a, const AttendItem& it, uint64_t kb, uint64_t vb,
                                              int32_t t1, NarrowShared<DP>& sh)
@@ -783,12 +788,15 @@ __device__ __forceinline__ void wide_half_with_care(RowState<DP> (&st)[NB], cons
 // the tokens together, kWideTile at a time, K and V brought into LDS once for
 // the four waves while the tile before is computed.
 //
-// Bound: the exponentials with the splitting of P (vector units about 60 % of
-// the time) beside the products (matrix cores about 50 %).  An 8192-token
-// prompt, 32 heads of 128: 750 us, 733 TFLOP/s of the formula's products; the
-// second part of P makes them half as many again.  Without it 14 % shorter and
-// an error 1.4 times the output's own rounding.  128 rows a workgroup and two
-// workgroups a CU; with 64 rows K and V come through LDS twice as often.
+// Bound: the vector and the matrix units, which mostly take turns.  Per 64
+// scores there are 11.8 vector instructions (the exponential, the splitting of
+// P, the maximum, the transposition of V) and three products: the vector units
+// are busy 45 % of the cycles and the matrix cores 41 % (counters, at 2.2 GHz,
+// four prompts of up to 1024 tokens behind 4096).  An 8192-token prompt, 32
+// heads of 128: 750 us, 733 TFLOP/s of the formula's products; the second part
+// of P makes them half as many again.  Without it 14 % shorter and an error 1.4
+// times the output's own rounding.  128 rows a workgroup and two workgroups a
+// CU; with 64 rows K and V come through LDS twice as often.
 template <int DP, int NB>
 __device__ __forceinline__ void wide_piece(const AttendArgs& a, const AttendItem& it, uint64_t kb, uint64_t vb,
                                            int32_t t1, WideTile<DP>& tile0, WideTile<DP>& tile1)
@@ -973,8 +981,8 @@ __device__ __forceinline__ RowPieces row_pieces(const AttendArgs& a, int32_t r)
 }
 
 // Bound: a row's waits -- its sequence, its group, its parts -- and for many
-// rows the read of the parts: 4.0 us for 32 rows, 30 us for 2862 tokens of 32
-// heads and two pieces each (119 MB, 4.0 TB/s).
+// rows the read of the parts: 3.9 us for one token, 5.0 for 32, 28 for 2862 tokens
+// of 32 heads and two pieces each (119 MB, 4.2 TB/s).
 constexpr int kJoinAhead = 4;      // pieces of a lane whose sums are on their way at once
 
 // Joins the pieces of (row, query head), G lanes' worth of slots at a time:

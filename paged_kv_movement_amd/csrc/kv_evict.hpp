@@ -23,7 +23,7 @@
 //                them, evict_select makes them itself.
 //
 // Bound: select, of latency: some twenty waits of a workgroup for loads, LDS
-// counts and each other; 8.3 us for rows of 2049 with their moves, 26 for 256
+// counts and each other; 8.0 us for rows of 2049 with their moves, 25 for 256
 // rows of up to 10000.  Move, of memory: a scattered copy of rows of head_dim
 // elements, past the caches (each is read or written once: both kernels 134 us
 // with the streaming policy, 147 without): 105 us for 440 MB of 256-byte rows,

@@ -304,9 +304,10 @@ struct WideCuts {
 // CU to itself and 2.9 beside another; 512 run at once.  With more than one
 // piece a row there is a join: 6, and the parts' way to memory and back.
 // As many pieces as fill the GPU, whatever they cost to join, measured longer:
-// 512 new tokens behind 2048 (32 query heads) 108 us, so 56; 1024 new ones 108
-// and 90; 700 and no prefix 57 and 30; 512 at the end of 16384 own ones 226 and
-// 212.
+// 512 new tokens behind 2048 (32 query heads) 103 us, so 53; 1024 new ones 109
+// and 91; 700 and no prefix 33 and 29; 512 at the end of 16384 own ones the
+// same, 213.  Every row tile counts as if each sequence had max_new rows, so a
+// prompt beside single tokens is cut less than alone.
 void cut_wide(const kv_paged* p, const kv_step* s, int32_t q_heads, int64_t pre, int64_t own, AttendShape* a)
 {
     const double wide = std::max(1.0, p->head_dim / 128.0), tile = wide / 64;
@@ -354,14 +355,17 @@ int attend_shape(const kv_paged* p, const kv_step* s, int32_t q_heads, AttendSha
     a.own_tiles = int32_t(ot);
     const int64_t pre = s->prefix.n * heads * pt, own = s->own.n * heads * ot;
     // Two workgroups fit a CU, so 512 pieces run at once.  Narrow own pieces alone are cut into 256: a CU's loads in
-    // flight are enough from one of them, and there is half as much to join (one 10000-token sequence: 15.6 us, with 128
-    // pieces 17.6, with 512 17.1; 24 of them 180, 180, 201).  A wide prefix beside narrow own pieces
+    // flight are enough from one of them, and there is half as much to join (one 10000-token sequence: 15.1 us, with 128
+    // pieces 17.0, with 512 16.7; 24 of them 190, 190, 210).  A wide prefix beside narrow own pieces
     // takes its share of them, so that its pieces, which start first, last as long as the own ones take on the rest of
     // the GPU: the ones wait for the matrix cores, the others for memory.  A token of a narrow piece costs what one of a
-    // wide tile does; the own lengths are taken to be a little over half their bound.  (32 sequences behind an
-    // 8192-token prefix: 46 us, with 256 wide pieces 52, with 512 63; 64 behind two 32768-token ones: 201, 213, 220.)  The
-    // own pieces are then cut once more, as sequences of different lengths end at different times (24 ragged ones: 109 us,
-    // not cut 121).
+    // wide tile does; the own lengths are taken to be a little over half their bound, which holds for ragged batches under
+    // an exact bound and is a guess for others.  (32 sequences behind an 8192-token prefix: 58 us, with 256 wide pieces
+    // 67, with 512 79; 64 behind two 32768-token ones: 200, 210, 226; inputs not in a cache.)  The own pieces are then cut
+    // once more, as sequences of different lengths end at different times (24 ragged ones of up to 10000 tokens 144 us,
+    // not cut 177; the 32 sequences 67; but the two documents 183).
+    // All pieces are cut by the bounds: lengths far below them leave most pieces empty (10000 tokens under a bound of
+    // 10000 15 us, of 32768 20, of 131072 45; eight such sequences 67, 124 and 146).
     const int64_t room = 512, narrow_room = 256;
     const int64_t prefix_work = pre * s->prefix.max_len, own_work = own * s->own.max_len * 6 / 10;
     const bool wide = a.own_wide && (a.prefix_wide || prefix_work == 0);
@@ -471,7 +475,7 @@ int attend(const kv_paged* paged, const kv_step* step, int32_t layer, const kv_r
                       : dim <= 128 ? attend_kernel<128>(sh.blocks)
                                    : attend_kernel<256>(sh.blocks);
     // Rows enough to fill the GPU: a workgroup a row and some of its heads, so that 4096 of them make up for the
-    // shared look-ups' wait.  (512 new tokens behind 2048: by row 56 us, by row and head 75; one token over 10000: 23 and 17.)
+    // shared look-ups' wait.  (512 new tokens behind 2048: by row 53 us, by row and head 72; one token over 10000: 19 and 15.)
     const bool by_row = step->n_rows >= 128;
     KernelFn join = dim <= 64    ? join_kernel<64>(by_row)
                     : dim <= 128 ? join_kernel<128>(by_row)
@@ -531,7 +535,7 @@ int add_weights_call(const kv_paged* paged, const kv_step* step, int32_t layer, 
     magic_of(a.rep, &a.rep_magic, &a.rep_shift);
     a.scale_log2 = float(double(scale) * 1.4426950408889634);
     // Many rows: the waves share a workgroup's tokens and split the rows.  (4 sequences of 4000 tokens, 4 heads a KV
-    // head: 32 new tokens 25 us, split 32; 64 new ones 40 and 36; 256 127 and 70.)
+    // head: 32 new tokens 23 us, split 30; 64 new ones 38 and 34; 256 126 and 65.)
     const int64_t rows = std::max(own != nullptr ? step->max_new : 0, prefix != nullptr ? step->max_group_rows : 0);
     if (rows * a.rep > INT32_MAX - 2 * kStageRows) return fail(KV_EINVAL, "too many rows for one launch");
     const bool split = rows * a.rep > 192;

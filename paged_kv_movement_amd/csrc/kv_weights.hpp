@@ -18,11 +18,15 @@
 // same bits.
 //
 // Bound: for single tokens the read of K, half of what the attention reads, in
-// three waits a wave: 32 us for 32 sequences of up to 2000 tokens behind an
-// 8192-token prefix, 92 MB, 2.9 TB/s.  For prompts one exponential (a
-// quarter-rate instruction), one fused product and one sum per (row, token):
-// 24 cycles a wave for 64 of them beside 16 of matrix products; four prompts
-// of 1000 to 1300 tokens, 32 heads of 128: 83 us, 560 TFLOP/s.
+// three waits a wave, and behind a large group's prefix the rows' q, which each
+// wave reads for itself (32 rows of 4 heads: four times its K): 31 to 34 us for
+// 32 sequences of up to 2000 tokens behind an 8192-token prefix, 92 MB, 2.7 to
+// 2.9 TB/s.  For prompts, instructions and waits: the formula needs three
+// vector instructions per 64 scores (exponential, fused product, sum: 16
+// cycles of a wave) beside 16 cycles of matrix products, the kernel issues 6.8.
+// The vector units are busy 43 % of the cycles, the matrix cores 22 %
+// (counters, at 2.3 GHz).  Four prompts of 1000 to 1300 tokens, 32 heads of
+// 128: 83 to 87 us, 540 to 560 TFLOP/s.
 #pragma once
 
 #include "kv_attend.hpp"
@@ -49,7 +53,8 @@ constexpr int kWeightsTokens = 16 * kWeightsTiles * kAttendWaves;       // of a 
 // add_weights_rows: groups of tokens by shares of the rows, and the rows whose
 // q is in LDS at a time.  Two tiles a wave and short stages leave room for two
 // workgroups a CU, which counts for more than a q read by fewer of them (four
-// prompts of 1000 to 1300 tokens: 90 us, with four tiles and 128 rows 97).
+// prompts of 1000 to 1300 tokens: 87 us, with four tiles and 128 rows 116, with
+// either alone 86; four tiles cost the form for few rows 68 us instead of 34).
 constexpr int kRowsGroups = 2, kRowsShares = 4, kRowsWaves = kRowsGroups * kRowsShares;
 constexpr int kRowsTokens = 16 * kWeightsTiles * kRowsGroups;
 constexpr int kStageRows = 64;
