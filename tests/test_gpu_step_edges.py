@@ -335,3 +335,118 @@ def test_attend_short_rows_under_a_long_bound(bound):
     wo, wl, eo, el = attend64(b, q, 64 ** -0.5, layer=1)
     within(lse, wl, el, "lse")
     within(out, wo, eo, "out")
+
+
+# Head ratios, forms and layouts: heads, rep, dim, page, lens, new, prefix, sizes
+LAYOUTS = [
+    (1, 128, 64, 16, [130, 20], [2, 1], [40], [2]),                         # a KV head for 128 query heads
+    (1, 64, 128, 16, [150, 3], [5, 3], [33], [1]),
+    (2, 48, 80, 12, [70, 41], [1, 4], [20], [2]),
+    (1, 20, 128, 16, [90], [1], [70], [1]),                                 # one token takes the wide form
+    (1, 17, 256, 16, [40, 9], [1, 1], [70], [2]),
+    (1, 2, 128, 16, [30, 200, 9], [1, 100, 1], [140], [1]),                 # narrow prefix beside a prompt of no group
+    (2, 4, 64, 16, [30, 400], [1, 77], [300], [1]),
+    (1, 1, 128, 16, [65, 64, 63, 129, 128, 127], [65, 1, 63, 2, 128, 1], [64, 63], [3, 2]),
+]
+
+
+@pytest.mark.parametrize("case", LAYOUTS, ids=[str(i) for i in range(len(LAYOUTS))])
+@pytest.mark.parametrize("gain", [1.0, 64.0])
+def test_attend_and_weights_in_more_layouts(case, gain):
+    """Against 64 bits, with scores of hundreds too; tables that are views of wider ones; prefix sums alone, in place and
+    from zero."""
+    say("layouts", case, gain)
+    H, rep, D, P, lens, new, prefix, sizes = case
+    b = su.Batch(28, H, D, P, lens, new, prefix, sizes, layers=2)
+    q = b.normal(b.q_start[-1], H * rep, D, gain=gain)
+    pool, paged, _ = device(b)
+
+    def view(t):
+        wide = torch.full((t.shape[0], t.shape[1] + 5), -9, dtype=torch.int32, device="cuda")
+        wide[:, 2:2 + t.shape[1]] = t.cuda()
+        return wide[:, 2:2 + t.shape[1]]
+    own = kvm.Tables(view(b.own_table), torch.tensor(lens, dtype=torch.int32).cuda(), max(lens))
+    pre = kvm.Tables(view(b.prefix_table), torch.tensor(prefix, dtype=torch.int32).cuda(), max(prefix))
+    step = kvm.Step(paged, own, new, prefix=pre, group_sizes=sizes)
+    out, lse = kvm.attend(paged, step, 1, q.cuda())
+    torch.cuda.synchronize()
+    assert kvm.take_faults() == 0
+    wo, wl, eo, el = su.attend64(b, q, D ** -0.5, layer=1)
+    within(lse, wl, el, "lse")
+    within(out, wo, eo, "out")
+    w0 = torch.rand((len(lens), H, max(lens)), generator=b.g)
+    p0 = torch.rand((len(prefix), H, max(prefix) + 1), generator=b.g)
+    lse = wl.float()
+    ww, wp, ew, ep = su.weights64(b, q, lse, D ** -0.5, w0, p0, layer=1)
+    gw, gp = kvm.add_weights(paged, step, 1, q.cuda(), lse.cuda(), w0.cuda(), p0.cuda())
+    within(gw, ww, ew, "weights")
+    within(gp, wp, ep, "prefix weights")
+    none, alone = kvm.add_weights(paged, step, 1, q.cuda(), lse.cuda(), prefix_weights=p0.cuda())
+    # the same rows in the same order, but perhaps by the other form (the larger side decides it)
+    assert none is None
+    within(alone, wp, ep, "prefix weights alone")
+    _, zero = kvm.add_weights(paged, step, 1, q.cuda(), lse.cuda(), prefix_out=torch.full(p0.shape, 9.0, device="cuda"))
+    for g, n in enumerate(prefix):
+        assert torch.all(zero[g, :, n:] == 9.0)
+    _, z64, _, ez = su.weights64(b, q, lse, D ** -0.5, torch.zeros_like(w0), torch.zeros_like(p0), layer=1)
+    # The exponential's result is 0 where it lies below float32's smallest normal number, 2^-126: each of a token's
+    # weights (one per row and query head) is off by up to that, which only sums from zero show.  64 bits hold it: with
+    # scores of hundreds e^(score - lse) goes down to e^-700.
+    for g, n in enumerate(prefix):
+        within(zero[g, :, :n], z64[g, :, :n], ez[g, :, :n] + b.q_start[-1] * rep * 2.0 ** -126, "prefix weights from zero")
+    torch.cuda.synchronize()
+    assert kvm.take_faults() == 0
+
+
+def test_step_calls_in_a_pool_past_4_gib():
+    """Pages whose bytes lie beyond 32 bits: append, attend (narrow, wide), add_weights and evict on a slab of 4.6 GB."""
+    H, rep, D, P, pages = 8, 4, 128, 16, 140000
+    lens, new, prefix = [40, 90, 33], [1, 70, 1], [100]
+    b = su.Batch(29, H, D, P, lens, new, prefix, [3], layers=1, table_room=1)
+    # the small batch's pages, spread over the top of a large pool
+    at = torch.linspace(pages - 9000, pages - 1, b.pages).long()
+    pool = torch.full((1, 2, pages, P, H, D), NAN, dtype=torch.bfloat16, device="cuda")
+    pool[:, :, at.cuda()] = b.pool.cuda()
+    paged = kvm.Paged.from_pool(pool, chunk_size=P)
+
+    def up(t):
+        return torch.where(t >= 0, at[t.clamp(min=0).long()].int(), t).cuda()
+    own = kvm.Tables(up(b.own_table), torch.tensor(lens, dtype=torch.int32).cuda(), max(lens))
+    pre = kvm.Tables(up(b.prefix_table), torch.tensor(prefix, dtype=torch.int32).cuda(), max(prefix))
+    small_pool, small_paged, small_step = device(b)
+    step = kvm.Step(paged, own, new, prefix=pre, group_sizes=[3])
+    rope = kvm.Rope(D)
+    rows = b.q_start[-1]
+    q, k, v = (b.normal(rows, h, D).cuda() for h in (H * rep, H, H))
+    pos = torch.arange(rows, dtype=torch.int32, device="cuda")
+    results = []
+    for pg, st, pl in ((paged, step, pool), (small_paged, small_step, small_pool)):
+        w = torch.zeros((1, 3, H, max(lens)), device="cuda")
+        pw = torch.zeros((1, H, 100), device="cuda")
+        sp = torch.arange(max(lens), dtype=torch.int32, device="cuda").expand(1, 3, H, max(lens)).contiguous()
+        qr = kvm.append(pg, st, 0, q, k, v, pos, rope, weights=w[0], slot_positions=sp[0])
+        out, lse = kvm.attend(pg, st, 0, qr)
+        kvm.add_weights(pg, st, 0, qr, lse, w[0], pw)
+        n = kvm.evict(pg, st.own, 0, 1, w, sp, 30, recent=3)
+        torch.cuda.synchronize()
+        assert kvm.take_faults() == 0
+        results.append([qr, out, lse, w, pw, sp, n, pl[:, :, at.cuda()] if pl is pool else pl])
+    for i, (x, y) in enumerate(zip(*results)):
+        if x.dtype == torch.bfloat16:
+            x, y = x.view(torch.int16), y.view(torch.int16)
+        assert torch.equal(x, y), i
+    assert torch.isnan(pool[0, :, :pages - 9001].flatten(1)[:, ::997].float()).all()
+
+
+def test_attend_of_subnormal_values_and_weights():
+    """V below bf16's smallest normal number, and weights far below the largest."""
+    b = su.Batch(31, 1, 128, 16, [200], [1], [50], [1], layers=2)
+    f = b.flat()
+    x = torch.cat([b.rows(b.own_table, 0, 200), b.rows(b.prefix_table, 0, 50)])
+    f[1, 1, x] = (torch.randn((250, 1, 128), generator=b.g) * 2.0 ** -130).bfloat16()
+    q = b.normal(1, 4, 128, gain=8.0)
+    pool, paged, step = device(b)
+    out, lse = kvm.attend(paged, step, 1, q.cuda())
+    wo, wl, eo, el = su.attend64(b, q, 128 ** -0.5, layer=1)
+    within(lse, wl, el, "lse")
+    within(out, wo, eo, "out")
