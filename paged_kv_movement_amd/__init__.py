@@ -662,7 +662,8 @@ def _t():
 
 
 def _int32(what: str, *numbers) -> None:
-    """Refuse what a C int32 does not hold: ctypes would pass its low bits."""
+    """Refuse what a C int32 does not hold: ctypes would pass its low bits.
+    The calls of a step ask only where a number has bits past the 31st."""
     for x in numbers:
         if not -0x80000000 <= x <= 0x7FFFFFFF:
             raise KvError(KV_EINVAL, f"{what} = {x} does not fit 32 bits")
@@ -733,7 +734,8 @@ class Step:
     Tables of the shared prefixes, one row per group; ``group_sizes``: the
     sequences of each group, in order (sequences left over share nothing).
     The tables' contents and lengths may change between calls; a Step keeps
-    no result."""
+    no result.  A graph that captured calls reads the Step's, the Rope's and
+    the Paged's own arrays: keep the three for as long as it is replayed."""
 
     def __init__(self, paged: Paged, own: Tables, new_tokens, prefix: Tables | None = None, group_sizes=None):
         import torch
@@ -917,7 +919,8 @@ def append(paged: Paged, step: Step, layer: int, q, k, v, positions, rope: Rope,
     ``weights`` / ``slot_positions`` [sequences, H or 1, slots]: this layer's
     eviction state; the new slots' weights become 0 and their positions the
     tokens'.  Returns the rotated q."""
-    _int32("layer", layer)
+    if layer >> 31:
+        _int32("layer", layer)
     torch = _t()
     types = _types()
     st = step
@@ -969,7 +972,8 @@ def attend(paged: Paged, step: Step, layer: int, q, scale=None, out=None, lse=No
     ``scale``: 1/sqrt(D) unless given.  ``workspace``: a device uint8 tensor of
     step.attend_workspace_bytes(q_heads) (None: one is allocated for the call).
     Returns (out bf16 like q, lse float32 [rows, q_heads])."""
-    _int32("layer", layer)
+    if layer >> 31:
+        _int32("layer", layer)
     torch = _t()
     cq, heads = _q(paged, step, q)
     if out is None:
@@ -1012,7 +1016,8 @@ def add_weights(paged: Paged, step: Step, layer: int, q, lse, weights=None, pref
     (either may be None: not computed), in place, or into ``out`` /
     ``prefix_out`` (with weights None: from zero).  ``lse``: what attend
     returned.  Returns (own sums, prefix sums)."""
-    _int32("layer", layer)
+    if layer >> 31:
+        _int32("layer", layer)
     torch = _t()
     cq, heads = _q(paged, step, q)
     if lse.dtype != torch.float32 or not lse.is_contiguous() or lse.shape != (step.n_rows, heads):
@@ -1037,8 +1042,8 @@ def evict(paged: Paged, tables: Tables, layer_begin: int, layer_end: int, weight
     [layers, sequences, H or 1, >= keep] are given.  ``workspace``: a device
     uint8 tensor of tables.evict_workspace_bytes(...) (None: allocated for the
     call).  Returns the new lengths, an int32 tensor [sequences]."""
-    _int32("layer", layer_begin, layer_end)
-    _int32("keep or recent", keep, recent)
+    if (layer_begin | layer_end | keep | recent) >> 31:
+        _int32("layer, keep or recent", layer_begin, layer_end, keep, recent)
     torch = _t()
     shape = (layer_end - layer_begin, tables.n)
     ci = _slots(weights, positions, shape, "evict:")

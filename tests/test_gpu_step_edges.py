@@ -450,3 +450,67 @@ def test_attend_of_subnormal_values_and_weights():
     wo, wl, eo, el = su.attend64(b, q, 128 ** -0.5, layer=1)
     within(lse, wl, el, "lse")
     within(out, wo, eo, "out")
+
+
+def test_two_graphs_share_a_workspace():
+    """Two steps of different shapes captured with one workspace for attend and one for evict, replayed in turn with eager
+    work between: each replay equals its eager calls."""
+    H, rep, D = 2, 4, 128
+    rope = kvm.Rope(D)
+    batches = [su.Batch(33, H, D, 16, [700, 90], [1, 1], [400], [2], layers=1),
+               su.Batch(34, H, D, 16, [120, 60, 33], [40, 1, 33], [90], [3], layers=1)]
+
+    def make(b):
+        pool, paged, step = device(b)
+        n, cap = len(b.lens), max(b.lens)
+        return {"pool": pool, "first": pool.clone(), "paged": paged, "step": step,
+                "q": b.normal(b.q_start[-1], H * rep, D).cuda(), "k": b.normal(b.q_start[-1], H, D).cuda(),
+                "pos": torch.arange(b.q_start[-1], dtype=torch.int32, device="cuda"),
+                "qr": torch.empty((b.q_start[-1], H * rep, D), dtype=torch.bfloat16, device="cuda"),
+                "out": torch.empty((b.q_start[-1], H * rep, D), dtype=torch.bfloat16, device="cuda"),
+                "lse": torch.empty((b.q_start[-1], H * rep), device="cuda"),
+                "w": torch.zeros((1, n, H, cap), device="cuda"),
+                "p": torch.arange(cap, dtype=torch.int32, device="cuda").expand(1, n, H, cap).contiguous(),
+                "ow": torch.zeros((1, n, H, 50), device="cuda"),
+                "op": torch.zeros((1, n, H, 50), dtype=torch.int32, device="cuda"),
+                "lens": torch.zeros(n, dtype=torch.int32, device="cuda")}
+
+    def run(d, ws, es):
+        kvm.append(d["paged"], d["step"], 0, d["q"], d["k"], d["k"], d["pos"], rope, q_out=d["qr"])
+        kvm.attend(d["paged"], d["step"], 0, d["qr"], out=d["out"], lse=d["lse"], workspace=ws)
+        kvm.add_weights(d["paged"], d["step"], 0, d["qr"], d["lse"], None, out=d["w"][0])
+        kvm.evict(d["paged"], d["step"].own, 0, 1, d["w"], d["p"], 50, recent=5, out_weights=d["ow"], out_positions=d["op"],
+                  out_lens=d["lens"], workspace=es)
+
+    def again(d):
+        d["pool"].copy_(d["first"])
+        for x in ("qr", "out", "lse", "ow", "op", "lens"):
+            d[x].zero_()
+    sides = [make(b) for b in batches]
+    ws = max((d["step"].new_attend_workspace(H * rep) for d in sides), key=lambda t: t.numel())
+    es = max((d["step"].own.new_evict_workspace(d["paged"], 1, H, 50) for d in sides), key=lambda t: t.numel())
+    names = ("pool", "qr", "out", "lse", "w", "ow", "op", "lens")
+    want = []
+    for d in sides:
+        run(d, ws, es)
+        want.append({x: d[x].clone() for x in names})
+        again(d)
+    torch.cuda.synchronize()
+    graphs = []
+    for d in sides:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            run(d, ws, es)
+        graphs.append(g)
+    for _ in range(4):
+        for g, d, w in zip(graphs, sides, want):
+            again(d)
+            g.replay()
+            torch.cuda.synchronize()
+            for x in names:
+                a, c = d[x], w[x]
+                if a.dtype == torch.bfloat16:
+                    a, c = a.view(torch.int16), c.view(torch.int16)
+                assert torch.equal(a, c), x
+            (torch.randn(512, 512, device="cuda") @ torch.randn(512, 512, device="cuda")).sum().item()
+    assert kvm.take_faults() == 0
