@@ -229,7 +229,7 @@ def test_what_the_binding_made_outlives_calls_on_another_current_stream(what):
     call()                                        # loads the code
     torch.cuda.synchronize()
     with torch.cuda.stream(side):
-        for _ in range(40):
+        for _ in range(150):
             busy @ busy
         call()
         done.record()
