@@ -481,6 +481,83 @@ int kv_evict(const kv_paged* paged, const kv_tables* tables, int32_t layer_begin
              const kv_slots* in, const kv_slots* out, int32_t keep, int32_t recent, int32_t* out_lens,
              void* workspace, size_t workspace_bytes, hipStream_t stream);
 
+/* ---- A window, normalised heads, and a pool in 8 bits. */
+
+/* A row at position p -- its own token's, counted from the start of its group's
+ * prefix -- sees the tokens t <= p with t > p - window or t < sinks. */
+typedef struct {
+    int32_t window; /* >= 1; 1: the token itself (and the sinks) */
+    int32_t sinks;  /* >= 0 first tokens that stay visible */
+} kv_window;
+
+/* kv_attend with a window (NULL: none).  Only what some row sees is read; a
+ * row that lens leaves no slot for counts as standing on the prefix's last
+ * token.  The weights that kv_add_weights adds know no window. */
+size_t kv_attend_window_workspace_bytes(const kv_paged* paged, const kv_step* step, int32_t q_heads,
+                                        const kv_window* window);
+int kv_attend_window(const kv_paged* paged, const kv_step* step, int32_t layer, const kv_rows* q, int32_t q_heads,
+                     float scale, const kv_window* window, const kv_rows* out, float* lse, void* workspace,
+                     size_t workspace_bytes, hipStream_t stream);
+
+/* Each head x of q and of k becomes (x - c) / sqrt(mean((x - c)^2) + eps) * w
+ * before it is rotated; c = 0, or the head's mean. */
+typedef struct {
+    const float* q_weight; /* DEVICE float32 [q_heads][head_dim], 16-byte aligned; NULL: ones */
+    const float* k_weight; /* the same for k's heads */
+    int64_t q_stride;      /* elements from a head's weights to the next one's, a multiple of 4; 0: all heads share them */
+    int64_t k_stride;
+    float eps;             /* >= 0 */
+    int32_t centered;      /* 1: less the mean */
+} kv_norm;
+
+/* kv_append with q's and k's heads normalised (norm NULL: as kv_append), in
+ * float32 throughout; each result is rounded once. */
+int kv_append_normed(const kv_paged* paged, const kv_step* step, int32_t layer, const kv_rows* q, const kv_rows* k,
+                     const kv_rows* v, const kv_rows* q_out, int32_t q_heads, kv_type type, kv_type q_out_type,
+                     const int32_t* positions, const kv_rope* rope, const kv_norm* norm, const kv_slots* slots,
+                     hipStream_t stream);
+
+/* A pool of e4m3 bytes.  A block is what one head has in one page, of K or of
+ * V.  Its scale s is the least power of two with |x| <= 448 s for every finite
+ * value x of the block, within 2^-100 .. 2^119; a byte is e4m3(x / s), ties to
+ * even, saturating, and stands for byte * s, which is exact in bf16.  What is
+ * not finite is held as NaN.  head_dim must be a multiple of 16.  Of a scale
+ * that is read only the exponent counts. */
+typedef struct {
+    kv_paged pages;           /* k_pages / v_pages: e4m3 [num_pages][page_size][H][D] */
+    const uint64_t* k_scales; /* DEVICE uint64[L]: address of layer l's float32 [num_pages][H], 4-byte aligned */
+    const uint64_t* v_scales;
+} kv_paged8;
+
+/* kv_append (norm NULL) or kv_append_normed into an 8-bit pool: a block's scale
+ * covers its new tokens and, where it holds earlier ones of the sequence, is at
+ * least what it was; if it rises, their bytes are held anew under it.  A block
+ * that begins with a new token starts afresh.  The pages written by one call
+ * must be distinct: sequences cannot share a page that either appends to. */
+int kv_append8(const kv_paged8* paged, const kv_step* step, int32_t layer, const kv_rows* q, const kv_rows* k,
+               const kv_rows* v, const kv_rows* q_out, int32_t q_heads, kv_type type, kv_type q_out_type,
+               const int32_t* positions, const kv_rope* rope, const kv_norm* norm, hipStream_t stream);
+
+/* kv_attend over an 8-bit pool, with a window or (NULL) without. */
+size_t kv_attend8_workspace_bytes(const kv_paged8* paged, const kv_step* step, int32_t q_heads,
+                                  const kv_window* window);
+int kv_attend8(const kv_paged8* paged, const kv_step* step, int32_t layer, const kv_rows* q, int32_t q_heads,
+               float scale, const kv_window* window, const kv_rows* out, float* lse, void* workspace,
+               size_t workspace_bytes, hipStream_t stream);
+
+/* The cached tokens of layers [layer_begin, layer_end) from bf16 pages into
+ * 8-bit ones and back: tokens [0, lens[s]) of each sequence, from the pages of
+ * `tables` into those of to_table (DEVICE int32 [n][to_stride]; NULL: the same
+ * page ids).  Both pools have one page size, heads, head size and number of
+ * layers.  pack8 makes each block's scale from the tokens it holds; unpack8
+ * writes byte * s, exactly.  What lies behind the last token is left as it was.
+ * The pages written by one call must be distinct.  A store of an 8-bit pool is
+ * unpack8 and kv_store_chunks, a retrieve kv_retrieve_chunks and pack8. */
+int kv_pack8(const kv_paged* from, const kv_tables* tables, const kv_paged8* to, const int32_t* to_table,
+             int64_t to_stride, int32_t layer_begin, int32_t layer_end, hipStream_t stream);
+int kv_unpack8(const kv_paged8* from, const kv_tables* tables, const kv_paged* to, const int32_t* to_table,
+               int64_t to_stride, int32_t layer_begin, int32_t layer_end, hipStream_t stream);
+
 /* Message for the last non-OK return on this thread ("" if none). */
 const char* kv_last_error(void);
 

@@ -28,6 +28,7 @@ __all__ = ["FMT_BF16", "FMT_FP8", "FMT_FP8_E5M2", "FMT_K16_V8", "FMT_CACHEGEN", 
            "retrieve", "retrieve_noalloc", "retrieve_layer", "retrieve_layer_ex", "retrieve_layers", "take_faults",
            "copy_bytes",
            "Tables", "Step", "Rope", "append", "attend", "add_weights", "evict",
+           "Paged8", "Norm", "pack8", "unpack8",
            "library_path", "load"]
 
 FMT_BF16 = 0          # K and V bf16, copied bit for bit
@@ -105,6 +106,19 @@ class _KvRope(ctypes.Structure):
                 ("gain", ctypes.c_float)]
 
 
+class _KvPaged8(ctypes.Structure):
+    _fields_ = [("pages", _KvPaged), ("k_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p)]
+
+
+class _KvNorm(ctypes.Structure):
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("q_stride", ctypes.c_int64),
+                ("k_stride", ctypes.c_int64), ("eps", ctypes.c_float), ("centered", ctypes.c_int32)]
+
+
+class _KvWindow(ctypes.Structure):
+    _fields_ = [("window", ctypes.c_int32), ("sinks", ctypes.c_int32)]
+
+
 class _KvSlots(ctypes.Structure):
     _fields_ = [("weights", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("heads", ctypes.c_int32),
                 ("cap", ctypes.c_int64)]
@@ -129,6 +143,7 @@ def load():
     L = ctypes.CDLL(_LIB_PATH)
     P, S = ctypes.POINTER(_KvPaged), ctypes.POINTER(_KvSeq)
     T, B, R, O, W, M = (ctypes.POINTER(c) for c in (_KvStep, _KvTables, _KvRows, _KvRope, _KvSlots, _KvSums))
+    P8, N, V = (ctypes.POINTER(c) for c in (_KvPaged8, _KvNorm, _KvWindow))
     i32, i64, vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p
     sig = {
         "kv_chunk_bytes": (ctypes.c_size_t, [P, i64, ctypes.c_int]),
@@ -155,6 +170,14 @@ def load():
         "kv_add_weights": (ctypes.c_int, [P, T, i32, R, vp, i32, ctypes.c_float, M, M, vp]),
         "kv_evict_workspace_bytes": (ctypes.c_size_t, [P, B, i32, i32, i32]),
         "kv_evict": (ctypes.c_int, [P, B, i32, i32, W, W, i32, i32, vp, vp, ctypes.c_size_t, vp]),
+        "kv_append_normed": (ctypes.c_int, [P, T, i32, R, R, R, R, i32, ctypes.c_int, ctypes.c_int, vp, O, N, W, vp]),
+        "kv_append8": (ctypes.c_int, [P8, T, i32, R, R, R, R, i32, ctypes.c_int, ctypes.c_int, vp, O, N, vp]),
+        "kv_attend_window_workspace_bytes": (ctypes.c_size_t, [P, T, i32, V]),
+        "kv_attend_window": (ctypes.c_int, [P, T, i32, R, i32, ctypes.c_float, V, R, vp, vp, ctypes.c_size_t, vp]),
+        "kv_attend8_workspace_bytes": (ctypes.c_size_t, [P8, T, i32, V]),
+        "kv_attend8": (ctypes.c_int, [P8, T, i32, R, i32, ctypes.c_float, V, R, vp, vp, ctypes.c_size_t, vp]),
+        "kv_pack8": (ctypes.c_int, [P, B, P8, vp, i64, i32, i32, vp]),
+        "kv_unpack8": (ctypes.c_int, [P8, B, P, vp, i64, i32, i32, vp]),
         "kv_last_error": (ctypes.c_char_p, []),
         "kv_take_faults": (ctypes.c_int, []),
         "kv_copy_bytes": (ctypes.c_int, [vp, vp, ctypes.c_size_t, vp]),
@@ -240,6 +263,7 @@ class Paged:
         self.page_size, self.chunk_size, self.num_pages = page_size, chunk_size, num_pages
         self.c = _KvPaged(num_layers, num_kv_heads, head_dim, page_size, chunk_size, num_pages,
                           k_addrs.data_ptr(), v_addrs.data_ptr())
+        self._arrays = (k_addrs, v_addrs)
         self._on_streams = set()        # streams that calls without a Batch or Step of their own were made on
 
     @classmethod
@@ -302,6 +326,62 @@ class Paged:
         return int(n)
 
 
+def _addresses(tensors):
+    """Their addresses, as a device int64 tensor."""
+    import torch
+    return torch.tensor([t.data_ptr() for t in tensors], dtype=torch.int64).to(tensors[0].device)
+
+
+class Paged8:
+    """A paged pool in 8 bits: e4m3 bytes, and for each block (one head's tokens
+    in one page) of K and of V a float32 scale, the least power of two of which
+    448 reach every value of the block.  A byte stands for byte * scale.
+
+    append, attend, pack8 and unpack8 take it; the chunk movers, add_weights
+    and evict work on the bf16 pool (unpack8 and store, retrieve and pack8)."""
+
+    def __init__(self, k_layers, v_layers, k_scales, v_scales):
+        import torch
+        _need(len(k_layers) == len(v_layers) == len(k_scales) == len(v_scales) > 0,
+              "need one K and one V tensor per layer, and their scales")
+        _need(k_layers[0].dim() == 4, "per-layer pools must be [num_pages, page_size, H, D]")
+        n, P, H, D = k_layers[0].shape
+        for t in (*k_layers, *v_layers):
+            _need(t.dtype in (torch.uint8, torch.float8_e4m3fn) and t.is_contiguous() and t.is_cuda
+                  and tuple(t.shape) == (n, P, H, D),
+                  "per-layer pools must be contiguous uint8 or float8_e4m3fn device tensors of one shape "
+                  "[num_pages, page_size, H, D]")
+        for t in (*k_scales, *v_scales):
+            _need(t.dtype == torch.float32 and t.is_contiguous() and t.is_cuda and tuple(t.shape) == (n, H),
+                  "scales must be contiguous float32 device tensors [num_pages, H]")
+        dev = k_layers[0].device
+        _need(all(t.device == dev for t in (*k_layers, *v_layers, *k_scales, *v_scales)),
+              "a pool's tensors must be on one device")
+        _need(D % 16 == 0, "head_dim must be a multiple of 16 in an 8-bit pool")
+        self._keep = (*k_layers, *v_layers, *k_scales, *v_scales)
+        self.num_layers, self.num_kv_heads, self.head_dim = len(k_layers), H, D
+        self.page_size, self.num_pages = P, n
+        self.k_addrs, self.v_addrs = _addresses(k_layers), _addresses(v_layers)
+        self.k_scale_addrs, self.v_scale_addrs = _addresses(k_scales), _addresses(v_scales)
+        self._arrays = (self.k_addrs, self.v_addrs, self.k_scale_addrs, self.v_scale_addrs)
+        self._on_streams = set()
+        self.c = _KvPaged8(_KvPaged(self.num_layers, H, D, P, P, n, self.k_addrs.data_ptr(), self.v_addrs.data_ptr()),
+                           self.k_scale_addrs.data_ptr(), self.v_scale_addrs.data_ptr())
+
+    @classmethod
+    def from_pool(cls, pool, scales) -> "Paged8":
+        """From one tensor [L, 2, num_pages, page_size, H, D] (uint8 or float8_e4m3fn; K at [:, 0], V at [:, 1])
+        and its float32 scales [L, 2, num_pages, H]."""
+        _need(pool.dim() == 6 and pool.size(1) == 2 and scales.dim() == 4 and scales.shape[:3] == pool.shape[:3],
+              "need a pool [L, 2, num_pages, page_size, H, D] and scales [L, 2, num_pages, H]")
+        return cls(pool[:, 0].unbind(0), pool[:, 1].unbind(0), scales[:, 0].unbind(0), scales[:, 1].unbind(0))
+
+
+def _bf16_pool(paged, call: str) -> None:
+    if isinstance(paged, Paged8):
+        raise KvError(KV_EINVAL, f"{call} works on a bf16 pool, not on a Paged8")
+
+
 class Seq:
     """One sequence's job: a device int32 block table, a token range and its
     chunk buffers (device int64 tensor of addresses, or uint8 tensors).
@@ -345,6 +425,7 @@ class Batch:
     """Prebuilt C descriptors for a list of Seq (reusable across calls)."""
 
     def __init__(self, paged: Paged, seqs):
+        _bf16_pool(paged, "a Batch")
         self.seqs = list(seqs)
         self.paged = paged
         n = len(self.seqs)
@@ -762,7 +843,7 @@ class Step:
         self.c = _KvStep(own.c, prefix.c if prefix is not None else _KvTables(), self.q_start.data_ptr(),
                          self.group_start.data_ptr(), self.n_rows, max(new, default=0),
                          max((starts[groups[i + 1]] - starts[groups[i]] for i in range(len(sizes))), default=0))
-        self._tensors = [paged.k_addrs, paged.v_addrs, own.table, own.lens, self.q_start, self.group_start]
+        self._tensors = [*paged._arrays, own.table, own.lens, self.q_start, self.group_start]
         if prefix is not None:
             self._tensors += [prefix.table, prefix.lens]
         self._on_streams = set()
@@ -770,18 +851,25 @@ class Step:
         self._device = _here(*self._tensors)
         self._ref = ctypes.byref(self.c)
 
-    def attend_workspace_bytes(self, q_heads: int) -> int:
-        """Device bytes attend needs (kv_attend_workspace_bytes)."""
+    def attend_workspace_bytes(self, q_heads: int, window: int | None = None, sinks: int = 0) -> int:
+        """Device bytes attend needs with this window (kv_attend_workspace_bytes and its other forms)."""
         _int32("q_heads", q_heads)
-        n = load().kv_attend_workspace_bytes(ctypes.byref(self.paged.c), ctypes.byref(self.c), q_heads)
+        w, p, c = _window(window, sinks), ctypes.byref(self.paged.c), ctypes.byref(self.c)
+        if isinstance(self.paged, Paged8):
+            n = load().kv_attend8_workspace_bytes(p, c, q_heads, _ref(w))
+        elif w is not None:
+            n = load().kv_attend_window_workspace_bytes(p, c, q_heads, _ref(w))
+        else:
+            n = load().kv_attend_workspace_bytes(p, c, q_heads)
         if n == 0:
             _check(KV_EINVAL)
         return int(n)
 
-    def new_attend_workspace(self, q_heads: int):
+    def new_attend_workspace(self, q_heads: int, window: int | None = None, sinks: int = 0):
         """A device tensor of attend_workspace_bytes (torch aligns it to 256)."""
         import torch
-        return torch.empty(self.attend_workspace_bytes(q_heads), dtype=torch.uint8, device=self.own.table.device)
+        return torch.empty(self.attend_workspace_bytes(q_heads, window, sinks), dtype=torch.uint8,
+                           device=self.own.table.device)
 
     def _rows(self, t, heads, what, types):
         """kv_rows of a tensor [n_rows, heads, head_dim] of one of the types."""
@@ -809,11 +897,11 @@ class Step:
             if h not in self._on_streams:
                 _used_on_current(self._tensors, self._on_streams)
             if paged is not self.paged and h not in paged._on_streams:
-                _used_on_current((paged.k_addrs, paged.v_addrs), paged._on_streams)
+                _used_on_current(paged._arrays, paged._on_streams)
             return h or None
         _used_on(stream, self._tensors, self._on_streams)
         if paged is not self.paged:
-            _used_on(stream, (paged.k_addrs, paged.v_addrs))
+            _used_on(stream, paged._arrays)
         _used_on(stream, tensors)
         return _stream_handle(stream)
 
@@ -872,6 +960,53 @@ class Rope:
         return f, gain
 
 
+class Norm:
+    """Normalisation of each head of q and k before the rotation:
+    (x - c) / sqrt(mean((x - c)^2) + eps) * weight, c = 0 or, ``centered``, the
+    head's mean.  ``q_weight`` / ``k_weight``: [head_dim], [heads, head_dim], or
+    None for ones; float32 device tensors are read where they are at each call,
+    others are copied once.  A graph that captured calls reads the Norm's
+    arrays: keep it for as long as it is replayed."""
+
+    def __init__(self, q_weight=None, k_weight=None, eps: float = 1e-6, centered: bool = False, device="cuda"):
+        import torch
+
+        def held(w, name):
+            if w is None:
+                return None
+            _need(w.dim() in (1, 2) and w.dtype.is_floating_point, f"{name} must be [head_dim] or [heads, head_dim]")
+            w = w.to(device=device, dtype=torch.float32).contiguous()
+            return w.clone() if w.data_ptr() % 16 else w
+        self.q_weight, self.k_weight = held(q_weight, "q_weight"), held(k_weight, "k_weight")
+        self.eps, self.centered = float(eps), bool(centered)
+        self._on_streams = set()
+        self._tensors = [w for w in (self.q_weight, self.k_weight) if w is not None]
+
+        def stride(w):
+            return 0 if w is None or w.dim() == 1 else w.size(1)
+        self.c = _KvNorm(0 if self.q_weight is None else self.q_weight.data_ptr(),
+                         0 if self.k_weight is None else self.k_weight.data_ptr(),
+                         stride(self.q_weight), stride(self.k_weight), self.eps, int(self.centered))
+
+    def _fits(self, w, heads, dim, name):
+        if w is not None and tuple(w.shape) not in ((dim,), (heads, dim)):
+            raise KvError(KV_EINVAL, f"{name} must be [{dim}] or [{heads}, {dim}], got {list(w.shape)}")
+        # the stride of head weights is in whole vectors of four
+        if w is not None and w.dim() == 2 and heads > 1 and dim % 4:
+            raise KvError(KV_EINVAL, f"{name} of each head needs a head_dim that is a multiple of 4")
+
+
+def _window(window, sinks):
+    """kv_window, or None without one."""
+    if window is None:
+        if sinks:
+            raise KvError(KV_EINVAL, "sinks without a window")
+        return None
+    if (window | sinks) >> 31:
+        _int32("window or sinks", window, sinks)
+    return _KvWindow(window, sinks)
+
+
 _type_codes = None
 
 
@@ -909,10 +1044,11 @@ def _slots(weights, positions, shape, what):
     return _KvSlots(weights.data_ptr(), positions.data_ptr(), weights.shape[-2], weights.shape[-1])
 
 
-def append(paged: Paged, step: Step, layer: int, q, k, v, positions, rope: Rope, q_out=None, weights=None,
-           slot_positions=None, stream=None):
-    """Rotate the new tokens' q and k and write k and v into layer ``layer``'s
-    pages (kv_append).  q [rows, q_heads, D] (None: only k and v), k and v
+def append(paged: Paged | Paged8, step: Step, layer: int, q, k, v, positions, rope: Rope, q_out=None, weights=None,
+           slot_positions=None, stream=None, norm: Norm | None = None):
+    """Rotate the new tokens' q and k, normalised first by ``norm`` if one is
+    given, and write k and v into layer ``layer``'s pages (kv_append,
+    kv_append_normed; of a Paged8 kv_append8, which takes no eviction state).  q [rows, q_heads, D] (None: only k and v), k and v
     [rows, H, D]: bf16, fp16 or float32, any row and head strides;
     ``positions``: int32 [rows].  ``q_out``: where the rotated q goes (q
     itself, or a tensor of q's type or bf16; None: a new tensor of q's type).
@@ -945,12 +1081,30 @@ def append(paged: Paged, step: Step, layer: int, q, k, v, positions, rope: Rope,
     cs = None
     if weights is not None or slot_positions is not None:
         cs = _slots(weights, slot_positions, (st.own.n,), "append:")
-    h = st._call(paged, stream, q, k, v, positions, rope.freqs, q_out, weights, slot_positions)
+    bits8 = isinstance(paged, Paged8)
+    cn, more = None, ()
+    if norm is not None:
+        norm._fits(norm.q_weight if q is not None else None, q_heads, paged.head_dim, "q_weight")
+        norm._fits(norm.k_weight, H, paged.head_dim, "k_weight")
+        cn, more = ctypes.byref(norm.c), norm._tensors
+    h = st._call(paged, stream, q, k, v, positions, rope.freqs, q_out, weights, slot_positions, *more)
     if stream is None and (h or 0) not in rope._on_streams:
         _used_on_current((rope.freqs,), rope._on_streams)
-    rc = load().kv_append(ctypes.byref(paged.c), st._ref, layer, _ref(cq), ctypes.byref(ck), ctypes.byref(cv),
-                          _ref(co), q_heads, types[k.dtype], out_type, positions.data_ptr(), ctypes.byref(rope.c),
-                          _ref(cs), h)
+    if stream is None and more and (h or 0) not in norm._on_streams:
+        _used_on_current(more, norm._on_streams)
+    if bits8:
+        _need(cs is None, "a Paged8 keeps no eviction state")
+        rc = load().kv_append8(ctypes.byref(paged.c), st._ref, layer, _ref(cq), ctypes.byref(ck), ctypes.byref(cv),
+                               _ref(co), q_heads, types[k.dtype], out_type, positions.data_ptr(),
+                               ctypes.byref(rope.c), cn, h)
+    elif cn is not None:
+        rc = load().kv_append_normed(ctypes.byref(paged.c), st._ref, layer, _ref(cq), ctypes.byref(ck),
+                                     ctypes.byref(cv), _ref(co), q_heads, types[k.dtype], out_type,
+                                     positions.data_ptr(), ctypes.byref(rope.c), cn, _ref(cs), h)
+    else:
+        rc = load().kv_append(ctypes.byref(paged.c), st._ref, layer, _ref(cq), ctypes.byref(ck), ctypes.byref(cv),
+                              _ref(co), q_heads, types[k.dtype], out_type, positions.data_ptr(),
+                              ctypes.byref(rope.c), _ref(cs), h)
     if rc != KV_OK:
         _check(rc)
     return q_out
@@ -966,11 +1120,15 @@ def _scale(paged, scale) -> float:
     return paged.head_dim ** -0.5 if scale is None else float(scale)
 
 
-def attend(paged: Paged, step: Step, layer: int, q, scale=None, out=None, lse=None, workspace=None, stream=None):
+def attend(paged: Paged | Paged8, step: Step, layer: int, q, scale=None, out=None, lse=None, workspace=None,
+           stream=None, window: int | None = None, sinks: int = 0):
     """Attention of the new tokens' bf16 q [rows, q_heads, D] over their
-    group's shared prefix and their own pages up to themselves (kv_attend).
-    ``scale``: 1/sqrt(D) unless given.  ``workspace``: a device uint8 tensor of
-    step.attend_workspace_bytes(q_heads) (None: one is allocated for the call).
+    group's shared prefix and their own pages up to themselves (kv_attend; of a
+    Paged8 kv_attend8).  With ``window`` (kv_attend_window) a row sees only the
+    last ``window`` tokens up to its own, counted over prefix and own pages,
+    and the first ``sinks`` of all.  ``scale``: 1/sqrt(D) unless given.
+    ``workspace``: a device uint8 tensor of step.attend_workspace_bytes(q_heads,
+    window, sinks) (None: one is allocated for the call).
     Returns (out bf16 like q, lse float32 [rows, q_heads])."""
     if layer >> 31:
         _int32("layer", layer)
@@ -983,12 +1141,21 @@ def attend(paged: Paged, step: Step, layer: int, q, scale=None, out=None, lse=No
     co = step._rows(out, heads, "out", (torch.bfloat16,))
     if lse.dtype != torch.float32 or not lse.is_contiguous() or lse.shape != (step.n_rows, heads):
         raise KvError(KV_EINVAL, f"lse must be a contiguous float32 device tensor [{step.n_rows}, {heads}]")
+    cw = _window(window, sinks)
     if workspace is None:
-        workspace = _empty(step.attend_workspace_bytes(heads), torch.uint8, q.device, stream)
+        workspace = _empty(step.attend_workspace_bytes(heads, window, sinks), torch.uint8, q.device, stream)
     ws, n_ws = _workspace(workspace)
     h = step._call(paged, stream, q, out, lse, workspace)
-    rc = load().kv_attend(ctypes.byref(paged.c), step._ref, layer, ctypes.byref(cq), heads, _scale(paged, scale),
-                          ctypes.byref(co), lse.data_ptr(), ws, n_ws, h)
+    if isinstance(paged, Paged8):
+        rc = load().kv_attend8(ctypes.byref(paged.c), step._ref, layer, ctypes.byref(cq), heads,
+                               _scale(paged, scale), _ref(cw), ctypes.byref(co), lse.data_ptr(), ws, n_ws, h)
+    elif cw is not None:
+        rc = load().kv_attend_window(ctypes.byref(paged.c), step._ref, layer, ctypes.byref(cq), heads,
+                                     _scale(paged, scale), ctypes.byref(cw), ctypes.byref(co), lse.data_ptr(), ws,
+                                     n_ws, h)
+    else:
+        rc = load().kv_attend(ctypes.byref(paged.c), step._ref, layer, ctypes.byref(cq), heads, _scale(paged, scale),
+                              ctypes.byref(co), lse.data_ptr(), ws, n_ws, h)
     if rc != KV_OK:
         _check(rc)
     return out, lse
@@ -1016,6 +1183,7 @@ def add_weights(paged: Paged, step: Step, layer: int, q, lse, weights=None, pref
     (either may be None: not computed), in place, or into ``out`` /
     ``prefix_out`` (with weights None: from zero).  ``lse``: what attend
     returned.  Returns (own sums, prefix sums)."""
+    _bf16_pool(paged, "add_weights")
     if layer >> 31:
         _int32("layer", layer)
     torch = _t()
@@ -1042,6 +1210,7 @@ def evict(paged: Paged, tables: Tables, layer_begin: int, layer_end: int, weight
     [layers, sequences, H or 1, >= keep] are given.  ``workspace``: a device
     uint8 tensor of tables.evict_workspace_bytes(...) (None: allocated for the
     call).  Returns the new lengths, an int32 tensor [sequences]."""
+    _bf16_pool(paged, "evict")
     if (layer_begin | layer_end | keep | recent) >> 31:
         _int32("layer, keep or recent", layer_begin, layer_end, keep, recent)
     torch = _t()
@@ -1075,3 +1244,57 @@ def evict(paged: Paged, tables: Tables, layer_begin: int, layer_end: int, weight
     if rc != KV_OK:
         _check(rc)
     return out_lens
+
+
+def _pack(call, source, tables, target, to_table, layer_begin, layer_end, stream) -> None:
+    torch = _t()
+    if layer_end is None:
+        layer_end = source.num_layers
+    if (layer_begin | layer_end) >> 31:
+        _int32("layer", layer_begin, layer_end)
+    tables._check(source)
+    table, stride = None, 0
+    if to_table is not None:
+        if to_table.dtype != torch.int32 or to_table.dim() != 2 or to_table.size(0) != tables.n or not (
+                to_table.stride(1) == 1 or to_table.size(1) <= 1):
+            raise KvError(KV_EINVAL, f"to_table must be an int32 device tensor [{tables.n}, entries], entries contiguous")
+        if tables.max_len > to_table.size(1) * source.page_size:
+            raise KvError(KV_ERANGE, f"max_len {tables.max_len} beyond to_table ({to_table.size(1)} pages of "
+                                     f"{source.page_size})")
+        _need(tables.n <= 1 or to_table.stride(0) >= to_table.size(1), "to_table's rows must not overlap")
+        table, stride = to_table.data_ptr(), to_table.stride(0) if tables.n > 1 else to_table.size(1)
+    used = (*source._arrays, *target._arrays, tables.table, tables.lens, to_table)
+    dev = _here(*used)
+    if stream is None:
+        h = torch._C._cuda_getCurrentRawStream(dev) or None
+        for p in (source, target):
+            if (h or 0) not in p._on_streams:
+                _used_on_current(p._arrays, p._on_streams)
+    else:
+        _used_on(stream, used)
+        h = _stream_handle(stream)
+    rc = call(ctypes.byref(source.c), ctypes.byref(tables.c), ctypes.byref(target.c), table, stride, layer_begin,
+              layer_end, h)
+    if rc != KV_OK:
+        _check(rc)
+
+
+def pack8(paged: Paged, tables: Tables, paged8: Paged8, to_table=None, layer_begin: int = 0,
+          layer_end: int | None = None, stream=None) -> None:
+    """The cached tokens of ``tables``' sequences from the bf16 pool's pages into
+    the 8-bit pool's (kv_pack8), of layers [layer_begin, layer_end) (all unless
+    given): into the pages of ``to_table``, int32 [sequences, entries], or
+    those of the same ids.  Each block's scale is made from the tokens it
+    holds.  After retrieve it brings chunks into an 8-bit pool."""
+    _bf16_pool(paged, "pack8's source")
+    _need(isinstance(paged8, Paged8), "pack8 needs a Paged8 to write to")
+    _pack(load().kv_pack8, paged, tables, paged8, to_table, layer_begin, layer_end, stream)
+
+
+def unpack8(paged8: Paged8, tables: Tables, paged: Paged, to_table=None, layer_begin: int = 0,
+            layer_end: int | None = None, stream=None) -> None:
+    """The reverse of pack8 (kv_unpack8): byte * scale as bf16, exactly, into the
+    bf16 pool's pages, for store, add_weights or evict."""
+    _bf16_pool(paged, "unpack8's target")
+    _need(isinstance(paged8, Paged8), "unpack8 needs a Paged8 to read from")
+    _pack(load().kv_unpack8, paged8, tables, paged, to_table, layer_begin, layer_end, stream)

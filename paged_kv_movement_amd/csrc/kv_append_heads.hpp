@@ -1,0 +1,535 @@
+// kv_append_heads.hpp -- append with each head of q and k normalised before it
+// is rotated, and append into an 8-bit pool.
+//
+// Norm: y = (x - c) / sqrt(mean((x - c)^2) + eps) * w over a head's elements,
+// c = 0 or their mean.  The sums are float32, two passes over registers for the
+// centered form (mean of squares less square of mean would cancel); where the
+// squares leave float32's range the head is first scaled by a power of two.
+// Then the rotation of kv_append.hpp, and one rounding.
+//
+// A head lies in a group of G lanes, the next power of two to its units, so
+// that its sums are exchanges within a wave and no head waits for another.
+//
+// append_heads_rows   one workgroup per token, for q (and, into a bf16 pool, k
+//                     and v): as append_rows, memory-bound;
+// append8             those workgroups for q, and behind them one per (sequence,
+//                     page, some of the heads) for k and v: a wave takes one
+//                     head's K or V of the page, all its new tokens, finds the
+//                     block's scale and writes the bytes.
+#pragma once
+
+#include "kv_append.hpp"
+#include "kv_pool8.hpp"
+
+namespace kvmove {
+
+enum : int { kNormNone = 0, kNormRms = 1, kNormCentered = 2 };
+
+struct NormArg {
+    uint64_t q_weight, k_weight;       // float32 [heads][dim], or 0: ones
+    int64_t q_stride, k_stride;        // elements from head to head
+    int32_t kind;
+    float eps;
+};
+
+struct AppendHeadsArgs {
+    AppendArgs a;
+    NormArg norm;
+    ScalesArg scales;                  // of an 8-bit pool
+    int32_t lanes_log2, per;           // lanes G of a head of q or k, its units of a lane
+    int32_t v_units, v_lanes_log2, v_per;   // append8: the same for a head of v, in units of two vectors
+    uint32_t token_items;              // append8: workgroups [0, token_items) take a token's q
+    int32_t pages, splits;             // append8: pages of a sequence, workgroups that share a page's heads
+};
+
+__device__ __forceinline__ float sum_over(float x, int lanes)
+{
+    for (int d = 1; d < lanes; d *= 2) x += __shfl_xor(x, d);
+    return x;
+}
+
+__device__ __forceinline__ float max_over(float x, int lanes)
+{
+    for (int d = 1; d < lanes; d *= 2) x = __builtin_fmaxf(x, __shfl_xor(x, d));
+    return x;
+}
+
+// A unit's two vectors as they lie in memory; without a second one, the first again.
+template <class TI, int kVec>
+struct RawUnit {
+    Vec<TI, kVec> x, y;
+};
+
+template <class TI, int kVec>
+__device__ __forceinline__ RawUnit<TI, kVec> load_raw(const TI* head, const Unit& u)
+{
+    return {*reinterpret_cast<const Vec<TI, kVec>*>(head + u.d0), *reinterpret_cast<const Vec<TI, kVec>*>(head + u.d1)};
+}
+
+// The same as float32; n of the 2 kVec elements count, the others are 0.
+template <int kVec>
+struct Values {
+    float x[2 * kVec];
+};
+
+template <class TI, int kVec>
+__device__ __forceinline__ Values<kVec> values_of(const RawUnit<TI, kVec>& r, const Unit& u, bool live)
+{
+    Values<kVec> v;
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+        v.x[i] = live ? float(r.x.x[i]) : 0.0f;
+        v.x[kVec + i] = live && u.kind == kUnitPairs ? float(r.y.x[i]) : 0.0f;
+    }
+    return v;
+}
+
+__device__ __forceinline__ int values_in(const Unit& u, int vec, bool live)
+{
+    return !live ? 0 : u.kind == kUnitPairs ? 2 * vec : vec;
+}
+
+// What a head is normalised with: (x * scale - c) * r.
+struct HeadNorm {
+    float scale, c, r;
+};
+
+// Of a group of lanes: each(f) calls f with every (values, number of them that
+// count) of the lane's units.  Squares leave float32 where a head's largest
+// magnitude is beyond 2^+-60; it is then brought near 1 by a power of two (below,
+// only where eps does not outweigh the squares anyway, and no further than eps
+// stays finite).  A head with an infinity or a NaN takes the formula as it is.
+template <int kVec, class Each>
+__device__ __forceinline__ HeadNorm head_norm(const NormArg& n, int dim, int lanes, Each&& each)
+{
+    float big = 0.0f;
+    bool odd = false;
+    each([&](const Values<kVec>& v, int count) {
+#pragma unroll
+        for (int i = 0; i < 2 * kVec; ++i) {
+            const float a = __builtin_fabsf(v.x[i]);
+            odd = odd || !(a < __builtin_inff());
+            big = __builtin_fmaxf(big, a);
+        }
+    });
+    big = max_over(odd ? __builtin_inff() : big, lanes);
+    float scale = 1.0f;
+    if (big < __builtin_inff() && (big > 0x1p60f || (big < 0x1p-60f && n.eps < 0x1p-96f))) {
+        const int e = 127 - int(__float_as_uint(big) >> 23), most = n.eps == 0.0f ? 126 : 60;
+        scale = exp2_int(clamp_i32(e, -126, most));
+    }
+    float c = 0.0f;
+    if (n.kind == kNormCentered) {
+        each([&](const Values<kVec>& v, int count) {
+#pragma unroll
+            for (int i = 0; i < 2 * kVec; ++i) c = __builtin_fmaf(v.x[i], scale, c);
+        });
+        c = sum_over(c, lanes) / float(dim);
+    }
+    float q = 0.0f;
+    each([&](const Values<kVec>& v, int count) {
+#pragma unroll
+        for (int i = 0; i < 2 * kVec; ++i) {
+            const float d = i < count ? __builtin_fmaf(v.x[i], scale, -c) : 0.0f;
+            q = __builtin_fmaf(d, d, q);
+        }
+    });
+    q = sum_over(q, lanes) / float(dim) + n.eps * scale * scale;
+    return {scale, c, 1.0f / __builtin_sqrtf(q)};
+}
+
+// The unit normalised; w: weights of its elements.
+template <int kVec>
+__device__ __forceinline__ void normalise(Values<kVec>& v, const HeadNorm& h, const RawUnit<float, kVec>& w)
+{
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+        v.x[i] = __builtin_fmaf(v.x[i], h.scale, -h.c) * h.r * w.x.x[i];
+        v.x[kVec + i] = __builtin_fmaf(v.x[kVec + i], h.scale, -h.c) * h.r * w.y.x[i];
+    }
+}
+
+// Weights of a unit of head `head` of q or k; ones where there are none.
+template <int kVec>
+__device__ __forceinline__ RawUnit<float, kVec> load_weights(const NormArg& n, bool k, int head, const Unit& u)
+{
+    const uint64_t base = k ? n.k_weight : n.q_weight;
+    RawUnit<float, kVec> w;
+    if (base == 0) {
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) w.x.x[i] = w.y.x[i] = 1.0f;
+        return w;
+    }
+    return load_raw<float, kVec>(reinterpret_cast<const float*>(base) + head * (k ? n.k_stride : n.q_stride), u);
+}
+
+// The unit rotated; angle(i): cosine and sine of its i-th pair.
+template <int kVec, class Angle>
+__device__ __forceinline__ void rotate(Values<kVec>& v, const Unit& u, Angle&& angle)
+{
+    // one form for both layouts, by selects: with the values changed in either of two branches the compiler keeps them
+    // in memory
+    const bool pairs = u.kind == kUnitPairs, turns = u.kind != kUnitPass;
+    Values<kVec> o;
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+        const int j = kVec > 1 ? i ^ 1 : i;
+        const float2 c = turns ? angle(kVec > 1 && !pairs ? i / 2 : i) : float2{1.0f, 0.0f};
+        const float a = v.x[i], b = v.x[kVec + i];
+        const float other = pairs ? b : v.x[j];
+        const float turned = __builtin_fmaf(a, c.x, pairs || i % 2 == 0 ? -(other * c.y) : other * c.y);
+        o.x[i] = turns ? turned : a;
+        o.x[kVec + i] = __builtin_fmaf(b, c.x, a * c.y);
+    }
+    v = o;
+}
+
+// Cosine and sine of pair j at a position, formed as kv_append.hpp says.
+__device__ __forceinline__ float2 angle_of(const AppendArgs& a, int32_t pos, int j)
+{
+    const double turns_per_radian = 0.15915494309189533577;
+    const double f = gptr<const __attribute__((address_space(1))) double>(a.freqs)[j];
+    const double turns = double(pos) * (f * turns_per_radian);
+    const float frac = float(turns - __builtin_rint(turns));
+    float sn, cn;
+    sincospif(2.0f * frac, &sn, &cn);
+    return {cn * a.gain, sn * a.gain};
+}
+
+template <class TO, int kVec>
+__device__ __forceinline__ void put_values(TO* head, const Unit& u, const Values<kVec>& v)
+{
+    Vec<TO, kVec> x, y;
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+        x.x[i] = TO(v.x[i]);
+        y.x[i] = TO(v.x[kVec + i]);
+    }
+    *reinterpret_cast<Vec<TO, kVec>*>(head + u.d0) = x;
+    if (u.kind == kUnitPairs) *reinterpret_cast<Vec<TO, kVec>*>(head + u.d1) = y;
+}
+
+// One token: its heads of q, and with kKv those of k and its v, into a bf16
+// pool.  cs: room for its angles.  As in append_rows, the first heads' values
+// are asked for before the owner, the page and the angles are known.
+template <class TI, class TO, int kVec, bool kKv>
+__device__ __forceinline__ void token_heads(const AppendHeadsArgs& h, int32_t r, float2* cs)
+{
+    constexpr int kAhead = 2;                      // heads of a lane in flight
+    const AppendArgs& a = h.a;
+    const int32_t tid = threadIdx.x;
+    const int dim = a.pool.dim, kv_heads = kKv ? a.pool.heads : 0, lanes = 1 << h.lanes_log2;
+    const int heads = a.q_heads + kv_heads, stride = kAppendBlock >> h.lanes_log2;
+    const int first = tid >> h.lanes_log2, lane = tid & (lanes - 1);
+    auto source = [&](int head) {
+        const bool k = head >= a.q_heads;
+        return reinterpret_cast<const TI*>(k ? a.k : a.q) + r * (k ? a.k_row : a.q_row) +
+               (k ? head - a.q_heads : head) * (k ? a.k_head : a.q_head);
+    };
+    auto unit = [&](int i) { return head_unit<kVec>(i < a.units ? i : 0, a.rot, a.interleaved != 0); };
+    auto weights = [&](int head, const Unit& u) {
+        const bool k = head >= a.q_heads;
+        return load_weights<kVec>(h.norm, k, k ? head - a.q_heads : head, u);
+    };
+    const Unit u0 = unit(lane);
+    RawUnit<TI, kVec> raw[kAhead];
+    RawUnit<float, kVec> w[kAhead];
+#pragma unroll
+    for (int x = 0; x < kAhead; ++x) {
+        const int head = first + x * stride;
+        if (head >= heads) continue;
+        raw[x] = load_raw<TI, kVec>(source(head), u0);
+        if (h.norm.kind != kNormNone) w[x] = weights(head, u0);
+    }
+    Vec<TI, kVec> v{};
+    const int v_vectors = kv_heads * (dim / kVec);
+    auto v_at = [&](int i) {
+        const int head = int((uint64_t(uint32_t(i)) * a.vec_magic) >> a.vec_shift);
+        return reinterpret_cast<const TI*>(a.v) + r * a.v_row + head * a.v_head + (i - head * (dim / kVec)) * kVec;
+    };
+    if (tid < v_vectors) v = *reinterpret_cast<const Vec<TI, kVec>*>(v_at(tid));
+    const int32_t pos = gptr<const gi32>(a.positions)[r];
+    uint64_t kd = 0, vd = 0;
+    int32_t slot = 0, s = -1;
+    if constexpr (kKv) {
+        // where k and v go; 0: nowhere (a row of no sequence, no slot left, a bad page)
+        const uint64_t kb = gptr<const gu64>(a.pool.k_pages)[a.pool.layer];
+        const uint64_t vb = gptr<const gu64>(a.pool.v_pages)[a.pool.layer];
+        const RowOwner o = row_owner(a.step, r);
+        s = o.s;
+        slot = o.len - o.count + (r - o.first);
+        if (o.s >= 0 && slot >= 0) {
+            const uint32_t pi = page_of(a.pool, uint32_t(slot));
+            const int32_t page = gptr<const gi32>(a.step.own.table)[o.s * a.step.own.stride + pi];
+            if (uint32_t(page) >= a.pool.num_pages) {
+                raise_fault(kFaultPage);
+            } else if (bad_addr(kb) || bad_addr(vb)) {
+                raise_fault(kFaultPool);
+            } else {
+                const int64_t row = int64_t(page) * a.pool.page_size + (uint32_t(slot) - pi * a.pool.page_size);
+                kd = kb + uint64_t(row) * a.pool.heads * dim * 2;
+                vd = vb + uint64_t(row) * a.pool.heads * dim * 2;
+            }
+        }
+    }
+    for (int j = tid; j < a.rot / 2; j += kAppendBlock) cs[j] = angle_of(a, pos, j);
+    __syncthreads();
+    auto finish = [&](int head, const RawUnit<TI, kVec>& r0, const RawUnit<float, kVec>& w0) {
+        const TI* src = source(head);
+        const bool live = lane < a.units;
+        auto put = [&](const Unit& u, Values<kVec>& x) {
+            rotate<kVec>(x, u, [&](int j) { return cs[u.pair + j]; });
+            if (head < a.q_heads)
+                put_values<TO, kVec>(reinterpret_cast<TO*>(a.q_out) + r * a.o_row + head * a.o_head, u, x);
+            else if (kd != 0)
+                put_values<__bf16, kVec>(reinterpret_cast<__bf16*>(kd) + (head - a.q_heads) * dim, u, x);
+        };
+        Values<kVec> x0 = values_of<TI, kVec>(r0, u0, live);
+        HeadNorm n{};
+        if (h.norm.kind != kNormNone) {
+            n = head_norm<kVec>(h.norm, dim, lanes, [&](auto&& f) {
+                f(x0, values_in(u0, kVec, live));
+                for (int i = lane + lanes; i < h.per * lanes; i += lanes) {
+                    const Unit u = unit(i);
+                    f(values_of<TI, kVec>(load_raw<TI, kVec>(src, u), u, i < a.units), values_in(u, kVec, i < a.units));
+                }
+            });
+            normalise<kVec>(x0, n, w0);
+        }
+        if (live) put(u0, x0);
+        for (int i = lane + lanes; i < a.units; i += lanes) {
+            const Unit u = unit(i);
+            Values<kVec> x = values_of<TI, kVec>(load_raw<TI, kVec>(src, u), u, true);
+            if (h.norm.kind != kNormNone) normalise<kVec>(x, n, weights(head, u));
+            put(u, x);
+        }
+    };
+    // the lanes of a head go through this together, whatever the wave's other heads do
+    for (int base = 0; base < heads; base += kAhead * stride) {
+        if (base > 0)
+#pragma unroll
+            for (int x = 0; x < kAhead; ++x) {
+                const int head = base + first + x * stride;
+                if (head >= heads) continue;
+                raw[x] = load_raw<TI, kVec>(source(head), u0);
+                if (h.norm.kind != kNormNone) w[x] = weights(head, u0);
+            }
+#pragma unroll
+        for (int x = 0; x < kAhead; ++x)
+            if (base + first + x * stride < heads) finish(base + first + x * stride, raw[x], w[x]);
+    }
+    if (kd == 0) return;
+    for (int i = tid; i < v_vectors; i += kAppendBlock) {
+        if (i != tid) v = *reinterpret_cast<const Vec<TI, kVec>*>(v_at(i));
+        Vec<__bf16, kVec> o;
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) o.x[e] = __bf16(float(v.x[e]));
+        *reinterpret_cast<Vec<__bf16, kVec>*>(reinterpret_cast<__bf16*>(vd) + i * kVec) = o;
+    }
+    if (a.weights != 0)
+        for (int x = tid; x < a.w_heads; x += kAppendBlock) {
+            const int64_t at = (int64_t(s) * a.w_heads + x) * a.w_cap + slot;
+            gptr<gf32>(a.weights)[at] = 0.0f;
+            gptr<gi32>(a.slot_positions)[at] = pos;
+        }
+}
+
+template <class TI, class TO, int kVec>
+__global__ __launch_bounds__(kAppendBlock) void append_heads_rows(AppendHeadsArgs h)
+{
+    __shared__ float2 cs[kMaxRot / 2];
+    token_heads<TI, TO, kVec, true>(h, blockIdx.x, cs);
+}
+
+constexpr int kPageAngles = 4096;      // angles of a page's new tokens kept in LDS, else each is formed where it is used
+constexpr int kHeldUnits = 4;          // units of a lane kept between the look for the scale and the bytes
+
+// New tokens of one page of a sequence, heads [h0, h1): a wave takes one head's K or V at a time.
+template <class TI, int kVec>
+__device__ __forceinline__ void page_heads(const AppendHeadsArgs& h, uint32_t item, float2* cs)
+{
+    const AppendArgs& a = h.a;
+    const PoolArg& p = a.pool;
+    const int dim = p.dim, half = a.rot / 2, lane = threadIdx.x & 63;
+    const int split = int(item % uint32_t(h.splits)), at = int(item / uint32_t(h.splits));
+    const int32_t s = at / h.pages;
+    const Rows rows = seq_rows(a.step, s);
+    const int32_t len = table_len(a.step.own, s);
+    const int32_t ahead = len - rows.count, begin = ahead < 0 ? 0 : ahead;       // slots before the new tokens
+    const int32_t pi = int32_t(page_of(p, uint32_t(begin))) + (at - s * h.pages);
+    const int64_t slot0 = int64_t(pi) * p.page_size;                             // may be far past len
+    if (rows.count == 0 || slot0 >= len) return;
+    const int32_t lo = slot0 > begin ? int32_t(slot0) : begin;
+    const int32_t hi = len - slot0 < p.page_size ? len : int32_t(slot0) + int32_t(p.page_size);
+    const int n = hi - lo, old = lo - int32_t(slot0);
+    const int64_t row0 = rows.first + int64_t(lo - ahead);
+    const int32_t page = __builtin_amdgcn_readfirstlane(gptr<const gi32>(a.step.own.table)[s * a.step.own.stride + pi]);
+    const LayerAt l = layer_at<true>(p, h.scales);
+    if (uint32_t(page) >= p.num_pages) {
+        raise_fault(kFaultPage);
+        return;
+    }
+    if (bad_layer<true>(l)) {
+        raise_fault(kFaultPool);
+        return;
+    }
+    const bool kept = int64_t(n) * half <= kPageAngles;
+    if (kept && half > 0) {
+        for (int i = threadIdx.x; i < n * half; i += kAppendBlock) {
+            const int tok = i / half;
+            cs[i] = angle_of(a, gptr<const gi32>(a.positions)[row0 + tok], i - tok * half);
+        }
+        __syncthreads();
+    }
+    const int heads = (int(p.heads) + h.splits - 1) / h.splits, h0 = split * heads;
+    const int h1 = h0 + heads < int(p.heads) ? h0 + heads : int(p.heads);
+#pragma unroll 1
+    for (int task = 2 * h0 + (threadIdx.x >> 6); task < 2 * h1; task += kAppendBlock / 64) {
+        const int head = __builtin_amdgcn_readfirstlane(task >> 1);
+        const bool is_v = __builtin_amdgcn_readfirstlane(task & 1) != 0;
+        const int lg = is_v ? h.v_lanes_log2 : h.lanes_log2, lanes = 1 << lg, per = is_v ? h.v_per : h.per;
+        const int units = is_v ? h.v_units : a.units, steps = ((n + (64 >> lg) - 1) >> (6 - lg)) * per;
+        const uint64_t scale_at = (is_v ? l.v_scales : l.k_scales) + (uint64_t(page) * p.heads + head) * 4;
+        const uint64_t dst = (is_v ? l.v : l.k) + (uint64_t(page) * p.page_size * p.heads + head) * dim;
+        const uint64_t row_bytes = uint64_t(p.heads) * dim;
+        const float was = *gptr<const gf32>(scale_at);
+        const TI* base = reinterpret_cast<const TI*>(is_v ? a.v : a.k) + row0 * (is_v ? a.v_row : a.k_row) +
+                         head * (is_v ? a.v_head : a.k_head);
+        const int64_t row = is_v ? a.v_row : a.k_row;
+        struct Place {
+            int tok, i;
+            bool live;
+        };
+        auto place = [&](int step) {
+            const int round = per == 1 ? step : step / per;
+            Place x;
+            x.tok = (round << (6 - lg)) + (lane >> lg);
+            x.i = (lane & (lanes - 1)) + ((step - round * per) << lg);
+            x.live = x.tok < n && x.i < units;
+            return x;
+        };
+        auto unit = [&](const Place& x) {
+            const int i = x.i < units ? x.i : 0;
+            return is_v ? Unit{kUnitPairs, i * kVec, dim / 2 + i * kVec, 0}
+                        : head_unit<kVec>(i, a.rot, a.interleaved != 0);
+        };
+        auto load = [&](const Place& x, const Unit& u) {
+            return load_raw<TI, kVec>(base + int64_t(x.tok < n ? x.tok : 0) * row, u);
+        };
+        // a step's values as they are to be cached; all lanes together
+        auto ready = [&](const Place& x, const Unit& u, const RawUnit<TI, kVec>& raw) {
+            Values<kVec> v = values_of<TI, kVec>(raw, u, x.live);
+            if (is_v) return v;
+            if (h.norm.kind != kNormNone) {
+                const HeadNorm m = head_norm<kVec>(h.norm, dim, lanes, [&](auto&& f) {
+                    f(v, values_in(u, kVec, x.live));
+                    for (int k = 1; k < per; ++k) {             // the head's other units, in whatever order
+                        Place y = x;
+                        y.i = x.i + (k << lg);
+                        if (y.i >= per << lg) y.i -= per << lg;
+                        y.live = y.tok < n && y.i < units;
+                        const Unit w = unit(y);
+                        f(values_of<TI, kVec>(load(y, w), w, y.live), values_in(w, kVec, y.live));
+                    }
+                });
+                normalise<kVec>(v, m, load_weights<kVec>(h.norm, true, head, u));
+            }
+            const int tok = x.tok < n ? x.tok : 0;
+            if (kept) {
+                rotate<kVec>(v, u, [&](int j) { return cs[tok * half + u.pair + j]; });
+            } else {
+                const int32_t pos = gptr<const gi32>(a.positions)[row0 + tok];
+                rotate<kVec>(v, u, [&](int j) { return angle_of(a, pos, u.pair + j); });
+            }
+            return v;
+        };
+        auto largest = [&](const Place& x, const Unit& u, const Values<kVec>& v, float m) {
+            const int count = values_in(u, kVec, x.live);
+#pragma unroll
+            for (int i = 0; i < 2 * kVec; ++i)
+                if (i < count) m = __builtin_fmaxf(m, finite_magnitude(v.x[i]));
+            return m;
+        };
+        RawUnit<TI, kVec> raw[kHeldUnits];
+        Values<kVec> held[kHeldUnits];
+#pragma unroll
+        for (int i = 0; i < kHeldUnits; ++i) {
+            if (i >= 2 && steps <= 2) break;
+            const Place x = place(i);
+            raw[i] = load(x, unit(x));
+        }
+        float most = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kHeldUnits; ++i) {
+            if (i >= steps) break;
+            const Place x = place(i);
+            const Unit u = unit(x);
+            held[i] = ready(x, u, raw[i]);
+            most = largest(x, u, held[i], most);
+        }
+#pragma unroll 1
+        for (int i = kHeldUnits; i < steps; ++i) {
+            const Place x = place(i);
+            const Unit u = unit(x);
+            most = largest(x, u, ready(x, u, load(x, u)), most);
+        }
+        int e = scale_exponent(wave_max(most));
+        const int e_was = stored_exponent(was);
+        if (old > 0 && e_was > e) e = e_was;
+        if (old > 0 && e > e_was) {                             // the tokens that are there, held anew
+            const float factor = exp2_int(e - e_was > 30 ? -30 : e_was - e);     // 448 2^-30 is below the least byte
+            const int vectors = dim / 16;
+            for (int i = lane; i < old * vectors; i += 64) {
+                const int tok = i / vectors;
+                const uint64_t at16 = dst + tok * row_bytes + (i - tok * vectors) * 16;
+                u32x4 b = *gptr<const gvec4>(at16);
+#pragma unroll
+                for (int w = 0; w < 4; ++w) b[w] = bytes_under(b[w], factor);
+                *gptr<gvec4>(at16) = b;
+            }
+        }
+        const float inv = exp2_int(-e);
+        auto put = [&](const Place& x, const Unit& u, const Values<kVec>& v) {
+            if (!x.live) return;
+            const uint64_t to = dst + (old + x.tok) * row_bytes;
+            float y[2 * kVec];
+#pragma unroll
+            for (int i = 0; i < 2 * kVec; ++i) y[i] = for_byte(v.x[i], inv);
+            if constexpr (kVec == 8) {
+                *gptr<gvec2>(to + u.d0) = u32x2{bytes_of(y[0], y[1], y[2], y[3]), bytes_of(y[4], y[5], y[6], y[7])};
+                if (u.kind == kUnitPairs)
+                    *gptr<gvec2>(to + u.d1) =
+                        u32x2{bytes_of(y[8], y[9], y[10], y[11]), bytes_of(y[12], y[13], y[14], y[15])};
+            } else {
+                const uint32_t b = bytes_of(y[0], y[1], 0.0f, 0.0f);
+                *gptr<gbyte>(to + u.d0) = uint8_t(b);
+                if (u.kind == kUnitPairs) *gptr<gbyte>(to + u.d1) = uint8_t(b >> 8);
+            }
+        };
+#pragma unroll
+        for (int i = 0; i < kHeldUnits; ++i) {
+            if (i >= steps) break;
+            const Place x = place(i);
+            put(x, unit(x), held[i]);
+        }
+#pragma unroll 1
+        for (int i = kHeldUnits; i < steps; ++i) {
+            const Place x = place(i);
+            const Unit u = unit(x);
+            put(x, u, ready(x, u, load(x, u)));
+        }
+        if (lane == 0) *gptr<gf32>(scale_at) = exp2_int(e);
+    }
+}
+
+template <class TI, class TO, int kVec>
+__global__ __launch_bounds__(kAppendBlock) void append8_rows(AppendHeadsArgs h)
+{
+    __shared__ float2 cs[kPageAngles];
+    if (blockIdx.x < h.token_items)
+        token_heads<TI, TO, kVec, false>(h, blockIdx.x, cs);
+    else
+        page_heads<TI, kVec>(h, blockIdx.x - h.token_items, cs);
+}
+
+}  // namespace kvmove

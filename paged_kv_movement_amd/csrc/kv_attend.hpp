@@ -27,7 +27,7 @@
 // weights.  A third part would keep all 24 bits for a third more products.
 #pragma once
 
-#include "kv_step.hpp"
+#include "kv_pool8.hpp"
 
 namespace kvmove {
 
@@ -38,9 +38,18 @@ constexpr int kAttendRows = 16;        // columns of one matrix product: the nar
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
+// What the kernels are made for besides a head's size: a pool of bytes with
+// scales, and a window.
+template <bool kBytePool, bool kWindow>
+struct Form {
+    static constexpr bool byte = kBytePool, win = kWindow;
+};
+
 struct AttendArgs {
     PoolArg pool;
     StepArg step;
+    ScalesArg scales;              // of an 8-bit pool
+    int32_t window, sinks;         // a windowed form's
     uint64_t q, out, lse;          // bf16 rows [n_rows][q_heads][dim] with strides, bf16, float32 [n_rows][q_heads]
     int64_t q_row, q_head;         // strides in elements
     int64_t o_row, o_head;
@@ -54,8 +63,51 @@ struct AttendArgs {
     int32_t slots;                 // prefix_pieces + own_pieces
     uint32_t prefix_items;         // workgroups [0, prefix_items) take prefix pieces
     int32_t prefix_wide, own_wide; // which form a piece takes
+    int32_t own_tile_rows;         // rows of an own item, a power of two
     int32_t direct;                // one slot in all: out and lse are written at once, nothing is left to join
 };
+
+// With a window a row at position p (its own token counted from the start of
+// the prefix) sees the tokens t <= p with t > p - window or t < sinks.  What
+// some row of an item sees of a table is then a head [0, sink) and a run that
+// begins at the first row's window.  A span numbers the two without the gap
+// between them, whole 64s left out, so that no tile lies in both: pieces are cut
+// from what is seen, wherever in the table it lies.
+struct Span {
+    int32_t head, gap, n; // token u is u < head ? u : u + gap; n in all
+};
+
+constexpr int kSpanTile = 64;
+
+// Tokens [0, sink) and [lo, end) of a table.
+__device__ __forceinline__ Span make_span(int32_t sink, int32_t lo, int32_t end)
+{
+    const int32_t head = int32_t((uint32_t(sink) + kSpanTile - 1) & ~uint32_t(kSpanTile - 1));
+    const int32_t begin = lo & ~(kSpanTile - 1);
+    const bool apart = lo < end && begin > head;
+    const int32_t gap = apart ? begin - head : 0;
+    const int32_t n = lo < end ? end - gap : sink < end ? sink : end;
+    return {apart ? head : 0, gap, n};
+}
+
+template <class F>
+__device__ __forceinline__ int32_t token_at(const Span& s, int32_t u)
+{
+    if constexpr (!F::win) return u;
+    return u < s.head ? u : u + s.gap;
+}
+
+// Tokens that a row sees of a table: [0, end), and with a window of those the ones from lo on or below sink.
+struct Seen {
+    int32_t end, lo, sink;
+};
+
+template <class F>
+__device__ __forceinline__ bool sees(const Seen& s, int32_t t)
+{
+    if constexpr (F::win) return t < s.end && (t >= s.lo || t < s.sink);
+    return t < s.end;
+}
 
 // What one workgroup does: rows [row0, row0 + n_rows) of the flattened (new
 // token, head of the KV head's group), against tokens [t0, t1) of a table.
@@ -68,6 +120,11 @@ struct AttendItem {
     int32_t t0, t1;       // tokens of the piece, t1 cut to the length
     int32_t len;          // tokens of the table's row
     int32_t slot;
+    // with a window: t0 and t1 count the tokens of `span`, not those of the table
+    Span span;
+    int32_t sink;         // the table's tokens [0, sink) are seen by every row that comes after them
+    int32_t seq0, seqs;   // the sequences of a prefix's group
+    int32_t start, past;  // of up to 64 of them, in lane i the i-th's: first row, tokens ahead of it
 };
 
 __device__ __forceinline__ AttendItem attend_item(const AttendArgs& a, uint32_t b, int wide_rows)
@@ -96,6 +153,7 @@ __device__ __forceinline__ AttendItem attend_item(const AttendArgs& a, uint32_t 
     it.t0 = piece * tokens;
     it.t1 = it.len - it.t0 < tokens ? it.len : it.t0 + tokens;
     it.slot = it.prefix ? piece : a.prefix_pieces + piece;
+    it.sink = 0;
     return it;
 }
 
@@ -112,6 +170,146 @@ __device__ __forceinline__ int32_t visible_end(const AttendArgs& a, const Attend
 {
     if (it.prefix) return it.len;
     return clamp_i32(it.len - it.rows.count + new_token(a, it.flat0 + f) + 1, 0, it.len);
+}
+
+// First token that is inside the window of a row at position p.
+__device__ __forceinline__ int32_t window_begin(const AttendArgs& a, int32_t p)
+{
+    return p < a.window ? 0 : p - a.window + 1;
+}
+
+// Own tokens that are among the first `sinks`, behind a prefix of `ahead`; no table holds more than 2^30.
+__device__ __forceinline__ int32_t own_sink(const AttendArgs& a, int32_t ahead)
+{
+    return clamp_i32(a.sinks - ahead, 0, 1 << 30);
+}
+
+// Prefix tokens ahead of sequence s.
+__device__ __forceinline__ int32_t prefix_ahead(const StepArg& a, int32_t s)
+{
+    if (a.prefix.n == 0) return 0;
+    const int32_t i0 = ranges_around(a.group_start, a.prefix.n, s), i = i0 + int32_t(threadIdx.x & 63);
+    int32_t b = 0, e = 0, n = 0;
+    if (i < a.prefix.n) {
+        b = gptr<const gi32>(a.group_start)[i];
+        e = gptr<const gi32>(a.group_start)[i + 1];
+        n = table_len(a.prefix, i);
+    }
+    const uint64_t m = __ballot(b <= s && s < e);
+    return m == 0 ? 0 : __builtin_amdgcn_readlane(n, __builtin_ctzll(m));
+}
+
+// Position in its own pages of a sequence's first new token; one that the
+// lengths leave no slot for counts as standing right behind the prefix.
+__device__ __forceinline__ int32_t first_position(int32_t len, int32_t count) { return len - count; }
+
+__device__ __forceinline__ int32_t row_position(int32_t first, int32_t i) { return first + i < -1 ? -1 : first + i; }
+
+// What a group's rows see of a prefix of len tokens: the sinks, and all from
+// the first window of its sequences on.  Lane i gets the i-th of the first 64
+// sequences.
+struct GroupWindow {
+    Span span;
+    int32_t seq0, seqs, start, past;
+};
+
+__device__ __forceinline__ GroupWindow group_window(const AttendArgs& a, int32_t g, int32_t len)
+{
+    const StepArg& st = a.step;
+    const int32_t lane = threadIdx.x & 63;
+    GroupWindow w;
+    w.seq0 = clamp_i32(__builtin_amdgcn_readfirstlane(gptr<const gi32>(st.group_start)[g]), 0, st.own.n);
+    w.seqs = clamp_i32(__builtin_amdgcn_readfirstlane(gptr<const gi32>(st.group_start)[g + 1]), w.seq0, st.own.n) - w.seq0;
+    int32_t least = 0x7FFFFFFF;                                // first position of the group's new tokens
+    w.start = 0x7FFFFFFF;
+    w.past = 0;
+    for (int32_t i = lane; i < w.seqs; i += 64) {
+        const Rows r = seq_rows(st, w.seq0 + i);
+        const int32_t p = first_position(table_len(st.own, w.seq0 + i), r.count);
+        if (i == lane) {
+            w.start = r.first;
+            w.past = p;
+        }
+        if (r.count > 0 && p < least) least = p;
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const int32_t x = __shfl_xor(least, d);
+        least = x < least ? x : least;
+    }
+    least = __builtin_amdgcn_readfirstlane(least);
+    // 2^30 tokens of each table at most: no sum passes 31 bits
+    const int32_t lo = least == 0x7FFFFFFF ? len : window_begin(a, len + row_position(least, 0));
+    w.span = make_span(a.sinks < len ? a.sinks : len, lo, len);
+    return w;
+}
+
+// Position in its own pages of row `row` of a group.  A row of a sequence that
+// has fewer rows than counted is never read.
+__device__ __forceinline__ int32_t group_row_position(const AttendArgs& a, const AttendItem& it, int32_t row)
+{
+    int32_t at = 0, start, past;                               // the last sequence that starts at or before it
+    if (it.seqs <= 64) {
+        for (int32_t step = 32; step > 0; step >>= 1) {
+            const int32_t b = __shfl(it.start, at + step);
+            if (at + step < it.seqs && b <= row) at += step;
+        }
+        start = __shfl(it.start, at);
+        past = __shfl(it.past, at);
+    } else {
+        int32_t n = it.seqs;                                   // among [at, at + n)
+        while (n > 1) {
+            const int32_t half = n / 2;
+            if (clamp_i32(gptr<const gi32>(a.step.q_start)[it.seq0 + at + half], 0, a.step.n_rows) <= row) {
+                at += half;
+                n -= half;
+            } else {
+                n = half;
+            }
+        }
+        const Rows r = seq_rows(a.step, it.seq0 + at);
+        start = r.first;
+        past = first_position(table_len(a.step.own, it.seq0 + at), r.count);
+    }
+    return row_position(past, row - start);
+}
+
+// Tokens that the flattened row f sees of the item's table.  All lanes of a wave together.
+template <class F>
+__device__ __forceinline__ Seen seen_by(const AttendArgs& a, const AttendItem& it, int32_t f)
+{
+    Seen s{visible_end(a, it, f), 0, it.sink};
+    if constexpr (F::win) {
+        const int32_t i = new_token(a, it.flat0 + f);
+        if (it.prefix)
+            s.lo = window_begin(a, it.len + group_row_position(a, it, it.rows.first + i));
+        else
+            s.lo = window_begin(a, row_position(first_position(it.len, it.rows.count), i));
+    }
+    return s;
+}
+
+// The item's piece of what its rows see.
+__device__ __forceinline__ void window_item(const AttendArgs& a, AttendItem& it)
+{
+    GroupWindow w{};
+    int32_t sink;
+    if (it.prefix) {
+        sink = a.sinks < it.len ? a.sinks : it.len;
+        w = group_window(a, it.table_row, it.len);
+    } else {
+        sink = own_sink(a, a.sinks > 0 ? prefix_ahead(a.step, it.table_row) : 0);
+        const int32_t first = row_position(first_position(it.len, it.rows.count), new_token(a, it.flat0));
+        w.span = make_span(sink, window_begin(a, first), visible_end(a, it, it.flat_n - 1));
+    }
+    it.sink = sink;
+    it.span = w.span;
+    it.seq0 = w.seq0;
+    it.seqs = w.seqs;
+    it.start = w.start;
+    it.past = w.past;
+    const int32_t tokens = it.prefix ? a.prefix_tokens : a.own_tokens;
+    it.t1 = it.span.n - it.t0 < tokens ? it.span.n : it.t0 + tokens;
 }
 
 // Page id of token tok; the load is started here, what waits for it is
@@ -181,6 +379,19 @@ __device__ __forceinline__ float max_over_groups(float x)
     return max3(__builtin_bit_cast(float, q0), __builtin_bit_cast(float, q1), __builtin_bit_cast(float, q1));
 }
 
+// Maximum over the 16 rows of a wave: of lane l % 16, the same in every group.
+__device__ __forceinline__ int32_t max_of_rows(int32_t x)
+{
+#pragma unroll
+    for (int d = 1; d < 16; d *= 2) {
+        const int32_t y = __shfl_xor(x, d);
+        x = y > x ? y : x;
+    }
+    return x;
+}
+
+__device__ __forceinline__ int32_t min_of_rows(int32_t x) { return -max_of_rows(-x); }
+
 // A wave's registers of the online softmax over 16 rows (matrix columns):
 // lane l holds column l % 16 and, of every 16 matrix rows, the four from
 // 4 * (l / 16).
@@ -212,8 +423,9 @@ __device__ __forceinline__ constexpr int acc_element(int r, int m)
 constexpr float kLag = 8.0f;
 
 // Scores of 32 tokens that this lane's row does not see to -infinity: token
-// t + x counts if t + x < vis and bit x of valid is set.
-__device__ __forceinline__ void mask_scores(f32x4 (&s)[2], int32_t t, int32_t vis, uint32_t valid)
+// t + x counts if the row sees it and bit x of valid is set.
+template <class F>
+__device__ __forceinline__ void mask_scores(f32x4 (&s)[2], int32_t t, const Seen& vis, uint32_t valid)
 {
     const int g = (threadIdx.x & 63) >> 4;
 #pragma unroll
@@ -221,7 +433,7 @@ __device__ __forceinline__ void mask_scores(f32x4 (&s)[2], int32_t t, int32_t vi
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
             const int x = 16 * i + 4 * g + n;
-            if (t + x >= vis || !((valid >> x) & 1)) s[i][n] = -__builtin_inff();
+            if (!sees<F>(vis, t + x) || !((valid >> x) & 1)) s[i][n] = -__builtin_inff();
         }
 }
 
@@ -321,8 +533,8 @@ __device__ __forceinline__ void take_nonfinite(uint32_t (&v)[8][DP / 32])
 
 // row_of(x): LDS address of the 32 tokens' V row x, as it came from the pool;
 // at(d): where its elements [d, d + 4) are in the row, in bf16 elements.
-template <int DP, class RowOf, class At>
-__device__ __forceinline__ void add_nonfinite(RowState<DP>& st, u32x4 ph, u32x4 pl, int32_t t, int32_t vis,
+template <int DP, class F, class RowOf, class At>
+__device__ __forceinline__ void add_nonfinite(RowState<DP>& st, u32x4 ph, u32x4 pl, int32_t t, const Seen& vis,
                                               uint32_t valid, RowOf&& row_of, At&& at)
 {
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
@@ -334,7 +546,7 @@ __device__ __forceinline__ void add_nonfinite(RowState<DP>& st, u32x4 ph, u32x4 
         const int from = ((x & 15) >> 2) * 16 + r;                   // the lane that holds this weight
         const uint32_t h = uint32_t(__shfl(int(hi), from)) << shift, l = uint32_t(__shfl(int(lo), from)) << shift;
         const float p = __builtin_bit_cast(float, h & 0xFFFF0000u) + __builtin_bit_cast(float, l & 0xFFFF0000u);
-        if (t + x >= vis || !((valid >> x) & 1)) continue;
+        if (!sees<F>(vis, t + x) || !((valid >> x) & 1)) continue;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -379,12 +591,43 @@ __device__ __forceinline__ void load_row(u32x4 (&x)[DP / 32], uint64_t base, int
     }
 }
 
-template <int DP>
+// q of one block of 16 rows in the layout of the first product's right
+// operand: column r, elements q_element(j, g) ..+8.  The order of a head's
+// elements does not matter to q.k: where K's bytes are a left operand straight
+// from memory, a lane's 16 of them serve two products.
+template <bool kBytes>
+__device__ __forceinline__ constexpr int q_element(int j, int g)
+{
+    return kBytes ? j / 2 * 64 + g * 16 + j % 2 * 8 : j * 32 + g * 8;
+}
+
+template <int DP, bool kBytes = false>
 __device__ __forceinline__ void clear_past(u32x4 (&x)[DP / 32], int g, int dim)
 {
 #pragma unroll
     for (int j = 0; j < DP / 32; ++j)
-        if (j * 32 + g * 8 >= dim) x[j] = u32x4{0, 0, 0, 0};
+        if (q_element<kBytes>(j, g) >= dim) x[j] = u32x4{0, 0, 0, 0};
+}
+
+// The same of an 8-bit row: elements 64 j + 16 g ..+16.
+template <int DP>
+__device__ __forceinline__ void load_row8(u32x4 (&x)[DP / 64], uint64_t base, int g, int dim)
+{
+#pragma unroll
+    for (int j = 0; j < DP / 64; ++j) {
+        const int d = j * 64 + g * 16;
+        x[j] = *gptr<const gvec4>(base + (d < dim ? d : 0));
+    }
+}
+
+template <int DP>
+__device__ __forceinline__ void widen_row(u32x4 (&x)[DP / 32], const u32x4 (&b)[DP / 64], float scale)
+{
+#pragma unroll
+    for (int j = 0; j < DP / 64; ++j) {
+        x[2 * j] = bf16_of_bytes8(b[j][0], b[j][1], scale);
+        x[2 * j + 1] = bf16_of_bytes8(b[j][2], b[j][3], scale);
+    }
 }
 
 // Lane r's elements of a V row at `base`; past dim the first ones.
@@ -406,9 +649,36 @@ __device__ __forceinline__ void load_v(uint32_t (&v)[DP / 32], uint64_t base, in
     }
 }
 
-// q of one block of 16 rows in the layout of the first product's right
-// operand: column r, elements 32 j + 8 g ..+8.
+// The same of an 8-bit row, as bytes.
 template <int DP>
+__device__ __forceinline__ void load_v8(uint32_t (&v)[DP / 64], uint64_t base, int r, int dim)
+{
+    if constexpr (DP == 64) {
+        v[0] = *gptr<const gu32>(base + (r * 4 < dim ? r * 4 : 0));
+    } else {
+#pragma unroll
+        for (int y = 0; y < DP / 128; ++y) {
+            const int d = y * 128 + r * 8;
+            const u32x2 x = *gptr<const gvec2>(base + (d < dim ? d : 0));
+            v[2 * y] = x[0];
+            v[2 * y + 1] = x[1];
+        }
+    }
+}
+
+template <int DP>
+__device__ __forceinline__ void widen_v(uint32_t (&v)[DP / 32], const uint32_t (&b)[DP / 64], float scale)
+{
+#pragma unroll
+    for (int y = 0; y < DP / 64; ++y) {
+        const u32x2 x = bf16_of_bytes(b[y], scale);
+        v[2 * y] = x[0];
+        v[2 * y + 1] = x[1];
+    }
+}
+
+// q of one block of 16 rows: column r of the first product's right operand.
+template <int DP, bool kBytes>
 __device__ __forceinline__ void load_q(u32x4 (&q)[DP / 32], const AttendArgs& a, const AttendItem& it, int32_t f,
                                        bool live)
 {
@@ -420,7 +690,7 @@ __device__ __forceinline__ void load_q(u32x4 (&q)[DP / 32], const AttendArgs& a,
 #pragma unroll
     for (int j = 0; j < DP / 32; ++j) {
         q[j] = u32x4{0, 0, 0, 0};
-        if (live) q[j] = load_k8(qb, j * 32 + g * 8, a.pool.dim);
+        if (live) q[j] = load_k8(qb, q_element<kBytes>(j, g), a.pool.dim);
     }
 }
 
@@ -481,27 +751,30 @@ struct NarrowShared {
 // 64 sequences of 9000 to 10000 tokens, 8 KV heads of 128, in 442 to 452 us, 5.6 TB/s.
 // One such sequence is 27 pieces a head and the waits from page id to K and V,
 // three rounds of them, and the waves' join: 11.8 us for 41 MB.
-template <int DP>
-__device__ __forceinline__ void narrow_piece(const AttendArgs& a, const AttendItem& it, uint64_t kb, uint64_t vb,
-                                             int32_t t1, NarrowShared<DP>& sh)
+template <int DP, class F>
+__device__ __forceinline__ void narrow_piece(const AttendArgs& a, const AttendItem& it, const LayerAt& l, int32_t t1,
+                                             NarrowShared<DP>& sh)
 {
     constexpr int J = DP / 32;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
     const int dim = a.pool.dim;
     const int32_t all_see = visible_end(a, it, 0);          // tokens below it are seen by every row
     const bool live = r < it.flat_n;
-    const int32_t vis[1] = {live ? visible_end(a, it, r) : 0};
+    Seen vis[1] = {seen_by<F>(a, it, live ? r : 0)};
+    const int32_t all_from = F::win ? max_of_rows(vis[0].lo) : 0;            // and from here on, or below vis.sink
+    if (!live) vis[0].end = 0;
     u32x4 q[J];
-    load_q<DP>(q, a, it, r, live);
+    load_q<DP, F::byte>(q, a, it, r, live);
     RowState<DP> st[1];
 
     const TablesArg& tab = it.prefix ? a.step.prefix : a.step.own;
-    const uint32_t row_bytes = a.pool.heads * dim * 2;
-    const uint64_t kh = kb + uint64_t(it.h) * dim * 2, vh = vb + uint64_t(it.h) * dim * 2;
+    constexpr int kSize = F::byte ? 1 : 2;
+    const uint32_t row_bytes = a.pool.heads * dim * kSize;
+    const uint64_t kh = l.k + uint64_t(it.h) * dim * kSize, vh = l.v + uint64_t(it.h) * dim * kSize;
     // lane l < 32 looks up token t + l, its page a round ahead; the others take it from there
     auto mine = [&](int32_t t) { return lane < kAttendTile && lane < t1 - t; };
     auto page_at = [&](int32_t t) {                // of the last token where there is no such one: no branch to wait at
-        return token_page(a.pool, tab, it.table_row, lane < t1 - t ? t + lane : t1 - 1);
+        return token_page(a.pool, tab, it.table_row, token_at<F>(it.span, lane < t1 - t ? t + lane : t1 - 1));
     };
     const int32_t first = it.t0 + wave * kAttendTile;
     bool care = false;
@@ -509,27 +782,47 @@ __device__ __forceinline__ void narrow_piece(const AttendArgs& a, const AttendIt
     clear<DP>(st[0]);
     int32_t page = it.t0 < t1 ? page_at(first) : -1;
 #pragma unroll 1
-    for (int32_t t = first; t < t1; t += kAttendWaves * kAttendTile) {
-        const int32_t row = mine(t) ? row_in_page(a.pool, page, t + lane) : -1;
-        page = page_at(t + kAttendWaves * kAttendTile);
+    for (int32_t u = first; u < t1; u += kAttendWaves * kAttendTile) {
+        const int32_t t = token_at<F>(it.span, u);
+        const int32_t row = mine(u) ? row_in_page(a.pool, page, t + lane) : -1;
+        const int32_t here = page;
+        page = page_at(u + kAttendWaves * kAttendTile);
         const uint32_t valid = uint32_t(__ballot(row >= 0));
         u32x4 k[2][J];
         uint32_t v[8][J];
         // no load behind a branch (row 0 for a token that has none), so that the waits for K leave V in flight
         const int32_t some = row < 0 ? 0 : row;
+        if constexpr (F::byte) {
+            u32x4 kb[2][J / 2];
+            uint32_t vb[8][J / 2];
+            const uint64_t at = (uint64_t(row < 0 ? 0 : here) * a.pool.heads + it.h) * 4;
+            const float ks = *gptr<const gf32>(l.k_scales + at), vs = *gptr<const gf32>(l.v_scales + at);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint32_t kr = uint32_t(__shfl(some, 16 * i + r));
-            load_row<DP>(k[i], kh + uint64_t(kr) * row_bytes, g, dim);
-        }
+            for (int i = 0; i < 2; ++i)
+                load_row8<DP>(kb[i], kh + uint64_t(uint32_t(__shfl(some, 16 * i + r))) * row_bytes, g, dim);
 #pragma unroll
-        for (int x = 0; x < 8; ++x) {
-            const uint32_t vr = uint32_t(__shfl(some, 16 * (x / 4) + 4 * g + x % 4));
-            load_v<DP>(v[x], vh + uint64_t(vr) * row_bytes, r, dim);
+            for (int x = 0; x < 8; ++x)
+                load_v8<DP>(vb[x], vh + uint64_t(uint32_t(__shfl(some, 16 * (x / 4) + 4 * g + x % 4))) * row_bytes, r,
+                            dim);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) widen_row<DP>(k[i], kb[i], __shfl(ks, 16 * i + r));
+#pragma unroll
+            for (int x = 0; x < 8; ++x) widen_v<DP>(v[x], vb[x], __shfl(vs, 16 * (x / 4) + 4 * g + x % 4));
+        } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t kr = uint32_t(__shfl(some, 16 * i + r));
+                load_row<DP>(k[i], kh + uint64_t(kr) * row_bytes, g, dim);
+            }
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                const uint32_t vr = uint32_t(__shfl(some, 16 * (x / 4) + 4 * g + x % 4));
+                load_v<DP>(v[x], vh + uint64_t(vr) * row_bytes, r, dim);
+            }
         }
         if (dim < DP) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) clear_past<DP>(k[i], g, dim);
+            for (int i = 0; i < 2; ++i) clear_past<DP, F::byte>(k[i], g, dim);
 #pragma unroll
             for (int x = 0; x < 8; ++x)
 #pragma unroll
@@ -551,8 +844,9 @@ __device__ __forceinline__ void narrow_piece(const AttendArgs& a, const AttendIt
             for (int j = 0; j < J; ++j) s[i] = mfma16(k[i][j], q[j], s[i]);
         }
         u32x4 ph[1], pl[1];
-        const bool masked = valid != ~0u || t + kAttendTile > all_see;
-        if (masked) mask_scores(s, t, vis[0], valid);
+        bool masked = valid != ~0u || t + kAttendTile > all_see;
+        if constexpr (F::win) masked = masked || (t < all_from && t + kAttendTile > it.sink);
+        if (masked) mask_scores<F>(s, t, vis[0], valid);
         raise_base<DP>(st[0], max_over_groups(max_of(s)) * a.scale_log2);
         weights_of<DP>(st[0], s, ph[0], pl[0], a.scale_log2);
         if (care) {
@@ -566,7 +860,7 @@ __device__ __forceinline__ void narrow_piece(const AttendArgs& a, const AttendIt
             __builtin_amdgcn_s_waitcnt(0);
             __builtin_amdgcn_wave_barrier();
             take_nonfinite<DP>(v);
-            add_nonfinite<DP>(st[0], ph[0], pl[0], t, vis[0], valid,
+            add_nonfinite<DP, F>(st[0], ph[0], pl[0], t, vis[0], valid,
                               [&](int x) { return reinterpret_cast<const uint16_t*>(&sh.v[wave][x][0]); },
                               [](int, int d) { return d; });
             __builtin_amdgcn_wave_barrier();
@@ -671,6 +965,61 @@ __device__ __forceinline__ void wide_load(uint64_t kh, uint64_t vh, uint32_t row
     }
 }
 
+// A wave's share of a tile of an 8-bit pool on its way: 16 bytes a lane and
+// load, and the scales of the tile's tokens, lane x's of token x.
+template <int DP>
+struct Stage8 {
+    static constexpr int V = DP / 16;                                    // vectors of a row
+    static constexpr int kTokens = kWideTile<DP> / kAttendWaves, kLoads = kTokens * V / 64;
+    u32x4 k[kLoads], v[kLoads];
+    float ks, vs;
+    uint64_t there;
+
+    static __device__ __forceinline__ int token(int i)
+    {
+        const int lane = anew(threadIdx.x & 63), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        return wave * kTokens + i * (64 / V) + lane / V;
+    }
+
+    // rows, page: lane x's are token x's
+    __device__ __forceinline__ void load(const LayerAt& l, const PoolArg& p, int32_t h, uint64_t kh, uint64_t vh,
+                                         uint32_t row_bytes, int32_t rows, int32_t page)
+    {
+        const int chunk = anew(threadIdx.x & 63) % V;
+        const uint32_t off = chunk * 16 < int(p.dim) ? chunk * 16 : 0;
+        const uint64_t at = (uint64_t(rows < 0 ? 0 : page) * p.heads + h) * 4;
+        ks = *gptr<const gf32>(l.k_scales + at);
+        vs = *gptr<const gf32>(l.v_scales + at);
+        there = __ballot(rows >= 0);
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int32_t row = __shfl(rows, token(i));
+            const uint64_t from = uint64_t(uint32_t(row < 0 ? 0 : row)) * row_bytes + off;
+            k[i] = *gptr<const gvec4>(kh + from);
+            v[i] = *gptr<const gvec4>(vh + from);
+        }
+    }
+
+    // as bf16, in the places that wide_load would have put them; 0 where there is no token or no element
+    __device__ __forceinline__ void put(WideTile<DP>& tile, int dim) const
+    {
+        const int chunk = anew(threadIdx.x & 63) % V;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int tok = token(i), at = tok * (DP / 8), swz = wide_swizzle<DP>(tok);
+            const bool live = ((there >> tok) & 1) && chunk * 16 < dim;
+            const float sk = __shfl(ks, tok), sv = __shfl(vs, tok);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const uint32_t none = 0;
+                const int to = at + ((2 * chunk + e) ^ swz);
+                tile.k[to] = bf16_of_bytes8(live ? k[i][2 * e] : none, live ? k[i][2 * e + 1] : none, sk);
+                tile.v[to] = bf16_of_bytes8(live ? v[i][2 * e] : none, live ? v[i][2 * e + 1] : none, sv);
+            }
+        }
+    }
+};
+
 // Scores of 32 tokens (half h of a tile) for this wave's NB blocks of rows.
 template <int DP, int NB>
 __device__ __forceinline__ void wide_scores(f32x4 (&s)[NB][2], const u32x4 (&q)[NB][DP / 32],
@@ -719,10 +1068,10 @@ __device__ __forceinline__ void wide_values(uint32_t (&v)[8][DP / 32], const Wid
 // The products and the softmax of a tile for this wave's NB blocks of rows.
 // One maximum and one look at the base for the whole tile; the first half's
 // second product runs beside the second half's exponentials.
-template <int DP, int NB>
+template <int DP, int NB, class F>
 __device__ __forceinline__ void wide_tile(RowState<DP> (&st)[NB], const u32x4 (&q)[NB][DP / 32],
                                           const WideTile<DP>& tile, float c, bool masked, int32_t t,
-                                          const int32_t (&vis)[NB], uint64_t valid)
+                                          const Seen (&vis)[NB], uint64_t valid)
 {
     constexpr int H = kWideTile<DP> / 32;
     f32x4 s[H][NB][2];
@@ -732,7 +1081,7 @@ __device__ __forceinline__ void wide_tile(RowState<DP> (&st)[NB], const u32x4 (&
 #pragma unroll
         for (int h = 0; h < H; ++h)
 #pragma unroll
-            for (int b = 0; b < NB; ++b) mask_scores(s[h][b], t + 32 * h, vis[b], uint32_t(valid >> (32 * h)));
+            for (int b = 0; b < NB; ++b) mask_scores<F>(s[h][b], t + 32 * h, vis[b], uint32_t(valid >> (32 * h)));
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
         float mx = max_of(s[0][b]);
@@ -760,20 +1109,20 @@ __device__ __forceinline__ void wide_tile(RowState<DP> (&st)[NB], const u32x4 (&
 }
 
 // The same for a piece that is done again with care: half by half.
-template <int DP, int NB>
+template <int DP, int NB, class F>
 __device__ __forceinline__ void wide_half_with_care(RowState<DP> (&st)[NB], const u32x4 (&q)[NB][DP / 32],
                                                     const WideTile<DP>& tile, int h, float c, int32_t t,
-                                                    const int32_t (&vis)[NB], uint32_t valid)
+                                                    const Seen (&vis)[NB], uint32_t valid)
 {
     f32x4 s[NB][2];
     u32x4 ph[NB], pl[NB];
     wide_scores<DP, NB>(s, q, tile, h);
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-        mask_scores(s[b], t, vis[b], valid);
+        mask_scores<F>(s[b], t, vis[b], valid);
         raise_base<DP>(st[b], max_over_groups(max_of(s[b])) * c);
         weights_of<DP>(st[b], s[b], ph[b], pl[b], c);
-        add_nonfinite<DP>(
+        add_nonfinite<DP, F>(
             st[b], ph[b], pl[b], t, vis[b], valid,
             [&](int x) { return reinterpret_cast<const uint16_t*>(&tile.v[(32 * h + x) * (DP / 8)]); },
             [](int x, int d) { return ((d / 8) ^ wide_swizzle<DP>(x)) * 8 + d % 8; });
@@ -797,36 +1146,45 @@ __device__ __forceinline__ void wide_half_with_care(RowState<DP> (&st)[NB], cons
 // of P makes them half as many again.  Without it 14 % shorter and an error 1.4
 // times the output's own rounding.  128 rows a workgroup and two workgroups a
 // CU; with 64 rows K and V come through LDS twice as often.
-template <int DP, int NB>
-__device__ __forceinline__ void wide_piece(const AttendArgs& a, const AttendItem& it, uint64_t kb, uint64_t vb,
-                                           int32_t t1, WideTile<DP>& tile0, WideTile<DP>& tile1)
+template <int DP, int NB, class F>
+__device__ __forceinline__ void wide_piece(const AttendArgs& a, const AttendItem& it, const LayerAt& l, int32_t t1,
+                                           WideTile<DP>& tile0, WideTile<DP>& tile1)
 {
     constexpr int T = kWideTile<DP>;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15,
               g = lane >> 4;
     const int dim = a.pool.dim;
     const TablesArg& tab = it.prefix ? a.step.prefix : a.step.own;
-    const uint32_t row_bytes = a.pool.heads * dim * 2;
-    const uint64_t kh = kb + uint64_t(it.h) * dim * 2, vh = vb + uint64_t(it.h) * dim * 2;
+    constexpr int kSize = F::byte ? 1 : 2;
+    const uint32_t row_bytes = a.pool.heads * dim * kSize;
+    const uint64_t kh = l.k + uint64_t(it.h) * dim * kSize, vh = l.v + uint64_t(it.h) * dim * kSize;
     // lane x looks up token x of a tile, its page two tiles ahead
     auto page_at = [&](int32_t t) {                // of the last token where there is no such one: no branch to wait at
         const int x = anew(lane);
-        return token_page(a.pool, tab, it.table_row, x < t1 - t ? t + x : t1 - 1);
+        return token_page(a.pool, tab, it.table_row, token_at<F>(it.span, x < t1 - t ? t + x : t1 - 1));
     };
     auto row_at = [&](int32_t t, int32_t page) {
         const int x = anew(lane);
-        return x < T && x < t1 - t ? row_in_page(a.pool, page, t + x) : -1;
+        return x < T && x < t1 - t ? row_in_page(a.pool, page, token_at<F>(it.span, t + x)) : -1;
     };
 
     const int32_t f0 = wave * 16 * NB;                       // the wave's first row in the tile
     u32x4 q[NB][DP / 32];
     RowState<DP> st[NB];
-    int32_t vis[NB];
+    Seen vis[NB];
+    int32_t all_from = 0, some_from = 0;                     // from here on (or below the sinks) every row, some row sees
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
         const int32_t f = f0 + 16 * b + r;
-        vis[b] = f < it.flat_n ? visible_end(a, it, f) : 0;
-        load_q<DP>(q[b], a, it, f, f < it.flat_n);
+        vis[b] = seen_by<F>(a, it, f < it.flat_n ? f : 0);
+        if constexpr (F::win) {
+            const int32_t first = min_of_rows(f < it.flat_n ? vis[b].lo : 0x7FFFFFFF);
+            const int32_t last = max_of_rows(f < it.flat_n ? vis[b].lo : 0);
+            all_from = b == 0 || last > all_from ? last : all_from;
+            some_from = b == 0 || first < some_from ? first : some_from;
+        }
+        if (f >= it.flat_n) vis[b].end = 0;
+        load_q<DP, false>(q[b], a, it, f, f < it.flat_n);
     }
     const bool busy = f0 < it.flat_n;
     const int32_t all_see = busy ? visible_end(a, it, f0) : 0;
@@ -838,37 +1196,82 @@ __device__ __forceinline__ void wide_piece(const AttendArgs& a, const AttendItem
     for (int b = 0; b < NB; ++b) clear<DP>(st[b]);
     int32_t page = -1, rows = -1;
     uint64_t valid = 0;
-    if (it.t0 < t1) {
-        page = page_at(it.t0);
-        rows = row_at(it.t0, page);
-        page = page_at(it.t0 + T);
-        valid = __ballot(rows >= 0);
-        wide_load<DP>(kh, vh, row_bytes, dim, flat, rows, valid, tile0);
-        rows = row_at(it.t0 + T, page);
-        page = page_at(it.t0 + 2 * T);
-    }
     constexpr uint64_t full = T == 64 ? ~0ull : (1ull << (T & 63)) - 1;
-    // the loads of a tile are waited for one tile after they were issued; the barrier says both that every wave's share
-    // has landed and that the other tile is free again
-    auto one = [&](int32_t t, WideTile<DP>& now, WideTile<DP>& next) {
-        __builtin_amdgcn_s_waitcnt(0);
-        __syncthreads();
-        const uint64_t seen = valid;
-        if (t + T < t1) {
-            valid = __ballot(rows >= 0);
-            wide_load<DP>(kh, vh, row_bytes, dim, flat, rows, valid, next);
+    // the wave's part of a tile in LDS, at token u of the piece
+    auto compute = [&](int32_t u, uint64_t seen, WideTile<DP>& now) {
+        const int32_t t = token_at<F>(it.span, u);
+        bool masked = seen != full || t + T > all_see, any = t < end;
+        if constexpr (F::win) {
+            masked = masked || (t < all_from && t + T > it.sink);
+            any = any && (t + T > some_from || t < it.sink);
         }
-        rows = row_at(t + 2 * T, page);
-        page = page_at(t + 3 * T);
-        if (t < end)
-            wide_tile<DP, NB>(st, q, now, a.scale_log2, seen != full || t + T > all_see, t, vis, seen);
+        if (any) wide_tile<DP, NB, F>(st, q, now, a.scale_log2, masked, t, vis, seen);
     };
-    // two tiles by name: with an index between them the reads of one would wait for the loads of the other
+    if constexpr (F::byte) {
+        // bytes come through registers, which is where they are widened: those of a tile are asked for while the one
+        // before the one before it is computed, and put into LDS when that is done
+        Stage8<DP> stage;
+        uint64_t staged = 0;
+        auto ask = [&](int32_t u) {
+            rows = row_at(u, page);
+            stage.load(l, a.pool, it.h, kh, vh, row_bytes, rows, page);
+            staged = __ballot(rows >= 0);
+            page = page_at(u + T);
+        };
+        if (it.t0 < t1) {
+            page = page_at(it.t0);
+            ask(it.t0);
+            stage.put(tile0, dim);
+            valid = staged;
+            ask(it.t0 + T);
+        }
+        auto one = [&](int32_t u, WideTile<DP>& now, WideTile<DP>& next) {
+            __syncthreads();                                 // now is whole, and next is done with
+            const uint64_t seen = valid;
+            if (u + T < t1) {
+                stage.put(next, dim);
+                valid = staged;
+                ask(u + 2 * T);
+            }
+            compute(u, seen, now);
+        };
 #pragma unroll 1
-    for (int32_t t = it.t0; t < t1; t += 2 * T) {
-        one(t, tile0, tile1);
-        if (t + T >= t1) break;
-        one(t + T, tile1, tile0);
+        for (int32_t u = it.t0; u < t1; u += 2 * T) {
+            one(u, tile0, tile1);
+            if (u + T >= t1) break;
+            one(u + T, tile1, tile0);
+        }
+    } else {
+        if (it.t0 < t1) {
+            page = page_at(it.t0);
+            rows = row_at(it.t0, page);
+            page = page_at(it.t0 + T);
+            valid = __ballot(rows >= 0);
+            wide_load<DP>(kh, vh, row_bytes, dim, flat, rows, valid, tile0);
+            rows = row_at(it.t0 + T, page);
+            page = page_at(it.t0 + 2 * T);
+        }
+        // the loads of a tile are waited for one tile after they were issued; the barrier says both that every wave's
+        // share has landed and that the other tile is free again
+        auto one = [&](int32_t u, WideTile<DP>& now, WideTile<DP>& next) {
+            __builtin_amdgcn_s_waitcnt(0);
+            __syncthreads();
+            const uint64_t seen = valid;
+            if (u + T < t1) {
+                valid = __ballot(rows >= 0);
+                wide_load<DP>(kh, vh, row_bytes, dim, flat, rows, valid, next);
+            }
+            rows = row_at(u + 2 * T, page);
+            page = page_at(u + 3 * T);
+            compute(u, seen, now);
+        };
+        // two tiles by name: with an index between them the reads of one would wait for the loads of the other
+#pragma unroll 1
+        for (int32_t u = it.t0; u < t1; u += 2 * T) {
+            one(u, tile0, tile1);
+            if (u + T >= t1) break;
+            one(u + T, tile1, tile0);
+        }
     }
     bool finite = true;
 #pragma unroll
@@ -877,28 +1280,36 @@ __device__ __forceinline__ void wide_piece(const AttendArgs& a, const AttendItem
 #pragma unroll
         for (int b = 0; b < NB; ++b) clear<DP>(st[b]);
 #pragma unroll 1
-        for (int32_t t = it.t0; t < t1; t += T) {
-            rows = row_at(t, page_at(t));
+        for (int32_t u = it.t0; u < t1; u += T) {
+            const int32_t t = token_at<F>(it.span, u);
+            page = page_at(u);
+            rows = row_at(u, page);
             valid = __ballot(rows >= 0);
             __syncthreads();                               // the tile before is done with
-            wide_load<DP>(kh, vh, row_bytes, dim, flat, rows, valid, tile0);
-            __builtin_amdgcn_s_waitcnt(0);
+            if constexpr (F::byte) {
+                Stage8<DP> stage;
+                stage.load(l, a.pool, it.h, kh, vh, row_bytes, rows, page);
+                stage.put(tile0, dim);
+            } else {
+                wide_load<DP>(kh, vh, row_bytes, dim, flat, rows, valid, tile0);
+                __builtin_amdgcn_s_waitcnt(0);
+            }
             __syncthreads();
 #pragma unroll 1
             for (int h = 0; h < T / 32; ++h)
                 if (t + 32 * h < end)
-                    wide_half_with_care<DP, NB>(st, q, tile0, h, a.scale_log2, t + 32 * h, vis,
-                                                uint32_t(valid >> (32 * h)));
+                    wide_half_with_care<DP, NB, F>(st, q, tile0, h, a.scale_log2, t + 32 * h, vis,
+                                                   uint32_t(valid >> (32 * h)));
         }
     }
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-        float l = st[b].l;
-        l += __shfl_xor(l, 16);
-        l += __shfl_xor(l, 32);
+        float sum = st[b].l;
+        sum += __shfl_xor(sum, 16);
+        sum += __shfl_xor(sum, 32);
         const int32_t f = f0 + 16 * b + anew(r);
         if (f >= it.flat_n) continue;
-        const RowSink to = open_row(a, it, f, st[b].m, l, g == 0);
+        const RowSink to = open_row(a, it, f, st[b].m, sum, g == 0);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -912,21 +1323,26 @@ __device__ __forceinline__ void wide_piece(const AttendArgs& a, const AttendItem
 }
 
 // NB: blocks of 16 rows a wave of the wide form takes; 0: only the narrow form.
-template <int DP, int NB>
+template <int DP, int NB, class F>
 __global__ __launch_bounds__(kAttendBlock, DP <= 128 ? 2 : 1) void attend_pieces(AttendArgs a)
 {
-    const AttendItem it = attend_item(a, blockIdx.x, kAttendWaves * 16 * NB);
+    AttendItem it = attend_item(a, blockIdx.x, kAttendWaves * 16 * NB);
     if (it.flat_n <= 0) return;
-    // the last row sees the most: no later token is needed
-    const int32_t end_all = visible_end(a, it, it.flat_n - 1);
-    int32_t t1 = it.t1 < end_all ? it.t1 : end_all;
+    int32_t t1;
+    if constexpr (F::win) {
+        window_item(a, it);
+        t1 = it.t1;
+    } else {
+        // the last row sees the most: no later token is needed
+        const int32_t end_all = visible_end(a, it, it.flat_n - 1);
+        t1 = it.t1 < end_all ? it.t1 : end_all;
+    }
     if (it.t0 >= t1) {
         if (!a.direct) return;                              // nothing seen: the join takes no such piece
         t1 = it.t0;
     }
-    const uint64_t kb = wave_uniform(gptr<const gu64>(a.pool.k_pages)[a.pool.layer]);
-    const uint64_t vb = wave_uniform(gptr<const gu64>(a.pool.v_pages)[a.pool.layer]);
-    if (bad_addr(kb) || bad_addr(vb)) {
+    const LayerAt l = layer_at<F::byte>(a.pool, a.scales);
+    if (bad_layer<F::byte>(l)) {
         raise_fault(kFaultPool);
         t1 = it.t0;
     }
@@ -934,12 +1350,12 @@ __global__ __launch_bounds__(kAttendBlock, DP <= 128 ? 2 : 1) void attend_pieces
         __shared__ union { WideTile<DP> tile; NarrowShared<DP> narrow; } sh;
         __shared__ WideTile<DP> other;
         if (it.prefix ? a.prefix_wide : a.own_wide)
-            wide_piece<DP, NB>(a, it, kb, vb, t1, sh.tile, other);
+            wide_piece<DP, NB, F>(a, it, l, t1, sh.tile, other);
         else
-            narrow_piece<DP>(a, it, kb, vb, t1, sh.narrow);
+            narrow_piece<DP, F>(a, it, l, t1, sh.narrow);
     } else {
         __shared__ NarrowShared<DP> sh;
-        narrow_piece<DP>(a, it, kb, vb, t1, sh);
+        narrow_piece<DP, F>(a, it, l, t1, sh);
     }
 }
 
@@ -948,15 +1364,25 @@ __global__ __launch_bounds__(kAttendBlock, DP <= 128 ? 2 : 1) void attend_pieces
 // group may be larger than its bound.
 struct RowPieces {
     int32_t prefix, own;       // pieces; own < 0: a row of no sequence
+    int32_t i, first, end, sink;   // with a window: new token, the first one's position, tokens seen up to, sinks
 };
 
+// Own pieces of a row's head, the h-th of its KV head: they are cut from what the row's tile sees.
+__device__ __forceinline__ int32_t window_pieces(const AttendArgs& a, const RowPieces& n, int32_t h)
+{
+    const int32_t flat = n.i * a.rep + h, tile = flat & ~(a.own_tile_rows - 1);
+    const Span s = make_span(n.sink, window_begin(a, row_position(n.first, new_token(a, tile))), n.end);
+    return int32_t((uint32_t(s.n) + a.own_tokens - 1) / uint32_t(a.own_tokens));
+}
+
+template <bool kWindow>
 __device__ __forceinline__ RowPieces row_pieces(const AttendArgs& a, int32_t r)
 {
     const StepArg& st = a.step;
     const int32_t lane = threadIdx.x & 63;
     const RowOwner o = row_owner(st, r);
-    if (o.s < 0) return {0, -1};
-    int32_t prefix = 0;
+    if (o.s < 0) return {0, -1, 0, 0, 0, 0};
+    int32_t prefix = 0, ahead = 0;
     if (st.prefix.n > 0) {
         const int32_t i0 = ranges_around(st.group_start, st.prefix.n, o.s), i = i0 + lane;
         int32_t b = 0, e = 0, n = 0;
@@ -969,6 +1395,8 @@ __device__ __forceinline__ RowPieces row_pieces(const AttendArgs& a, int32_t r)
         if (m != 0) {
             const int j = __builtin_ctzll(m);
             prefix = __builtin_amdgcn_readlane(n, j);
+            ahead = prefix;
+            if constexpr (kWindow) prefix = group_window(a, i0 + j, prefix).span.n;
             if (st.max_group_rows < st.n_rows) {               // else no group can be cut
                 const Rows gr = group_rows(st, i0 + j);
                 if (r - gr.first >= gr.count) prefix = 0;
@@ -977,7 +1405,8 @@ __device__ __forceinline__ RowPieces row_pieces(const AttendArgs& a, int32_t r)
     }
     const int32_t own = clamp_i32(o.len - o.count + (r - o.first) + 1, 0, o.len);
     return {int32_t((uint32_t(prefix) + a.prefix_tokens - 1) / uint32_t(a.prefix_tokens)),
-            int32_t((uint32_t(own) + a.own_tokens - 1) / uint32_t(a.own_tokens))};
+            int32_t((uint32_t(own) + a.own_tokens - 1) / uint32_t(a.own_tokens)), r - o.first, o.len - o.count, own,
+            kWindow ? own_sink(a, ahead) : 0};
 }
 
 // Bound: a row's waits -- its sequence, its group, its parts -- and for many
@@ -1052,14 +1481,15 @@ __device__ __forceinline__ void put_joined(const AttendArgs& a, int32_t r, int32
 }
 
 // Few rows, many pieces: a workgroup per (row, query head).
-template <int DP>
+template <int DP, bool kWindow>
 __global__ __launch_bounds__(256) void attend_join(AttendArgs a)
 {
     constexpr int L = DP / 4, G = 256 / L;
     __shared__ f32x4 so[G][L];
     const int32_t r = blockIdx.x / a.q_heads, head = blockIdx.x - r * a.q_heads;
-    const RowPieces n = row_pieces(a, r);
+    RowPieces n = row_pieces<kWindow>(a, r);
     if (n.own < 0) return;
+    if constexpr (kWindow) n.own = window_pieces(a, n, head - new_token(a, head) * a.rep);
     const int c = threadIdx.x % L, grp = threadIdx.x / L;
     float m, l;
     f32x4 o = join_row<DP>(a, (int64_t(r) * a.q_heads + head) * a.slots, n, c, grp, G, m, l);
@@ -1074,17 +1504,18 @@ __global__ __launch_bounds__(256) void attend_join(AttendArgs a)
 
 // Many rows: a workgroup per row, a wave per query head at a time, so that a
 // row's lookups are made once for its heads.
-template <int DP>
+template <int DP, bool kWindow>
 __global__ __launch_bounds__(256) void attend_join_rows(AttendArgs a)
 {
     constexpr int L = DP / 4, G = 64 / L;
     const int32_t r = blockIdx.x;
-    const RowPieces n = row_pieces(a, r);
+    RowPieces n = row_pieces<kWindow>(a, r);
     if (n.own < 0) return;
     const int lane = threadIdx.x & 63, c = lane % L, grp = lane / L;
 #pragma unroll 1
     for (int32_t head = blockIdx.y * 4 + (threadIdx.x >> 6); head < a.q_heads; head += 4 * gridDim.y) {
         float m, l;
+        if constexpr (kWindow) n.own = window_pieces(a, n, head - new_token(a, head) * a.rep);
         f32x4 o = join_row<DP>(a, (int64_t(r) * a.q_heads + head) * a.slots, n, c, grp, G, m, l);
 #pragma unroll
         for (int d = L; d < 64; d *= 2)

@@ -116,6 +116,11 @@ PoolArg pool_arg(const kv_paged* p, int32_t layer)
     return a;
 }
 
+ScalesArg scales_arg(const kv_paged8* p)
+{
+    return {reinterpret_cast<uint64_t>(p->k_scales), reinterpret_cast<uint64_t>(p->v_scales)};
+}
+
 TablesArg tables_arg(const kv_tables* t)
 {
     return {reinterpret_cast<uint64_t>(t->table), reinterpret_cast<uint64_t>(t->lens), t->stride, t->n, t->max_len};
@@ -151,12 +156,18 @@ KernelFn append_kernel(bool vectors)
                    : reinterpret_cast<KernelFn>(&append_rows<TI, TO, 1>);
 }
 
-int append(const kv_paged* paged, const kv_step* step, int32_t layer, const kv_rows* q, const kv_rows* k,
-           const kv_rows* v, const kv_rows* q_out, int32_t q_heads, kv_type type, kv_type q_out_type,
-           const int32_t* positions, const kv_rope* rope, const kv_slots* slots, hipStream_t stream)
+// What the forms of append have in common: the checks, and the arguments of the kernels.
+struct AppendCall {
+    AppendArgs a;
+    bool vectors;              // 16-byte vectors, else element by element
+};
+
+int append_call(const kv_paged* paged, const kv_step* step, int32_t layer, const kv_rows* q, const kv_rows* k,
+                const kv_rows* v, const kv_rows* q_out, int32_t q_heads, kv_type type, kv_type q_out_type,
+                const int32_t* positions, const kv_rope* rope, const kv_slots* slots, hipStream_t stream,
+                AppendCall* call)
 {
-    int rc = check_step_pool(paged, layer, layer + 1);
-    if (rc == KV_OK) rc = check_step(paged, step);
+    int rc = check_step(paged, step);
     if (rc != KV_OK) return rc;
     if (rope == nullptr || k == nullptr || v == nullptr) return fail(KV_EINVAL, "k, v or rope is NULL");
     if ((q == nullptr) != (q_out == nullptr)) return fail(KV_EINVAL, "q and q_out are given together or not at all");
@@ -177,7 +188,7 @@ int append(const kv_paged* paged, const kv_step* step, int32_t layer, const kv_r
         if (slots->cap < step->own.max_len)
             return fail(KV_ERANGE, "slots: cap %lld below max_len %d", (long long)slots->cap, step->own.max_len);
     }
-    if (step->n_rows == 0) return ok();
+    if (step->n_rows == 0) return KV_OK;
     if (q_out != nullptr && rows_overlap(*q_out, step->n_rows, q_heads, paged->head_dim))
         return fail(KV_EINVAL, "q_out's rows overlap");
     if (k->data == nullptr || v->data == nullptr || positions == nullptr || (q != nullptr && (q->data == nullptr || q_out->data == nullptr)))
@@ -223,17 +234,189 @@ int append(const kv_paged* paged, const kv_step* step, int32_t layer, const kv_r
     if (int64_t(a.q_heads + 2 * int64_t(paged->num_kv_heads)) * dim > INT32_MAX / 2)
         return fail(KV_EINVAL, "a token's heads are too large for one workgroup");
     a.gain = rope->gain;
-    KernelFn f;
-    if (type == KV_TYPE_BF16)
-        f = append_kernel<__bf16, __bf16>(vectors);
-    else if (type == KV_TYPE_FP16)
-        f = q == nullptr || q_out_type == type ? append_kernel<_Float16, _Float16>(vectors)
-                                               : append_kernel<_Float16, __bf16>(vectors);
-    else
-        f = q == nullptr || q_out_type == type ? append_kernel<float, float>(vectors)
-                                               : append_kernel<float, __bf16>(vectors);
-    rc = launch(f, step->n_rows, kAppendBlock, &a, stream);
+    *call = {a, vectors};
+    return KV_OK;
+}
+
+// f<TI, TO>: the instance of a kernel for a call's types.
+template <class Pick>
+KernelFn by_types(kv_type type, bool same_out, Pick&& f)
+{
+    if (type == KV_TYPE_BF16) return f(__bf16{}, __bf16{});
+    if (type == KV_TYPE_FP16) return same_out ? f(_Float16{}, _Float16{}) : f(_Float16{}, __bf16{});
+    return same_out ? f(float{}, float{}) : f(float{}, __bf16{});
+}
+
+int append(const kv_paged* paged, const kv_step* step, int32_t layer, const kv_rows* q, const kv_rows* k,
+           const kv_rows* v, const kv_rows* q_out, int32_t q_heads, kv_type type, kv_type q_out_type,
+           const int32_t* positions, const kv_rope* rope, const kv_slots* slots, hipStream_t stream)
+{
+    int rc = check_step_pool(paged, layer, layer + 1);
+    if (rc != KV_OK) return rc;
+    AppendCall call{};
+    rc = append_call(paged, step, layer, q, k, v, q_out, q_heads, type, q_out_type, positions, rope, slots, stream,
+                     &call);
+    if (rc != KV_OK) return rc;
+    if (step->n_rows == 0) return ok();
+    const KernelFn f = by_types(type, q == nullptr || q_out_type == type, [&](auto in, auto out) {
+        return append_kernel<decltype(in), decltype(out)>(call.vectors);
+    });
+    rc = launch(f, step->n_rows, kAppendBlock, &call.a, stream);
     return rc == KV_OK ? ok() : rc;
+}
+
+// ---- append with normalised heads, and into an 8-bit pool
+
+int check_norm(const kv_norm* n)
+{
+    if (n == nullptr) return KV_OK;
+    if (!(n->eps >= 0.0f) || n->eps > 1e30f) return fail(KV_EINVAL, "norm: eps must be finite and >= 0");
+    if (n->centered != 0 && n->centered != 1) return fail(KV_EINVAL, "norm: centered must be 0 or 1");
+    if (misaligned(n->q_weight, 16) || misaligned(n->k_weight, 16) || n->q_stride < 0 || n->k_stride < 0 ||
+        n->q_stride % 4 != 0 || n->k_stride % 4 != 0)
+        return fail(KV_EINVAL, "norm: weights need 16-byte aligned addresses, strides multiples of 4 and >= 0");
+    return KV_OK;
+}
+
+int log2_up(int32_t x)
+{
+    int lg = 0;
+    while ((int64_t(1) << lg) < x) ++lg;
+    return lg;
+}
+
+AppendHeadsArgs heads_args(const AppendCall& call, const kv_norm* norm)
+{
+    AppendHeadsArgs h{};
+    h.a = call.a;
+    if (norm != nullptr)
+        h.norm = {reinterpret_cast<uint64_t>(norm->q_weight), reinterpret_cast<uint64_t>(norm->k_weight),
+                  norm->q_stride, norm->k_stride, norm->centered ? kNormCentered : kNormRms, norm->eps};
+    h.lanes_log2 = std::min(log2_up(h.a.units), 6);
+    h.per = int32_t(ceil_div(h.a.units, 1 << h.lanes_log2));
+    return h;
+}
+
+int append_normed(const kv_paged* paged, const kv_step* step, int32_t layer, const kv_rows* q, const kv_rows* k,
+                  const kv_rows* v, const kv_rows* q_out, int32_t q_heads, kv_type type, kv_type q_out_type,
+                  const int32_t* positions, const kv_rope* rope, const kv_norm* norm, const kv_slots* slots,
+                  hipStream_t stream)
+{
+    if (norm == nullptr)
+        return append(paged, step, layer, q, k, v, q_out, q_heads, type, q_out_type, positions, rope, slots, stream);
+    int rc = check_step_pool(paged, layer, layer + 1);
+    if (rc == KV_OK) rc = check_norm(norm);
+    if (rc != KV_OK) return rc;
+    AppendCall call{};
+    rc = append_call(paged, step, layer, q, k, v, q_out, q_heads, type, q_out_type, positions, rope, slots, stream,
+                     &call);
+    if (rc != KV_OK) return rc;
+    if (step->n_rows == 0) return ok();
+    AppendHeadsArgs h = heads_args(call, norm);
+    const KernelFn f = by_types(type, q == nullptr || q_out_type == type, [&](auto in, auto out) {
+        using TI = decltype(in);
+        using TO = decltype(out);
+        return call.vectors ? reinterpret_cast<KernelFn>(&append_heads_rows<TI, TO, 8>)
+                            : reinterpret_cast<KernelFn>(&append_heads_rows<TI, TO, 1>);
+    });
+    rc = launch(f, step->n_rows, kAppendBlock, &h, stream);
+    return rc == KV_OK ? ok() : rc;
+}
+
+int check_pool8(const kv_paged8* p, int32_t layer_begin, int32_t layer_end)
+{
+    if (p == nullptr) return fail(KV_EINVAL, "paged8 is NULL");
+    int rc = check_step_pool(&p->pages, layer_begin, layer_end);
+    if (rc != KV_OK) return rc;
+    if (p->pages.head_dim % 16 != 0)
+        return fail(KV_EINVAL, "head_dim = %d must be a multiple of 16 in an 8-bit pool", p->pages.head_dim);
+    if (p->k_scales == nullptr || p->v_scales == nullptr) return fail(KV_EINVAL, "k_scales / v_scales is NULL");
+    return KV_OK;
+}
+
+int append8(const kv_paged8* paged8, const kv_step* step, int32_t layer, const kv_rows* q, const kv_rows* k,
+            const kv_rows* v, const kv_rows* q_out, int32_t q_heads, kv_type type, kv_type q_out_type,
+            const int32_t* positions, const kv_rope* rope, const kv_norm* norm, hipStream_t stream)
+{
+    int rc = check_pool8(paged8, layer, layer + 1);
+    if (rc == KV_OK) rc = check_norm(norm);
+    if (rc != KV_OK) return rc;
+    const kv_paged* paged = &paged8->pages;
+    AppendCall call{};
+    rc = append_call(paged, step, layer, q, k, v, q_out, q_heads, type, q_out_type, positions, rope, nullptr, stream,
+                     &call);
+    if (rc != KV_OK) return rc;
+    if (step->n_rows == 0) return ok();
+    AppendHeadsArgs h = heads_args(call, norm);
+    h.scales = scales_arg(paged8);
+    h.v_units = paged->head_dim / 2 / (call.vectors ? 8 : 1);
+    h.v_lanes_log2 = std::min(log2_up(h.v_units), 6);
+    h.v_per = int32_t(ceil_div(h.v_units, 1 << h.v_lanes_log2));
+    h.token_items = q != nullptr ? uint32_t(step->n_rows) : 0;
+    // pages that a sequence's new tokens can touch; none hold more than max_len
+    const int64_t size = paged->page_size, most = ceil_div(step->own.max_len, size);
+    const int64_t touched = step->max_new == 0 ? 0 : (step->max_new + size - 2) / size + 1;
+    h.pages = int32_t(std::min(most, touched));
+    // A wave to each head's K and V where there are few pages, four to a wave where they fill the GPU without
+    const int64_t pairs = int64_t(step->own.n) * h.pages;
+    h.splits = int32_t(std::clamp<int64_t>(2048 / std::max<int64_t>(pairs, 1), 1, ceil_div(paged->num_kv_heads, 2)));
+    const KernelFn f = by_types(type, q == nullptr || q_out_type == type, [&](auto in, auto out) {
+        using TI = decltype(in);
+        using TO = decltype(out);
+        return call.vectors ? reinterpret_cast<KernelFn>(&append8_rows<TI, TO, 8>)
+                            : reinterpret_cast<KernelFn>(&append8_rows<TI, TO, 1>);
+    });
+    if (pairs > max_blocks(kAppendBlock) || pairs * h.splits + h.token_items > max_blocks(kAppendBlock))
+        return fail(KV_EINVAL, "too many pages for one launch");
+    rc = launch(f, h.token_items + pairs * h.splits, kAppendBlock, &h, stream);
+    return rc == KV_OK ? ok() : rc;
+}
+
+// ---- pages between a bf16 and an 8-bit pool
+
+int check_pack(const kv_paged* from, const kv_paged* to, const kv_tables* tables, const int32_t* to_table,
+               int64_t to_stride, int32_t layer_begin, int32_t layer_end, hipStream_t stream)
+{
+    if (tables == nullptr) return fail(KV_EINVAL, "tables is NULL");
+    int rc = check_tables(from, tables, "tables");
+    if (rc != KV_OK) return rc;
+    if (from->page_size != to->page_size || from->num_kv_heads != to->num_kv_heads || from->head_dim != to->head_dim ||
+        from->num_layers != to->num_layers)
+        return fail(KV_EINVAL, "the pools must have one page size, heads, head size and number of layers");
+    if (to_table != nullptr && (to_stride < 0 || to_stride > INT32_MAX))
+        return fail(KV_EINVAL, "to_stride %lld outside [0, 2^31)", (long long)to_stride);
+    if (to_table != nullptr && tables->n > 0 && tables->max_len > to_stride * from->page_size)
+        return fail(KV_ERANGE, "max_len %d beyond to_table (%lld pages of %d)", tables->max_len, (long long)to_stride,
+                    from->page_size);
+    return check_stream(stream);
+}
+
+int run_pack(bool pack, const kv_paged* from, const kv_paged* to, const kv_paged8* bytes, const kv_tables* tables,
+             const int32_t* to_table, int64_t to_stride, int32_t layer_begin, int32_t layer_end, hipStream_t stream)
+{
+    if (holds_nothing(*tables)) return ok();
+    PackArgs a{};
+    a.scales = scales_arg(bytes);
+    a.tables = tables_arg(tables);
+    a.to_table = reinterpret_cast<uint64_t>(to_table != nullptr ? to_table : tables->table);
+    a.to_stride = to_table != nullptr ? to_stride : tables->stride;
+    const int64_t size = from->page_size, vectors = from->head_dim / 16;
+    a.pages = int32_t(ceil_div(tables->max_len, size));
+    a.head_groups = int32_t(ceil_div(from->num_kv_heads, kPackBlock / 64));
+    magic_of(int32_t(vectors), &a.vec_magic, &a.vec_shift);
+    magic_of(int32_t(vectors * from->num_kv_heads), &a.row_magic, &a.row_shift);
+    const int64_t pages = int64_t(tables->n) * a.pages, items = pack ? pages * a.head_groups : pages;
+    if (pages > max_blocks(kPackBlock) || items > max_blocks(kPackBlock))
+        return fail(KV_EINVAL, "too many pages for one launch");
+    constexpr int32_t kLayers = 32767;                       // of a launch: its second dimension
+    for (int32_t l = layer_begin; l < layer_end; l += kLayers) {
+        a.from = pool_arg(from, l);
+        a.to = pool_arg(to, l);
+        const int rc = launch(pack ? reinterpret_cast<KernelFn>(&pack8_pages) : reinterpret_cast<KernelFn>(&unpack8_pages),
+                              items, kPackBlock, &a, stream, unsigned(2 * std::min(kLayers, layer_end - l)));
+        if (rc != KV_OK) return rc;
+    }
+    return ok();
 }
 
 // ---- attend
@@ -244,6 +427,7 @@ struct AttendShape {
     int32_t prefix_tiles, prefix_pieces, prefix_tokens;
     int32_t own_tiles, own_pieces, own_tokens;
     int32_t slots;
+    int32_t own_tile_rows;
     int32_t blocks;                // blocks of 16 rows of a wave of the wide form, 0: narrow only
     bool prefix_wide, own_wide, direct;
     int64_t prefix_items, own_items;
@@ -308,11 +492,11 @@ struct WideCuts {
 // and 91; 700 and no prefix 33 and 29; 512 at the end of 16384 own ones the
 // same, 213.  Every row tile counts as if each sequence had max_new rows, so a
 // prompt beside single tokens is cut less than alone.
-void cut_wide(const kv_paged* p, const kv_step* s, int32_t q_heads, int64_t pre, int64_t own, AttendShape* a)
+// pl, ol: tokens of a prefix and of own pages that an item may see; seen: of the own ones, by a row on average.
+void cut_wide(const kv_paged* p, const kv_step* s, int32_t q_heads, int64_t pre, int64_t own, int32_t pl, int32_t ol,
+              double seen, AttendShape* a)
 {
     const double wide = std::max(1.0, p->head_dim / 128.0), tile = wide / 64;
-    const int32_t pl = s->prefix.n > 0 ? s->prefix.max_len : 0, ol = std::max(s->own.max_len, 1);
-    const double seen = std::max(ol - s->max_new / 2.0, ol / 2.0) / ol;      // of the own tokens, by a row on average
     const WideCuts pc(pre, pl), oc(own, ol);
     double best = 0;
     for (int x = 0; x < pc.n; ++x)
@@ -336,7 +520,9 @@ void cut_wide(const kv_paged* p, const kv_step* s, int32_t q_heads, int64_t pre,
         }
 }
 
-int attend_shape(const kv_paged* p, const kv_step* s, int32_t q_heads, AttendShape* out)
+// A window (NULL: none) cuts what an item may see, and with it the pieces and the workspace: the sinks and the first row's
+// window are rounded to whole tiles (make_span), and an item's rows are some tokens apart.
+int attend_shape(const kv_paged* p, const kv_step* s, int32_t q_heads, const kv_window* win, AttendShape* out)
 {
     const int64_t heads = p->num_kv_heads, rep = q_heads / heads;
     AttendShape a{};
@@ -345,8 +531,15 @@ int attend_shape(const kv_paged* p, const kv_step* s, int32_t q_heads, AttendSha
     a.own_wide = orows > kAttendRows;
     if (a.prefix_wide || a.own_wide) a.blocks = std::max(pr, orows) > 64 && p->head_dim <= 128 ? 2 : 1;
     const int64_t wide_rows = kAttendWaves * 16 * a.blocks;
+    a.own_tile_rows = int32_t(a.own_wide ? wide_rows : kAttendRows);
     const int64_t pt = ceil_div(pr, a.prefix_wide ? wide_rows : kAttendRows);
-    const int64_t ot = ceil_div(orows, a.own_wide ? wide_rows : kAttendRows);
+    const int64_t ot = ceil_div(orows, a.own_tile_rows);
+    int64_t prefix_len = s->prefix.n > 0 ? s->prefix.max_len : 0, own_len = s->own.n > 0 ? s->own.max_len : 0;
+    if (win != nullptr) {
+        const int64_t most_seen = int64_t(win->window) + win->sinks + 2 * (kSpanTile - 1);
+        prefix_len = std::min(prefix_len, most_seen);
+        own_len = std::min(own_len, most_seen + std::min<int64_t>(s->max_new, (a.own_tile_rows - 1) / rep + 2));
+    }
     const int64_t most = max_blocks(kAttendBlock);
     if (pt > most || ot > most || s->prefix.n * heads > most || s->own.n * heads > most ||
         s->prefix.n * heads * pt > most || s->own.n * heads * ot > most)
@@ -367,15 +560,19 @@ int attend_shape(const kv_paged* p, const kv_step* s, int32_t q_heads, AttendSha
     // All pieces are cut by the bounds: lengths far below them leave most pieces empty (10000 tokens under a bound of
     // 10000 15 us, of 32768 20, of 131072 45; eight such sequences 67, 124 and 146).
     const int64_t room = 512, narrow_room = 256;
-    const int64_t prefix_work = pre * s->prefix.max_len, own_work = own * s->own.max_len * 6 / 10;
+    const int64_t prefix_work = pre * prefix_len, own_work = own * own_len * 6 / 10;
     const bool wide = a.own_wide && (a.prefix_wide || prefix_work == 0);
     const bool beside = a.prefix_wide && !a.own_wide && prefix_work > 0 && own_work > 0;
     const int64_t wide_room =
         beside ? std::max<int64_t>(room / 8, int64_t(double(room) * prefix_work / (double(prefix_work) + own_work)))
                : room;
-    cut_tokens(pre, s->prefix.n > 0 ? s->prefix.max_len : 0, wide_room, &a.prefix_tokens, &a.prefix_pieces);
-    cut_tokens(own, s->own.n > 0 ? s->own.max_len : 0, beside ? 2 * room : narrow_room, &a.own_tokens, &a.own_pieces);
-    if (wide) cut_wide(p, s, q_heads, pre, own, &a);
+    cut_tokens(pre, int32_t(prefix_len), wide_room, &a.prefix_tokens, &a.prefix_pieces);
+    cut_tokens(own, int32_t(own_len), beside ? 2 * room : narrow_room, &a.own_tokens, &a.own_pieces);
+    if (wide) {
+        const int32_t ol = int32_t(std::max<int64_t>(own_len, 1));
+        const double seen = own_len < s->own.max_len ? 1.0 : std::max(ol - s->max_new / 2.0, ol / 2.0) / ol;
+        cut_wide(p, s, q_heads, pre, own, int32_t(prefix_len), ol, seen, &a);
+    }
     a.own_pieces = std::max(1, a.own_pieces);
     a.slots = a.prefix_pieces + a.own_pieces;
     a.direct = a.slots == 1;
@@ -391,11 +588,20 @@ int attend_shape(const kv_paged* p, const kv_step* s, int32_t q_heads, AttendSha
     return KV_OK;
 }
 
-int attend_checks(const kv_paged* paged, const kv_step* step, int32_t layer, int32_t q_heads)
+// A pool for attention: bf16, or with its scales 8 bits.
+struct AttendPool {
+    const kv_paged* paged;
+    const kv_paged8* bytes;        // NULL: bf16
+};
+
+int attend_checks(const AttendPool& pool, const kv_step* step, int32_t layer, int32_t q_heads, const kv_window* win)
 {
-    int rc = check_step_pool(paged, layer, layer + 1);
-    if (rc == KV_OK) rc = check_step(paged, step);
-    if (rc == KV_OK) rc = check_heads(paged, q_heads);
+    int rc = pool.bytes != nullptr ? check_pool8(pool.bytes, layer, layer + 1)
+                                   : check_step_pool(pool.paged, layer, layer + 1);
+    if (rc == KV_OK) rc = check_step(pool.paged, step);
+    if (rc == KV_OK) rc = check_heads(pool.paged, q_heads);
+    if (rc == KV_OK && win != nullptr && (win->window < 1 || win->sinks < 0))
+        return fail(KV_EINVAL, "window = %d must be at least 1 and sinks = %d at least 0", win->window, win->sinks);
     return rc;
 }
 
@@ -407,28 +613,54 @@ int check_q(const kv_rows* q, float scale)
     return KV_OK;
 }
 
-template <int DP>
+template <int DP, class F>
 KernelFn attend_kernel(int blocks)
 {
     if constexpr (DP <= 128)
-        if (blocks == 2) return reinterpret_cast<KernelFn>(&attend_pieces<DP, 2>);
-    return blocks == 0 ? reinterpret_cast<KernelFn>(&attend_pieces<DP, 0>)
-                       : reinterpret_cast<KernelFn>(&attend_pieces<DP, 1>);
+        if (blocks == 2) return reinterpret_cast<KernelFn>(&attend_pieces<DP, 2, F>);
+    return blocks == 0 ? reinterpret_cast<KernelFn>(&attend_pieces<DP, 0, F>)
+                       : reinterpret_cast<KernelFn>(&attend_pieces<DP, 1, F>);
 }
 
 template <int DP>
-KernelFn join_kernel(bool by_row)
+KernelFn attend_kernel(int blocks, bool bytes, bool win)
 {
-    return by_row ? reinterpret_cast<KernelFn>(&attend_join_rows<DP>) : reinterpret_cast<KernelFn>(&attend_join<DP>);
+    if (bytes) return win ? attend_kernel<DP, Form<true, true>>(blocks) : attend_kernel<DP, Form<true, false>>(blocks);
+    return win ? attend_kernel<DP, Form<false, true>>(blocks) : attend_kernel<DP, Form<false, false>>(blocks);
 }
 
-int attend(const kv_paged* paged, const kv_step* step, int32_t layer, const kv_rows* q, int32_t q_heads, float scale,
-           const kv_rows* out, float* lse, void* workspace, size_t workspace_bytes, hipStream_t stream)
+template <int DP, bool kWindow>
+KernelFn join_kernel(bool by_row)
 {
-    int rc = attend_checks(paged, step, layer, q_heads);
+    return by_row ? reinterpret_cast<KernelFn>(&attend_join_rows<DP, kWindow>)
+                  : reinterpret_cast<KernelFn>(&attend_join<DP, kWindow>);
+}
+
+template <int DP>
+KernelFn join_kernel(bool by_row, bool win)
+{
+    return win ? join_kernel<DP, true>(by_row) : join_kernel<DP, false>(by_row);
+}
+
+size_t attend_workspace(const AttendPool& pool, const kv_step* step, int32_t q_heads, const kv_window* win)
+{
+    AttendShape sh;
+    if (attend_checks(pool, step, 0, q_heads, win) != KV_OK ||
+        attend_shape(pool.paged, step, q_heads, win, &sh) != KV_OK)
+        return 0;
+    ok();
+    return size_t(std::max<int64_t>(sh.bytes, 256));
+}
+
+int attend(const AttendPool& pool, const kv_step* step, int32_t layer, const kv_rows* q, int32_t q_heads, float scale,
+           const kv_window* win, const kv_rows* out, float* lse, void* workspace, size_t workspace_bytes,
+           hipStream_t stream)
+{
+    const kv_paged* paged = pool.paged;
+    int rc = attend_checks(pool, step, layer, q_heads, win);
     if (rc != KV_OK) return rc;
     AttendShape sh;
-    rc = attend_shape(paged, step, q_heads, &sh);
+    rc = attend_shape(paged, step, q_heads, win, &sh);
     if (rc != KV_OK) return rc;
     if (step->n_rows == 0 || step->own.n == 0) return ok();
     rc = check_q(q, scale);
@@ -465,21 +697,28 @@ int attend(const kv_paged* paged, const kv_step* step, int32_t layer, const kv_r
     a.own_tiles = sh.own_tiles;
     a.own_pieces = sh.own_pieces;
     a.own_tokens = sh.own_tokens;
+    a.own_tile_rows = sh.own_tile_rows;
+    if (pool.bytes != nullptr) a.scales = scales_arg(pool.bytes);
+    if (win != nullptr) {
+        a.window = win->window;
+        a.sinks = win->sinks;
+    }
     a.slots = sh.slots;
     a.prefix_items = uint32_t(sh.prefix_items);
     a.prefix_wide = sh.prefix_wide;
     a.own_wide = sh.own_wide;
     a.direct = sh.direct;
     const int dim = paged->head_dim;
-    KernelFn pieces = dim <= 64    ? attend_kernel<64>(sh.blocks)
-                      : dim <= 128 ? attend_kernel<128>(sh.blocks)
-                                   : attend_kernel<256>(sh.blocks);
+    const bool bytes = pool.bytes != nullptr, windowed = win != nullptr;
+    KernelFn pieces = dim <= 64    ? attend_kernel<64>(sh.blocks, bytes, windowed)
+                      : dim <= 128 ? attend_kernel<128>(sh.blocks, bytes, windowed)
+                                   : attend_kernel<256>(sh.blocks, bytes, windowed);
     // Rows enough to fill the GPU: a workgroup a row and some of its heads, so that 4096 of them make up for the
     // shared look-ups' wait.  (512 new tokens behind 2048: by row 53 us, by row and head 72; one token over 10000: 19 and 15.)
     const bool by_row = step->n_rows >= 128;
-    KernelFn join = dim <= 64    ? join_kernel<64>(by_row)
-                    : dim <= 128 ? join_kernel<128>(by_row)
-                                 : join_kernel<256>(by_row);
+    KernelFn join = dim <= 64    ? join_kernel<64>(by_row, windowed)
+                    : dim <= 128 ? join_kernel<128>(by_row, windowed)
+                                 : join_kernel<256>(by_row, windowed);
     rc = launch(pieces, sh.prefix_items + sh.own_items, kAttendBlock, &a, stream);
     if (rc == KV_OK && !sh.direct)
         rc = launch(join, by_row ? step->n_rows : int64_t(step->n_rows) * q_heads, 256, &a, stream,
@@ -500,7 +739,7 @@ KernelFn weights_kernel(bool rows, int32_t* tokens, int* block)
 int add_weights_call(const kv_paged* paged, const kv_step* step, int32_t layer, const kv_rows* q, const float* lse,
                      int32_t q_heads, float scale, const kv_sums* own, const kv_sums* prefix, hipStream_t stream)
 {
-    int rc = attend_checks(paged, step, layer, q_heads);
+    int rc = attend_checks({paged, nullptr}, step, layer, q_heads, nullptr);
     if (rc != KV_OK) return rc;
     if (own == nullptr && prefix == nullptr) return fail(KV_EINVAL, "own or prefix sums are needed");
     auto check_sums = [](const kv_sums* x, const kv_tables& t, bool may_be_null, const char* what) {
@@ -672,19 +911,88 @@ int kv_append(const kv_paged* paged, const kv_step* step, int32_t layer, const k
     return append(paged, step, layer, q, k, v, q_out, q_heads, type, q_out_type, positions, rope, slots, stream);
 }
 
+int kv_append_normed(const kv_paged* paged, const kv_step* step, int32_t layer, const kv_rows* q, const kv_rows* k,
+                     const kv_rows* v, const kv_rows* q_out, int32_t q_heads, kv_type type, kv_type q_out_type,
+                     const int32_t* positions, const kv_rope* rope, const kv_norm* norm, const kv_slots* slots,
+                     hipStream_t stream)
+{
+    return append_normed(paged, step, layer, q, k, v, q_out, q_heads, type, q_out_type, positions, rope, norm, slots,
+                         stream);
+}
+
+int kv_append8(const kv_paged8* paged, const kv_step* step, int32_t layer, const kv_rows* q, const kv_rows* k,
+               const kv_rows* v, const kv_rows* q_out, int32_t q_heads, kv_type type, kv_type q_out_type,
+               const int32_t* positions, const kv_rope* rope, const kv_norm* norm, hipStream_t stream)
+{
+    return append8(paged, step, layer, q, k, v, q_out, q_heads, type, q_out_type, positions, rope, norm, stream);
+}
+
+int kv_pack8(const kv_paged* from, const kv_tables* tables, const kv_paged8* to, const int32_t* to_table,
+             int64_t to_stride, int32_t layer_begin, int32_t layer_end, hipStream_t stream)
+{
+    int rc = check_step_pool(from, layer_begin, layer_end);
+    if (rc == KV_OK) rc = check_pool8(to, layer_begin, layer_end);
+    if (rc == KV_OK)
+        rc = check_pack(from, &to->pages, tables, to_table, to_stride, layer_begin, layer_end, stream);
+    if (rc != KV_OK) return rc;
+    return run_pack(true, from, &to->pages, to, tables, to_table, to_stride, layer_begin, layer_end, stream);
+}
+
+int kv_unpack8(const kv_paged8* from, const kv_tables* tables, const kv_paged* to, const int32_t* to_table,
+               int64_t to_stride, int32_t layer_begin, int32_t layer_end, hipStream_t stream)
+{
+    int rc = check_pool8(from, layer_begin, layer_end);
+    if (rc == KV_OK) rc = check_step_pool(to, layer_begin, layer_end);
+    if (rc == KV_OK)
+        rc = check_pack(&from->pages, to, tables, to_table, to_stride, layer_begin, layer_end, stream);
+    if (rc != KV_OK) return rc;
+    return run_pack(false, &from->pages, to, from, tables, to_table, to_stride, layer_begin, layer_end, stream);
+}
+
 size_t kv_attend_workspace_bytes(const kv_paged* paged, const kv_step* step, int32_t q_heads)
 {
-    AttendShape sh;
-    if (attend_checks(paged, step, 0, q_heads) != KV_OK || attend_shape(paged, step, q_heads, &sh) != KV_OK) return 0;
-    ok();
-    return size_t(std::max<int64_t>(sh.bytes, 256));
+    return attend_workspace({paged, nullptr}, step, q_heads, nullptr);
 }
 
 int kv_attend(const kv_paged* paged, const kv_step* step, int32_t layer, const kv_rows* q, int32_t q_heads,
               float scale, const kv_rows* out, float* lse, void* workspace, size_t workspace_bytes,
               hipStream_t stream)
 {
-    return attend(paged, step, layer, q, q_heads, scale, out, lse, workspace, workspace_bytes, stream);
+    return attend({paged, nullptr}, step, layer, q, q_heads, scale, nullptr, out, lse, workspace, workspace_bytes,
+                  stream);
+}
+
+size_t kv_attend_window_workspace_bytes(const kv_paged* paged, const kv_step* step, int32_t q_heads,
+                                        const kv_window* window)
+{
+    return attend_workspace({paged, nullptr}, step, q_heads, window);
+}
+
+int kv_attend_window(const kv_paged* paged, const kv_step* step, int32_t layer, const kv_rows* q, int32_t q_heads,
+                     float scale, const kv_window* window, const kv_rows* out, float* lse, void* workspace,
+                     size_t workspace_bytes, hipStream_t stream)
+{
+    return attend({paged, nullptr}, step, layer, q, q_heads, scale, window, out, lse, workspace, workspace_bytes,
+                  stream);
+}
+
+size_t kv_attend8_workspace_bytes(const kv_paged8* paged, const kv_step* step, int32_t q_heads,
+                                  const kv_window* window)
+{
+    if (paged == nullptr) {
+        fail(KV_EINVAL, "paged8 is NULL");
+        return 0;
+    }
+    return attend_workspace({&paged->pages, paged}, step, q_heads, window);
+}
+
+int kv_attend8(const kv_paged8* paged, const kv_step* step, int32_t layer, const kv_rows* q, int32_t q_heads,
+               float scale, const kv_window* window, const kv_rows* out, float* lse, void* workspace,
+               size_t workspace_bytes, hipStream_t stream)
+{
+    if (paged == nullptr) return fail(KV_EINVAL, "paged8 is NULL");
+    return attend({&paged->pages, paged}, step, layer, q, q_heads, scale, window, out, lse, workspace,
+                  workspace_bytes, stream);
 }
 
 int kv_add_weights(const kv_paged* paged, const kv_step* step, int32_t layer, const kv_rows* q, const float* lse,

@@ -16,6 +16,7 @@
 #include <string>
 
 #include "kv_append.hpp"
+#include "kv_append_heads.hpp"
 #include "kv_attend.hpp"
 #include "kv_cachegen.hpp"
 #include "kv_copy.hpp"
@@ -23,6 +24,7 @@
 #include "kv_fp8.hpp"
 #include "kv_move_bf16.hpp"
 #include "kv_order.hpp"
+#include "kv_pack8.hpp"
 #include "kv_weights.hpp"
 
 namespace {
