@@ -25,6 +25,8 @@ namespace kvmove {
 
 enum : int { kNormNone = 0, kNormRms = 1, kNormCentered = 2 };
 
+constexpr int kMaxShared = 512;        // weights of a head kept in LDS where all heads share them
+
 struct NormArg {
     uint64_t q_weight, k_weight;       // float32 [heads][dim], or 0: ones
     int64_t q_stride, k_stride;        // elements from head to head
@@ -36,10 +38,11 @@ struct AppendHeadsArgs {
     AppendArgs a;
     NormArg norm;
     ScalesArg scales;                  // of an 8-bit pool
-    int32_t lanes_log2, per;           // lanes G of a head of q or k, its units of a lane
+    int32_t lanes_log2, per;           // lanes G of a head of q or k, its units of a lane: one with vectors
     int32_t v_units, v_lanes_log2, v_per;   // append8: the same for a head of v, in units of two vectors
     uint32_t token_items;              // append8: workgroups [0, token_items) take a token's q
     int32_t pages, splits;             // append8: pages of a sequence, workgroups that share a page's heads
+    int32_t angles;                    // append8: room for angles in LDS, at least one token's
 };
 
 __device__ __forceinline__ float sum_over(float x, int lanes)
@@ -89,99 +92,164 @@ __device__ __forceinline__ int values_in(const Unit& u, int vec, bool live)
     return !live ? 0 : u.kind == kUnitPairs ? 2 * vec : vec;
 }
 
-// What a head is normalised with: (x * scale - c) * r.
+// What a head is normalised with: x * r - c.
 struct HeadNorm {
-    float scale, c, r;
+    float r, c;
 };
 
 // Of a group of lanes: each(f) calls f with every (values, number of them that
-// count) of the lane's units.  Squares leave float32 where a head's largest
-// magnitude is beyond 2^+-60; it is then brought near 1 by a power of two (below,
-// only where eps does not outweigh the squares anyway, and no further than eps
-// stays finite).  A head with an infinity or a NaN takes the formula as it is.
+// count) of the lane's units.  v: its first unit's.  Squares that leave float32
+// are rare, and looked for in their sum: such a head is done again, its values
+// brought near 1 by a power of two, v's too (below 1 only where eps does not
+// outweigh the squares anyway, and no further than eps stays finite).  A head
+// with an infinity or a NaN takes the formula as it is.
 template <int kVec, class Each>
-__device__ __forceinline__ HeadNorm head_norm(const NormArg& n, int dim, int lanes, Each&& each)
+__device__ __forceinline__ HeadNorm head_norm(const NormArg& n, int dim, int lanes, Values<kVec>& v, float& scale,
+                                              Each&& each)
 {
-    float big = 0.0f;
-    bool odd = false;
-    each([&](const Values<kVec>& v, int count) {
+    const float inv_dim = 1.0f / float(dim);
+    auto sums = [&](float s, float& mean, float& squares) {
+        mean = 0.0f;
+        if (n.kind == kNormCentered) {
+            each([&](const Values<kVec>& x, int count) {
 #pragma unroll
-        for (int i = 0; i < 2 * kVec; ++i) {
-            const float a = __builtin_fabsf(v.x[i]);
-            odd = odd || !(a < __builtin_inff());
-            big = __builtin_fmaxf(big, a);
+                for (int i = 0; i < 2 * kVec; ++i) mean = __builtin_fmaf(x.x[i], s, mean);
+            });
+            mean = sum_over(mean, lanes) * inv_dim;
         }
-    });
-    big = max_over(odd ? __builtin_inff() : big, lanes);
-    float scale = 1.0f;
-    if (big < __builtin_inff() && (big > 0x1p60f || (big < 0x1p-60f && n.eps < 0x1p-96f))) {
-        const int e = 127 - int(__float_as_uint(big) >> 23), most = n.eps == 0.0f ? 126 : 60;
-        scale = exp2_int(clamp_i32(e, -126, most));
-    }
-    float c = 0.0f;
-    if (n.kind == kNormCentered) {
-        each([&](const Values<kVec>& v, int count) {
+        squares = 0.0f;
+        each([&](const Values<kVec>& x, int count) {
+            if (n.kind == kNormCentered) {
 #pragma unroll
-            for (int i = 0; i < 2 * kVec; ++i) c = __builtin_fmaf(v.x[i], scale, c);
+                for (int i = 0; i < 2 * kVec; ++i) {
+                    const float d = i < count ? __builtin_fmaf(x.x[i], s, -mean) : 0.0f;
+                    squares = __builtin_fmaf(d, d, squares);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 2 * kVec; ++i) {
+                    const float d = x.x[i] * s;
+                    squares = __builtin_fmaf(d, d, squares);
+                }
+            }
         });
-        c = sum_over(c, lanes) / float(dim);
-    }
-    float q = 0.0f;
-    each([&](const Values<kVec>& v, int count) {
+        squares = sum_over(squares, lanes);
+    };
+    float mean, squares;
+    sums(1.0f, mean, squares);
+    scale = 1.0f;
+    const bool far = !(squares < 0x1p120f) || (squares < 0x1p-90f && n.eps < 0x1p-96f);
+    if (__any(far)) {
+        float big = 0.0f;
+        bool odd = false;
+        each([&](const Values<kVec>& x, int count) {
 #pragma unroll
-        for (int i = 0; i < 2 * kVec; ++i) {
-            const float d = i < count ? __builtin_fmaf(v.x[i], scale, -c) : 0.0f;
-            q = __builtin_fmaf(d, d, q);
-        }
-    });
-    q = sum_over(q, lanes) / float(dim) + n.eps * scale * scale;
-    return {scale, c, 1.0f / __builtin_sqrtf(q)};
+            for (int i = 0; i < 2 * kVec; ++i) {
+                const float a = __builtin_fabsf(x.x[i]);
+                odd = odd || !(a < __builtin_inff());
+                big = __builtin_fmaxf(big, a);
+            }
+        });
+        big = max_over(odd ? __builtin_inff() : big, lanes);
+        if (far && big < __builtin_inff())
+            scale = exp2_int(clamp_i32(127 - int(__float_as_uint(big) >> 23), -126, n.eps == 0.0f ? 126 : 60));
+        sums(scale, mean, squares);
+#pragma unroll
+        for (int i = 0; i < 2 * kVec; ++i) v.x[i] *= scale;
+    }
+    const float r = 1.0f / __builtin_sqrtf(__builtin_fmaf(squares, inv_dim, n.eps * scale * scale));
+    return {r, mean * r};
 }
 
-// The unit normalised; w: weights of its elements.
-template <int kVec>
-__device__ __forceinline__ void normalise(Values<kVec>& v, const HeadNorm& h, const RawUnit<float, kVec>& w)
+// Weights that all heads of q, all heads of k share, in LDS (ones where there are none).
+struct SharedWeights {
+    alignas(16) float w[2][kMaxShared];
+};
+
+__device__ __forceinline__ bool weights_shared(const NormArg& n, bool k, int dim)
 {
+    return ((k ? n.k_weight : n.q_weight) == 0 || (k ? n.k_stride : n.q_stride) == 0) && dim <= kMaxShared;
+}
+
+// For all threads; a barrier has to follow.
+__device__ __forceinline__ void share_weights(const NormArg& n, int dim, SharedWeights& sh)
+{
+    if (n.kind == kNormNone) return;
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) {
-        v.x[i] = __builtin_fmaf(v.x[i], h.scale, -h.c) * h.r * w.x.x[i];
-        v.x[kVec + i] = __builtin_fmaf(v.x[kVec + i], h.scale, -h.c) * h.r * w.y.x[i];
+    for (int k = 0; k < 2; ++k) {
+        const uint64_t base = k ? n.k_weight : n.q_weight;
+        if (weights_shared(n, k != 0, dim))
+            for (int d = threadIdx.x; d < dim; d += kAppendBlock) sh.w[k][d] = base == 0 ? 1.0f : gptr<const gf32>(base)[d];
     }
 }
 
-// Weights of a unit of head `head` of q or k; ones where there are none.
+// The unit of head `head` of q or k, its values scaled as head_norm says, normalised.
 template <int kVec>
-__device__ __forceinline__ RawUnit<float, kVec> load_weights(const NormArg& n, bool k, int head, const Unit& u)
+__device__ __forceinline__ void normalise(Values<kVec>& v, const HeadNorm& h, const NormArg& n, bool k, int head,
+                                          const Unit& u, int dim, const SharedWeights& sh)
 {
-    const uint64_t base = k ? n.k_weight : n.q_weight;
     RawUnit<float, kVec> w;
-    if (base == 0) {
+    if (weights_shared(n, k, dim))
+        w = load_raw<float, kVec>(sh.w[k ? 1 : 0], u);
+    else if ((k ? n.k_weight : n.q_weight) != 0)
+        w = load_raw<float, kVec>(reinterpret_cast<const float*>(k ? n.k_weight : n.q_weight) +
+                                      head * (k ? n.k_stride : n.q_stride), u);
+    else
 #pragma unroll
         for (int i = 0; i < kVec; ++i) w.x.x[i] = w.y.x[i] = 1.0f;
-        return w;
-    }
-    return load_raw<float, kVec>(reinterpret_cast<const float*>(base) + head * (k ? n.k_stride : n.q_stride), u);
-}
-
-// The unit rotated; angle(i): cosine and sine of its i-th pair.
-template <int kVec, class Angle>
-__device__ __forceinline__ void rotate(Values<kVec>& v, const Unit& u, Angle&& angle)
-{
-    // one form for both layouts, by selects: with the values changed in either of two branches the compiler keeps them
-    // in memory
-    const bool pairs = u.kind == kUnitPairs, turns = u.kind != kUnitPass;
-    Values<kVec> o;
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
-        const int j = kVec > 1 ? i ^ 1 : i;
-        const float2 c = turns ? angle(kVec > 1 && !pairs ? i / 2 : i) : float2{1.0f, 0.0f};
-        const float a = v.x[i], b = v.x[kVec + i];
-        const float other = pairs ? b : v.x[j];
-        const float turned = __builtin_fmaf(a, c.x, pairs || i % 2 == 0 ? -(other * c.y) : other * c.y);
-        o.x[i] = turns ? turned : a;
-        o.x[kVec + i] = __builtin_fmaf(b, c.x, a * c.y);
+        v.x[i] = __builtin_fmaf(v.x[i], h.r, -h.c) * w.x.x[i];
+        v.x[kVec + i] = __builtin_fmaf(v.x[kVec + i], h.r, -h.c) * w.y.x[i];
     }
-    v = o;
+}
+
+// The unit rotated; angle(i): cosine and sine of its i-th pair, 1 and 0 for a
+// unit that passes.  Not in place: the compiler would keep the values in memory.
+template <int kVec, bool kInterleaved, class Angle>
+__device__ __forceinline__ Values<kVec> rotated(const Values<kVec>& v, const Unit& u, int rot, Angle&& angle)
+{
+    Values<kVec> o = v;
+    if constexpr (kVec == 1 || !kInterleaved) {              // one that passes has no second vector: 0
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+            const float2 c = angle(i);
+            o.x[i] = __builtin_fmaf(v.x[i], c.x, -(v.x[kVec + i] * c.y));
+            o.x[kVec + i] = __builtin_fmaf(v.x[kVec + i], c.x, v.x[i] * c.y);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < kVec; i += 2) {
+            // the vector may lie across the end of what turns; there an infinity's pair would get its product with 0
+            const bool turns = u.d0 + i < rot;
+            const float2 c = angle(i / 2);
+            const float a = __builtin_fmaf(v.x[i], c.x, -(v.x[i + 1] * c.y));
+            const float b = __builtin_fmaf(v.x[i + 1], c.x, v.x[i] * c.y);
+            o.x[i] = turns ? a : v.x[i];
+            o.x[i + 1] = turns ? b : v.x[i + 1];
+        }
+    }
+    return o;
+}
+
+template <int kVec, class Angle>
+__device__ __forceinline__ Values<kVec> rotated(const AppendArgs& a, const Values<kVec>& v, const Unit& u, Angle&& angle)
+{
+    return a.interleaved != 0 ? rotated<kVec, true>(v, u, a.rot, angle) : rotated<kVec, false>(v, u, a.rot, angle);
+}
+
+// LDS for angles begins with the ones of a unit that passes, and ends with room
+// for a vector's that lies across the end of what turns.
+constexpr int kPassAngles = 8, kAngleRoom = kPassAngles + 4;
+
+__device__ __forceinline__ void put_pass_angles(float2* cs)
+{
+    if (threadIdx.x < kPassAngles) cs[threadIdx.x] = {1.0f, 0.0f};
+}
+
+__device__ __forceinline__ const float2* angles_at(const float2* cs, const Unit& u, int first)
+{
+    return u.kind == kUnitPass ? cs : cs + kPassAngles + first + u.pair;
 }
 
 // Cosine and sine of pair j at a position, formed as kv_append.hpp says.
@@ -213,7 +281,7 @@ __device__ __forceinline__ void put_values(TO* head, const Unit& u, const Values
 // pool.  cs: room for its angles.  As in append_rows, the first heads' values
 // are asked for before the owner, the page and the angles are known.
 template <class TI, class TO, int kVec, bool kKv>
-__device__ __forceinline__ void token_heads(const AppendHeadsArgs& h, int32_t r, float2* cs)
+__device__ __forceinline__ void token_heads(const AppendHeadsArgs& h, int32_t r, float2* cs, SharedWeights& sh)
 {
     constexpr int kAhead = 2;                      // heads of a lane in flight
     const AppendArgs& a = h.a;
@@ -227,19 +295,17 @@ __device__ __forceinline__ void token_heads(const AppendHeadsArgs& h, int32_t r,
                (k ? head - a.q_heads : head) * (k ? a.k_head : a.q_head);
     };
     auto unit = [&](int i) { return head_unit<kVec>(i < a.units ? i : 0, a.rot, a.interleaved != 0); };
-    auto weights = [&](int head, const Unit& u) {
+    auto norm = [&](Values<kVec>& v, const HeadNorm& n, int head, const Unit& u) {
         const bool k = head >= a.q_heads;
-        return load_weights<kVec>(h.norm, k, k ? head - a.q_heads : head, u);
+        normalise<kVec>(v, n, h.norm, k, k ? head - a.q_heads : head, u, dim, sh);
     };
     const Unit u0 = unit(lane);
     RawUnit<TI, kVec> raw[kAhead];
-    RawUnit<float, kVec> w[kAhead];
 #pragma unroll
     for (int x = 0; x < kAhead; ++x) {
         const int head = first + x * stride;
         if (head >= heads) continue;
         raw[x] = load_raw<TI, kVec>(source(head), u0);
-        if (h.norm.kind != kNormNone) w[x] = weights(head, u0);
     }
     Vec<TI, kVec> v{};
     const int v_vectors = kv_heads * (dim / kVec);
@@ -272,13 +338,16 @@ __device__ __forceinline__ void token_heads(const AppendHeadsArgs& h, int32_t r,
             }
         }
     }
-    for (int j = tid; j < a.rot / 2; j += kAppendBlock) cs[j] = angle_of(a, pos, j);
+    share_weights(h.norm, dim, sh);
+    put_pass_angles(cs);
+    for (int j = tid; j < a.rot / 2; j += kAppendBlock) cs[kPassAngles + j] = angle_of(a, pos, j);
     __syncthreads();
-    auto finish = [&](int head, const RawUnit<TI, kVec>& r0, const RawUnit<float, kVec>& w0) {
+    auto finish = [&](int head, const RawUnit<TI, kVec>& r0) {
         const TI* src = source(head);
         const bool live = lane < a.units;
-        auto put = [&](const Unit& u, Values<kVec>& x) {
-            rotate<kVec>(x, u, [&](int j) { return cs[u.pair + j]; });
+        auto put = [&](const Unit& u, const Values<kVec>& y) {
+            const float2* angles = angles_at(cs, u, 0);
+            const Values<kVec> x = rotated<kVec>(a, y, u, [&](int j) { return angles[j]; });
             if (head < a.q_heads)
                 put_values<TO, kVec>(reinterpret_cast<TO*>(a.q_out) + r * a.o_row + head * a.o_head, u, x);
             else if (kd != 0)
@@ -286,21 +355,28 @@ __device__ __forceinline__ void token_heads(const AppendHeadsArgs& h, int32_t r,
         };
         Values<kVec> x0 = values_of<TI, kVec>(r0, u0, live);
         HeadNorm n{};
+        float scale = 1.0f;
         if (h.norm.kind != kNormNone) {
-            n = head_norm<kVec>(h.norm, dim, lanes, [&](auto&& f) {
+            n = head_norm<kVec>(h.norm, dim, lanes, x0, scale, [&](auto&& f) {
                 f(x0, values_in(u0, kVec, live));
+                if constexpr (kVec > 1) return;
                 for (int i = lane + lanes; i < h.per * lanes; i += lanes) {
                     const Unit u = unit(i);
                     f(values_of<TI, kVec>(load_raw<TI, kVec>(src, u), u, i < a.units), values_in(u, kVec, i < a.units));
                 }
             });
-            normalise<kVec>(x0, n, w0);
+            norm(x0, n, head, u0);
         }
         if (live) put(u0, x0);
+        if constexpr (kVec > 1) return;
         for (int i = lane + lanes; i < a.units; i += lanes) {
             const Unit u = unit(i);
             Values<kVec> x = values_of<TI, kVec>(load_raw<TI, kVec>(src, u), u, true);
-            if (h.norm.kind != kNormNone) normalise<kVec>(x, n, weights(head, u));
+            if (h.norm.kind != kNormNone) {
+#pragma unroll
+                for (int e = 0; e < 2 * kVec; ++e) x.x[e] *= scale;
+                norm(x, n, head, u);
+            }
             put(u, x);
         }
     };
@@ -312,11 +388,10 @@ __device__ __forceinline__ void token_heads(const AppendHeadsArgs& h, int32_t r,
                 const int head = base + first + x * stride;
                 if (head >= heads) continue;
                 raw[x] = load_raw<TI, kVec>(source(head), u0);
-                if (h.norm.kind != kNormNone) w[x] = weights(head, u0);
             }
 #pragma unroll
         for (int x = 0; x < kAhead; ++x)
-            if (base + first + x * stride < heads) finish(base + first + x * stride, raw[x], w[x]);
+            if (base + first + x * stride < heads) finish(base + first + x * stride, raw[x]);
     }
     if (kd == 0) return;
     for (int i = tid; i < v_vectors; i += kAppendBlock) {
@@ -334,19 +409,21 @@ __device__ __forceinline__ void token_heads(const AppendHeadsArgs& h, int32_t r,
         }
 }
 
-template <class TI, class TO, int kVec>
+template <class TI, class TO, int kVec, bool kKv>
 __global__ __launch_bounds__(kAppendBlock) void append_heads_rows(AppendHeadsArgs h)
 {
-    __shared__ float2 cs[kMaxRot / 2];
-    token_heads<TI, TO, kVec, true>(h, blockIdx.x, cs);
+    __shared__ float2 cs[kAngleRoom + kMaxRot / 2];
+    __shared__ SharedWeights sh;
+    token_heads<TI, TO, kVec, kKv>(h, blockIdx.x, cs, sh);
 }
 
-constexpr int kPageAngles = 4096;      // angles of a page's new tokens kept in LDS, else each is formed where it is used
-constexpr int kHeldUnits = 4;          // units of a lane kept between the look for the scale and the bytes
+constexpr int kPageAngles = 7168;      // at most so many of a page's new tokens are kept in LDS, else each is formed
+                                       // where it is used
+constexpr int kHeldUnits = 2;          // units of a lane kept between the look for the scale and the bytes
 
 // New tokens of one page of a sequence, heads [h0, h1): a wave takes one head's K or V at a time.
 template <class TI, int kVec>
-__device__ __forceinline__ void page_heads(const AppendHeadsArgs& h, uint32_t item, float2* cs)
+__device__ __forceinline__ void page_heads(const AppendHeadsArgs& h, uint32_t item, float2* cs, SharedWeights& sh)
 {
     const AppendArgs& a = h.a;
     const PoolArg& p = a.pool;
@@ -373,21 +450,23 @@ __device__ __forceinline__ void page_heads(const AppendHeadsArgs& h, uint32_t it
         raise_fault(kFaultPool);
         return;
     }
-    const bool kept = int64_t(n) * half <= kPageAngles;
-    if (kept && half > 0) {
+    const bool kept = int64_t(n) * half <= h.angles;
+    share_weights(h.norm, dim, sh);
+    put_pass_angles(cs);
+    if (kept)
         for (int i = threadIdx.x; i < n * half; i += kAppendBlock) {
             const int tok = i / half;
-            cs[i] = angle_of(a, gptr<const gi32>(a.positions)[row0 + tok], i - tok * half);
+            cs[kPassAngles + i] = angle_of(a, gptr<const gi32>(a.positions)[row0 + tok], i - tok * half);
         }
-        __syncthreads();
-    }
+    __syncthreads();
     const int heads = (int(p.heads) + h.splits - 1) / h.splits, h0 = split * heads;
     const int h1 = h0 + heads < int(p.heads) ? h0 + heads : int(p.heads);
 #pragma unroll 1
     for (int task = 2 * h0 + (threadIdx.x >> 6); task < 2 * h1; task += kAppendBlock / 64) {
         const int head = __builtin_amdgcn_readfirstlane(task >> 1);
         const bool is_v = __builtin_amdgcn_readfirstlane(task & 1) != 0;
-        const int lg = is_v ? h.v_lanes_log2 : h.lanes_log2, lanes = 1 << lg, per = is_v ? h.v_per : h.per;
+        const int lg = is_v ? h.v_lanes_log2 : h.lanes_log2, lanes = 1 << lg;
+        const int per = kVec > 1 ? 1 : is_v ? h.v_per : h.per;
         const int units = is_v ? h.v_units : a.units, steps = ((n + (64 >> lg) - 1) >> (6 - lg)) * per;
         const uint64_t scale_at = (is_v ? l.v_scales : l.k_scales) + (uint64_t(page) * p.heads + head) * 4;
         const uint64_t dst = (is_v ? l.v : l.k) + (uint64_t(page) * p.page_size * p.heads + head) * dim;
@@ -421,8 +500,10 @@ __device__ __forceinline__ void page_heads(const AppendHeadsArgs& h, uint32_t it
             Values<kVec> v = values_of<TI, kVec>(raw, u, x.live);
             if (is_v) return v;
             if (h.norm.kind != kNormNone) {
-                const HeadNorm m = head_norm<kVec>(h.norm, dim, lanes, [&](auto&& f) {
+                float scale;
+                const HeadNorm m = head_norm<kVec>(h.norm, dim, lanes, v, scale, [&](auto&& f) {
                     f(v, values_in(u, kVec, x.live));
+                    if constexpr (kVec > 1) return;
                     for (int k = 1; k < per; ++k) {             // the head's other units, in whatever order
                         Place y = x;
                         y.i = x.i + (k << lg);
@@ -432,16 +513,17 @@ __device__ __forceinline__ void page_heads(const AppendHeadsArgs& h, uint32_t it
                         f(values_of<TI, kVec>(load(y, w), w, y.live), values_in(w, kVec, y.live));
                     }
                 });
-                normalise<kVec>(v, m, load_weights<kVec>(h.norm, true, head, u));
+                normalise<kVec>(v, m, h.norm, true, head, u, dim, sh);
             }
             const int tok = x.tok < n ? x.tok : 0;
             if (kept) {
-                rotate<kVec>(v, u, [&](int j) { return cs[tok * half + u.pair + j]; });
-            } else {
-                const int32_t pos = gptr<const gi32>(a.positions)[row0 + tok];
-                rotate<kVec>(v, u, [&](int j) { return angle_of(a, pos, u.pair + j); });
+                const float2* angles = angles_at(cs, u, tok * half);
+                return rotated<kVec>(a, v, u, [&](int j) { return angles[j]; });
             }
-            return v;
+            const int32_t pos = gptr<const gi32>(a.positions)[row0 + tok];
+            return rotated<kVec>(a, v, u, [&](int j) {
+                return u.pair + j < half && u.kind != kUnitPass ? angle_of(a, pos, u.pair + j) : float2{1.0f, 0.0f};
+            });
         };
         auto largest = [&](const Place& x, const Unit& u, const Values<kVec>& v, float m) {
             const int count = values_in(u, kVec, x.live);
@@ -454,7 +536,6 @@ __device__ __forceinline__ void page_heads(const AppendHeadsArgs& h, uint32_t it
         Values<kVec> held[kHeldUnits];
 #pragma unroll
         for (int i = 0; i < kHeldUnits; ++i) {
-            if (i >= 2 && steps <= 2) break;
             const Place x = place(i);
             raw[i] = load(x, unit(x));
         }
@@ -523,13 +604,14 @@ __device__ __forceinline__ void page_heads(const AppendHeadsArgs& h, uint32_t it
 }
 
 template <class TI, class TO, int kVec>
-__global__ __launch_bounds__(kAppendBlock) void append8_rows(AppendHeadsArgs h)
+__global__ __launch_bounds__(kAppendBlock, 4) void append8_rows(AppendHeadsArgs h)
 {
-    __shared__ float2 cs[kPageAngles];
+    extern __shared__ float2 cs[];
+    __shared__ SharedWeights sh;
     if (blockIdx.x < h.token_items)
-        token_heads<TI, TO, kVec, false>(h, blockIdx.x, cs);
+        token_heads<TI, TO, kVec, false>(h, blockIdx.x, cs, sh);
     else
-        page_heads<TI, kVec>(h, blockIdx.x - h.token_items, cs);
+        page_heads<TI, kVec>(h, blockIdx.x - h.token_items, cs, sh);
 }
 
 }  // namespace kvmove

@@ -1,9 +1,11 @@
 // kv_pack8.hpp -- cached tokens from bf16 pages into 8-bit ones and back.
 //
-// pack8_pages    a wave per (layer, sequence, page, head, K or V): the block's
-//                largest magnitude, its scale, its bytes (kv_pool8.hpp);
-// unpack8_pages  byte * scale, which bf16 holds exactly; a workgroup per
-//                (layer, sequence, page, K or V).
+// pack8_pages    a workgroup per (layer, sequence, page, group of heads, K or
+//                V): a thread always sees the same head, so that a block's
+//                largest magnitude is the maximum of some threads' own; then
+//                the scale and the bytes (kv_pool8.hpp).
+// unpack8_pages  byte * scale, which bf16 holds exactly; a wave per 4 KiB of
+//                the page's bf16.
 //
 // Bound: memory, 3 bytes an element either way.
 #pragma once
@@ -13,7 +15,8 @@
 namespace kvmove {
 
 constexpr int kPackBlock = 256;
-constexpr int kPackHeld = 4;           // vectors of 16 elements of a lane kept between the scale and the bytes
+constexpr int kPackHeld = 8;           // vectors of a thread kept between the scale and the bytes
+constexpr int kUnpackVectors = 4;      // vectors of a lane
 
 struct PackArgs {
     PoolArg from, to;                  // one page size, heads and head size
@@ -22,9 +25,11 @@ struct PackArgs {
     uint64_t to_table;                 // int32[n][to_stride]
     int64_t to_stride;
     int32_t pages;                     // of a sequence
-    int32_t head_groups;               // pack8: workgroups of a page
-    uint32_t vec_magic, vec_shift;     // i / (vectors of 16 elements of a head)
-    uint32_t row_magic, row_shift;     // i / (of a row)
+    int32_t parts;                     // workgroups of a page: head groups (pack8), tiles (unpack8)
+    int32_t group;                     // pack8: heads of a workgroup
+    int32_t cols;                      // pack8: their vectors of 8 elements in a row, at most a thread each
+    uint32_t vec_magic, vec_shift;     // i / (vectors of a head)
+    uint32_t row_magic, row_shift;     // i / cols (pack8), i / (vectors of a row) (unpack8)
 };
 
 // The page that workgroup b works on; n: its tokens.  n <= 0: none.
@@ -34,7 +39,7 @@ struct PackPage {
 
 __device__ __forceinline__ PackPage pack_page(const PackArgs& a, uint32_t b, bool bad)
 {
-    const int32_t s = int32_t(b / uint32_t(a.pages)), pi = int32_t(b % uint32_t(a.pages));
+    const int32_t s = __builtin_amdgcn_readfirstlane(b / uint32_t(a.pages)), pi = int32_t(b - uint32_t(s) * a.pages);
     const int64_t left = table_len(a.tables, s) - int64_t(pi) * a.from.page_size;
     PackPage p{0, 0, 0};
     if (left <= 0) return p;
@@ -76,75 +81,86 @@ __device__ __forceinline__ u32x2 bytes_of_bf16(u32x4 x, float inv)
 // grid: (pages of all sequences * head groups, K and V of every layer)
 __global__ __launch_bounds__(kPackBlock) void pack8_pages(PackArgs a)
 {
+    __shared__ unsigned int largest[kPackBlock / 2];         // of a head of the group, as bits: order of magnitudes
     a.from.layer += blockIdx.y / 2;
     a.to.layer += blockIdx.y / 2;
     const LayerAt from = layer_at<false>(a.from, a.scales), to = layer_at<true>(a.to, a.scales);
-    const uint32_t group = blockIdx.x % uint32_t(a.head_groups);
-    const PackPage p = pack_page(a, blockIdx.x / uint32_t(a.head_groups), bad_layer<false>(from) || bad_layer<true>(to));
-    const int32_t head = int32_t(group) * (kPackBlock / 64) + (threadIdx.x >> 6);
-    if (p.n <= 0 || head >= int32_t(a.from.heads)) return;
+    const uint32_t b = xcd_contiguous(blockIdx.x, gridDim.x), at = b / uint32_t(a.parts);
+    const PackPage p = pack_page(a, at, bad_layer<false>(from) || bad_layer<true>(to));
+    if (p.n <= 0) return;
     const bool v = blockIdx.y % 2 != 0;
-    const int lane = threadIdx.x & 63, dim = a.from.dim, vectors = dim / 16, total = p.n * vectors;
+    const int32_t h0 = int32_t(b - at * uint32_t(a.parts)) * a.group;
+    const int dim = a.from.dim, tid = threadIdx.x;
+    const int heads = a.group < int(a.from.heads) - h0 ? a.group : int(a.from.heads) - h0;
     const uint32_t row = a.from.heads * dim;                             // elements
-    const uint64_t src = (v ? from.v : from.k) + (uint64_t(p.from) * a.from.page_size * row + head * dim) * 2;
-    const uint64_t dst = (v ? to.v : to.k) + (uint64_t(p.to) * a.to.page_size * row + head * dim);
-    auto element = [&](int i) {                                          // where vector i begins
-        const int tok = int((uint64_t(uint32_t(i)) * a.vec_magic) >> a.vec_shift);
-        return uint32_t(tok) * row + uint32_t(i - tok * vectors) * 16;
+    // thread: vector `col` of the group's row, tokens first, first + step, ...
+    const int first = int((uint64_t(uint32_t(tid)) * a.row_magic) >> a.row_shift), col = tid - first * a.cols;
+    const int step = kPackBlock / a.cols, head = int((uint64_t(uint32_t(col)) * a.vec_magic) >> a.vec_shift);
+    const bool live = first < step && head < heads;
+    const uint32_t offset = first * row + h0 * dim + col * 8, stride = step * row;
+    const uint64_t page = uint64_t(a.from.page_size) * row;
+    const __amdgpu_buffer_rsrc_t src = byte_range((v ? from.v : from.k) + p.from * page * 2, p.n * row * 2);
+    const __amdgpu_buffer_rsrc_t dst = byte_range((v ? to.v : to.k) + p.to * page, p.n * row);
+    auto has = [&](int k) { return live && first + k * step < p.n; };
+    auto load = [&](int k) {
+        return has(k) ? __builtin_amdgcn_raw_buffer_load_b128(src, (offset + k * stride) * 2, 0, kCpolNt | kCpolSc1)
+                      : u32x4{0, 0, 0, 0};
     };
-    u32x4 x[kPackHeld][2];
+    if (tid < kPackBlock / 2) largest[tid] = 0;
+    u32x4 x[kPackHeld];
 #pragma unroll
-    for (int k = 0; k < kPackHeld; ++k) {
-        const int i = lane + 64 * k;
-        const uint64_t at = src + uint64_t(element(i < total ? i : 0)) * 2;   // the first again where there is no more
-        x[k][0] = *gptr<const gvec4>(at);
-        x[k][1] = *gptr<const gvec4>(at + 16);
-    }
+    for (int k = 0; k < kPackHeld; ++k) x[k] = load(k);
+    __syncthreads();
     float most = 0.0f;
 #pragma unroll
-    for (int k = 0; k < kPackHeld; ++k) most = largest_of(x[k][1], largest_of(x[k][0], most));
-    for (int i = lane + 64 * kPackHeld; i < total; i += 64) {
-        const uint64_t at = src + uint64_t(element(i)) * 2;
-        most = largest_of(*gptr<const gvec4>(at + 16), largest_of(*gptr<const gvec4>(at), most));
-    }
-    const int e = scale_exponent(wave_max(most));
+    for (int k = 0; k < kPackHeld; ++k) most = largest_of(x[k], most);
+    const int rounds = (p.n + step - 1) / step;
+    for (int k = kPackHeld; k < rounds; ++k) most = largest_of(load(k), most);
+    if (live) atomicMax(&largest[head], __float_as_uint(most));          // a maximum does not depend on the order
+    __syncthreads();
+    const int e = scale_exponent(__uint_as_float(largest[live ? head : 0]));
     const float inv = exp2_int(-e);
-    auto put = [&](int i, u32x4 y, u32x4 z) {
-        const u32x2 b = bytes_of_bf16(y, inv), c = bytes_of_bf16(z, inv);
-        *gptr<gvec4>(dst + element(i)) = u32x4{b[0], b[1], c[0], c[1]};
+    auto put = [&](int k, u32x4 y) {
+        if (has(k))
+            __builtin_amdgcn_raw_buffer_store_b64(bytes_of_bf16(y, inv), dst, offset + k * stride, 0, kCpolNt | kCpolSc1);
     };
 #pragma unroll
-    for (int k = 0; k < kPackHeld; ++k)
-        if (lane + 64 * k < total) put(lane + 64 * k, x[k][0], x[k][1]);
-    for (int i = lane + 64 * kPackHeld; i < total; i += 64) {
-        const uint64_t at = src + uint64_t(element(i)) * 2;
-        put(i, *gptr<const gvec4>(at), *gptr<const gvec4>(at + 16));
-    }
-    if (lane == 0)
-        gptr<gf32>(v ? to.v_scales : to.k_scales)[uint64_t(p.to) * a.to.heads + head] = exp2_int(e);
+    for (int k = 0; k < kPackHeld; ++k) put(k, x[k]);
+    for (int k = kPackHeld; k < rounds; ++k) put(k, load(k));
+    if (tid < heads)
+        gptr<gf32>(v ? to.v_scales : to.k_scales)[uint64_t(p.to) * a.to.heads + h0 + tid] =
+            exp2_int(scale_exponent(__uint_as_float(largest[tid])));
 }
 
-// grid: (pages of all sequences, K and V of every layer)
-__global__ __launch_bounds__(kPackBlock) void unpack8_pages(PackArgs a)
+// grid: (pages of all sequences * tiles, K and V of every layer)
+__global__ __launch_bounds__(64) void unpack8_pages(PackArgs a)
 {
     a.from.layer += blockIdx.y / 2;
     a.to.layer += blockIdx.y / 2;
     const LayerAt from = layer_at<true>(a.from, a.scales), to = layer_at<false>(a.to, a.scales);
-    const PackPage p = pack_page(a, blockIdx.x, bad_layer<true>(from) || bad_layer<false>(to));
-    if (p.n <= 0) return;
+    const uint32_t b = xcd_contiguous(blockIdx.x, gridDim.x), at = b / uint32_t(a.parts);
+    const PackPage p = pack_page(a, at, bad_layer<true>(from) || bad_layer<false>(to));
     const bool v = blockIdx.y % 2 != 0;
-    const int vectors = a.from.dim / 16, row = a.from.heads * vectors;   // vectors of 16 elements
-    const uint64_t bytes = uint64_t(a.from.page_size) * row * 16;
-    const uint64_t src = (v ? from.v : from.k) + p.from * bytes, dst = (v ? to.v : to.k) + p.to * bytes * 2;
+    const uint32_t dim = a.from.dim, row = a.from.heads * dim / 8;       // vectors of 8 elements
+    const uint32_t first = (b - at * uint32_t(a.parts)) * (64 * kUnpackVectors) + threadIdx.x;
+    if (p.n <= 0 || first - threadIdx.x >= p.n * row) return;
+    const uint64_t page = uint64_t(a.from.page_size) * row * 8;
+    const __amdgpu_buffer_rsrc_t src = byte_range((v ? from.v : from.k) + p.from * page, p.n * row * 8);
+    const __amdgpu_buffer_rsrc_t dst = byte_range((v ? to.v : to.k) + p.to * page * 2, p.n * row * 16);
     const uint64_t scales = (v ? from.v_scales : from.k_scales) + uint64_t(p.from) * a.from.heads * 4;
-    for (int64_t i = threadIdx.x; i < int64_t(p.n) * row; i += kPackBlock) {
-        const uint32_t in_row = uint32_t(i) - uint32_t((uint64_t(i) * a.row_magic) >> a.row_shift) * uint32_t(row);
-        const uint32_t head = uint32_t((uint64_t(in_row) * a.vec_magic) >> a.vec_shift);
-        const u32x4 b = *gptr<const gvec4>(src + i * 16);
-        const float s = gptr<const gf32>(scales)[head];
-        *gptr<gvec4>(dst + i * 32) = bf16_of_bytes8(b[0], b[1], s);
-        *gptr<gvec4>(dst + i * 32 + 16) = bf16_of_bytes8(b[2], b[3], s);
+    u32x2 x[kUnpackVectors];
+    float s[kUnpackVectors];
+#pragma unroll
+    for (int k = 0; k < kUnpackVectors; ++k) {
+        const uint32_t i = first + 64 * k, r = uint32_t((uint64_t(i) * a.row_magic) >> a.row_shift);
+        const uint32_t head = uint32_t((uint64_t(i - r * row) * a.vec_magic) >> a.vec_shift);
+        x[k] = __builtin_amdgcn_raw_buffer_load_b64(src, i * 8, 0, kCpolNt | kCpolSc1);
+        s[k] = gptr<const gf32>(scales)[head];
     }
+#pragma unroll
+    for (int k = 0; k < kUnpackVectors; ++k)
+        __builtin_amdgcn_raw_buffer_store_b128(bf16_of_bytes8(x[k][0], x[k][1], s[k]), dst, (first + 64 * k) * 16, 0,
+                                               kCpolNt | kCpolSc1);
 }
 
 }  // namespace kvmove

@@ -139,12 +139,12 @@ StepArg step_arg(const kv_step* s)
     return a;
 }
 
-int launch(KernelFn k, int64_t grid, int block, void* arg, hipStream_t stream, unsigned grid_y = 1)
+int launch(KernelFn k, int64_t grid, int block, void* arg, hipStream_t stream, unsigned grid_y = 1, size_t lds = 0)
 {
     if (grid <= 0) return KV_OK;
     if (grid > max_blocks(block)) return fail(KV_EINVAL, "%lld workgroups exceed one launch", (long long)grid);
     void* args[] = {arg};
-    const hipError_t e = hipLaunchKernel(k, dim3(unsigned(grid), grid_y), dim3(block), args, 0, stream);
+    const hipError_t e = hipLaunchKernel(k, dim3(unsigned(grid), grid_y), dim3(block), args, lds, stream);
     if (e != hipSuccess) return fail(KV_EHIP, "kernel launch failed: %s", hipGetErrorString(e));
     return KV_OK;
 }
@@ -160,7 +160,18 @@ KernelFn append_kernel(bool vectors)
 struct AppendCall {
     AppendArgs a;
     bool vectors;              // 16-byte vectors, else element by element
+    bool aligned;              // every address and stride allows vectors, whatever turns
 };
+
+void use_units(AppendCall& call, bool vectors)
+{
+    AppendArgs& a = call.a;
+    const int vec = vectors ? 8 : 1, dim = int(a.pool.dim);
+    call.vectors = vectors;
+    a.units = head_units(a.rot, dim, a.interleaved != 0, vec);
+    magic_of(a.units, &a.unit_magic, &a.unit_shift);
+    magic_of(dim / vec, &a.vec_magic, &a.vec_shift);
+}
 
 int append_call(const kv_paged* paged, const kv_step* step, int32_t layer, const kv_rows* q, const kv_rows* k,
                 const kv_rows* v, const kv_rows* q_out, int32_t q_heads, kv_type type, kv_type q_out_type,
@@ -196,8 +207,8 @@ int append_call(const kv_paged* paged, const kv_step* step, int32_t layer, const
     const int64_t size = type == KV_TYPE_FP32 ? 4 : 2, out_size = q_out_type == KV_TYPE_FP32 ? 4 : 2;
     // 16-byte vectors where every address, stride and the pairs' distance allow them, else element by element
     const int dim = paged->head_dim, unit = rope->interleaved ? 8 : 16;
-    bool vectors = dim % 8 == 0 && rope->rot % unit == 0 && rows_vectors(*k, size) && rows_vectors(*v, size);
-    if (q != nullptr) vectors = vectors && rows_vectors(*q, size) && rows_vectors(*q_out, out_size);
+    bool aligned = dim % 8 == 0 && rows_vectors(*k, size) && rows_vectors(*v, size);
+    if (q != nullptr) aligned = aligned && rows_vectors(*q, size) && rows_vectors(*q_out, out_size);
     for (const kv_rows* x : {k, v, q})
         if (x != nullptr && misaligned(x->data, size)) return fail(KV_EINVAL, "q, k or v is not aligned to its type");
     if (q != nullptr && misaligned(q_out->data, out_size)) return fail(KV_EINVAL, "q_out is not aligned to its type");
@@ -227,14 +238,11 @@ int append_call(const kv_paged* paged, const kv_step* step, int32_t layer, const
     a.rot = rope->rot;
     a.q_heads = q != nullptr ? q_heads : 0;
     a.interleaved = rope->interleaved;
-    const int vec = vectors ? 8 : 1;
-    a.units = head_units(a.rot, dim, a.interleaved != 0, vec);
-    magic_of(a.units, &a.unit_magic, &a.unit_shift);
-    magic_of(dim / vec, &a.vec_magic, &a.vec_shift);
     if (int64_t(a.q_heads + 2 * int64_t(paged->num_kv_heads)) * dim > INT32_MAX / 2)
         return fail(KV_EINVAL, "a token's heads are too large for one workgroup");
     a.gain = rope->gain;
-    *call = {a, vectors};
+    *call = {a, false, aligned};
+    use_units(*call, aligned && rope->rot % unit == 0);
     return KV_OK;
 }
 
@@ -285,9 +293,13 @@ int log2_up(int32_t x)
     return lg;
 }
 
-AppendHeadsArgs heads_args(const AppendCall& call, const kv_norm* norm)
+// Arguments of the kernels that take a head to a group of lanes.  With vectors no lane has more than one unit of it, which
+// wider heads would ask for: they go element by element.  Interleaved pairs may end inside a vector.
+AppendHeadsArgs heads_args(AppendCall& call, const kv_norm* norm)
 {
     AppendHeadsArgs h{};
+    use_units(call, call.aligned && (call.vectors || call.a.interleaved != 0));
+    if (call.a.units > 64) use_units(call, false);
     h.a = call.a;
     if (norm != nullptr)
         h.norm = {reinterpret_cast<uint64_t>(norm->q_weight), reinterpret_cast<uint64_t>(norm->k_weight),
@@ -295,6 +307,17 @@ AppendHeadsArgs heads_args(const AppendCall& call, const kv_norm* norm)
     h.lanes_log2 = std::min(log2_up(h.a.units), 6);
     h.per = int32_t(ceil_div(h.a.units, 1 << h.lanes_log2));
     return h;
+}
+
+template <bool kKv>
+KernelFn heads_rows_kernel(const AppendCall& call, kv_type type, bool same_out)
+{
+    return by_types(type, same_out, [&](auto in, auto out) {
+        using TI = decltype(in);
+        using TO = decltype(out);
+        return call.vectors ? reinterpret_cast<KernelFn>(&append_heads_rows<TI, TO, 8, kKv>)
+                            : reinterpret_cast<KernelFn>(&append_heads_rows<TI, TO, 1, kKv>);
+    });
 }
 
 int append_normed(const kv_paged* paged, const kv_step* step, int32_t layer, const kv_rows* q, const kv_rows* k,
@@ -313,13 +336,8 @@ int append_normed(const kv_paged* paged, const kv_step* step, int32_t layer, con
     if (rc != KV_OK) return rc;
     if (step->n_rows == 0) return ok();
     AppendHeadsArgs h = heads_args(call, norm);
-    const KernelFn f = by_types(type, q == nullptr || q_out_type == type, [&](auto in, auto out) {
-        using TI = decltype(in);
-        using TO = decltype(out);
-        return call.vectors ? reinterpret_cast<KernelFn>(&append_heads_rows<TI, TO, 8>)
-                            : reinterpret_cast<KernelFn>(&append_heads_rows<TI, TO, 1>);
-    });
-    rc = launch(f, step->n_rows, kAppendBlock, &h, stream);
+    rc = launch(heads_rows_kernel<true>(call, type, q == nullptr || q_out_type == type), step->n_rows, kAppendBlock, &h,
+                stream);
     return rc == KV_OK ? ok() : rc;
 }
 
@@ -333,6 +351,10 @@ int check_pool8(const kv_paged8* p, int32_t layer_begin, int32_t layer_end)
     if (p->k_scales == nullptr || p->v_scales == nullptr) return fail(KV_EINVAL, "k_scales / v_scales is NULL");
     return KV_OK;
 }
+
+// New tokens from which on their q has a launch of its own, where the page kernel's registers do not leave half as many waves
+// (45116 tokens 296 us, in one launch 308; 4000 tokens 36.5 and 33.8).
+constexpr int32_t kQApart = 16384;
 
 int append8(const kv_paged8* paged8, const kv_step* step, int32_t layer, const kv_rows* q, const kv_rows* k,
             const kv_rows* v, const kv_rows* q_out, int32_t q_heads, kv_type type, kv_type q_out_type,
@@ -368,7 +390,16 @@ int append8(const kv_paged8* paged8, const kv_step* step, int32_t layer, const k
     });
     if (pairs > max_blocks(kAppendBlock) || pairs * h.splits + h.token_items > max_blocks(kAppendBlock))
         return fail(KV_EINVAL, "too many pages for one launch");
-    rc = launch(f, h.token_items + pairs * h.splits, kAppendBlock, &h, stream);
+    // LDS for the angles of a page's new tokens, or if that is too much of one token
+    const int64_t half = h.a.rot / 2, page_angles = std::min<int64_t>(size, step->max_new) * half;
+    h.angles = int32_t(std::max<int64_t>(page_angles <= kPageAngles ? page_angles : half, 1));
+    const size_t lds = size_t(h.angles + kAngleRoom) * sizeof(float2);
+    if (q != nullptr && step->n_rows >= kQApart) {
+        rc = launch(heads_rows_kernel<false>(call, type, q_out_type == type), step->n_rows, kAppendBlock, &h, stream);
+        if (rc != KV_OK) return rc;
+        h.token_items = 0;
+    }
+    rc = launch(f, h.token_items + pairs * h.splits, kAppendBlock, &h, stream, 1, lds);
     return rc == KV_OK ? ok() : rc;
 }
 
@@ -383,6 +414,8 @@ int check_pack(const kv_paged* from, const kv_paged* to, const kv_tables* tables
     if (from->page_size != to->page_size || from->num_kv_heads != to->num_kv_heads || from->head_dim != to->head_dim ||
         from->num_layers != to->num_layers)
         return fail(KV_EINVAL, "the pools must have one page size, heads, head size and number of layers");
+    if (from->head_dim > 8 * kPackBlock)
+        return fail(KV_EINVAL, "head_dim = %d must be at most %d here", from->head_dim, 8 * kPackBlock);
     if (to_table != nullptr && (to_stride < 0 || to_stride > INT32_MAX))
         return fail(KV_EINVAL, "to_stride %lld outside [0, 2^31)", (long long)to_stride);
     if (to_table != nullptr && tables->n > 0 && tables->max_len > to_stride * from->page_size)
@@ -400,20 +433,28 @@ int run_pack(bool pack, const kv_paged* from, const kv_paged* to, const kv_paged
     a.tables = tables_arg(tables);
     a.to_table = reinterpret_cast<uint64_t>(to_table != nullptr ? to_table : tables->table);
     a.to_stride = to_table != nullptr ? to_stride : tables->stride;
-    const int64_t size = from->page_size, vectors = from->head_dim / 16;
-    a.pages = int32_t(ceil_div(tables->max_len, size));
-    a.head_groups = int32_t(ceil_div(from->num_kv_heads, kPackBlock / 64));
-    magic_of(int32_t(vectors), &a.vec_magic, &a.vec_shift);
-    magic_of(int32_t(vectors * from->num_kv_heads), &a.row_magic, &a.row_shift);
-    const int64_t pages = int64_t(tables->n) * a.pages, items = pack ? pages * a.head_groups : pages;
-    if (pages > max_blocks(kPackBlock) || items > max_blocks(kPackBlock))
-        return fail(KV_EINVAL, "too many pages for one launch");
+    const int32_t vectors = from->head_dim / 8, row = vectors * from->num_kv_heads;
+    a.pages = int32_t(ceil_div(tables->max_len, from->page_size));
+    magic_of(vectors, &a.vec_magic, &a.vec_shift);
+    int block = 64;
+    if (pack) {
+        block = kPackBlock;
+        a.group = std::min(std::max(kPackBlock / vectors, 1), from->num_kv_heads);
+        a.cols = a.group * vectors;
+        a.parts = int32_t(ceil_div(from->num_kv_heads, a.group));
+        magic_of(a.cols, &a.row_magic, &a.row_shift);
+    } else {
+        a.parts = int32_t(ceil_div(int64_t(from->page_size) * row, 64 * kUnpackVectors));
+        magic_of(row, &a.row_magic, &a.row_shift);
+    }
+    const int64_t pages = int64_t(tables->n) * a.pages, items = pages * a.parts;
+    if (pages > max_blocks(block) || items > max_blocks(block)) return fail(KV_EINVAL, "too many pages for one launch");
     constexpr int32_t kLayers = 32767;                       // of a launch: its second dimension
     for (int32_t l = layer_begin; l < layer_end; l += kLayers) {
         a.from = pool_arg(from, l);
         a.to = pool_arg(to, l);
         const int rc = launch(pack ? reinterpret_cast<KernelFn>(&pack8_pages) : reinterpret_cast<KernelFn>(&unpack8_pages),
-                              items, kPackBlock, &a, stream, unsigned(2 * std::min(kLayers, layer_end - l)));
+                              items, block, &a, stream, unsigned(2 * std::min(kLayers, layer_end - l)));
         if (rc != KV_OK) return rc;
     }
     return ok();
@@ -522,7 +563,7 @@ void cut_wide(const kv_paged* p, const kv_step* s, int32_t q_heads, int64_t pre,
 
 // A window (NULL: none) cuts what an item may see, and with it the pieces and the workspace: the sinks and the first row's
 // window are rounded to whole tiles (make_span), and an item's rows are some tokens apart.
-int attend_shape(const kv_paged* p, const kv_step* s, int32_t q_heads, const kv_window* win, AttendShape* out)
+int attend_shape(const kv_paged* p, bool bytes, const kv_step* s, int32_t q_heads, const kv_window* win, AttendShape* out)
 {
     const int64_t heads = p->num_kv_heads, rep = q_heads / heads;
     AttendShape a{};
@@ -559,15 +600,19 @@ int attend_shape(const kv_paged* p, const kv_step* s, int32_t q_heads, const kv_
     // not cut 177; the 32 sequences 67; but the two documents 183).
     // All pieces are cut by the bounds: lengths far below them leave most pieces empty (10000 tokens under a bound of
     // 10000 15 us, of 32768 20, of 131072 45; eight such sequences 67, 124 and 146).
-    const int64_t room = 512, narrow_room = 256;
-    const int64_t prefix_work = pre * prefix_len, own_work = own * own_len * 6 / 10;
+    // In 8 bits a narrow token costs half as much, and the wide ones have to be more: 64 sequences behind two 32768-token
+    // prefixes 192 us with the shares of bf16, 139 with these, 142 with half as many own pieces.  Under a window most own
+    // lengths are cut to it and three times `room` own pieces pay: 32 sequences behind a prefix under a window of 4096
+    // 107 us, with twice 110.
+    const int64_t room = 512, narrow_room = 256, beside_room = (bytes || win != nullptr ? 3 : 2) * room;
+    const int64_t prefix_work = pre * prefix_len, own_work = own * own_len * (bytes ? 25 : 60) / 100;
     const bool wide = a.own_wide && (a.prefix_wide || prefix_work == 0);
     const bool beside = a.prefix_wide && !a.own_wide && prefix_work > 0 && own_work > 0;
     const int64_t wide_room =
         beside ? std::max<int64_t>(room / 8, int64_t(double(room) * prefix_work / (double(prefix_work) + own_work)))
                : room;
     cut_tokens(pre, int32_t(prefix_len), wide_room, &a.prefix_tokens, &a.prefix_pieces);
-    cut_tokens(own, int32_t(own_len), beside ? 2 * room : narrow_room, &a.own_tokens, &a.own_pieces);
+    cut_tokens(own, int32_t(own_len), beside ? beside_room : narrow_room, &a.own_tokens, &a.own_pieces);
     if (wide) {
         const int32_t ol = int32_t(std::max<int64_t>(own_len, 1));
         const double seen = own_len < s->own.max_len ? 1.0 : std::max(ol - s->max_new / 2.0, ol / 2.0) / ol;
@@ -646,7 +691,7 @@ size_t attend_workspace(const AttendPool& pool, const kv_step* step, int32_t q_h
 {
     AttendShape sh;
     if (attend_checks(pool, step, 0, q_heads, win) != KV_OK ||
-        attend_shape(pool.paged, step, q_heads, win, &sh) != KV_OK)
+        attend_shape(pool.paged, pool.bytes != nullptr, step, q_heads, win, &sh) != KV_OK)
         return 0;
     ok();
     return size_t(std::max<int64_t>(sh.bytes, 256));
@@ -660,7 +705,7 @@ int attend(const AttendPool& pool, const kv_step* step, int32_t layer, const kv_
     int rc = attend_checks(pool, step, layer, q_heads, win);
     if (rc != KV_OK) return rc;
     AttendShape sh;
-    rc = attend_shape(paged, step, q_heads, win, &sh);
+    rc = attend_shape(paged, pool.bytes != nullptr, step, q_heads, win, &sh);
     if (rc != KV_OK) return rc;
     if (step->n_rows == 0 || step->own.n == 0) return ok();
     rc = check_q(q, scale);

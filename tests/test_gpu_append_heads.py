@@ -54,6 +54,8 @@ NORMS = [
     (2, 1, 520, 4, [6, 5], [2, 5], 500, True, FL, None, 10, False, False, 1e-6),
     (5, 7, 112, 16, [70], [3], 112, False, HF, None, 200, True, True, 1e-6),
     (1, 1, 2, 4, [3], [3], 2, False, BF, None, 0, False, False, 1e-6),
+    (4, 2, 128, 16, [20, 9], [3, 9], 46, True, BF, None, 500, False, False, 1e-6),   # pairs that end inside a vector
+    (2, 3, 80, 16, [20, 9], [3, 9], 2, True, HF, None, 500, True, True, 1e-6),
 ]
 
 
@@ -133,6 +135,27 @@ def test_norm_of_heads_far_from_one(centered, eps):
         assert torch.all(q_out[:, 9, :5] == 0)
 
 
+@pytest.mark.parametrize("interleaved,rot", [(True, 40), (True, 42), (False, 32)])
+@pytest.mark.parametrize("bits", [16, 8])
+def test_what_does_not_turn_passes(interleaved, rot, bits):
+    """An infinity or a NaN behind the elements that turn stays where it is."""
+    b = (pu.Batch8 if bits == 8 else su.Batch)(3, 2, 64, 16, [4], [4])
+    paged, step = (device8 if bits == 8 else device)(b)[-2:]
+    x = b.normal(4, 2, 64, dtype=BF)
+    x[0, 0, rot], x[1, 1, 63], x[2, 0, 62], x[3, 1, rot + 1] = math.inf, -math.inf, math.nan, math.inf
+    pos = torch.arange(7, 11, dtype=torch.int32).cuda()
+    rope = kvm.Rope(rot, interleaved=interleaved)
+    norm = None if bits == 8 else kvm.Norm(torch.ones(64))
+    got = kvm.append(paged, step, 0, x.cuda(), x.cuda(), x.cuda(), pos, rope, norm=norm).cpu()
+    if bits == 8:
+        assert torch.equal(got[:, :, rot:].view(torch.int16), x[:, :, rot:].view(torch.int16))
+    assert torch.isfinite(got[:, :, :rot]).all() or bits == 16
+    for r, h, d in ((0, 0, rot), (1, 1, 63), (2, 0, 62), (3, 1, rot + 1)):
+        assert torch.isfinite(torch.cat([got[r, h, :d], got[r, h, d + 1:]])).all() or r == 2 or bits == 16
+        assert not torch.isfinite(got[r, h, d])
+    assert kvm.take_faults() == 0
+
+
 def test_append_normed_in_place_without_q_and_without_norm():
     b = su.Batch(2, 2, 64, 16, [20, 3], [4, 1])
     pool, paged, step = device(b)
@@ -172,6 +195,7 @@ EIGHT = [
     (1, 1, 128, 64, [150, 64], [149, 1], 128, False, HF, None, 10, False),
     (3, 1, 128, 128, [300], [299], 128, False, FL, None, 10, True),          # more angles than a workgroup keeps
     (1, 3, 96, 300, [299], [299], 96, True, BF, None, 0, False),
+    (8, 8, 128, 16, [78, 204, 90], [5, 5, 17], 122, True, BF, None, 40, True),   # pairs that end inside a vector
 ]
 
 
