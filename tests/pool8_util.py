@@ -61,9 +61,13 @@ class Batch8(su.Batch):
 
 
 def attend_window64(b, q, scale, window=None, sinks=0, layer=0):
-    """(out, lse, bound of out, bound of lse) as su.attend64 (whose derivation of the bounds holds as it stands: an 8-bit
-    pool's values are exact in bf16), of rows that see the tokens t <= p with t > p - window or t < sinks, p counted from
-    the start of the prefix.  A row without a slot of its own stands on the prefix's last token."""
+    """(out, lse, bound of out, bound of lse) as su.attend64, of rows that see the tokens t <= p with t > p - window or
+    t < sinks, p counted from the start of the prefix.  A row without a slot of its own stands on the prefix's last token.
+
+    The bounds are derived there.  An 8-bit pool's values are exact in bf16, and in fp16 beside each other; its weights go
+    into the second product as fp16 (or, more exactly, as two bf16): half a step of 2^-11, so 2^-12 of each, and half of
+    fp16's least step, 2^-25, for one below 2^-14, relative to the row's largest weight, which is 1 or more before the
+    division by their sum, itself 1 or more."""
     rows, hq, D = q.shape
     rep = hq // b.heads
     out = torch.full((rows, hq, D), math.nan, dtype=torch.float64)
@@ -90,8 +94,10 @@ def attend_window64(b, q, scale, window=None, sinks=0, layer=0):
                 rel = (D + 4) * U * S + (len(t) + 12) * U
                 if math.isfinite(rel):
                     el[r, h] = rel + 4 * U * (abs(float(lse[r, h])) + S)
-                    eo[r, h] = ((2 * rel + 2.0 ** -16) * (w @ vv.abs())) * (1 + 2.0 ** -8) \
-                        + 2.0 ** -8 * out[r, h].abs() + 2.0 ** -133
+                    part = (2 * rel + 2.0 ** -16) * (w @ vv.abs())
+                    if isinstance(b, Batch8):
+                        part = (2 * rel + 2.0 ** -12) * (w @ vv.abs()) + 2.0 ** -25 * vv.abs().sum(0)
+                    eo[r, h] = part * (1 + 2.0 ** -8) + 2.0 ** -8 * out[r, h].abs() + 2.0 ** -133
     return out, lse, eo, el
 
 

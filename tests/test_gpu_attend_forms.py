@@ -118,6 +118,28 @@ def test_what_the_window_hides_does_not_reach_a_row(where, bits):
             within(lse, wl, el, "lse")
 
 
+@pytest.mark.parametrize("spread", [6, 30, 60])
+def test_attend8_blocks_far_apart(spread):
+    """V blocks of magnitudes from 2^-spread to 2^spread, in an order that begins small, large or anywhere; the window
+    leaves some rows only small ones.  What the larger ones add to an output bounds what a row that sees them may be off;
+    a row that does not see them is as exact as without them."""
+    for seed in range(3):
+        for case in ((1, 4, 128, 16, [300, 70], [150, 70], [200], [2]), (2, 2, 64, 16, [260, 33], [100, 20], [150], [2]),
+                     (1, 2, 256, 16, [150, 9], [75, 9], [40], [2]), (1, 1, 128, 16, [300], [1], [], [])):
+            b = su.Batch(seed, *case[:1], *case[2:], layers=2)
+            for table, lens in ((b.own_table, b.lens), (b.prefix_table, b.prefix)):
+                for i, n in enumerate(lens):
+                    for p in range(-(-n // b.page)):
+                        e = int(torch.randint(-spread, spread + 1, (1,), generator=b.g)) if p or seed else -spread
+                        rows = b.rows(table, i, min(n, (p + 1) * b.page), p * b.page)
+                        b.flat()[:, 1, rows] *= 2.0 ** e
+            b.__class__ = pu.Batch8
+            b.quantise()
+            q = b.normal(b.q_start[-1], case[0] * case[1], case[2], gain=2.0)
+            compare(b, q, 8, None, 0)
+            compare(b, q, 8, 20, 3)
+
+
 def test_lengths_and_rows_that_change_on_the_device():
     """Lengths past their bound are cut, row ranges out of order touch nothing outside."""
     b, q = batch((2, 2, 128, 16, [64, 48], [1, 1], [32], [2]), 8)
