@@ -87,12 +87,17 @@ def attend_window64(b, q, scale, window=None, sinks=0, layer=0):
             for h in range(hq):
                 kk, vv, x = kt[:, h // rep], vt[:, h // rep], q[r, h].double()
                 sc = (kk @ x) * scale
-                S = float((kk.abs() @ x.abs()).max() * scale)
                 lse[r, h] = torch.logsumexp(sc, 0)
+                if float(lse[r, h]) == -math.inf:
+                    out[r, h] = 0.0
+                    continue
                 w = torch.exp(sc - lse[r, h])
                 out[r, h] = w @ vv
+                # an infinite score has no error of its own: the bounds are those of the finite ones
+                size = ((kk.abs() @ x.abs()) * scale)[torch.isfinite(sc)]
+                S = float(size.max()) if size.numel() else 0.0
                 rel = (D + 4) * U * S + (len(t) + 12) * U
-                if math.isfinite(rel):
+                if math.isfinite(float(lse[r, h])):
                     el[r, h] = rel + 4 * U * (abs(float(lse[r, h])) + S)
                     part = (2 * rel + 2.0 ** -16) * (w @ vv.abs())
                     if isinstance(b, Batch8):
