@@ -42,7 +42,7 @@ struct AppendHeadsArgs {
     int32_t v_units, v_lanes_log2, v_per;   // append8: the same for a head of v, in units of two vectors
     uint32_t token_items;              // append8: workgroups [0, token_items) take a token's q
     int32_t pages, splits;             // append8: pages of a sequence, workgroups that share a page's heads
-    int32_t angles;                    // append8: room for angles in LDS, at least one token's
+    int32_t angles;                    // append8: angles that LDS has room for, a token's at least
 };
 
 __device__ __forceinline__ float sum_over(float x, int lanes)
@@ -183,10 +183,10 @@ __device__ __forceinline__ void share_weights(const NormArg& n, int dim, SharedW
     }
 }
 
-// The unit of head `head` of q or k, its values scaled as head_norm says, normalised.
+// Weights of a unit of head `head` of q or k.
 template <int kVec>
-__device__ __forceinline__ void normalise(Values<kVec>& v, const HeadNorm& h, const NormArg& n, bool k, int head,
-                                          const Unit& u, int dim, const SharedWeights& sh)
+__device__ __forceinline__ RawUnit<float, kVec> weights_of_unit(const NormArg& n, bool k, int head, const Unit& u,
+                                                                int dim, const SharedWeights& sh)
 {
     RawUnit<float, kVec> w;
     if (weights_shared(n, k, dim))
@@ -197,6 +197,15 @@ __device__ __forceinline__ void normalise(Values<kVec>& v, const HeadNorm& h, co
     else
 #pragma unroll
         for (int i = 0; i < kVec; ++i) w.x.x[i] = w.y.x[i] = 1.0f;
+    return w;
+}
+
+// The unit of head `head` of q or k, its values scaled as head_norm says, normalised.
+template <int kVec>
+__device__ __forceinline__ void normalise(Values<kVec>& v, const HeadNorm& h, const NormArg& n, bool k, int head,
+                                          const Unit& u, int dim, const SharedWeights& sh)
+{
+    const RawUnit<float, kVec> w = weights_of_unit<kVec>(n, k, head, u, dim, sh);
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
         v.x[i] = __builtin_fmaf(v.x[i], h.r, -h.c) * w.x.x[i];
@@ -417,14 +426,89 @@ __global__ __launch_bounds__(kAppendBlock) void append_heads_rows(AppendHeadsArg
     token_heads<TI, TO, kVec, kKv>(h, blockIdx.x, cs, sh);
 }
 
-constexpr int kPageAngles = 7168;      // at most so many of a page's new tokens are kept in LDS, else each is formed
-                                       // where it is used
+// ---- keys and values of an 8-bit pool
+//
+// A byte keeps four bits, so a key that is off by the last bit of a float32
+// falls on the other side of a border, a 16th of it away, once in 10^6; a
+// block's scale does so by a factor of two.  k is therefore normalised and
+// rotated in 64 bits, and becomes a float32 only by rounding to odd, which
+// leaves it on its own side of every border of fewer bits: the bytes and
+// scales are those of the formula.  (v is what it was.)  It costs 6 us of 200
+// for 45116 tokens, and little of q, k and v's way through memory.
+
+template <int kVec>
+struct WideValues {
+    double x[2 * kVec];
+};
+
+template <class TI, int kVec>
+__device__ __forceinline__ WideValues<kVec> wide_values_of(const RawUnit<TI, kVec>& r, const Unit& u, bool live)
+{
+    const Values<kVec> v = values_of<TI, kVec>(r, u, live);
+    WideValues<kVec> w;
+#pragma unroll
+    for (int i = 0; i < 2 * kVec; ++i) w.x[i] = double(v.x[i]);
+    return w;
+}
+
+__device__ __forceinline__ double sum_over(double x, int lanes)
+{
+    for (int d = 1; d < lanes; d *= 2) x += __shfl_xor(x, d);
+    return x;
+}
+
+// (mean, 1 / sqrt(mean square + eps)) of a head; each as for head_norm.  No square of a float32 leaves 64 bits.
+template <int kVec, class Each>
+__device__ __forceinline__ double2 wide_norm(const NormArg& n, int dim, int lanes, Each&& each)
+{
+    double mean = 0.0, squares = 0.0;
+    if (n.kind == kNormCentered) {
+        each([&](const WideValues<kVec>& x, int count) {
+#pragma unroll
+            for (int i = 0; i < 2 * kVec; ++i) mean += x.x[i];
+        });
+        mean = sum_over(mean, lanes) / double(dim);
+    }
+    each([&](const WideValues<kVec>& x, int count) {
+#pragma unroll
+        for (int i = 0; i < 2 * kVec; ++i) {
+            const double d = i < count ? x.x[i] - mean : 0.0;
+            squares = __builtin_fma(d, d, squares);
+        }
+    });
+    return {mean, 1.0 / __builtin_sqrt(sum_over(squares, lanes) / double(dim) + double(n.eps))};
+}
+
+// Cosine and sine of an angle in turns.
+__device__ __forceinline__ double2 wide_angle(double turns)
+{
+    double sn, cn;
+    sincospi(2.0 * (turns - __builtin_rint(turns)), &sn, &cn);
+    return {cn, sn};
+}
+
+// float32 by rounding to odd: towards 0, and the last bit set where that lost
+// something.  What is beyond float32 becomes its largest value (infinity's bits
+// less one); NaN and infinities stay.
+__device__ __forceinline__ float to_odd(double x)
+{
+    const float f = float(x);
+    const double back = double(f);
+    const uint32_t u = __float_as_uint(f), down = __builtin_fabs(back) > __builtin_fabs(x) ? u - 1u : u;
+    return __uint_as_float(back != x ? down | 1u : u);
+}
+
+constexpr int kPageAngles = 4096;      // angles of a page's new tokens in LDS at once, 16 bytes each
+constexpr int kChunkHeads = 64;        // heads of a workgroup at most where that is not all of them
 constexpr int kHeldUnits = 2;          // units of a lane kept between the look for the scale and the bytes
 
-// New tokens of one page of a sequence, heads [h0, h1): a wave takes one head's K or V at a time.
+// New tokens of one page of a sequence, some of its heads: a wave takes one head's K or V at a time.
+//
+// Bound: memory, with q's workgroups; of 45116 tokens of 32 query heads and 8 KV heads of 128 (1.0 GB) 200 us, 5.1 TB/s.
 template <class TI, int kVec>
-__device__ __forceinline__ void page_heads(const AppendHeadsArgs& h, uint32_t item, float2* cs, SharedWeights& sh)
+__device__ __forceinline__ void page_heads(const AppendHeadsArgs& h, uint32_t item, double2* cs, SharedWeights& sh)
 {
+    __shared__ float found_by[2][kAppendBlock / 64];
     const AppendArgs& a = h.a;
     const PoolArg& p = a.pool;
     const int dim = p.dim, half = a.rot / 2, lane = threadIdx.x & 63;
@@ -450,31 +534,49 @@ __device__ __forceinline__ void page_heads(const AppendHeadsArgs& h, uint32_t it
         raise_fault(kFaultPool);
         return;
     }
-    const bool kept = int64_t(n) * half <= h.angles;
-    share_weights(h.norm, dim, sh);
-    put_pass_angles(cs);
-    if (kept)
-        for (int i = threadIdx.x; i < n * half; i += kAppendBlock) {
-            const int tok = i / half;
-            cs[kPassAngles + i] = angle_of(a, gptr<const gi32>(a.positions)[row0 + tok], i - tok * half);
-        }
-    __syncthreads();
     const int heads = (int(p.heads) + h.splits - 1) / h.splits, h0 = split * heads;
     const int h1 = h0 + heads < int(p.heads) ? h0 + heads : int(p.heads);
-#pragma unroll 1
-    for (int task = 2 * h0 + (threadIdx.x >> 6); task < 2 * h1; task += kAppendBlock / 64) {
+    // Angles of new tokens [c0, c0 + count), times the gain: a thread takes a pair over a run of tokens, and where their
+    // positions follow one another it turns on by one position's angle, which is 4 operations for the 100 of a new one.
+    auto fill = [&](int c0, int count) {
+        if (half == 0) return;
+        const double turns_per_radian = 0.15915494309189533577, gain = double(a.gain);
+        const int shares = kAppendBlock / half < 1 ? 1 : kAppendBlock / half < count ? kAppendBlock / half : count;
+        const int run = (count + shares - 1) / shares, share = int(threadIdx.x) / half;
+        const int t0 = share * run, t1 = t0 + run < count ? t0 + run : count;
+        if (share >= shares) return;
+        const int j = int(threadIdx.x) - share * half;
+        const double f = gptr<const __attribute__((address_space(1))) double>(a.freqs)[j] * turns_per_radian;
+        const double2 step = wide_angle(f);
+        double2 c{};
+        int32_t last = 0;
+        for (int t = t0; t < t1; ++t) {
+            const int32_t pos = gptr<const gi32>(a.positions)[row0 + c0 + t];
+            if (t > t0 && int64_t(pos) == int64_t(last) + 1)
+                c = {__builtin_fma(c.x, step.x, -(c.y * step.y)), __builtin_fma(c.y, step.x, c.x * step.y)};
+            else
+                c = wide_angle(double(pos) * f);
+            last = pos;
+            cs[t * half + j] = {c.x * gain, c.y * gain};
+        }
+    };
+    // a task's work on those tokens: kFind looks for the largest magnitude, kPut writes; kBoth does both, with what
+    // join(largest) makes of it between them.  lead: the wave that sees to the tokens that were there and the scale.
+    enum { kFind, kPut, kBoth };
+    auto work = [&](int task, int c0, int count, int what, float found, bool lead, auto&& join) {
         const int head = __builtin_amdgcn_readfirstlane(task >> 1);
         const bool is_v = __builtin_amdgcn_readfirstlane(task & 1) != 0;
         const int lg = is_v ? h.v_lanes_log2 : h.lanes_log2, lanes = 1 << lg;
         const int per = kVec > 1 ? 1 : is_v ? h.v_per : h.per;
-        const int units = is_v ? h.v_units : a.units, steps = ((n + (64 >> lg) - 1) >> (6 - lg)) * per;
+        const int units = is_v ? h.v_units : a.units, steps = ((count + (64 >> lg) - 1) >> (6 - lg)) * per;
         const uint64_t scale_at = (is_v ? l.v_scales : l.k_scales) + (uint64_t(page) * p.heads + head) * 4;
         const uint64_t dst = (is_v ? l.v : l.k) + (uint64_t(page) * p.page_size * p.heads + head) * dim;
         const uint64_t row_bytes = uint64_t(p.heads) * dim;
         const float was = *gptr<const gf32>(scale_at);
-        const TI* base = reinterpret_cast<const TI*>(is_v ? a.v : a.k) + row0 * (is_v ? a.v_row : a.k_row) +
-                         head * (is_v ? a.v_head : a.k_head);
+        const int in_lds = what == kBoth ? c0 : 0;              // the first of them among the angles
         const int64_t row = is_v ? a.v_row : a.k_row;
+        const TI* base = reinterpret_cast<const TI*>(is_v ? a.v : a.k) + (row0 + c0) * row +
+                         head * (is_v ? a.v_head : a.k_head);
         struct Place {
             int tok, i;
             bool live;
@@ -484,7 +586,7 @@ __device__ __forceinline__ void page_heads(const AppendHeadsArgs& h, uint32_t it
             Place x;
             x.tok = (round << (6 - lg)) + (lane >> lg);
             x.i = (lane & (lanes - 1)) + ((step - round * per) << lg);
-            x.live = x.tok < n && x.i < units;
+            x.live = x.tok < count && x.i < units;
             return x;
         };
         auto unit = [&](const Place& x) {
@@ -493,37 +595,57 @@ __device__ __forceinline__ void page_heads(const AppendHeadsArgs& h, uint32_t it
                         : head_unit<kVec>(i, a.rot, a.interleaved != 0);
         };
         auto load = [&](const Place& x, const Unit& u) {
-            return load_raw<TI, kVec>(base + int64_t(x.tok < n ? x.tok : 0) * row, u);
+            return load_raw<TI, kVec>(base + int64_t(x.tok < count ? x.tok : 0) * row, u);
         };
         // a step's values as they are to be cached; all lanes together
         auto ready = [&](const Place& x, const Unit& u, const RawUnit<TI, kVec>& raw) {
-            Values<kVec> v = values_of<TI, kVec>(raw, u, x.live);
-            if (is_v) return v;
+            if (is_v) return values_of<TI, kVec>(raw, u, x.live);
+            WideValues<kVec> v = wide_values_of<TI, kVec>(raw, u, x.live);
             if (h.norm.kind != kNormNone) {
-                float scale;
-                const HeadNorm m = head_norm<kVec>(h.norm, dim, lanes, v, scale, [&](auto&& f) {
+                const double2 m = wide_norm<kVec>(h.norm, dim, lanes, [&](auto&& f) {
                     f(v, values_in(u, kVec, x.live));
                     if constexpr (kVec > 1) return;
                     for (int k = 1; k < per; ++k) {             // the head's other units, in whatever order
                         Place y = x;
                         y.i = x.i + (k << lg);
                         if (y.i >= per << lg) y.i -= per << lg;
-                        y.live = y.tok < n && y.i < units;
+                        y.live = y.tok < count && y.i < units;
                         const Unit w = unit(y);
-                        f(values_of<TI, kVec>(load(y, w), w, y.live), values_in(w, kVec, y.live));
+                        f(wide_values_of<TI, kVec>(load(y, w), w, y.live), values_in(w, kVec, y.live));
                     }
                 });
-                normalise<kVec>(v, m, h.norm, true, head, u, dim, sh);
+                const RawUnit<float, kVec> w = weights_of_unit<kVec>(h.norm, true, head, u, dim, sh);
+#pragma unroll
+                for (int i = 0; i < kVec; ++i) {
+                    v.x[i] = (v.x[i] - m.x) * m.y * double(w.x.x[i]);
+                    v.x[kVec + i] = (v.x[kVec + i] - m.x) * m.y * double(w.y.x[i]);
+                }
             }
-            const int tok = x.tok < n ? x.tok : 0;
-            if (kept) {
-                const float2* angles = angles_at(cs, u, tok * half);
-                return rotated<kVec>(a, v, u, [&](int j) { return angles[j]; });
+            const double2* angles = cs + (in_lds + (x.tok < count ? x.tok : 0)) * half + u.pair;
+            Values<kVec> o;
+            if (kVec == 1 || a.interleaved == 0) {
+                const bool turns = u.kind == kUnitPairs;
+#pragma unroll
+                for (int i = 0; i < kVec; ++i) {
+                    const double2 c = turns ? angles[i] : double2{1.0, 0.0};
+                    const double b = turns ? v.x[kVec + i] : 0.0;
+                    o.x[i] = to_odd(__builtin_fma(v.x[i], c.x, -(b * c.y)));
+                    o.x[kVec + i] = to_odd(__builtin_fma(b, c.x, v.x[i] * c.y));
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < kVec; i += 2) {
+                    // as for q: the vector may lie across the end of what turns
+                    const bool turns = u.d0 + i < a.rot;
+                    const double2 c = turns ? angles[i / 2] : double2{1.0, 0.0};
+                    const double x0 = __builtin_fma(v.x[i], c.x, -(v.x[i + 1] * c.y));
+                    const double x1 = __builtin_fma(v.x[i + 1], c.x, v.x[i] * c.y);
+                    o.x[i] = to_odd(turns ? x0 : v.x[i]);
+                    o.x[i + 1] = to_odd(turns ? x1 : v.x[i + 1]);
+                    o.x[kVec + i] = o.x[kVec + i + 1] = 0.0f;
+                }
             }
-            const int32_t pos = gptr<const gi32>(a.positions)[row0 + tok];
-            return rotated<kVec>(a, v, u, [&](int j) {
-                return u.pair + j < half && u.kind != kUnitPass ? angle_of(a, pos, u.pair + j) : float2{1.0f, 0.0f};
-            });
+            return o;
         };
         auto largest = [&](const Place& x, const Unit& u, const Values<kVec>& v, float m) {
             const int count = values_in(u, kVec, x.live);
@@ -532,32 +654,36 @@ __device__ __forceinline__ void page_heads(const AppendHeadsArgs& h, uint32_t it
                 if (i < count) m = __builtin_fmaxf(m, finite_magnitude(v.x[i]));
             return m;
         };
-        RawUnit<TI, kVec> raw[kHeldUnits];
         Values<kVec> held[kHeldUnits];
+        if (what != kPut) {
+            RawUnit<TI, kVec> raw[kHeldUnits];
 #pragma unroll
-        for (int i = 0; i < kHeldUnits; ++i) {
-            const Place x = place(i);
-            raw[i] = load(x, unit(x));
-        }
-        float most = 0.0f;
+            for (int i = 0; i < kHeldUnits; ++i) {
+                const Place x = place(i);
+                raw[i] = load(x, unit(x));
+            }
 #pragma unroll
-        for (int i = 0; i < kHeldUnits; ++i) {
-            if (i >= steps) break;
-            const Place x = place(i);
-            const Unit u = unit(x);
-            held[i] = ready(x, u, raw[i]);
-            most = largest(x, u, held[i], most);
-        }
+            for (int i = 0; i < kHeldUnits; ++i) {
+                if (i >= steps) break;
+                const Place x = place(i);
+                const Unit u = unit(x);
+                held[i] = ready(x, u, raw[i]);
+                found = largest(x, u, held[i], found);
+            }
 #pragma unroll 1
-        for (int i = kHeldUnits; i < steps; ++i) {
-            const Place x = place(i);
-            const Unit u = unit(x);
-            most = largest(x, u, ready(x, u, load(x, u)), most);
+            for (int i = kHeldUnits; i < steps; ++i) {
+                const Place x = place(i);
+                const Unit u = unit(x);
+                found = largest(x, u, ready(x, u, load(x, u)), found);
+            }
+            found = wave_max(found);
         }
-        int e = scale_exponent(wave_max(most));
+        if (what == kFind) return found;
+        if (what == kBoth) found = join(found);
+        int e = scale_exponent(found);
         const int e_was = stored_exponent(was);
         if (old > 0 && e_was > e) e = e_was;
-        if (old > 0 && e > e_was) {                             // the tokens that are there, held anew
+        if (lead && old > 0 && e > e_was) {                  // the tokens that are there, held anew
             const float factor = exp2_int(e - e_was > 30 ? -30 : e_was - e);     // 448 2^-30 is below the least byte
             const int vectors = dim / 16;
             for (int i = lane; i < old * vectors; i += 64) {
@@ -572,7 +698,7 @@ __device__ __forceinline__ void page_heads(const AppendHeadsArgs& h, uint32_t it
         const float inv = exp2_int(-e);
         auto put = [&](const Place& x, const Unit& u, const Values<kVec>& v) {
             if (!x.live) return;
-            const uint64_t to = dst + (old + x.tok) * row_bytes;
+            const uint64_t to = dst + (old + c0 + x.tok) * row_bytes;
             float y[2 * kVec];
 #pragma unroll
             for (int i = 0; i < 2 * kVec; ++i) y[i] = for_byte(v.x[i], inv);
@@ -587,29 +713,84 @@ __device__ __forceinline__ void page_heads(const AppendHeadsArgs& h, uint32_t it
                 if (u.kind == kUnitPairs) *gptr<gbyte>(to + u.d1) = uint8_t(b >> 8);
             }
         };
+        int from = 0;
+        if (what == kBoth) {
 #pragma unroll
-        for (int i = 0; i < kHeldUnits; ++i) {
-            if (i >= steps) break;
-            const Place x = place(i);
-            put(x, unit(x), held[i]);
+            for (int i = 0; i < kHeldUnits; ++i) {
+                if (i >= steps) break;
+                const Place x = place(i);
+                put(x, unit(x), held[i]);
+            }
+            from = kHeldUnits;
         }
 #pragma unroll 1
-        for (int i = kHeldUnits; i < steps; ++i) {
+        for (int i = from; i < steps; ++i) {
             const Place x = place(i);
             const Unit u = unit(x);
             put(x, u, ready(x, u, load(x, u)));
         }
-        if (lane == 0) *gptr<gf32>(scale_at) = exp2_int(e);
+        if (lead && lane == 0) *gptr<gf32>(scale_at) = exp2_int(e);
+        return found;
+    };
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = kAppendBlock / 64;
+    const int first = 2 * h0 + wave, last = 2 * h1;
+    auto alone = [](float x) { return x; };
+    share_weights(h.norm, dim, sh);
+    if (int64_t(n) * half <= h.angles) {
+        fill(0, n);
+        __syncthreads();
+        if (n <= kHeldUnits * (64 >> h.lanes_log2)) {
+#pragma unroll 1
+            for (int task = first; task < last; task += waves) work(task, 0, n, kBoth, 0.0f, true, alone);
+            return;
+        }
+        // Pages of more tokens than a wave keeps: the waves share a task's.  What they found lies in LDS twice over, so
+        // that one barrier a task keeps the next one's from this one's.
+        const int share = (n + waves - 1) / waves, c0 = wave * share < n ? wave * share : n - 1;
+        const int count = n - wave * share < 0 ? 0 : n - wave * share < share ? n - wave * share : share;
+#pragma unroll 1
+        for (int task = 2 * h0; task < last; ++task)
+            work(task, c0, count, kBoth, 0.0f, wave == 0, [&](float x) {
+                float* f = found_by[task & 1];
+                if (lane == 0) f[wave] = x;
+                __syncthreads();
+                float m = f[0];
+#pragma unroll
+                for (int w = 1; w < waves; ++w) m = __builtin_fmaxf(m, f[w]);
+                return m;
+            });
+        return;
     }
+    // More angles than fit: some tokens at a time, first for the scales, then for the bytes; a block's largest magnitude
+    // waits behind the angles, where only its own wave looks.
+    float* most = reinterpret_cast<float*>(cs + h.angles);
+    const int chunk = h.angles / half;
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass)
+#pragma unroll 1
+        for (int c0 = 0; c0 < n; c0 += chunk) {
+            const int count = n - c0 < chunk ? n - c0 : chunk;
+            __syncthreads();
+            fill(c0, count);
+            __syncthreads();
+#pragma unroll 1
+            for (int task = first; task < last; task += kAppendBlock / 64) {
+                float& m = most[task - 2 * h0];
+                // in the second pass the scale is read before the last tokens' call writes it
+                const float found = work(task, c0, count, pass == 0 ? kFind : kPut, pass == 0 && c0 == 0 ? 0.0f : m,
+                                         pass == 1 && c0 == 0, alone);
+                if (pass == 0) m = found;
+            }
+        }
 }
 
 template <class TI, class TO, int kVec>
-__global__ __launch_bounds__(kAppendBlock, 4) void append8_rows(AppendHeadsArgs h)
+__global__ __launch_bounds__(kAppendBlock, 3) void append8_rows(AppendHeadsArgs h)
 {
-    extern __shared__ float2 cs[];
+    extern __shared__ double2 cs[];
     __shared__ SharedWeights sh;
     if (blockIdx.x < h.token_items)
-        token_heads<TI, TO, kVec, false>(h, blockIdx.x, cs, sh);
+        token_heads<TI, TO, kVec, false>(h, blockIdx.x, reinterpret_cast<float2*>(cs), sh);
     else
         page_heads<TI, kVec>(h, blockIdx.x - h.token_items, cs, sh);
 }

@@ -199,10 +199,9 @@ __device__ __forceinline__ int32_t prefix_ahead(const StepArg& a, int32_t s)
     return m == 0 ? 0 : __builtin_amdgcn_readlane(n, __builtin_ctzll(m));
 }
 
-// Position in its own pages of a sequence's first new token; one that the
-// lengths leave no slot for counts as standing right behind the prefix.
-__device__ __forceinline__ int32_t first_position(int32_t len, int32_t count) { return len - count; }
-
+// Position in its own pages of a sequence's i-th new token, the first being at
+// `first`; one that the lengths leave no slot for counts as standing on the
+// prefix's last token.
 __device__ __forceinline__ int32_t row_position(int32_t first, int32_t i) { return first + i < -1 ? -1 : first + i; }
 
 // What a group's rows see of a prefix of len tokens: the sinks, and all from
@@ -225,7 +224,7 @@ __device__ __forceinline__ GroupWindow group_window(const AttendArgs& a, int32_t
     w.past = 0;
     for (int32_t i = lane; i < w.seqs; i += 64) {
         const Rows r = seq_rows(st, w.seq0 + i);
-        const int32_t p = first_position(table_len(st.own, w.seq0 + i), r.count);
+        const int32_t p = table_len(st.own, w.seq0 + i) - r.count;
         if (i == lane) {
             w.start = r.first;
             w.past = p;
@@ -269,7 +268,7 @@ __device__ __forceinline__ int32_t group_row_position(const AttendArgs& a, const
         }
         const Rows r = seq_rows(a.step, it.seq0 + at);
         start = r.first;
-        past = first_position(table_len(a.step.own, it.seq0 + at), r.count);
+        past = table_len(a.step.own, it.seq0 + at) - r.count;
     }
     return row_position(past, row - start);
 }
@@ -284,7 +283,7 @@ __device__ __forceinline__ Seen seen_by(const AttendArgs& a, const AttendItem& i
         if (it.prefix)
             s.lo = window_begin(a, it.len + group_row_position(a, it, it.rows.first + i));
         else
-            s.lo = window_begin(a, row_position(first_position(it.len, it.rows.count), i));
+            s.lo = window_begin(a, row_position(it.len - it.rows.count, i));
     }
     return s;
 }
@@ -299,7 +298,7 @@ __device__ __forceinline__ void window_item(const AttendArgs& a, AttendItem& it)
         w = group_window(a, it.table_row, it.len);
     } else {
         sink = own_sink(a, a.sinks > 0 ? prefix_ahead(a.step, it.table_row) : 0);
-        const int32_t first = row_position(first_position(it.len, it.rows.count), new_token(a, it.flat0));
+        const int32_t first = row_position(it.len - it.rows.count, new_token(a, it.flat0));
         w.span = make_span(sink, window_begin(a, first), visible_end(a, it, it.flat_n - 1));
     }
     it.sink = __builtin_amdgcn_readfirstlane(sink);

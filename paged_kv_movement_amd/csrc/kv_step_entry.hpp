@@ -382,6 +382,7 @@ int append8(const kv_paged8* paged8, const kv_step* step, int32_t layer, const k
     // A wave to each head's K and V where there are few pages, four to a wave where they fill the GPU without
     const int64_t pairs = int64_t(step->own.n) * h.pages;
     h.splits = int32_t(std::clamp<int64_t>(2048 / std::max<int64_t>(pairs, 1), 1, ceil_div(paged->num_kv_heads, 2)));
+    h.splits = std::max(h.splits, int32_t(ceil_div(paged->num_kv_heads, kChunkHeads)));
     const KernelFn f = by_types(type, q == nullptr || q_out_type == type, [&](auto in, auto out) {
         using TI = decltype(in);
         using TO = decltype(out);
@@ -390,10 +391,12 @@ int append8(const kv_paged8* paged8, const kv_step* step, int32_t layer, const k
     });
     if (pairs > max_blocks(kAppendBlock) || pairs * h.splits + h.token_items > max_blocks(kAppendBlock))
         return fail(KV_EINVAL, "too many pages for one launch");
-    // LDS for the angles of a page's new tokens, or if that is too much of one token
+    // LDS: the angles of a page's new tokens, or as many as fit and the blocks' largest magnitudes; or of one token's q
     const int64_t half = h.a.rot / 2, page_angles = std::min<int64_t>(size, step->max_new) * half;
-    h.angles = int32_t(std::max<int64_t>(page_angles <= kPageAngles ? page_angles : half, 1));
-    const size_t lds = size_t(h.angles + kAngleRoom) * sizeof(float2);
+    h.angles = int32_t(std::min<int64_t>(std::max<int64_t>(page_angles, 1), kPageAngles));
+    size_t lds = size_t(h.angles) * sizeof(double2);
+    if (page_angles > kPageAngles) lds += 2 * size_t(ceil_div(paged->num_kv_heads, h.splits)) * sizeof(float);
+    if (h.token_items > 0) lds = std::max(lds, size_t(half + kAngleRoom) * sizeof(float2));
     if (q != nullptr && step->n_rows >= kQApart) {
         rc = launch(heads_rows_kernel<false>(call, type, q_out_type == type), step->n_rows, kAppendBlock, &h, stream);
         if (rc != KV_OK) return rc;
@@ -406,7 +409,7 @@ int append8(const kv_paged8* paged8, const kv_step* step, int32_t layer, const k
 // ---- pages between a bf16 and an 8-bit pool
 
 int check_pack(const kv_paged* from, const kv_paged* to, const kv_tables* tables, const int32_t* to_table,
-               int64_t to_stride, int32_t layer_begin, int32_t layer_end, hipStream_t stream)
+               int64_t to_stride, hipStream_t stream)
 {
     if (tables == nullptr) return fail(KV_EINVAL, "tables is NULL");
     int rc = check_tables(from, tables, "tables");
@@ -978,7 +981,7 @@ int kv_pack8(const kv_paged* from, const kv_tables* tables, const kv_paged8* to,
     int rc = check_step_pool(from, layer_begin, layer_end);
     if (rc == KV_OK) rc = check_pool8(to, layer_begin, layer_end);
     if (rc == KV_OK)
-        rc = check_pack(from, &to->pages, tables, to_table, to_stride, layer_begin, layer_end, stream);
+        rc = check_pack(from, &to->pages, tables, to_table, to_stride, stream);
     if (rc != KV_OK) return rc;
     return run_pack(true, from, &to->pages, to, tables, to_table, to_stride, layer_begin, layer_end, stream);
 }
@@ -989,7 +992,7 @@ int kv_unpack8(const kv_paged8* from, const kv_tables* tables, const kv_paged* t
     int rc = check_pool8(from, layer_begin, layer_end);
     if (rc == KV_OK) rc = check_step_pool(to, layer_begin, layer_end);
     if (rc == KV_OK)
-        rc = check_pack(&from->pages, to, tables, to_table, to_stride, layer_begin, layer_end, stream);
+        rc = check_pack(&from->pages, to, tables, to_table, to_stride, stream);
     if (rc != KV_OK) return rc;
     return run_pack(false, &from->pages, to, from, tables, to_table, to_stride, layer_begin, layer_end, stream);
 }
