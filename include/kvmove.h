@@ -14,7 +14,10 @@
  *   optional fp8 serde: quantise to e4m3 on store, dequantise on retrieve;
  *   a model step on the same pool: append new tokens with rotary positions,
  *            attend to shared prefixes and own pages, add up the attention
- *            weight of every cached token, evict by it.
+ *            weight of every cached token, evict by it;
+ *   the same with heads of q and k normalised on append, with a sliding window
+ *            and first tokens that stay visible, and on a pool of 8 bits,
+ *            which is packed from the bf16 pool and unpacked into it.
  *
  * Sources (web pages, cited by title and section):
  *   [paper]  "LMCache: An Efficient KV Cache Layer for Enterprise-Scale LLM
@@ -532,7 +535,8 @@ typedef struct {
 /* kv_append (norm NULL) or kv_append_normed into an 8-bit pool: a block's scale
  * covers its new tokens and, where it holds earlier ones of the sequence, is at
  * least what it was; if it rises, their bytes are held anew under it.  A block
- * that begins with a new token starts afresh.  The pages written by one call
+ * that begins with a new token starts afresh.  Keys are normalised and rotated
+ * in 64 bits, so that bytes and scales are those of the formula.  The pages written by one call
  * must be distinct: sequences cannot share a page that either appends to. */
 int kv_append8(const kv_paged8* paged, const kv_step* step, int32_t layer, const kv_rows* q, const kv_rows* k,
                const kv_rows* v, const kv_rows* q_out, int32_t q_heads, kv_type type, kv_type q_out_type,

@@ -15,6 +15,11 @@ Typical use::
     kvm.store(paged, batch)                            # gather pages -> chunks
     n = kvm.retrieve(paged, batch, masks=[hit_mask])   # scatter hit chunks -> pages
 
+A model step on the same pool (``Tables``, ``Step``, ``Rope``): ``append``,
+``attend``, ``add_weights`` and ``evict``; append takes a ``Norm``, attend a
+window, and both a ``Paged8``, the pool in 8 bits that ``pack8`` and ``unpack8``
+convert from and to.
+
 Chunk tensors made with ``pin_memory=True`` instead of on the device turn the
 same calls into the offload to host memory and the onload from it.
 """
@@ -1048,8 +1053,9 @@ def append(paged: Paged | Paged8, step: Step, layer: int, q, k, v, positions, ro
            slot_positions=None, stream=None, norm: Norm | None = None):
     """Rotate the new tokens' q and k, normalised first by ``norm`` if one is
     given, and write k and v into layer ``layer``'s pages (kv_append,
-    kv_append_normed; of a Paged8 kv_append8, which takes no eviction state).  q [rows, q_heads, D] (None: only k and v), k and v
-    [rows, H, D]: bf16, fp16 or float32, any row and head strides;
+    kv_append_normed; of a Paged8 kv_append8, which takes no eviction state).
+    q [rows, q_heads, D] (None: only k and v), k and v [rows, H, D]: bf16, fp16
+    or float32, any row and head strides;
     ``positions``: int32 [rows].  ``q_out``: where the rotated q goes (q
     itself, or a tensor of q's type or bf16; None: a new tensor of q's type).
     ``weights`` / ``slot_positions`` [sequences, H or 1, slots]: this layer's

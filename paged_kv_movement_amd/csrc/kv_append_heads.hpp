@@ -5,14 +5,18 @@
 // c = 0 or their mean.  The sums are float32, two passes over registers for the
 // centered form (mean of squares less square of mean would cancel); where the
 // squares leave float32's range the head is first scaled by a power of two.
-// Then the rotation of kv_append.hpp, and one rounding.
+// Then the rotation of kv_append.hpp, and one rounding.  Keys on their way into
+// 8 bits go through all of it in 64 bits (see above wide_norm).
 //
 // A head lies in a group of G lanes, the next power of two to its units, so
 // that its sums are exchanges within a wave and no head waits for another.
 //
 // append_heads_rows   one workgroup per token, for q (and, into a bf16 pool, k
-//                     and v): as append_rows, memory-bound;
-// append8             those workgroups for q, and behind them one per (sequence,
+//                     and v).  Bound: memory, as append_rows: 45116 tokens of
+//                     32 query heads and 8 KV heads of 128 in 220 us, 5.0 TB/s
+//                     (without a norm 200); one token in 5.7 us, of which 1.9
+//                     are the weights and the two sums.
+// append8_rows        those workgroups for q, and behind them one per (sequence,
 //                     page, some of the heads) for k and v: a wave takes one
 //                     head's K or V of the page, all its new tokens, finds the
 //                     block's scale and writes the bytes.
@@ -433,8 +437,8 @@ __global__ __launch_bounds__(kAppendBlock) void append_heads_rows(AppendHeadsArg
 // block's scale does so by a factor of two.  k is therefore normalised and
 // rotated in 64 bits, and becomes a float32 only by rounding to odd, which
 // leaves it on its own side of every border of fewer bits: the bytes and
-// scales are those of the formula.  (v is what it was.)  It costs 6 us of 200
-// for 45116 tokens, and little of q, k and v's way through memory.
+// scales are those of the formula.  (v is what it was.)  Of 45116 tokens the
+// pages' part takes 115 to 130 us so and took 90 with keys in float32.
 
 template <int kVec>
 struct WideValues {
@@ -504,7 +508,9 @@ constexpr int kHeldUnits = 2;          // units of a lane kept between the look 
 
 // New tokens of one page of a sequence, some of its heads: a wave takes one head's K or V at a time.
 //
-// Bound: memory, with q's workgroups; of 45116 tokens of 32 query heads and 8 KV heads of 128 (1.0 GB) 200 us, 5.1 TB/s.
+// Bound: registers, and by them waits.  64-bit keys take 163 of them, so three waves a SIMD, which wait for memory and LDS
+// 70 % of their time: 45116 tokens of 8 KV heads of 128 (277 MB) in 115 to 130 us, 2.1 to 2.4 TB/s; one token of each of 64
+// sequences 9 us.  Asking for the next task's values and scale while one is worked on took 125 to 133.
 template <class TI, int kVec>
 __device__ __forceinline__ void page_heads(const AppendHeadsArgs& h, uint32_t item, double2* cs, SharedWeights& sh)
 {

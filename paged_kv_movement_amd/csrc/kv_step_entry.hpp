@@ -353,7 +353,7 @@ int check_pool8(const kv_paged8* p, int32_t layer_begin, int32_t layer_end)
 }
 
 // New tokens from which on their q has a launch of its own, where the page kernel's registers do not leave half as many waves
-// (45116 tokens 296 us, in one launch 308; 4000 tokens 36.5 and 33.8).
+// (with keys in float32, 45116 tokens 296 us and in one launch 308; 4000 tokens 36.5 and 33.8).
 constexpr int32_t kQApart = 16384;
 
 int append8(const kv_paged8* paged8, const kv_step* step, int32_t layer, const kv_rows* q, const kv_rows* k,
@@ -452,12 +452,12 @@ int run_pack(bool pack, const kv_paged* from, const kv_paged* to, const kv_paged
     }
     const int64_t pages = int64_t(tables->n) * a.pages, items = pages * a.parts;
     if (pages > max_blocks(block) || items > max_blocks(block)) return fail(KV_EINVAL, "too many pages for one launch");
-    constexpr int32_t kLayers = 32767;                       // of a launch: its second dimension
-    for (int32_t l = layer_begin; l < layer_end; l += kLayers) {
-        a.from = pool_arg(from, l);
-        a.to = pool_arg(to, l);
+    constexpr int64_t kLayers = 32767;                       // of a launch: its second dimension
+    for (int64_t l = layer_begin; l < layer_end; l += kLayers) {
+        a.from = pool_arg(from, int32_t(l));
+        a.to = pool_arg(to, int32_t(l));
         const int rc = launch(pack ? reinterpret_cast<KernelFn>(&pack8_pages) : reinterpret_cast<KernelFn>(&unpack8_pages),
-                              items, block, &a, stream, unsigned(2 * std::min(kLayers, layer_end - l)));
+                              items, block, &a, stream, unsigned(2 * std::min<int64_t>(kLayers, layer_end - l)));
         if (rc != KV_OK) return rc;
     }
     return ok();

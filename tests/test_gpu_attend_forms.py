@@ -268,7 +268,7 @@ def test_pack8_bad_pages_are_left_out_and_reported():
 
 def test_an_8bit_cache_from_chunks_to_decoding():
     """Chunks retrieved into bf16 pages, packed, then a decode loop on the 8-bit pool with normalised heads and a window;
-    at the end unpacked and stored.  Each attention is checked against the values the pool holds."""
+    at the end unpacked.  Each attention is checked against the values the pool holds."""
     H, rep, D, P, steps, layers = 2, 4, 128, 16, 20, 2
     start = [100, 37, 250]
     room = [-(-(n + steps) // P) for n in start]
