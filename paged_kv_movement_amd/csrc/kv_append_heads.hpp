@@ -508,9 +508,10 @@ constexpr int kHeldUnits = 2;          // units of a lane kept between the look 
 
 // New tokens of one page of a sequence, some of its heads: a wave takes one head's K or V at a time.
 //
-// Bound: registers, and by them waits.  64-bit keys take 163 of them, so three waves a SIMD, which wait for memory and LDS
-// 70 % of their time: 45116 tokens of 8 KV heads of 128 (277 MB) in 115 to 130 us, 2.1 to 2.4 TB/s; one token of each of 64
-// sequences 9 us.  Asking for the next task's values and scale while one is worked on took 125 to 133.
+// Bound: waits.  64-bit keys take 163 registers, so there are three waves a SIMD, and they wait 70 % of their time: 45116
+// tokens of 8 KV heads of 128 (277 MB) in 115 to 130 us, 2.1 to 2.4 TB/s; one token of each of 64 sequences 9 us.  Asking for
+// the next task's values while one is worked on, or for the first ahead of the angles, took as long (122 to 137), as did
+// angles without bank conflicts; rounding to odd is 7 us of it and the sines 1.5.
 template <class TI, int kVec>
 __device__ __forceinline__ void page_heads(const AppendHeadsArgs& h, uint32_t item, double2* cs, SharedWeights& sh)
 {
