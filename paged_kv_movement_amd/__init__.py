@@ -969,8 +969,8 @@ class Norm:
     """Normalisation of each head of q and k before the rotation:
     (x - c) / sqrt(mean((x - c)^2) + eps) * weight, c = 0 or, ``centered``, the
     head's mean.  ``q_weight`` / ``k_weight``: [head_dim], [heads, head_dim], or
-    None for ones; float32 device tensors are read where they are at each call,
-    others are copied once.  A graph that captured calls reads the Norm's
+    None for ones; contiguous, 16-byte aligned float32 device tensors are read
+    where they are at each call, others are copied once.  A graph that captured calls reads the Norm's
     arrays: keep it for as long as it is replayed."""
 
     def __init__(self, q_weight=None, k_weight=None, eps: float = 1e-6, centered: bool = False, device="cuda"):
