@@ -531,48 +531,6 @@ __device__ __forceinline__ void add_v(RowState<DP> (&st)[NB], const uint32_t (&v
     }
 }
 
-// The same where V is held in 8 bits: fp16 holds its bytes exactly, times a
-// power of two near 1, and a weight to 11 bits, 2^-12 of it (2^-25 where it is
-// below 2^-14; the largest of a row is 1 or more).  Over n tokens that is 2^-12
-// of one weight's share of the output, where the output itself is rounded to
-// 2^-9, so one part is enough: a third fewer products and a quarter of the
-// splitting's instructions (four ragged prompts behind a prefix 426 -> 377 us).
-using f16x8 = __attribute__((ext_vector_type(8))) _Float16;
-using f16x2 = __attribute__((ext_vector_type(2))) _Float16;
-
-__device__ __forceinline__ f32x4 mfma16h(u32x4 a, u32x4 b, f32x4 c)
-{
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
-}
-
-template <int DP>
-__device__ __forceinline__ void half_weights_of(RowState<DP>& st, const f32x4 (&s)[2], u32x4& p, float c)
-{
-    const float base = st.m == -__builtin_inff() ? 0.0f : st.m;       // a row that has seen nothing yet
-    float sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int n = 0; n < 4; n += 2) {
-            const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i][n], c, -base));
-            const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i][n + 1], c, -base));
-            sum += p0 + p1;
-            p[2 * i + n / 2] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{p0, p1}, f16x2));
-        }
-    st.l += sum;
-}
-
-template <int DP, int NB>
-__device__ __forceinline__ void add_half_v(RowState<DP> (&st)[NB], const uint32_t (&v)[8][DP / 32], const u32x4 (&p)[NB])
-{
-#pragma unroll
-    for (int m = 0; m < DP / 16; ++m) {
-        const u32x4 vt = v_column<DP>(v, m);
-#pragma unroll
-        for (int b = 0; b < NB; ++b) st[b].acc[m] = mfma16h(vt, p[b], st[b].acc[m]);
-    }
-}
-
 // A V that is not finite does not go through add_v: 0 times it is NaN, for a
 // row that does not see its token and for the second part of a weight alike.
 // A piece is therefore done without a thought of it, and if a result is not
@@ -1133,24 +1091,24 @@ struct Stage8 {
         }
     }
 
-    // in the places that wide_load would have put them, K as bf16, V too or (kHalf) times the scale `v_scale`, lane x's
-    // that of token x, as fp16; 0 where there is no token or no element
-    template <bool kHalf>
-    __device__ __forceinline__ void put(WideTile<DP>& tile, int dim, float v_scale) const
+    // as bf16, in the places that wide_load would have put them; 0 where there is no token or no element, and no scale
+    // either: the one that was read in its place may be NaN, and 0 times it would be
+    __device__ __forceinline__ void put(WideTile<DP>& tile, int dim) const
     {
-        const int chunk = anew(threadIdx.x & 63) % V;
+        const int lane = anew(threadIdx.x & 63), chunk = lane % V;
+        const bool mine = (there >> lane) & 1;
+        const float ks1 = mine ? ks : 1.0f, vs1 = mine ? vs : 1.0f;
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
             const int tok = token(i), at = tok * (DP / 8), swz = wide_swizzle<DP>(tok);
             const bool live = ((there >> tok) & 1) && chunk * 16 < dim;
-            const float sk = __shfl(ks, tok), sv = __shfl(v_scale, tok);
+            const float sk = __shfl(ks1, tok), sv = __shfl(vs1, tok);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const uint32_t none = 0;
                 const int to = at + ((2 * chunk + e) ^ swz);
                 tile.k[to] = bf16_of_bytes8(live ? k[i][2 * e] : none, live ? k[i][2 * e + 1] : none, sk);
-                const uint32_t v0 = live ? v[i][2 * e] : none, v1 = live ? v[i][2 * e + 1] : none;
-                tile.v[to] = kHalf ? f16_of_bytes8(v0, v1, sv) : bf16_of_bytes8(v0, v1, sv);
+                tile.v[to] = bf16_of_bytes8(live ? v[i][2 * e] : none, live ? v[i][2 * e + 1] : none, sv);
             }
         }
     }
@@ -1229,21 +1187,6 @@ __device__ __forceinline__ void wide_tile(RowState<DP> (&st)[NB], const u32x4 (&
     }
     u32x4 ph[NB], pl[NB];
     uint32_t v[8][DP / 32];
-    if constexpr (F::byte) {
-#pragma unroll
-        for (int b = 0; b < NB; ++b) half_weights_of<DP>(st[b], s[0][b], ph[b], c);
-        wide_values<DP>(v, tile, 0);
-        if (H > 1) {
-#pragma unroll
-            for (int b = 0; b < NB; ++b) half_weights_of<DP>(st[b], s[H - 1][b], pl[b], c);
-            add_half_v<DP, NB>(st, v, ph);
-            wide_values<DP>(v, tile, H - 1);
-            add_half_v<DP, NB>(st, v, pl);
-        } else {
-            add_half_v<DP, NB>(st, v, ph);
-        }
-        return;
-    }
 #pragma unroll
     for (int b = 0; b < NB; ++b) weights_of<DP>(st[b], s[0][b], ph[b], pl[b], c);
     wide_values<DP>(v, tile, 0);
@@ -1299,6 +1242,11 @@ __device__ __forceinline__ void wide_half_with_care(RowState<DP> (&st)[NB], cons
 // CU; with 64 rows K and V come through LDS twice as often.  A window costs what
 // its rows see and the tiles at its two edges: 16262 new tokens of two prompts
 // under a window of 1024 in 510 to 526 us.
+//
+// Over bytes the same two parts: four ragged prompts behind a prefix 430 us.  One
+// fp16 part takes 378, but its range ends 2^-25 below the heaviest weight of a
+// piece, and what it drops is still in l: where a few tokens draw the attention
+// and their V is small, the output is the sum of the light ones.
 template <int DP, int NB, class F>
 __device__ __forceinline__ void wide_piece(const AttendArgs& a, const AttendItem& it, const LayerAt& l, int32_t t1,
                                            WideTile<DP>& tile0, WideTile<DP>& tile1)
@@ -1360,27 +1308,11 @@ __device__ __forceinline__ void wide_piece(const AttendArgs& a, const AttendItem
         }
         if (any) wide_tile<DP, NB, F>(st, q, now, a.scale_log2, masked, t, vis, seen);
     };
-    bool care = false;                                       // V has blocks too far apart for fp16
     if constexpr (F::byte) {
         // bytes come through registers, which is where they are widened: those of a tile are asked for while the one
         // before the one before it is computed, and put into LDS when that is done
         Stage8<DP> stage;
         uint64_t staged = 0;
-        // exponent that V's scales are taken relative to: the largest of the first tile's, the same in every wave
-        int ref = 0;
-        bool known = false;
-        auto put = [&](WideTile<DP>& tile) {
-            const int x = anew(lane), e = raw_exponent(stage.vs);
-            const bool mine = (staged >> x) & 1;
-            if (!known && staged != 0) {
-                float most = mine ? float(e) : -1000.0f;
-                ref = int(__builtin_amdgcn_readfirstlane(int(wave_max(most))));
-                known = true;
-            }
-            const bool near = e - ref >= kLeastHalf && e - ref <= kMostHalf;
-            care = care || __any(mine && !near);
-            stage.template put<true>(tile, dim, exp2_int(near ? e - ref : 0));
-        };
         auto ask = [&](int32_t u) {
             rows = row_at(u, page);
             stage.load(l, a.pool, it.h, kh, vh, row_bytes, rows, page);
@@ -1390,7 +1322,7 @@ __device__ __forceinline__ void wide_piece(const AttendArgs& a, const AttendItem
         if (it.t0 < t1) {
             page = page_at(it.t0);
             ask(it.t0);
-            put(tile0);
+            stage.put(tile0, dim);
             valid = staged;
             ask(it.t0 + T);
         }
@@ -1398,7 +1330,7 @@ __device__ __forceinline__ void wide_piece(const AttendArgs& a, const AttendItem
             __syncthreads();                                 // now is whole, and next is done with
             const uint64_t seen = valid;
             if (u + T < t1) {
-                put(next);
+                stage.put(next, dim);
                 valid = staged;
                 ask(u + 2 * T);
             }
@@ -1410,12 +1342,6 @@ __device__ __forceinline__ void wide_piece(const AttendArgs& a, const AttendItem
             if (u + T >= t1) break;
             one(u + T, tile1, tile0);
         }
-        const float unit = exp2_int(ref < -126 ? -126 : ref > 127 ? 127 : ref);      // beyond them: done again below
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-            for (int m = 0; m < DP / 16; ++m) st[b].acc[m] *= unit;
-        care = care || ref < -126 || ref > 127;
     } else {
         if (it.t0 < t1) {
             page = page_at(it.t0);
@@ -1451,7 +1377,7 @@ __device__ __forceinline__ void wide_piece(const AttendArgs& a, const AttendItem
     bool finite = true;
 #pragma unroll
     for (int b = 0; b < NB; ++b) finite = finite && all_finite<DP>(st[b]);
-    if (__syncthreads_or(!finite || care)) {
+    if (__syncthreads_or(!finite)) {
 #pragma unroll
         for (int b = 0; b < NB; ++b) clear<DP>(st[b]);
 #pragma unroll 1
@@ -1464,7 +1390,7 @@ __device__ __forceinline__ void wide_piece(const AttendArgs& a, const AttendItem
             if constexpr (F::byte) {
                 Stage8<DP> stage;
                 stage.load(l, a.pool, it.h, kh, vh, row_bytes, rows, page);
-                stage.template put<false>(tile0, dim, stage.vs);
+                stage.put(tile0, dim);
             } else {
                 wide_load<DP>(kh, vh, row_bytes, dim, flat, rows, valid, tile0);
                 __builtin_amdgcn_s_waitcnt(0);

@@ -73,20 +73,6 @@ __device__ __forceinline__ u32x4 bf16_of_bytes8(uint32_t b0, uint32_t b1, float 
     return {x[0], x[1], y[0], y[1]};
 }
 
-// The same as fp16, exact where the scale is within 2^-15 .. 2^7: a byte's
-// least step is 2^-9 and its largest value 448, fp16's 2^-24 and 65504.
-constexpr int kLeastHalf = -15, kMostHalf = 7;
-
-__device__ __forceinline__ u32x4 f16_of_bytes8(uint32_t b0, uint32_t b1, float scale)
-{
-    u32x4 x;
-    x[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b0, scale, false));
-    x[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b0, scale, true));
-    x[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b1, scale, false));
-    x[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b1, scale, true));
-    return x;
-}
-
 // e with 2^e the scale that a largest magnitude asks for: 448 = 1.75 * 2^8, so
 // amax = m * 2^x (1 <= m < 2) needs 2^(x - 8) if m <= 1.75, else 2^(x - 7).
 // Subnormal and zero amax are below the least scale either way.
@@ -102,9 +88,6 @@ __device__ __forceinline__ int stored_exponent(float scale)
 {
     return clamp_i32(int32_t((__float_as_uint(scale) >> 23) & 0xFFu) - 127, kLeastExponent, kMostExponent);
 }
-
-// The exponent that the conversions take of it, -127 .. 128.
-__device__ __forceinline__ int raw_exponent(float scale) { return int((__float_as_uint(scale) >> 23) & 0xFFu) - 127; }
 
 __device__ __forceinline__ float exp2_int(int e) { return __uint_as_float(uint32_t(e + 127) << 23); }
 
