@@ -856,11 +856,15 @@ class Step:
         self._device = _here(*self._tensors)
         self._ref = ctypes.byref(self.c)
 
-    def attend_workspace_bytes(self, q_heads: int, window: int | None = None, sinks: int = 0) -> int:
-        """Device bytes attend needs with this window (kv_attend_workspace_bytes and its other forms)."""
+    def attend_workspace_bytes(self, q_heads: int, window: int | None = None, sinks: int = 0,
+                               paged: Paged | Paged8 | None = None) -> int:
+        """Device bytes attend needs with this window over ``paged`` (None: the
+        step's own pool); kv_attend_workspace_bytes and its other forms.  An
+        8-bit pool can need more than a bf16 one."""
         _int32("q_heads", q_heads)
-        w, p, c = _window(window, sinks), ctypes.byref(self.paged.c), ctypes.byref(self.c)
-        if isinstance(self.paged, Paged8):
+        paged = self.paged if paged is None else paged
+        w, p, c = _window(window, sinks), ctypes.byref(paged.c), ctypes.byref(self.c)
+        if isinstance(paged, Paged8):
             n = load().kv_attend8_workspace_bytes(p, c, q_heads, _ref(w))
         elif w is not None:
             n = load().kv_attend_window_workspace_bytes(p, c, q_heads, _ref(w))
@@ -870,10 +874,11 @@ class Step:
             _check(KV_EINVAL)
         return int(n)
 
-    def new_attend_workspace(self, q_heads: int, window: int | None = None, sinks: int = 0):
+    def new_attend_workspace(self, q_heads: int, window: int | None = None, sinks: int = 0,
+                             paged: Paged | Paged8 | None = None):
         """A device tensor of attend_workspace_bytes (torch aligns it to 256)."""
         import torch
-        return torch.empty(self.attend_workspace_bytes(q_heads, window, sinks), dtype=torch.uint8,
+        return torch.empty(self.attend_workspace_bytes(q_heads, window, sinks, paged), dtype=torch.uint8,
                            device=self.own.table.device)
 
     def _rows(self, t, heads, what, types):
@@ -1134,7 +1139,7 @@ def attend(paged: Paged | Paged8, step: Step, layer: int, q, scale=None, out=Non
     last ``window`` tokens up to its own, counted over prefix and own pages,
     and the first ``sinks`` of all.  ``scale``: 1/sqrt(D) unless given.
     ``workspace``: a device uint8 tensor of step.attend_workspace_bytes(q_heads,
-    window, sinks) (None: one is allocated for the call).
+    window, sinks, paged) (None: one is allocated for the call).
     Returns (out bf16 like q, lse float32 [rows, q_heads])."""
     if layer >> 31:
         _int32("layer", layer)
@@ -1149,7 +1154,7 @@ def attend(paged: Paged | Paged8, step: Step, layer: int, q, scale=None, out=Non
         raise KvError(KV_EINVAL, f"lse must be a contiguous float32 device tensor [{step.n_rows}, {heads}]")
     cw = _window(window, sinks)
     if workspace is None:
-        workspace = _empty(step.attend_workspace_bytes(heads, window, sinks), torch.uint8, q.device, stream)
+        workspace = _empty(step.attend_workspace_bytes(heads, window, sinks, paged), torch.uint8, q.device, stream)
     ws, n_ws = _workspace(workspace)
     h = step._call(paged, stream, q, out, lse, workspace)
     if isinstance(paged, Paged8):
