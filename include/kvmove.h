@@ -495,7 +495,12 @@ typedef struct {
 
 /* kv_attend with a window (NULL: none).  Only what some row sees is read; a
  * row that lens leaves no slot for counts as standing on the prefix's last
- * token.  The weights that kv_add_weights adds know no window. */
+ * token.  The weights that kv_add_weights adds know no window.
+ *
+ * The workspace depends on the window, and not in one direction: tokens are cut
+ * into pieces by what is seen of them, and less to see can mean more pieces.  A
+ * workspace for several windows, or for layers with and without one, has to be
+ * as large as the largest of their sizes. */
 size_t kv_attend_window_workspace_bytes(const kv_paged* paged, const kv_step* step, int32_t q_heads,
                                         const kv_window* window);
 int kv_attend_window(const kv_paged* paged, const kv_step* step, int32_t layer, const kv_rows* q, int32_t q_heads,

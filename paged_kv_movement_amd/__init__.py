@@ -860,7 +860,9 @@ class Step:
                                paged: Paged | Paged8 | None = None) -> int:
         """Device bytes attend needs with this window over ``paged`` (None: the
         step's own pool); kv_attend_workspace_bytes and its other forms.  An
-        8-bit pool can need more than a bf16 one."""
+        8-bit pool can need more than a bf16 one, and a window more than
+        another or none: a workspace for several calls has to be as large as
+        the largest of theirs."""
         _int32("q_heads", q_heads)
         paged = self.paged if paged is None else paged
         w, p, c = _window(window, sinks), ctypes.byref(paged.c), ctypes.byref(self.c)

@@ -77,3 +77,19 @@ def test_a_step_of_one_pool_on_the_other(seen):
         with pytest.raises(kvm.KvError, match="workspace"):
             kvm.attend(p8, step8, 0, q.cuda(), workspace=step8.new_attend_workspace(8, paged=p16))
     assert kvm.take_faults() == 0
+
+
+def test_a_window_can_need_more_than_none():
+    """Sizes are not ordered by the window; the largest of those asked for serves them all, as the header says."""
+    L, p = _lib(), _paged(n=1 << 20)
+    c = step(own=tables(n=32, max_len=6000, stride=512), prefix=tables(n=1, max_len=8192, stride=512), n_rows=32,
+             max_new=1, max_group_rows=32)
+    none = L.kv_attend_workspace_bytes(ref(p), ref(c), 32)
+    sizes = [L.kv_attend_window_workspace_bytes(ref(p), ref(c), 32, ref(window(w, 4))) for w in (64, 4096, 1 << 30)]
+    assert 0 < none < sizes[1] < sizes[2] and sizes[0] < none
+    # a workspace of one call's size is refused where another one's is larger, before anything is launched
+    q, out = kvm._KvRows(0x10000, 32 * 128, 128), kvm._KvRows(0x1000000, 32 * 128, 128)
+
+    def call(ws_bytes, w):
+        return L.kv_attend_window(ref(p), ref(c), 0, ref(q), 32, 0.1, ref(w), ref(out), 0x10000, 0x10000, ws_bytes, None)
+    assert call(none, window(4096, 4)) == kvm.KV_EINVAL and "workspace" in L.kv_last_error().decode()
