@@ -363,6 +363,10 @@ class Paged8:
         _need(all(t.device == dev for t in (*k_layers, *v_layers, *k_scales, *v_scales)),
               "a pool's tensors must be on one device")
         _need(D % 16 == 0, "head_dim must be a multiple of 16 in an 8-bit pool")
+        # a view of bytes can begin anywhere; the kernels move 16 at a time
+        _need(all(t.data_ptr() % 16 == 0 for t in (*k_layers, *v_layers)) and
+              all(t.data_ptr() % 4 == 0 for t in (*k_scales, *v_scales)),
+              "per-layer pools must begin at multiples of 16 bytes, scales of 4")
         self._keep = (*k_layers, *v_layers, *k_scales, *v_scales)
         self.num_layers, self.num_kv_heads, self.head_dim = len(k_layers), H, D
         self.page_size, self.num_pages = P, n
