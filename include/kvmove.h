@@ -512,7 +512,8 @@ int kv_attend_window(const kv_paged* paged, const kv_step* step, int32_t layer, 
 typedef struct {
     const float* q_weight; /* DEVICE float32 [q_heads][head_dim], 16-byte aligned; NULL: ones */
     const float* k_weight; /* the same for k's heads */
-    int64_t q_stride;      /* elements from a head's weights to the next one's, a multiple of 4; 0: all heads share them */
+    int64_t q_stride;      /* elements from a head's weights to the next one's, a multiple of 4 where head_dim is one of 8;
+                              0: all heads share them */
     int64_t k_stride;
     float eps;             /* >= 0 */
     int32_t centered;      /* 1: less the mean */

@@ -1007,9 +1007,6 @@ class Norm:
     def _fits(self, w, heads, dim, name):
         if w is not None and tuple(w.shape) not in ((dim,), (heads, dim)):
             raise KvError(KV_EINVAL, f"{name} must be [{dim}] or [{heads}, {dim}], got {list(w.shape)}")
-        # the stride of head weights is in whole vectors of four
-        if w is not None and w.dim() == 2 and heads > 1 and dim % 4:
-            raise KvError(KV_EINVAL, f"{name} of each head needs a head_dim that is a multiple of 4")
 
 
 def _window(window, sinks):

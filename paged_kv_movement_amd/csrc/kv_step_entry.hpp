@@ -275,14 +275,17 @@ int append(const kv_paged* paged, const kv_step* step, int32_t layer, const kv_r
 
 // ---- append with normalised heads, and into an 8-bit pool
 
-int check_norm(const kv_norm* n)
+// Heads of other sizes than multiples of 8 go element by element, their weights too.
+int check_norm(const kv_norm* n, int32_t head_dim)
 {
     if (n == nullptr) return KV_OK;
     if (!(n->eps >= 0.0f) || n->eps > 1e30f) return fail(KV_EINVAL, "norm: eps must be finite and >= 0");
     if (n->centered != 0 && n->centered != 1) return fail(KV_EINVAL, "norm: centered must be 0 or 1");
+    const int64_t step = head_dim % 8 == 0 ? 4 : 1;
     if (misaligned(n->q_weight, 16) || misaligned(n->k_weight, 16) || n->q_stride < 0 || n->k_stride < 0 ||
-        n->q_stride % 4 != 0 || n->k_stride % 4 != 0)
-        return fail(KV_EINVAL, "norm: weights need 16-byte aligned addresses, strides multiples of 4 and >= 0");
+        n->q_stride % step != 0 || n->k_stride % step != 0)
+        return fail(KV_EINVAL, "norm: weights need 16-byte aligned addresses and strides >= 0, multiples of 4 where "
+                    "head_dim is one of 8");
     return KV_OK;
 }
 
@@ -328,7 +331,7 @@ int append_normed(const kv_paged* paged, const kv_step* step, int32_t layer, con
     if (norm == nullptr)
         return append(paged, step, layer, q, k, v, q_out, q_heads, type, q_out_type, positions, rope, slots, stream);
     int rc = check_step_pool(paged, layer, layer + 1);
-    if (rc == KV_OK) rc = check_norm(norm);
+    if (rc == KV_OK) rc = check_norm(norm, paged->head_dim);
     if (rc != KV_OK) return rc;
     AppendCall call{};
     rc = append_call(paged, step, layer, q, k, v, q_out, q_heads, type, q_out_type, positions, rope, slots, stream,
@@ -361,7 +364,7 @@ int append8(const kv_paged8* paged8, const kv_step* step, int32_t layer, const k
             const int32_t* positions, const kv_rope* rope, const kv_norm* norm, hipStream_t stream)
 {
     int rc = check_pool8(paged8, layer, layer + 1);
-    if (rc == KV_OK) rc = check_norm(norm);
+    if (rc == KV_OK) rc = check_norm(norm, paged8->pages.head_dim);
     if (rc != KV_OK) return rc;
     const kv_paged* paged = &paged8->pages;
     AppendCall call{};
