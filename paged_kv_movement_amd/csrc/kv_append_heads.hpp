@@ -783,7 +783,8 @@ __device__ __forceinline__ void page_heads(const AppendHeadsArgs& h, uint32_t it
 #pragma unroll 1
             for (int task = first; task < last; task += kAppendBlock / 64) {
                 float& m = most[task - 2 * h0];
-                // in the second pass the scale is read before the last tokens' call writes it
+                // in the second pass the first tokens' call holds the old ones anew and writes the scale; the later calls
+                // read that scale, which is the largest of what they found and what was there, and come to it again
                 const float found = work(task, c0, count, pass == 0 ? kFind : kPut, pass == 0 && c0 == 0 ? 0.0f : m,
                                          pass == 1 && c0 == 0, alone);
                 if (pass == 0) m = found;
