@@ -844,10 +844,12 @@ __device__ __forceinline__ void narrow_piece(const AttendArgs& a, const AttendIt
     constexpr int32_t kRound = kAttendWaves * kAttendTile;
     clear<DP>(st[0]);
     // 32 tokens' scores, and with them what they add to the state
-    auto scores = [&](f32x4 (&s)[2], u32x4 (&k)[2][J]) {
+    auto clean_k = [&](u32x4 (&k)[2][J]) {
         if (dim < DP)
 #pragma unroll
             for (int i = 0; i < 2; ++i) clear_past<DP, F::byte>(k[i], g, dim);
+    };
+    auto scores = [&](f32x4 (&s)[2], const u32x4 (&k)[2][J]) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             s[i] = f32x4{0, 0, 0, 0};
@@ -855,7 +857,8 @@ __device__ __forceinline__ void narrow_piece(const AttendArgs& a, const AttendIt
             for (int j = 0; j < J; ++j) s[i] = mfma16(k[i][j], q[j], s[i]);
         }
     };
-    auto take = [&](int32_t t, uint32_t valid, f32x4 (&s)[2], uint32_t (&v)[8][J], bool care) {
+    // V where there is no element or no token: 0
+    auto clean_v = [&](uint32_t valid, uint32_t (&v)[8][J]) {
         if (dim < DP)
 #pragma unroll
             for (int x = 0; x < 8; ++x)
@@ -869,6 +872,8 @@ __device__ __forceinline__ void narrow_piece(const AttendArgs& a, const AttendIt
                 for (int y = 0; y < J; ++y)
                     if (!((valid >> (16 * (x / 4) + 4 * g + x % 4)) & 1)) v[x][y] = 0;
         }
+    };
+    auto take = [&](int32_t t, uint32_t valid, f32x4 (&s)[2], uint32_t (&v)[8][J], bool care) {
         u32x4 ph[1], pl[1];
         bool masked = valid != ~0u || t + kAttendTile > all_see;
         if constexpr (F::win) masked = masked || (t < all_from && t + kAttendTile > it.sink);
@@ -907,10 +912,12 @@ __device__ __forceinline__ void narrow_piece(const AttendArgs& a, const AttendIt
             uint32_t v[8][J];
             f32x4 s[2];
             b.keys(k);
+            clean_k(k);
             scores(s, k);
             b.values(v);
             const uint32_t valid = b.valid;
             if (!care) ask(u + kRound);
+            clean_v(valid, v);
             take(token_at<F>(it.span, u), valid, s, v, care);
         };
         if (it.t0 < t1) {
@@ -953,6 +960,10 @@ __device__ __forceinline__ void narrow_piece(const AttendArgs& a, const AttendIt
                 const uint32_t vr = uint32_t(__shfl(some, 16 * (x / 4) + 4 * g + x % 4));
                 load_v<DP>(v[x], vh + uint64_t(vr) * row_bytes, r, dim);
             }
+            // V's zeros before the scores: behind them the compiler waits for all of V ahead of K's second product (one
+            // token over 10000 16.3 us, so 15.5; eight on one KV head 15.9 and 15.0; 24 ragged sequences 150 and 156)
+            clean_k(k);
+            clean_v(valid, v);
             scores(s, k);
             take(t, valid, s, v, care);
         }
