@@ -355,9 +355,9 @@ int check_pool8(const kv_paged8* p, int32_t layer_begin, int32_t layer_end)
     return KV_OK;
 }
 
-// New tokens from which on their q has a launch of its own, where the page kernel's registers do not leave half as many waves
-// (with keys in float32, 45116 tokens 296 us and in one launch 308; 4000 tokens 36.5 and 33.8).
-constexpr int32_t kQApart = 16384;
+// New tokens from which on their q has a launch of its own, where the page kernel's registers do not leave it three waves a
+// SIMD (45116 tokens 231 us and in one launch 269, 16000 97 and 105, 8000 59 and 61; 4000 33 and 32).
+constexpr int32_t kQApart = 8000;
 
 int append8(const kv_paged8* paged8, const kv_step* step, int32_t layer, const kv_rows* q, const kv_rows* k,
             const kv_rows* v, const kv_rows* q_out, int32_t q_heads, kv_type type, kv_type q_out_type,
@@ -607,9 +607,12 @@ int attend_shape(const kv_paged* p, bool bytes, const kv_step* s, int32_t q_head
     // All pieces are cut by the bounds: lengths far below them leave most pieces empty (10000 tokens under a bound of
     // 10000 15 us, of 32768 20, of 131072 45; eight such sequences 67, 124 and 146).
     // In 8 bits a narrow token costs half as much, and the wide ones have to be more: 64 sequences behind two 32768-token
-    // prefixes 192 us with the shares of bf16, 139 with these, 142 with half as many own pieces.  Under a window most own
-    // lengths are cut to it and three times `room` own pieces pay: 32 sequences behind a prefix under a window of 4096
-    // 107 us, with twice 110.
+    // prefixes 131 us, 192 with the shares of bf16, 137 with half as many own pieces, which is better where the own tokens
+    // are few (32 of up to 2000 behind 8192: 46, 50, 45; 48 of up to 400 behind 16384: 60, 60, 58; 32 of up to 8000 behind
+    // 8192: 98, 98, 104).  Under a window most own lengths are cut to it, and three times `room` own pieces pay: 32 sequences
+    // behind 8192 under a window of 4096 105 us, with twice 109; 64 behind two of 32768 under 8192 155 and 174; 24 behind
+    // 4096 under 1024 32.6 and 33.9; but 16 long ones behind 8192 70 and 69, and 48 of up to 400 behind 16384 under as
+    // much 66 and 62.
     const int64_t room = 512, narrow_room = 256, beside_room = (bytes || win != nullptr ? 3 : 2) * room;
     const int64_t prefix_work = pre * prefix_len, own_work = own * own_len * (bytes ? 25 : 60) / 100;
     const bool wide = a.own_wide && (a.prefix_wide || prefix_work == 0);

@@ -116,3 +116,28 @@ def test_append8_of_a_rotation_with_a_gain(dim, rot, interleaved, page, lens, ne
     check_blocks(b, 1, (want, v.double()), (float_bound(k.double(), pos, f, g, rot, interleaved),
                                             torch.zeros(v.shape, dtype=torch.float64)), b.bytes8, b.scales, bytes8, scales,
                  b.q_start)
+
+
+def test_append8_of_many_rows_is_that_of_few():
+    """New tokens enough for q to have a launch of its own: q and the pool as from calls of one sequence each."""
+    H, rep, D, P, n = 2, 2, 64, 16, 2700
+    b = pu.Batch8(11, H, D, P, [n, n + 5, n, 30], [n, n, n - 9, 30], layers=1)
+    bytes8, scales, paged, step = device8(b)
+    rows = b.q_start[-1]
+    assert rows > 8000
+    q, k, v = (b.normal(rows, h, D).cuda() for h in (H * rep, H, H))
+    pos = torch.arange(rows, dtype=torch.int32).cuda()
+    rope, norm = kvm.Rope(D), kvm.Norm(b.normal(D, dtype=FL) + 1, b.normal(D, dtype=FL) + 1)
+    got = kvm.append(paged, step, 0, q, k, v, pos, rope, norm=norm)
+    many = [x.clone() for x in (bytes8, scales)]
+    bytes8.copy_(b.bytes8)
+    scales.copy_(b.scales)
+    own = step.own
+    for s, m in enumerate(b.new):
+        one = kvm.Step(paged, kvm.Tables(own.table[s:s + 1], own.lens[s:s + 1], b.lens[s]), [m])
+        r = slice(b.q_start[s], b.q_start[s] + m)
+        part = kvm.append(paged, one, 0, q[r], k[r], v[r], pos[r], rope, norm=norm)
+        assert torch.equal(part, got[r])
+    torch.cuda.synchronize()
+    assert torch.equal(many[0], bytes8) and torch.equal(many[1].view(torch.int32), scales.view(torch.int32))
+    assert kvm.take_faults() == 0
