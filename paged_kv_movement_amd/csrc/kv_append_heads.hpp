@@ -13,9 +13,11 @@
 //
 // append_heads_rows   one workgroup per token, for q (and, into a bf16 pool, k
 //                     and v).  Bound: memory, as append_rows: 45116 tokens of
-//                     32 query heads and 8 KV heads of 128 in 220 us, 5.0 TB/s
-//                     (without a norm 200); one token in 5.7 us, of which 1.9
-//                     are the weights and the two sums.
+//                     32 query heads and 8 KV heads of 128 in 222 us, 5.0 TB/s
+//                     (without a norm 200; fp16 251, float32, nearly twice the
+//                     bytes, 381); one token in 5.7 us, of which 1.9 are the
+//                     weights and the two sums.  Element by element (rot 20 of
+//                     128) 1025 us.
 // append8_rows        those workgroups for q, and behind them one per (sequence,
 //                     page, some of the heads) for k and v: a wave takes one
 //                     head's K or V of the page, all its new tokens, finds the
@@ -438,7 +440,7 @@ __global__ __launch_bounds__(kAppendBlock) void append_heads_rows(AppendHeadsArg
 // rotated in 64 bits, and becomes a float32 only by rounding to odd, which
 // leaves it on its own side of every border of fewer bits: the bytes and
 // scales are those of the formula.  (v is what it was.)  Of 45116 tokens the
-// pages' part takes 115 to 130 us so and took 90 with keys in float32.
+// pages' part takes 115 us so and took 90 with keys in float32.
 
 template <int kVec>
 struct WideValues {
@@ -508,10 +510,12 @@ constexpr int kHeldUnits = 2;          // units of a lane kept between the look 
 
 // New tokens of one page of a sequence, some of its heads: a wave takes one head's K or V at a time.
 //
-// Bound: waits.  64-bit keys take 163 registers, so there are three waves a SIMD, and they wait 70 % of their time: 45116
-// tokens of 8 KV heads of 128 (277 MB) in 115 to 130 us, 2.1 to 2.4 TB/s; one token of each of 64 sequences 9 us.  Asking for
-// the next task's values while one is worked on, or for the first ahead of the angles, took as long (122 to 137), as did
-// angles without bank conflicts; rounding to odd is 7 us of it and the sines 1.5.
+// Bound: 64-bit arithmetic, and waits.  The vector units work 63 % of the cycles, and with 163 registers there are three
+// waves a SIMD to hide the rest, which wait 48 % of their time: 45116 tokens of 8 KV heads of 128 (277 MB) in 115 us,
+// 2.4 TB/s; one token of each of 64 sequences 8.3 us with its q.  Asking for the next task's values while one is worked on,
+// or for the first ahead of the angles, took as long, as did angles without bank conflicts; rounding to odd is 7 us of it
+// and the sines 1.5.  The whole call takes 232 us with pages of 16 tokens, 255 of 32, 270 of 64, 421 of 128 (whose angles
+// do not fit and are made twice); in float32 392.
 template <class TI, int kVec>
 __device__ __forceinline__ void page_heads(const AppendHeadsArgs& h, uint32_t item, double2* cs, SharedWeights& sh)
 {

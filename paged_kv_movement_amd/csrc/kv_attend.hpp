@@ -810,11 +810,12 @@ struct NarrowShared {
 // they lie are the first product's left operand), and join at the end.
 //
 // Bound: the read of K and V.  16 KiB a wave are in flight, two waves a SIMD:
-// 64 sequences of 9000 to 10000 tokens, 8 KV heads of 128, in 442 to 452 us, 5.6 TB/s.
+// 64 sequences of 9000 to 10000 tokens, 8 KV heads of 128, in 454 us, 5.5 TB/s.
 // One such sequence is 27 pieces a head and the waits from page id to K and V,
 // three rounds of them, and the waves' join: 11.8 us for 41 MB.  In 8 bits the 64
-// take 267 us, 4.7 TB/s, which is what 128-byte rows 1 KiB apart can be read at;
-// the one 10.5 to 11, and a window of 4096 of 32768 tokens in bf16 9.4.
+// take 262 to 268 us, 4.7 TB/s, which is what 128-byte rows 1 KiB apart can be read at;
+// the one 9.3.  A window of 4096 of 32768 tokens 9.5, in 8 bits 8.3; of 4096 of the
+// 64 sequences' 202 and 121.
 template <int DP, class F>
 __device__ __forceinline__ void narrow_piece(const AttendArgs& a, const AttendItem& it, const LayerAt& l, int32_t t1,
                                              NarrowShared<DP>& sh)
@@ -1247,17 +1248,20 @@ __device__ __forceinline__ void wide_half_with_care(RowState<DP> (&st)[NB], cons
 // P, the maximum, the transposition of V) and three products: the vector units
 // are busy 45 % of the cycles and the matrix cores 41 % (counters, at 2.2 GHz,
 // four prompts of up to 1024 tokens behind 4096).  An 8192-token prompt, 32
-// heads of 128: 750 us, 733 TFLOP/s of the formula's products; the second part
+// heads of 128: 742 us, 741 TFLOP/s of the formula's products; the second part
 // of P makes them half as many again.  Without it 14 % shorter and an error 1.4
 // times the output's own rounding.  128 rows a workgroup and two workgroups a
 // CU; with 64 rows K and V come through LDS twice as often.  A window costs what
 // its rows see and the tiles at its two edges: 16262 new tokens of two prompts
-// under a window of 1024 in 510 to 526 us.
+// under a window of 1024 in 519 to 530 us, of 128 in 224.
 //
-// Over bytes the same two parts: four ragged prompts behind a prefix 430 us.  One
-// fp16 part takes 378, but its range ends 2^-25 below the heaviest weight of a
-// piece, and what it drops is still in l: where a few tokens draw the attention
-// and their V is small, the output is the sum of the light ones.
+// Over bytes the same two parts, and every byte is widened by each workgroup that
+// takes it: four ragged prompts behind a prefix 431 us (bf16 383), an 8192-token
+// prompt 823, the window of 1024 590; the vector units are busy 60 %.  One fp16
+// part takes 378, but its range ends 2^-25 below the heaviest weight of a piece,
+// and what it drops is still in l: where a few tokens draw the attention and their
+// V is small, the output is the sum of the light ones.  V's scales had to be near
+// one another for it, too: with pages of zeros in between it was 10.7 ms.
 template <int DP, int NB, class F>
 __device__ __forceinline__ void wide_piece(const AttendArgs& a, const AttendItem& it, const LayerAt& l, int32_t t1,
                                            WideTile<DP>& tile0, WideTile<DP>& tile1)

@@ -8,8 +8,8 @@
 //                the page's bf16.
 //
 // Bound: memory, 3 bytes an element either way.  4 layers of 77482 tokens of 8 KV
-// heads of 128 (1.9 GB) in 347 us and back in 361, 5.5 and 5.3 TB/s, where a
-// large copy reaches 6.7; one layer of 4 x 256 tokens in 5.0 and 4.6.
+// heads of 128 (1.9 GB) in 355 us and back in 365, 5.4 and 5.2 TB/s, where a
+// large copy reaches 6.7; one layer of 4 x 256 tokens in 5.7 and 4.3.
 #pragma once
 
 #include "kv_pool8.hpp"
