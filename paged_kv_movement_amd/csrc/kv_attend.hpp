@@ -844,21 +844,12 @@ __device__ __forceinline__ void narrow_piece(const AttendArgs& a, const AttendIt
     const int32_t first = it.t0 + wave * kAttendTile;
     constexpr int32_t kRound = kAttendWaves * kAttendTile;
     clear<DP>(st[0]);
-    // 32 tokens' scores, and with them what they add to the state
+    // K, V where there is no element (of V no token either): 0
     auto clean_k = [&](u32x4 (&k)[2][J]) {
         if (dim < DP)
 #pragma unroll
             for (int i = 0; i < 2; ++i) clear_past<DP, F::byte>(k[i], g, dim);
     };
-    auto scores = [&](f32x4 (&s)[2], const u32x4 (&k)[2][J]) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            s[i] = f32x4{0, 0, 0, 0};
-#pragma unroll
-            for (int j = 0; j < J; ++j) s[i] = mfma16(k[i][j], q[j], s[i]);
-        }
-    };
-    // V where there is no element or no token: 0
     auto clean_v = [&](uint32_t valid, uint32_t (&v)[8][J]) {
         if (dim < DP)
 #pragma unroll
@@ -872,6 +863,15 @@ __device__ __forceinline__ void narrow_piece(const AttendArgs& a, const AttendIt
 #pragma unroll
                 for (int y = 0; y < J; ++y)
                     if (!((valid >> (16 * (x / 4) + 4 * g + x % 4)) & 1)) v[x][y] = 0;
+        }
+    };
+    // 32 tokens' scores, and with them what they add to the state
+    auto scores = [&](f32x4 (&s)[2], const u32x4 (&k)[2][J]) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            s[i] = f32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int j = 0; j < J; ++j) s[i] = mfma16(k[i][j], q[j], s[i]);
         }
     };
     auto take = [&](int32_t t, uint32_t valid, f32x4 (&s)[2], uint32_t (&v)[8][J], bool care) {
